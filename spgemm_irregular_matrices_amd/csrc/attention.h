@@ -1,0 +1,131 @@
+// Launchers and shared types of the attention kernels
+// (include/spgemm_attention.h).
+#pragma once
+
+#include "../../include/spgemm_attention.h"
+#include "attention_tile.h"
+#include "common.h"
+
+namespace sg {
+
+// A piece of one row of the mask (or of its transpose): the work of one
+// wavefront per key head. slot is where its partial result goes, -1 if it is
+// the whole row and so writes the result itself.
+struct AttnPiece {
+    int64_t first;  // first entry
+    int32_t row;
+    int32_t len;    // entries; 0 only for a row without any
+    int32_t slot;
+    int32_t lead;   // 1 for the first piece of its row
+};
+// A row of more than one piece: the slots that make it up.
+struct AttnSplit {
+    int32_t row;
+    int32_t slot;
+    int32_t count;
+    int32_t pad;
+};
+
+// One direction of the mask, cut into pieces.
+struct AttnSide {
+    int64_t n = 0;          // rows
+    int64_t npieces = 0;
+    int64_t nslots = 0;
+    int64_t nsplits = 0;
+    const AttnPiece* pieces = nullptr;
+    const AttnSplit* splits = nullptr;
+    const int32_t* idx = nullptr;  // the entries' columns
+};
+
+// Rows of a gathered tensor. A row's offset is unit * (its index) << shift
+// bytes, so that it fits 32 bits before the shift; the strides of every
+// dimension are multiples of 1 << shift.
+struct AttnGather {
+    const char* base = nullptr;
+    int64_t head = 0;   // bytes between heads
+    uint32_t unit = 0;
+    uint32_t shift = 0;
+};
+struct AttnRows {
+    char* base = nullptr;
+    int64_t row = 0;    // bytes between rows
+    int64_t head = 0;
+};
+
+struct AttnShape {
+    int type = 0;
+    int hq = 0, hkv = 0, group = 0, dim = 0;
+    int mtiles = 1;      // ceil(group / 16)
+    float scale = 0.f;   // of the scores
+    float c = 0.f;       // scale * log2(e)
+};
+
+struct ForwardArgs {
+    AttnShape s;
+    AttnSide side;
+    AttnRows q, out;
+    AttnGather k, v;
+    float* lse = nullptr;      // may be null
+    float* part = nullptr;     // [slot][hq][dim] unnormalised outputs
+    float* part_ml = nullptr;  // [slot][hq][2]: maximum (base 2) and sum
+};
+void attention_forward(const ForwardArgs& a, hipStream_t st);
+
+struct BackwardArgs {
+    AttnShape s;
+    AttnSide rows, cols;
+    AttnRows q, out, dout, dq, dk, dv;
+    AttnGather k, v;        // gathered by the row pass
+    AttnGather gq, gdout;   // q and dout, gathered by the column pass
+    AttnRows krow, vrow;    // k and v, one row per column of the mask
+    const float* lse = nullptr;
+    float* delta = nullptr;    // [row][hq]
+    float* part_q = nullptr;   // [slot][hq][dim]
+    float* part_kv = nullptr;  // [slot of cols][hkv][2][dim]
+    FastDiv group_div;
+};
+void attention_backward(const BackwardArgs& a, hipStream_t st);
+
+struct PagedArgs {
+    AttnShape s;
+    AttnRows q, out;
+    const char* k = nullptr;
+    const char* v = nullptr;
+    // offsets in units of 1 << shift bytes, as AttnGather
+    uint32_t k_page = 0, k_slot = 0, v_page = 0, v_slot = 0;
+    uint32_t k_shift = 0, v_shift = 0;
+    int64_t k_head = 0, v_head = 0;  // bytes
+    int64_t npages = 0;
+    FastDiv page_div;
+    int64_t seqs = 0, tokens = 0, room = 0;  // room: entries of col
+    const int64_t* rowptr = nullptr;
+    const int32_t* col = nullptr;
+    const int64_t* q_rowptr = nullptr;
+    const int64_t* lengths = nullptr;
+    int32_t max_new = 0, max_length = 0;
+    int32_t piece = 0;     // keys per piece, a multiple of 32
+    int32_t npieces = 1;   // ceil(max_length / piece)
+    float* lse = nullptr;
+    float* part = nullptr;     // [piece][token][hq][dim]
+    float* part_ml = nullptr;  // [piece][token][hq][2]
+};
+void paged_attention(const PagedArgs& a, hipStream_t st);
+
+// XCD x of the 8 gets every eighth work group; this gives each XCD a
+// contiguous eighth of the logical blocks, so that neighbouring pieces of one
+// head, which gather the same key rows, meet in one XCD's L2.
+constexpr int kXcds = 8;
+inline int64_t xcd_grid(int64_t blocks) { return ceil_div(blocks, kXcds) * kXcds; }
+__device__ __forceinline__ int64_t xcd_block() {
+    const uint32_t per = gridDim.x / kXcds;
+    return (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+}
+
+template <class F>
+void with_type(int type, int dim, F&& f) {
+    if (type == SPGEMM_TYPE_BF16) with_dim<__bf16>(dim, f);
+    else if (type == SPGEMM_TYPE_F16) with_dim<_Float16>(dim, f);
+    else with_dim<float>(dim, f);
+}
+
+}  // namespace sg

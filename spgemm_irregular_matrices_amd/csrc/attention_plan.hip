@@ -1,0 +1,553 @@
+// Plans of attention over a CSR mask, argument checks, and the C ABI of
+// include/spgemm_attention.h.
+#include <cmath>
+#include <new>
+
+#include "attention.h"
+#include "kernels.h"
+#include "primitives.h"
+
+using namespace sg;
+
+struct spgemm_attention_plan_s {
+    int device = 0;
+    int64_t nrows = 0, ncols = 0, nnz = 0;
+    bool backward = false;
+    AttnSide rows, cols;
+    Arena ar;  // pieces, splits and entries of both sides; never changed after creation
+};
+
+namespace {
+
+// ---------------------------------------------------------------- plan
+// Entries per piece. Long rows are cut so that the longest wavefront stays
+// near the mean one's work: about 4096 pieces over all entries, between 128
+// entries (a piece's fixed costs, its partial result among them, are about
+// those of 16 entries) and 1024.
+int64_t piece_length(int64_t nnz) {
+    const int64_t want = ceil_div(ceil_div(nnz, 4096), 32) * 32;
+    return want < 128 ? 128 : want > 1024 ? 1024 : want;
+}
+
+struct RowPieces {
+    const int64_t* rp;
+    int64_t len;
+    __host__ __device__ int64_t count(int64_t i) const {
+        const int64_t n = rp[i + 1] - rp[i];
+        return n <= len ? 1 : (n + len - 1) / len;
+    }
+    __device__ int64_t operator()(int64_t i) const { return count(i); }
+};
+struct RowSlots {
+    RowPieces p;
+    __device__ int64_t operator()(int64_t i) const {
+        const int64_t c = p.count(i);
+        return c > 1 ? c : 0;
+    }
+};
+struct RowSplit {
+    RowPieces p;
+    __device__ int64_t operator()(int64_t i) const { return p.count(i) > 1 ? 1 : 0; }
+};
+
+__global__ void k_fill_pieces(RowPieces rows, int64_t n, const int64_t* piece0,
+                              const int64_t* slot0, const int64_t* split0, AttnPiece* pieces,
+                              AttnSplit* splits, int64_t npieces) {
+    const int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (g >= npieces) return;
+    const int64_t row = upper_index(piece0, int64_t(0), n, g);
+    const int64_t b = rows.rp[row], e = rows.rp[row + 1];
+    const int64_t count = piece0[row + 1] - piece0[row], k = g - piece0[row];
+    // equal pieces, of whole tiles
+    const int64_t each = ((e - b + count - 1) / count + 31) / 32 * 32;
+    AttnPiece p;
+    p.first = min(b + k * each, e);
+    p.row = (int32_t)row;
+    p.len = (int32_t)min(each, e - p.first);
+    p.slot = count > 1 ? (int32_t)(slot0[row] + k) : -1;
+    p.lead = k == 0;
+    pieces[g] = p;
+    if (count > 1 && k == 0) splits[split0[row]] = {(int32_t)row, p.slot, (int32_t)count, 0};
+}
+
+__global__ void k_count_cols(const int32_t* col, int64_t nnz, int32_t* count) {
+    for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < nnz;
+         e += (int64_t)gridDim.x * blockDim.x)
+        atomicAdd(&count[col[e]], 1);
+}
+__global__ void k_entry_rows(const int64_t* rp, int64_t n, int64_t nnz, int32_t* row,
+                             int32_t* entry) {
+    const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (e >= nnz) return;
+    row[e] = (int32_t)upper_index(rp, int64_t(0), n, e);
+    entry[e] = (int32_t)e;
+}
+__global__ void k_gather(const int32_t* src, const int32_t* perm, int64_t n, int32_t* dst) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < n) dst[i] = src[perm[i]];
+}
+struct LoadI32 {
+    const int32_t* p;
+    __device__ int64_t operator()(int64_t i) const { return p[i]; }
+};
+struct ColDigit {
+    const int32_t* col;
+    const int32_t* entry;
+    int shift;
+    __device__ int operator()(int64_t i) const { return (col[entry[i]] >> shift) & 15; }
+};
+
+
+AttnSide make_side(const char* name, const int64_t* rp, int64_t n, int64_t nnz, const int32_t* idx,
+                   Arena& keep, Arena& tmp, hipStream_t st) {
+    AttnSide s;
+    s.n = n;
+    s.idx = idx;
+    if (n == 0) return s;
+    const std::string nm(name);
+    const RowPieces rows{rp, piece_length(nnz)};
+    int64_t* piece0 = tmp.get<int64_t>("piece0", (size_t)n + 1);
+    int64_t* slot0 = tmp.get<int64_t>("slot0", (size_t)n + 1);
+    int64_t* split0 = tmp.get<int64_t>("split0", (size_t)n + 1);
+    scan_exclusive(rows, n, piece0, tmp, st);
+    scan_exclusive(RowSlots{rows}, n, slot0, tmp, st);
+    scan_exclusive(RowSplit{rows}, n, split0, tmp, st);
+    int64_t tot[3];
+    SG_HIP(hipMemcpyAsync(&tot[0], piece0 + n, 8, hipMemcpyDeviceToHost, st));
+    SG_HIP(hipMemcpyAsync(&tot[1], slot0 + n, 8, hipMemcpyDeviceToHost, st));
+    SG_HIP(hipMemcpyAsync(&tot[2], split0 + n, 8, hipMemcpyDeviceToHost, st));
+    SG_HIP(hipStreamSynchronize(st));
+    s.npieces = tot[0];
+    s.nslots = tot[1];
+    s.nsplits = tot[2];
+    if (s.npieces > 0x7fffffffLL) throw OverflowError("more pieces than supported");
+    AttnPiece* pieces = static_cast<AttnPiece*>(
+        keep.get(nm + "_pieces", (size_t)s.npieces * sizeof(AttnPiece)));
+    AttnSplit* splits = static_cast<AttnSplit*>(
+        keep.get(nm + "_splits", (size_t)s.nsplits * sizeof(AttnSplit)));
+    hipLaunchKernelGGL(k_fill_pieces, dim3(grid_1d(ceil_div(s.npieces, 256))), dim3(256), 0, st,
+                       rows, n, piece0, slot0, split0, pieces, splits, s.npieces);
+    SG_LAUNCH_CHECK();
+    s.pieces = pieces;
+    s.splits = splits;
+    return s;
+}
+
+int build_plan(spgemm_attention_plan p, const spgemm_csr* mask, bool backward, hipStream_t st) {
+    Arena tmp;
+    DevCSR m;
+    m.n = mask->nrows;
+    m.m = mask->ncols;
+    m.nnz = mask->nnz;
+    m.rp = mask->rowptr;
+    m.col = mask->col;
+    int* flag = tmp.get<int>("flag", 1);
+    fill<int>(flag, 1, 0, st);
+    launch_validate(m, flag, st);
+    int bad = 0;
+    SG_HIP(hipMemcpyAsync(&bad, flag, sizeof(int), hipMemcpyDeviceToHost, st));
+    SG_HIP(hipStreamSynchronize(st));
+    if (bad) return SPGEMM_ERR_INDEX_RANGE;
+    p->nrows = m.n;
+    p->ncols = m.m;
+    p->nnz = m.nnz;
+    p->backward = backward;
+    int32_t* col = p->ar.get<int32_t>("col", (size_t)m.nnz);
+    copy<int32_t>(col, m.col, m.nnz, st);
+    p->rows = make_side("rows", m.rp, m.n, m.nnz, col, p->ar, tmp, st);
+    if (backward) {
+        int32_t* count = tmp.get<int32_t>("count", (size_t)m.m + 1);
+        int64_t* cp = tmp.get<int64_t>("colptr", (size_t)m.m + 1);
+        int32_t* trow = p->ar.get<int32_t>("trow", (size_t)m.nnz);
+        fill<int32_t>(count, m.m + 1, 0, st);
+        if (m.nnz > 0) {
+            hipLaunchKernelGGL(k_count_cols,
+                               dim3(grid_1d(std::min<int64_t>(ceil_div(m.nnz, 256), 8192))),
+                               dim3(256), 0, st, col, m.nnz, count);
+            SG_LAUNCH_CHECK();
+        }
+        scan_exclusive(LoadI32{count}, m.m, cp, tmp, st);
+        if (m.nnz > 0) {
+            // a stable radix sort of the entries by column, 4 bits a pass, so
+            // that the rows of a column ascend (and its sums have one order)
+            const unsigned g = grid_1d(ceil_div(m.nnz, 256));
+            int32_t* row = tmp.get<int32_t>("row", (size_t)m.nnz);
+            int32_t* cur = tmp.get<int32_t>("cur", (size_t)m.nnz);
+            int32_t* next = tmp.get<int32_t>("next", (size_t)m.nnz);
+            int32_t* perm = tmp.get<int32_t>("perm", (size_t)m.nnz);
+            int64_t* bins = tmp.get<int64_t>("bins", 17);
+            hipLaunchKernelGGL(k_entry_rows, dim3(g), dim3(256), 0, st, m.rp, m.n, m.nnz, row, cur);
+            SG_LAUNCH_CHECK();
+            for (int shift = 0; shift < 31 && (m.m - 1) >> shift > 0; shift += 4) {
+                partition(ColDigit{col, cur, shift}, m.nnz, 16, perm, nullptr, bins, tmp, st);
+                hipLaunchKernelGGL(k_gather, dim3(g), dim3(256), 0, st, cur, perm, m.nnz, next);
+                SG_LAUNCH_CHECK();
+                std::swap(cur, next);
+            }
+            hipLaunchKernelGGL(k_gather, dim3(g), dim3(256), 0, st, row, cur, m.nnz, trow);
+            SG_LAUNCH_CHECK();
+        }
+        p->cols = make_side("cols", cp, m.m, m.nnz, trow, p->ar, tmp, st);
+    }
+    SG_HIP(hipStreamSynchronize(st));  // before the temporary buffers go
+    return SPGEMM_OK;
+}
+
+// ---------------------------------------------------------------- checks
+int type_size(int32_t t) { return t == SPGEMM_TYPE_F32 ? 4 : 2; }
+
+bool desc_valid(const spgemm_attention_desc* d) {
+    if (!d || d->type < SPGEMM_TYPE_BF16 || d->type > SPGEMM_TYPE_F32) return false;
+    if (d->heads_q < 1 || d->heads_kv < 1 || d->heads_q > SPGEMM_ATTENTION_MAX_HEADS ||
+        d->heads_q % d->heads_kv != 0)
+        return false;
+    if (d->head_dim < 1 || d->head_dim > SPGEMM_ATTENTION_MAX_HEAD_DIM ||
+        d->head_dim * type_size(d->type) % 16 != 0)
+        return false;
+    return std::isfinite(d->scale) && std::fabs(d->scale) < 1e30;
+}
+
+AttnShape make_shape(const spgemm_attention_desc* d) {
+    AttnShape s;
+    s.type = d->type;
+    s.hq = d->heads_q;
+    s.hkv = d->heads_kv;
+    s.group = s.hq / s.hkv;
+    s.dim = d->head_dim;
+    s.mtiles = (s.group + 15) / 16;
+    s.scale = (float)d->scale;
+    s.c = (float)(d->scale * 1.4426950408889634);
+    return s;
+}
+
+// A stride over a dimension of n places, in bytes: 0 where it is never used.
+// -1 if it is not a stride this library takes.
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+int64_t stride_bytes(int64_t stride, int64_t n, int size) {
+    if (n <= 1) return 0;
+    if (stride < 0 || stride > kMaxStride || stride * size % 16 != 0) return -1;
+    return stride * size;
+}
+
+bool rows_valid(const spgemm_rows* x, int64_t n, int32_t heads, const spgemm_attention_desc* d,
+                bool output, AttnRows* r) {
+    if (!x) return false;
+    if (n == 0) return true;  // no element: nothing of it is used
+    const int size = type_size(d->type);
+    r->base = static_cast<char*>(x->data);
+    r->row = stride_bytes(x->stride_row, n, size);
+    r->head = stride_bytes(x->stride_head, heads, size);
+    if (!r->base || reinterpret_cast<uintptr_t>(r->base) % 16 != 0 || r->row < 0 || r->head < 0)
+        return false;
+    if (!output) return true;
+    // rows of an output do not overlap: one dimension's stride passes the
+    // whole of the other
+    const int64_t line = (int64_t)d->head_dim * size;
+    const __int128 heads_span = (__int128)r->head * (heads - 1) + line;
+    const __int128 rows_span = (__int128)r->row * (n - 1) + line;
+    const bool rows_out = (heads == 1 || r->head >= line) && (n == 1 || r->row >= heads_span);
+    const bool heads_out = (n == 1 || r->row >= line) && (heads == 1 || r->head >= rows_span);
+    return rows_out || heads_out;
+}
+
+// The largest power of two that divides every (nonzero) stride, and whether
+// the extent in units of it fits 32 bits.
+bool gather_unit(const int64_t* strides, const int64_t* counts, int n, uint32_t* shift) {
+    int64_t all = int64_t(1) << 30;
+    for (int i = 0; i < n; ++i) all |= strides[i];
+    *shift = (uint32_t)__builtin_ctzll((unsigned long long)all);
+    __int128 span = 0;
+    for (int i = 0; i < n; ++i)
+        if (counts[i] > 1) span += (__int128)(strides[i] >> *shift) * (counts[i] - 1);
+    return span <= 0xffffffffLL;
+}
+
+// heads = 1: the head is added to the base by the kernel, in 64 bits.
+bool make_gather(const AttnRows& r, int64_t n, int64_t heads, AttnGather* g) {
+    const int64_t strides[2] = {r.row, r.head}, counts[2] = {n, heads};
+    g->base = r.base;
+    g->head = r.head;
+    if (!gather_unit(strides, counts, 2, &g->shift)) return false;
+    g->unit = (uint32_t)(r.row >> g->shift);
+    return true;
+}
+
+// Carves a workspace into 256-byte aligned parts.
+struct Carver {
+    char* base;
+    int64_t used = 0;
+    float* take(__int128 floats) {
+        const int64_t at = used;
+        const __int128 end = (__int128)at + (floats * 4 + 255) / 256 * 256;
+        if (end > ((__int128)1 << 60)) throw OverflowError("workspace size");
+        used = (int64_t)end;
+        return base && floats > 0 ? reinterpret_cast<float*>(base + at) : nullptr;
+    }
+};
+
+int64_t carve_forward(spgemm_attention_plan p, const AttnShape& s, void* ws, ForwardArgs* a) {
+    Carver c{static_cast<char*>(ws)};
+    a->part = c.take((__int128)p->rows.nslots * s.hq * s.dim);
+    a->part_ml = c.take((__int128)p->rows.nslots * s.hq * 2);
+    return c.used;
+}
+int64_t carve_backward(spgemm_attention_plan p, const AttnShape& s, void* ws, BackwardArgs* a) {
+    Carver c{static_cast<char*>(ws)};
+    a->delta = c.take((__int128)p->nrows * s.hq);
+    a->part_q = c.take((__int128)p->rows.nslots * s.hq * s.dim);
+    a->part_kv = c.take((__int128)p->cols.nslots * s.hkv * 2 * s.dim);
+    return c.used;
+}
+
+bool workspace_valid(const void* ws, int64_t bytes, int64_t need) {
+    return need == 0 || (ws && reinterpret_cast<uintptr_t>(ws) % 256 == 0 && bytes >= need);
+}
+
+bool plan_here(spgemm_attention_plan p) {
+    int dev = -1;
+    return hipGetDevice(&dev) == hipSuccess && dev == p->device;
+}
+
+// ---------------------------------------------------------------- paged
+bool batch_sizes_valid(const spgemm_paged_batch* b) {
+    return b && b->pages && b->pages->nrows >= 0 && b->tokens >= 0 && b->max_new >= 0 &&
+           b->max_length >= 0;
+}
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+bool batch_sizes_fit(const spgemm_paged_batch* b, const spgemm_attention_desc* d) {
+    return b->pages->nrows < kMaxTokens && b->tokens * d->heads_q < 0x7fffffffLL &&
+           b->tokens <= kMaxTokens && b->max_length <= kMaxTokens;
+}
+
+// Keys per piece. Few rows: the keys are cut until about 4096 wavefronts (16
+// per compute unit) have a piece each, of 64 keys at least.
+void shape_pieces(PagedArgs* a) {
+    const int64_t tiles = ceil_div((int64_t)a->max_new * a->s.group, 16);
+    const int64_t units = std::max<int64_t>(a->seqs * a->s.hkv * tiles, 1);
+    const int64_t most = std::max<int64_t>(ceil_div(a->max_length, 64), 1);
+    const int64_t want = std::min(std::max<int64_t>(4096 / units, 1), most);
+    a->piece = (int32_t)std::max<int64_t>(ceil_div(ceil_div(a->max_length, want), 32) * 32, 32);
+    a->npieces = (int32_t)std::max<int64_t>(ceil_div(a->max_length, a->piece), 1);
+}
+
+int64_t carve_paged(void* ws, PagedArgs* a) {
+    Carver c{static_cast<char*>(ws)};
+    if (a->npieces > 1) {
+        const __int128 rows = (__int128)a->npieces * a->tokens * a->s.hq;
+        a->part = c.take(rows * a->s.dim);
+        a->part_ml = c.take(rows * 2);
+    }
+    return c.used;
+}
+
+void batch_sizes(const spgemm_paged_batch* b, PagedArgs* a) {
+    a->seqs = b->pages->nrows;
+    a->tokens = b->tokens;
+    a->max_new = (int32_t)std::min(b->max_new, b->tokens);
+    a->max_length = (int32_t)b->max_length;
+    shape_pieces(a);
+}
+
+template <class F>
+int guarded(F&& f) {
+    try {
+        return f();
+    } catch (const OomError&) {
+        return SPGEMM_ERR_OUT_OF_MEMORY;
+    } catch (const OverflowError&) {
+        return SPGEMM_ERR_OVERFLOW;
+    } catch (const HipError& e) {
+        return e.code == hipErrorOutOfMemory ? SPGEMM_ERR_OUT_OF_MEMORY : SPGEMM_ERR_HIP;
+    } catch (const std::bad_alloc&) {
+        return SPGEMM_ERR_OUT_OF_MEMORY;
+    } catch (...) {
+        return SPGEMM_ERR_HIP;
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+SPGEMM_API int spgemm_attention_plan_create(spgemm_attention_plan* out, const spgemm_csr* mask,
+                                            int32_t backward, void* stream) {
+    if (!out) return SPGEMM_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!mask || mask->nrows < 0 || mask->ncols < 0 || mask->nnz < 0 || !mask->rowptr ||
+        (mask->nnz > 0 && !mask->col))
+        return SPGEMM_ERR_INVALID_ARG;
+    if (mask->ncols > 0x7fffffffLL || mask->nrows >= 0x7fffffffLL || mask->nnz > 0x7fffffffLL)
+        return SPGEMM_ERR_OVERFLOW;
+    spgemm_attention_plan p = nullptr;
+    const int rc = guarded([&]() -> int {
+        p = new spgemm_attention_plan_s();
+        SG_HIP(hipGetDevice(&p->device));
+        return build_plan(p, mask, backward != 0, (hipStream_t)stream);
+    });
+    if (rc != SPGEMM_OK) {
+        if (p) (void)hipStreamSynchronize((hipStream_t)stream);
+        delete p;
+        return rc;
+    }
+    *out = p;
+    return SPGEMM_OK;
+}
+
+SPGEMM_API void spgemm_attention_plan_destroy(spgemm_attention_plan p) {
+    if (!p) return;
+    (void)hipDeviceSynchronize();
+    delete p;
+}
+
+SPGEMM_API int spgemm_attention_workspace(spgemm_attention_plan p,
+                                          const spgemm_attention_desc* desc, int32_t backward,
+                                          int64_t* bytes) {
+    if (!p || !desc_valid(desc) || !bytes) return SPGEMM_ERR_INVALID_ARG;
+    if (backward && !p->backward) return SPGEMM_ERR_NOT_READY;
+    return guarded([&]() -> int {
+        const AttnShape s = make_shape(desc);
+        ForwardArgs f;
+        BackwardArgs b;
+        *bytes = backward ? carve_backward(p, s, nullptr, &b) : carve_forward(p, s, nullptr, &f);
+        return SPGEMM_OK;
+    });
+}
+
+SPGEMM_API int spgemm_attention_forward(spgemm_attention_plan p, const spgemm_attention_desc* desc,
+                                        const spgemm_rows* q, const spgemm_rows* k,
+                                        const spgemm_rows* v, const spgemm_rows* out, float* lse,
+                                        void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!p || !desc_valid(desc)) return SPGEMM_ERR_INVALID_ARG;
+    return guarded([&]() -> int {
+        ForwardArgs a;
+        a.s = make_shape(desc);
+        a.side = p->rows;
+        AttnRows kr, vr;
+        if (!rows_valid(q, p->nrows, a.s.hq, desc, false, &a.q) ||
+            !rows_valid(k, p->ncols, a.s.hkv, desc, false, &kr) ||
+            !rows_valid(v, p->ncols, a.s.hkv, desc, false, &vr) ||
+            !rows_valid(out, p->nrows, a.s.hq, desc, true, &a.out))
+            return SPGEMM_ERR_INVALID_ARG;
+        if (!make_gather(kr, p->ncols, 1, &a.k) || !make_gather(vr, p->ncols, 1, &a.v))
+            return SPGEMM_ERR_OVERFLOW;
+        if (!workspace_valid(workspace, workspace_bytes, carve_forward(p, a.s, workspace, &a)) ||
+            !plan_here(p))
+            return SPGEMM_ERR_INVALID_ARG;
+        a.lse = lse;
+        attention_forward(a, (hipStream_t)stream);
+        return SPGEMM_OK;
+    });
+}
+
+SPGEMM_API int spgemm_attention_backward(spgemm_attention_plan p,
+                                         const spgemm_attention_desc* desc, const spgemm_rows* q,
+                                         const spgemm_rows* k, const spgemm_rows* v,
+                                         const spgemm_rows* out, const float* lse,
+                                         const spgemm_rows* dout, const spgemm_rows* dq,
+                                         const spgemm_rows* dk, const spgemm_rows* dv,
+                                         void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!p || !desc_valid(desc) || (!lse && p->nrows > 0)) return SPGEMM_ERR_INVALID_ARG;
+    if (!p->backward) return SPGEMM_ERR_NOT_READY;
+    return guarded([&]() -> int {
+        BackwardArgs a;
+        a.s = make_shape(desc);
+        a.rows = p->rows;
+        a.cols = p->cols;
+        if (!rows_valid(q, p->nrows, a.s.hq, desc, false, &a.q) ||
+            !rows_valid(k, p->ncols, a.s.hkv, desc, false, &a.krow) ||
+            !rows_valid(v, p->ncols, a.s.hkv, desc, false, &a.vrow) ||
+            !rows_valid(out, p->nrows, a.s.hq, desc, false, &a.out) ||
+            !rows_valid(dout, p->nrows, a.s.hq, desc, false, &a.dout) ||
+            !rows_valid(dq, p->nrows, a.s.hq, desc, true, &a.dq) ||
+            !rows_valid(dk, p->ncols, a.s.hkv, desc, true, &a.dk) ||
+            !rows_valid(dv, p->ncols, a.s.hkv, desc, true, &a.dv))
+            return SPGEMM_ERR_INVALID_ARG;
+        if (!make_gather(a.krow, p->ncols, 1, &a.k) || !make_gather(a.vrow, p->ncols, 1, &a.v) ||
+            !make_gather(a.q, p->nrows, a.s.hq, &a.gq) ||
+            !make_gather(a.dout, p->nrows, a.s.hq, &a.gdout))
+            return SPGEMM_ERR_OVERFLOW;
+        if (!workspace_valid(workspace, workspace_bytes, carve_backward(p, a.s, workspace, &a)) ||
+            !plan_here(p))
+            return SPGEMM_ERR_INVALID_ARG;
+        a.lse = lse;
+        a.group_div = FastDiv((uint32_t)a.s.group);
+        attention_backward(a, (hipStream_t)stream);
+        return SPGEMM_OK;
+    });
+}
+
+SPGEMM_API int spgemm_paged_attention_workspace(const spgemm_attention_desc* desc,
+                                                const spgemm_paged_batch* batch, int64_t* bytes) {
+    if (!desc_valid(desc) || !batch_sizes_valid(batch) || !bytes) return SPGEMM_ERR_INVALID_ARG;
+    if (!batch_sizes_fit(batch, desc)) return SPGEMM_ERR_OVERFLOW;
+    return guarded([&]() -> int {
+        PagedArgs a;
+        a.s = make_shape(desc);
+        batch_sizes(batch, &a);
+        *bytes = carve_paged(nullptr, &a);
+        return SPGEMM_OK;
+    });
+}
+
+SPGEMM_API int spgemm_paged_attention(const spgemm_attention_desc* desc, const spgemm_rows* q,
+                                      const spgemm_paged_cache* cache,
+                                      const spgemm_paged_batch* batch, const spgemm_rows* out,
+                                      float* lse, void* workspace, int64_t workspace_bytes,
+                                      void* stream) {
+    if (!desc_valid(desc) || !batch_sizes_valid(batch) || !cache) return SPGEMM_ERR_INVALID_ARG;
+    const spgemm_csr* pg = batch->pages;
+    if (pg->nnz < 0 || cache->npages < 0 || cache->page_size < 1 || pg->ncols != cache->npages)
+        return SPGEMM_ERR_INVALID_ARG;
+    if (!batch_sizes_fit(batch, desc) || pg->nnz > 0x7fffffffLL || cache->npages > 0x7fffffffLL ||
+        cache->page_size > kMaxTokens)
+        return SPGEMM_ERR_OVERFLOW;
+    return guarded([&]() -> int {
+        PagedArgs a;
+        a.s = make_shape(desc);
+        batch_sizes(batch, &a);
+        if (!rows_valid(q, a.tokens, a.s.hq, desc, false, &a.q) ||
+            !rows_valid(out, a.tokens, a.s.hq, desc, true, &a.out))
+            return SPGEMM_ERR_INVALID_ARG;
+        if (a.seqs == 0 || a.tokens == 0 || a.max_new == 0) return SPGEMM_OK;
+        if (!pg->rowptr || (pg->nnz > 0 && !pg->col) || !batch->q_rowptr || !batch->lengths)
+            return SPGEMM_ERR_INVALID_ARG;
+        const int size = type_size(desc->type);
+        const int64_t counts[2] = {cache->npages, cache->page_size};
+        const int64_t ks[3] = {stride_bytes(cache->k_stride_page, counts[0], size),
+                               stride_bytes(cache->k_stride_slot, counts[1], size),
+                               stride_bytes(cache->k_stride_head, a.s.hkv, size)};
+        const int64_t vs[3] = {stride_bytes(cache->v_stride_page, counts[0], size),
+                               stride_bytes(cache->v_stride_slot, counts[1], size),
+                               stride_bytes(cache->v_stride_head, a.s.hkv, size)};
+        for (int i = 0; i < 3; ++i)
+            if (ks[i] < 0 || vs[i] < 0) return SPGEMM_ERR_INVALID_ARG;
+        a.k = static_cast<const char*>(cache->k);
+        a.v = static_cast<const char*>(cache->v);
+        if (cache->npages > 0 &&
+            (!a.k || !a.v || reinterpret_cast<uintptr_t>(a.k) % 16 != 0 ||
+             reinterpret_cast<uintptr_t>(a.v) % 16 != 0))
+            return SPGEMM_ERR_INVALID_ARG;
+        if (!gather_unit(ks, counts, 2, &a.k_shift) || !gather_unit(vs, counts, 2, &a.v_shift))
+            return SPGEMM_ERR_OVERFLOW;
+        a.k_page = (uint32_t)(ks[0] >> a.k_shift);
+        a.k_slot = (uint32_t)(ks[1] >> a.k_shift);
+        a.v_page = (uint32_t)(vs[0] >> a.v_shift);
+        a.v_slot = (uint32_t)(vs[1] >> a.v_shift);
+        a.k_head = ks[2];
+        a.v_head = vs[2];
+        a.npages = cache->npages;
+        a.page_div = FastDiv((uint32_t)cache->page_size);
+        a.room = pg->nnz;
+        a.rowptr = pg->rowptr;
+        a.col = pg->col;
+        a.q_rowptr = batch->q_rowptr;
+        a.lengths = batch->lengths;
+        a.lse = lse;
+        if (!workspace_valid(workspace, workspace_bytes, carve_paged(workspace, &a)))
+            return SPGEMM_ERR_INVALID_ARG;
+        paged_attention(a, (hipStream_t)stream);
+        return SPGEMM_OK;
+    });
+}
+
+}  // extern "C"

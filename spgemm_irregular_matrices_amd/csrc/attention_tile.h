@@ -1,0 +1,328 @@
+// One wavefront's share of softmax attention over a list of gathered keys:
+// the tile operations that the attention kernels are put together from.
+//
+// A tile is 16 query rows (the query heads that share one key head, or
+// neighbouring tokens too) against KT keys that lie anywhere in memory. Both
+// products run on the matrix units with the keys on the side that needs no
+// transpose of the probabilities:
+//
+//   S^T = K Q^T     A operand: K rows (lane l: key l%16), B operand: Q rows
+//   O^T += V^T P^T  A operand: V^T (lane l: an index of the head dimension),
+//                   B operand: P^T (lane l: query l%16)
+//
+// A 16x16 result holds, in lane l and register r, row 4*(l/16)+r of column
+// l%16. So S^T leaves 4 keys of one query in each lane, which is what the B
+// operand of the second product wants if its inner index numbers the keys as
+// (4*(l/16)+r of the tile's first 16, then of its second 16): the
+// probabilities never leave the lane, and a query's running maximum, sum and
+// rescaling are one value per lane. V^T is not loaded transposed: each lane
+// takes 16 bytes of each of its 8 keys' rows (16 lanes read a whole row), and
+// the 8x8 block is turned over in registers with byte permutes; the c-th of
+// the lane's 8 head-dimension indices goes into the c-th product.
+#pragma once
+
+#include "common.h"
+
+namespace sg {
+
+using f32x4 = float __attribute__((ext_vector_type(4)));
+using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
+using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
+using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
+using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
+using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
+using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// exp2 and log2 of the vector unit (1 ulp; results below the smallest normal
+// number become 0, which is far below the rounding of any sum they enter)
+__device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float fast_log2(float x) { return __builtin_amdgcn_logf(x); }
+
+// Two floats rounded to nearest even and packed, the first in the low half.
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (std::is_same<T, __bf16>::value)
+        return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+    else
+        return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+}
+template <class T>
+__device__ __forceinline__ void unpack2(uint32_t x, float& a, float& b) {
+    if constexpr (std::is_same<T, __bf16>::value) {
+        a = __builtin_bit_cast(float, x << 16);
+        b = __builtin_bit_cast(float, x & 0xffff0000u);
+    } else {
+        const f16x2 h = __builtin_bit_cast(f16x2, x);
+        a = (float)h[0];
+        b = (float)h[1];
+    }
+}
+
+template <class T>
+__device__ __forceinline__ f32x4 mfma32(u32x4 a, u32x4 b, f32x4 c) {
+    if constexpr (std::is_same<T, __bf16>::value)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// Largest / sum over the four lanes that hold one query (l%16 alike).
+__device__ __forceinline__ float quad_max(float x) {
+    x = fmaxf(x, __shfl_xor(x, 16, kWave));
+    return fmaxf(x, __shfl_xor(x, 32, kWave));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+    x += __shfl_xor(x, 16, kWave);
+    return x + __shfl_xor(x, 32, kWave);
+}
+
+// Unsigned division of n < 2^31 by a divisor fixed at launch: with
+// s = ceil(log2 d) and mul = floor(2^(31+s) / d) + 1, the error of
+// mul * n / 2^(31+s) is below n * d / (d * 2^(31+s)) < 1 / d.
+struct FastDiv {
+    uint32_t d = 1, mul = 0, shift = 0;
+    __host__ __device__ FastDiv() = default;
+    __host__ explicit FastDiv(uint32_t d_) : d(d_) {
+        if (d <= 1) return;
+        uint32_t s = 0;
+        while ((1ull << s) < d) ++s;
+        mul = (uint32_t)((1ull << (31 + s)) / d + 1);
+        shift = s - 1;
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t n) const {
+        return d == 1 ? n : __umulhi(n, mul) >> shift;
+    }
+};
+
+// The tile geometry for element type T and a head dimension padded to DP.
+// FULL: the head dimension is DP itself, so that no chunk needs a check.
+template <class T, int DP, bool FULL>
+struct Tile {
+    static constexpr bool k16 = sizeof(T) == 2;
+    static constexpr int KT = k16 ? 32 : 16;     // keys per tile
+    static constexpr int KSUB = KT / 16;         // 16-key results of S^T
+    static constexpr int VK = KT / 4;            // keys per lane
+    static constexpr int QS = DP * (int)sizeof(T) / 64;  // 64-byte steps of a row
+    static constexpr int CHL = k16 && DP >= 128 ? 8 : 4;  // head-dimension values per V chunk
+    static constexpr int U = DP / (16 * CHL);    // V chunks per lane and key
+    static constexpr int VW = CHL * (int)sizeof(T) / 4;   // words per V chunk
+
+    struct RowFrag { u32x4 w[QS]; };        // a row as A or B operand of S^T
+    struct Acc { f32x4 o[U][CHL]; };        // O^T
+    struct Probs { uint32_t w[k16 ? 4 : 4]; };  // P^T as B operand (floats' bits if T is float)
+    struct VBlock { uint32_t w[VK][VW]; };  // one V chunk of the lane's keys
+
+    // The 16-byte pieces 4*t + l/16 of a row; pieces from row_bytes on are 0.
+    static __device__ __forceinline__ void load_row(const char* row, int row_bytes, RowFrag& f) {
+        const int at = 16 * (lane_id() >> 4);
+#pragma unroll
+        for (int t = 0; t < QS; ++t) {
+            if (FULL || 64 * t + at < row_bytes)
+                f.w[t] = *reinterpret_cast<const u32x4*>(row + 64 * t + at);
+            else
+                f.w[t] = u32x4{0, 0, 0, 0};
+        }
+    }
+    static __device__ __forceinline__ void zero_row(RowFrag& f) {
+#pragma unroll
+        for (int t = 0; t < QS; ++t) f.w[t] = u32x4{0, 0, 0, 0};
+    }
+
+    // This lane's share of the products a[i] * b[i].
+    static __device__ __forceinline__ float dot_lane(const RowFrag& a, const RowFrag& b) {
+        float x = 0.f;
+#pragma unroll
+        for (int t = 0; t < QS; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (k16) {
+                    float a0, a1, b0, b1;
+                    unpack2<T>(a.w[t][i], a0, a1);
+                    unpack2<T>(b.w[t][i], b0, b1);
+                    x = fmaf(a0, b0, x);
+                    x = fmaf(a1, b1, x);
+                } else {
+                    x = fmaf(__builtin_bit_cast(float, (uint32_t)a.w[t][i]),
+                             __builtin_bit_cast(float, (uint32_t)b.w[t][i]), x);
+                }
+            }
+        return x;
+    }
+
+    // c + A B^T over the head dimension.
+    static __device__ __forceinline__ f32x4 dot(const RowFrag& a, const RowFrag& b, f32x4 c) {
+#pragma unroll
+        for (int t = 0; t < QS; ++t) {
+            if constexpr (k16) {
+                c = mfma32<T>(a.w[t], b.w[t], c);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    c = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                        __builtin_bit_cast(float, (uint32_t)a.w[t][j]),
+                        __builtin_bit_cast(float, (uint32_t)b.w[t][j]), c, 0, 0, 0);
+            }
+        }
+        return c;
+    }
+
+    // The position in the tile of this lane's j-th key of P^T and V.
+    static __device__ __forceinline__ int key_of(int j) {
+        return 4 * (lane_id() >> 4) + (j & 3) + 16 * (j >> 2);
+    }
+
+    // Bytes from a row's start to this lane's chunk u, and whether the row has it.
+    static __device__ __forceinline__ int chunk_at(int u) {
+        return 4 * VW * (16 * u + (lane_id() & 15));
+    }
+    static __device__ __forceinline__ void load_chunk(const char* row, int u, int row_bytes,
+                                                      uint32_t (&w)[VW]) {
+        const int at = chunk_at(u);
+        if (FULL || at < row_bytes) {
+            if constexpr (VW == 4) {
+                const u32x4 x = *reinterpret_cast<const u32x4*>(row + at);
+                w[0] = x[0]; w[1] = x[1]; w[2] = x[2]; w[3] = x[3];
+            } else {
+                const u32x2 x = *reinterpret_cast<const u32x2*>(row + at);
+                w[0] = x[0]; w[1] = x[1];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VW; ++i) w[i] = 0;
+        }
+    }
+
+    static __device__ __forceinline__ void zero_acc(Acc& a) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int c = 0; c < CHL; ++c) a.o[u][c] = f32x4{0, 0, 0, 0};
+    }
+    // a += b in the lanes of `on`.
+    static __device__ __forceinline__ void add_acc(Acc& a, const Acc& b, bool on) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int c = 0; c < CHL; ++c)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) a.o[u][c][r] += on ? b.o[u][c][r] : 0.f;
+    }
+    static __device__ __forceinline__ void scale_acc(Acc& a, float f) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int c = 0; c < CHL; ++c) a.o[u][c] *= f;
+    }
+
+    // Whether a chunk holds an infinity or a NaN.
+    static __device__ __forceinline__ bool chunk_wild(const uint32_t (&w)[VW]) {
+        bool wild = false;
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+            if constexpr (k16) {
+                constexpr uint32_t e = std::is_same<T, __bf16>::value ? 0x7f80u : 0x7c00u;
+                wild |= (w[i] & e) == e || ((w[i] >> 16) & e) == e;
+            } else {
+                wild |= (w[i] & 0x7f800000u) == 0x7f800000u;
+            }
+        }
+        return wild;
+    }
+
+    // P^T from the lane's KT/4 probabilities (in key_of order), rounded to T.
+    static __device__ __forceinline__ void pack_probs(const float (&p)[VK], Probs& out) {
+        if constexpr (k16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out.w[i] = pack2<T>(p[2 * i], p[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out.w[i] = __builtin_bit_cast(uint32_t, p[i]);
+        }
+    }
+
+    // O^T += V^T P^T for chunk u.
+    static __device__ __forceinline__ void accumulate(const VBlock& v, const Probs& p, int u,
+                                                      Acc& a) {
+        if constexpr (k16) {
+            const u32x4 b{p.w[0], p.w[1], p.w[2], p.w[3]};
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+                u32x4 lo, hi;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    lo[j] = __builtin_amdgcn_perm(v.w[2 * j + 1][i], v.w[2 * j][i], 0x05040100u);
+                    hi[j] = __builtin_amdgcn_perm(v.w[2 * j + 1][i], v.w[2 * j][i], 0x07060302u);
+                }
+                a.o[u][2 * i] = mfma32<T>(lo, b, a.o[u][2 * i]);
+                a.o[u][2 * i + 1] = mfma32<T>(hi, b, a.o[u][2 * i + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < CHL; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    a.o[u][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                        __builtin_bit_cast(float, v.w[j][c]),
+                        __builtin_bit_cast(float, p.w[j]), a.o[u][c], 0, 0, 0);
+        }
+    }
+
+    // Element index of the accumulator's first value in register r of chunk
+    // u; the CHL values o[u][0..CHL)[r] follow one another.
+    static __device__ __forceinline__ int dim_of(int u, int r) {
+        return CHL * (16 * u + 4 * (lane_id() >> 4) + r);
+    }
+    // Register r of chunk u, times f, rounded to T and stored at row + dim_of.
+    static __device__ __forceinline__ void store_out(const Acc& a, int u, int r, float f, char* row,
+                                                     int row_bytes) {
+        const int at = dim_of(u, r) * (int)sizeof(T);
+        if (!FULL && at >= row_bytes) return;
+        if constexpr (k16) {
+            uint32_t w[VW];
+#pragma unroll
+            for (int i = 0; i < VW; ++i)
+                w[i] = pack2<T>(a.o[u][2 * i][r] * f, a.o[u][2 * i + 1][r] * f);
+            if constexpr (VW == 4)
+                *reinterpret_cast<u32x4*>(row + at) = u32x4{w[0], w[1], w[2], w[3]};
+            else
+                *reinterpret_cast<u32x2*>(row + at) = u32x2{w[0], w[1]};
+        } else {
+            *reinterpret_cast<f32x4*>(row + at) =
+                f32x4{a.o[u][0][r] * f, a.o[u][1][r] * f, a.o[u][2][r] * f, a.o[u][3][r] * f};
+        }
+    }
+    // The same values as floats at dst (a row of the head dimension's floats).
+    static __device__ __forceinline__ void store_part(const Acc& a, int u, int r, float f,
+                                                      float* dst, int dim) {
+        const int at = dim_of(u, r);
+        if (!FULL && at >= dim) return;
+#pragma unroll
+        for (int c = 0; c < CHL; c += 4)
+            *reinterpret_cast<f32x4*>(dst + at + c) =
+                f32x4{a.o[u][c][r] * f, a.o[u][c + 1][r] * f, a.o[u][c + 2][r] * f,
+                      a.o[u][c + 3][r] * f};
+    }
+};
+
+// Calls f(Tag<T, DP, FULL>) for the run-time element type and head dimension.
+template <class T, int DP, bool FULL>
+struct TileTag {
+    using Elem = T;
+    using Geo = Tile<T, DP, FULL>;
+};
+template <class T, class F>
+void with_dim(int dim, F&& f) {
+    if (dim == 64) f(TileTag<T, 64, true>{});
+    else if (dim < 64) f(TileTag<T, 64, false>{});
+    else if (dim == 128) f(TileTag<T, 128, true>{});
+    else if (dim < 128) f(TileTag<T, 128, false>{});
+    else if (dim == 256) f(TileTag<T, 256, true>{});
+    else f(TileTag<T, 256, false>{});
+}
+
+}  // namespace sg
