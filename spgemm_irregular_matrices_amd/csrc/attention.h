@@ -35,7 +35,15 @@ struct AttnSide {
     const AttnPiece* pieces = nullptr;
     const AttnSplit* splits = nullptr;
     const int32_t* idx = nullptr;  // the entries' columns
+    const uint16_t* bits = nullptr;  // see kColBlock
 };
+
+// The transposed mask, by blocks of 16 columns: an entry of block b is a row
+// (idx) with the set of the block's columns that the row stores (bits), so
+// that one trip for the row's q and dout serves up to 16 keys. Within a block
+// rows ascend; a row comes again where it stores a column twice, or columns
+// out of order.
+constexpr int kColBlock = 16;
 
 // Rows of a gathered tensor. A row's offset is unit * (its index) << shift
 // bytes, so that it fits 32 bits before the shift; the strides of every
@@ -81,7 +89,8 @@ struct BackwardArgs {
     const float* lse = nullptr;
     float* delta = nullptr;    // [row][hq]
     float* part_q = nullptr;   // [slot][hq][dim]
-    float* part_kv = nullptr;  // [slot of cols][hkv][2][dim]
+    float* part_kv = nullptr;  // [slot of cols][hkv][kColBlock][2][dim]
+    int64_t ncols = 0;
     FastDiv group_div;
 };
 void attention_backward(const BackwardArgs& a, hipStream_t st);
@@ -120,6 +129,64 @@ __device__ __forceinline__ int64_t xcd_block() {
     const uint32_t per = gridDim.x / kXcds;
     return (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
 }
+
+// Pieces that one wavefront takes in turn: enough to hide the first trip to
+// memory of each but the first, few enough that the chip's about 3000
+// wavefronts are replaced several times over (the pieces differ in length).
+inline int pieces_per_wave(int64_t units) {
+    const int64_t n = units / 12288;
+    return (int)(n < 1 ? 1 : n > 16 ? 16 : n);
+}
+
+// A wavefront's pieces, the i-th one's record in lane i, and the stream of
+// their tiles: the cursor names a tile and moves on to the next piece's first
+// one. Empty pieces are not in the stream.
+struct PieceStream {
+    struct Cursor {
+        int i, t0, len;
+        const int32_t* idx;
+        bool more;
+    };
+    AttnPiece mine{};
+    uint64_t empty, todo;
+    const int32_t* idx;
+
+    __device__ __forceinline__ PieceStream(const AttnSide& side, int64_t first, int stride,
+                                           int each)
+        : idx(side.idx) {
+        const int64_t u = first + (int64_t)lane_id() * stride;
+        const bool there = lane_id() < each && u < side.npieces;
+        if (there) mine = side.pieces[u];
+        empty = __ballot(there && mine.len == 0);
+        todo = __ballot(there && mine.len > 0);
+    }
+    static __device__ __forceinline__ int lane_value(int v, int i) {
+        return __builtin_amdgcn_readlane(v, i);
+    }
+    __device__ __forceinline__ int row(int i) const { return lane_value(mine.row, i); }
+    __device__ __forceinline__ int slot(int i) const { return lane_value(mine.slot, i); }
+    __device__ __forceinline__ int lead(int i) const { return lane_value(mine.lead, i); }
+    __device__ __forceinline__ void open(Cursor& c) {
+        c.more = todo != 0;
+        if (!c.more) return;
+        c.i = __builtin_ctzll(todo);
+        todo &= todo - 1;
+        c.t0 = 0;
+        c.len = lane_value(mine.len, c.i);
+        const uint32_t lo = (uint32_t)lane_value((int)(mine.first & 0xffffffff), c.i);
+        const uint32_t hi = (uint32_t)lane_value((int)(mine.first >> 32), c.i);
+        c.idx = idx + ((uint64_t)hi << 32 | lo);
+    }
+    __device__ __forceinline__ void next(Cursor& c, int tile) {
+        c.t0 += tile;
+        if (c.t0 >= c.len) open(c);
+    }
+    // This lane's index of the tile. Lanes past the piece's end repeat its
+    // last entry: every address made from one is a row that the piece names.
+    static __device__ __forceinline__ uint32_t id(const Cursor& c, int tile) {
+        return (uint32_t)c.idx[min(c.t0 + (lane_id() & (tile - 1)), c.len - 1)];
+    }
+};
 
 template <class F>
 void with_type(int type, int dim, F&& f) {

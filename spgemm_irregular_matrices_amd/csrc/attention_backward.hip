@@ -33,60 +33,132 @@ struct HalfScale {
 template <class T>
 constexpr float kProbScale = std::is_same<T, _Float16>::value ? 0x1p14f : 1.f;
 
-// dq: one wavefront per piece of a row and 16 query heads of a key head, as
-// in the forward pass. S^T and dP^T = V dO^T come from the same gathered rows
-// in the same layout, dQ^T += K^T dS^T takes K again in the chunk layout
-// (the rows were read a moment before, so these loads hit the caches).
+// dq: one wavefront per piece of a row and 16 query heads of a key head, its
+// pieces' tiles in one stream as in the forward pass. S^T and dP^T = V dO^T
+// take the gathered rows as rows, dQ^T += K^T dS^T takes K as chunks: K rows
+// come from memory as chunks, a tile ahead, and are staged in the
+// wavefront's own LDS for the other layout.
 template <class G, class T>
-__global__ __launch_bounds__(kWaves* kWave) void k_attn_grad_q(BackwardArgs a) {
+__global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_grad_q(BackwardArgs a, int each,
+                                                               int64_t groups) {
+    __shared__ __align__(16) char stage[kWaves][G::KT * G::kRowBytes];
     const int lane = lane_id();
-    const int64_t unit = xcd_block() * kWaves + threadIdx.x / kWave;
-    const int64_t npieces = a.rows.npieces;
-    if (unit >= npieces * a.s.hkv * a.s.mtiles) return;
-    const int hm = (int)(unit / npieces);
-    const AttnPiece pc = a.rows.pieces[unit - (int64_t)hm * npieces];
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t block = xcd_block();
+    const int hm = (int)(block / groups);
+    if (hm >= a.s.hkv * a.s.mtiles) return;
+    const int64_t u0 = (block - hm * groups) * kWaves * each + w;
     const int h = hm / a.s.mtiles, mt = hm - h * a.s.mtiles;
     const int n = lane & 15;
     const int g = 16 * mt + n;
     const bool has = g < a.s.group;
     const int hq = h * a.s.group + g;
     const int row_bytes = a.s.dim * (int)sizeof(T);
+    char* krows = stage[w];
 
-    typename G::RowFrag q, dout;
-    G::zero_row(q);
-    G::zero_row(dout);
-    float lse2 = INFINITY, delta = 0.f;  // lanes without a head: weights 0
-    if (has) {
-        G::load_row(a.q.base + pc.row * a.q.row + hq * a.q.head, row_bytes, q);
-        G::load_row(a.dout.base + pc.row * a.dout.row + hq * a.dout.head, row_bytes, dout);
-        typename G::RowFrag out;
-        G::load_row(a.out.base + pc.row * a.out.row + hq * a.out.head, row_bytes, out);
-        delta = G::dot_lane(dout, out);
-        const float x = a.lse[(int64_t)pc.row * a.s.hq + hq];
-        lse2 = x == -INFINITY ? INFINITY : x * kLog2e;
+    PieceStream st(a.rows, u0, kWaves, each);
+    for (uint64_t e = st.empty; e; e &= e - 1) {
+        if (!has) continue;
+        typename G::Acc zero;
+        G::zero_acc(zero);
+        char* row = a.dq.base + st.row(__builtin_ctzll(e)) * a.dq.row + hq * a.dq.head;
+#pragma unroll
+        for (int u = 0; u < G::U; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) G::store_out(zero, u, r, 0.f, row, row_bytes);
     }
-    delta = quad_sum(delta);
-    if (has && lane < 16 && pc.lead)
-        a.delta[(int64_t)pc.row * a.s.hq + hq] = delta;
+    if (!st.todo) return;
+
+    const char* kb = a.k.base + h * a.k.head;
+    const char* vb = a.v.base + h * a.v.head;
+    typename G::RowFrag q, dout, out, v[G::KSUB];
+    typename G::VBlock k[G::U];
+    float lse = INFINITY;  // lanes without a head: weights 0
+    const auto load_q = [&](int i) {
+        const int row = st.row(i);
+        G::zero_row(q);
+        G::zero_row(dout);
+        G::zero_row(out);
+        if (has) {
+            G::load_row(a.q.base + row * a.q.row + hq * a.q.head, row_bytes, q);
+            G::load_row(a.dout.base + row * a.dout.row + hq * a.dout.head, row_bytes, dout);
+            G::load_row(a.out.base + row * a.out.row + hq * a.out.head, row_bytes, out);
+            lse = a.lse[(int64_t)row * a.s.hq + hq];
+        }
+    };
+    const auto load_k = [&](uint32_t id) {
+        const uint32_t off = id * a.k.unit;
+#pragma unroll
+        for (int j = 0; j < G::VK; ++j) {
+            const char* row = kb + ((uint64_t)(uint32_t)__shfl(off, G::key_of(j), kWave)
+                                    << a.k.shift);
+#pragma unroll
+            for (int u = 0; u < G::U; ++u) G::load_chunk(row, u, row_bytes, k[u].w[j]);
+        }
+    };
+    const auto load_v = [&](uint32_t id) {
+        const uint32_t off = id * a.v.unit;
+#pragma unroll
+        for (int b = 0; b < G::KSUB; ++b)
+            G::load_row(vb + ((uint64_t)(uint32_t)__shfl(off, 16 * b + n, kWave) << a.v.shift),
+                        row_bytes, v[b]);
+    };
+
+    PieceStream::Cursor cur, ahead;
+    st.open(cur);
+    uint32_t id = st.id(cur, G::KT);
+    load_q(cur.i);
+    load_k(id);
+    load_v(id);
+    ahead = cur;
+    st.next(ahead, G::KT);
+    if (ahead.more) id = st.id(ahead, G::KT);
 
     typename G::Acc o;
     G::zero_acc(o);
     HalfScale hs;
-    const char* kb = a.k.base + h * a.k.head;
-    const char* vb = a.v.base + h * a.v.head;
-    const int32_t* idx = a.rows.idx + pc.first;
-    for (int t0 = 0; t0 < pc.len; t0 += G::KT) {
-        const int left = pc.len - t0;
-        const uint32_t id = (uint32_t)idx[t0 + min(lane & (G::KT - 1), left - 1)];
-        const uint32_t ko = id * a.k.unit, vo = id * a.v.unit;
+    float lse2 = 0.f, delta = 0.f;
+    bool fresh = true;  // first tile of its piece
+    while (true) {
+        const int left = cur.len - cur.t0;
+        const bool last = left <= G::KT, more = ahead.more;
+        if (fresh) {
+            delta = quad_sum(G::dot_lane(dout, out));
+            lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
+            if (has && lane < 16 && st.lead(cur.i))
+                a.delta[(int64_t)st.row(cur.i) * a.s.hq + hq] = delta;
+            fresh = false;
+        }
+        wave_lds_sync();
+#pragma unroll
+        for (int j = 0; j < G::VK; ++j)
+#pragma unroll
+            for (int u = 0; u < G::U; ++u) {
+                if (G::key_of(j) >= left) {  // 0 times what a repeated row holds may be NaN
+#pragma unroll
+                    for (int i = 0; i < G::VW; ++i) k[u].w[j][i] = 0;
+                }
+                G::stage_chunk(krows, G::key_of(j), u, k[u].w[j]);
+            }
+        wave_lds_sync();
+        const uint32_t idn = id;
+        if (more) load_k(idn);
         f32x4 s[G::KSUB], dp[G::KSUB];
 #pragma unroll
         for (int b = 0; b < G::KSUB; ++b) {
+            dp[b] = G::dot(v[b], dout, f32x4{0, 0, 0, 0});
             typename G::RowFrag x;
-            G::load_row(kb + ((uint64_t)__shfl(ko, 16 * b + n, kWave) << a.k.shift), row_bytes, x);
+            G::staged_row(krows, 16 * b + n, x);
             s[b] = G::dot(x, q, f32x4{0, 0, 0, 0});
-            G::load_row(vb + ((uint64_t)__shfl(vo, 16 * b + n, kWave) << a.v.shift), row_bytes, x);
-            dp[b] = G::dot(x, dout, f32x4{0, 0, 0, 0});
+        }
+        if (more) {
+            load_v(idn);
+            if (last) load_q(ahead.i);
+        }
+        const PieceStream::Cursor after = ahead;
+        if (more) {
+            st.next(ahead, G::KT);
+            if (ahead.more) id = st.id(ahead, G::KT);
         }
         float ds[G::VK];
 #pragma unroll
@@ -109,189 +181,381 @@ __global__ __launch_bounds__(kWaves* kWave) void k_attn_grad_q(BackwardArgs a) {
         for (int u = 0; u < G::U; ++u) {
             typename G::VBlock x;
 #pragma unroll
-            for (int j = 0; j < G::VK; ++j) {
-                const uint32_t off = __shfl(ko, G::key_of(j), kWave);
-                G::load_chunk(kb + ((uint64_t)off << a.k.shift), u, row_bytes, x.w[j]);
-                if (G::key_of(j) >= left) {
-#pragma unroll
-                    for (int i = 0; i < G::VW; ++i) x.w[j][i] = 0;
-                }
-            }
+            for (int j = 0; j < G::VK; ++j) G::staged_chunk(krows, G::key_of(j), u, x.w[j]);
             G::accumulate(x, pr, u, o);
         }
-    }
-    if (!has) return;
-    float f = a.s.scale;
-    if constexpr (std::is_same<T, _Float16>::value) f /= hs.s;
-    if (pc.slot < 0) {
-        char* row = a.dq.base + pc.row * a.dq.row + hq * a.dq.head;
+        if (last) {
+            float f = a.s.scale;
+            if constexpr (std::is_same<T, _Float16>::value) f /= hs.s;
+            const int row = st.row(cur.i), slot = st.slot(cur.i);
+            if (has && slot < 0) {
+                char* dst = a.dq.base + row * a.dq.row + hq * a.dq.head;
 #pragma unroll
-        for (int u = 0; u < G::U; ++u)
+                for (int u = 0; u < G::U; ++u)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) G::store_out(o, u, r, f, row, row_bytes);
-    } else {
-        float* dst = a.part_q + ((int64_t)pc.slot * a.s.hq + hq) * a.s.dim;
+                    for (int r = 0; r < 4; ++r) G::store_out(o, u, r, f, dst, row_bytes);
+            } else if (has) {
+                float* dst = a.part_q + ((int64_t)slot * a.s.hq + hq) * a.s.dim;
 #pragma unroll
-        for (int u = 0; u < G::U; ++u)
+                for (int u = 0; u < G::U; ++u)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) G::store_part(o, u, r, f, dst, a.s.dim);
+                    for (int r = 0; r < 4; ++r) G::store_part(o, u, r, f, dst, a.s.dim);
+            }
+            if (!more) break;
+            G::zero_acc(o);
+            hs = HalfScale();
+            fresh = true;
+        }
+        cur = after;
     }
 }
 
-// dk and dv: one wavefront per piece of a column and key head. The gathered
-// list is the (row, query head) pairs of the piece's entries, and the other
-// operand is the column's one k (or v) row in all 16 places: S, dP and so P
-// and dS come out alike in 16 columns, which is what lets them go straight
-// into the second products; the matrix units have the room (a pair costs
-// about as many cycles as its two gathered rows take to arrive).
-template <class G, class T>
-__global__ __launch_bounds__(kWaves* kWave) void k_attn_grad_kv(BackwardArgs a) {
-    const int lane = lane_id();
-    const int64_t unit = xcd_block() * kWaves + threadIdx.x / kWave;
-    const int64_t npieces = a.cols.npieces;
-    if (unit >= npieces * a.s.hkv) return;
-    const int h = (int)(unit / npieces);
-    const AttnPiece pc = a.cols.pieces[unit - (int64_t)h * npieces];
-    const int n = lane & 15;
-    const int row_bytes = a.s.dim * (int)sizeof(T);
-    constexpr bool half = std::is_same<T, _Float16>::value;
+// dk and dv: one work group of 4 wavefronts per piece of a block of 16 columns
+// and key head. The gathered list is the (row, query head) pairs of the
+// piece's entries, kTilePairs at a time; the other operand of S and dP is the
+// block's 16 k (or v) rows, and an entry's bits say which of the 16 scores
+// are the mask's. A tile's q and dout rows come from memory once, a tile ahead
+// of their use, and are shared in LDS. Each wavefront makes S, P, dP and dS of
+// 16 pairs (of TP / 16 wavefronts' worth), and after these are exchanged in
+// LDS too, one output (dv from dout and P, dk from q and dS) of one half of
+// the head dimension: that keeps the accumulators at an eighth of the
+// output each, where one wavefront with both outputs would need over 256
+// registers with a tile under way.
+constexpr int kKvWaves = 4;
+template <class G>
+constexpr int kTilePairs = G::kRowBytes <= 256 ? 64 : 32;
 
-    typename G::RowFrag k, v;
-    G::load_row(a.krow.base + pc.row * a.krow.row + h * a.krow.head, row_bytes, k);
-    G::load_row(a.vrow.base + pc.row * a.vrow.row + h * a.vrow.head, row_bytes, v);
-    typename G::Acc dk, dv;
-    G::zero_acc(dk);
-    G::zero_acc(dv);
+template <class G, class T>
+__global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 1) void k_attn_grad_kv(BackwardArgs a) {
+    constexpr bool half = std::is_same<T, _Float16>::value;
+    constexpr int TP = kTilePairs<G>, NT = kKvWaves * kWave;
+    constexpr int kPieces = G::kRowBytes / 16;        // 16-byte pieces of a row
+    constexpr int kLoads = TP * kPieces / NT;         // of each tensor per thread
+    constexpr int kPitch = TP * (int)sizeof(T) + 16;  // bytes between keys of P and dS
+    constexpr int kSets = G::kDim / 2 / (16 * G::kPerWord);  // 16-row results per wavefront
+    constexpr int kSteps = TP / G::KT;                // products over G::KT pairs each
+    static_assert(TP * kPieces % NT == 0 && kSets >= 1, "tile shape");
+    __shared__ __align__(16) char rows[2][TP * G::kRowBytes];  // q, dout
+    __shared__ __align__(16) char weights[2][kColBlock * kPitch];  // dS, P: [key][pair]
+    __shared__ __align__(16) char keys[2][kColBlock * G::kRowBytes];  // k, v
+    __shared__ uint32_t off[2][TP];
+    __shared__ __align__(16) float lse_s[TP], delta_s[TP];
+    __shared__ __align__(16) uint32_t bits_s[TP];
+    __shared__ float most[kKvWaves][kColBlock];
+    __shared__ int wild_s[kKvWaves];
+
+    const int tid = threadIdx.x, lane = lane_id();
+    const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
+    // every XCD has an eighth of each head's pieces, and all are at one head
+    // at a time: what they gather of it together stays in the last-level cache
+    const uint32_t per = (uint32_t)ceil_div(a.cols.npieces, kXcds);
+    const int h = (int)(blockIdx.x / kXcds / per);
+    const int64_t piece = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds % per;
+    if (piece >= a.cols.npieces) return;
+    const AttnPiece pc = a.cols.pieces[piece];
+    const int n = lane & 15, quad = lane >> 4;
+    const int64_t col = (int64_t)pc.row * kColBlock + n;  // this lane's key
+    const int row_bytes = a.s.dim * (int)sizeof(T);
+
+    // the block's k and v rows wait in LDS too: 32 registers more (at 128 x 16
+    // bits) would cost a third of the wavefronts
+    if (w < 2) {
+        typename G::RowFrag f;
+        G::zero_row(f);
+        const AttnRows& src = w ? a.vrow : a.krow;
+        if (col < a.ncols) G::load_row(src.base + col * src.row + h * src.head, row_bytes, f);
+#pragma unroll
+        for (int t = 0; t < G::QS; ++t)
+            *reinterpret_cast<u32x4*>(keys[w] + G::stage_at(n, 64 * t + 16 * quad)) = f.w[t];
+    }
+    f32x4 acc[kSets][G::kPerWord];
+#pragma unroll
+    for (int i = 0; i < kSets; ++i)
+#pragma unroll
+        for (int c = 0; c < G::kPerWord; ++c) acc[i][c] = f32x4{0, 0, 0, 0};
     HalfScale hs;
     const char* qb = a.gq.base + (int64_t)h * a.s.group * a.gq.head;
     const char* gb = a.gdout.base + (int64_t)h * a.s.group * a.gdout.head;
     const uint32_t qhead = (uint32_t)(a.gq.head >> a.gq.shift);
     const uint32_t ghead = (uint32_t)(a.gdout.head >> a.gdout.shift);
     const int32_t* idx = a.cols.idx + pc.first;
-    const int64_t pairs = (int64_t)pc.len * a.s.group;
-    for (int64_t t0 = 0; t0 < pairs; t0 += G::KT) {
-        const int left = (int)min(pairs - t0, (int64_t)G::KT);
-        const uint32_t x = (uint32_t)t0 + min(lane & (G::KT - 1), left - 1);
-        const uint32_t e = a.group_div.div(x), g = x - e * a.s.group;
-        const uint32_t id = (uint32_t)idx[e];
-        const uint32_t qo = id * a.gq.unit + g * qhead, go = id * a.gdout.unit + g * ghead;
-        const int64_t at = (int64_t)id * a.s.hq + h * a.s.group + g;
-        const float lse = a.lse[at], dl = a.delta[at];
-        const float lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
-        f32x4 s[G::KSUB], dp[G::KSUB];
-#pragma unroll
-        for (int b = 0; b < G::KSUB; ++b) {
-            typename G::RowFrag f;
-            G::load_row(qb + ((uint64_t)__shfl(qo, 16 * b + n, kWave) << a.gq.shift), row_bytes, f);
-            s[b] = G::dot(f, k, f32x4{0, 0, 0, 0});
-            G::load_row(gb + ((uint64_t)__shfl(go, 16 * b + n, kWave) << a.gdout.shift), row_bytes,
-                        f);
-            dp[b] = G::dot(f, v, f32x4{0, 0, 0, 0});
+    const uint16_t* bits = a.cols.bits + pc.first;
+    const int pairs = pc.len * a.s.group;
+
+    // one pair per thread of the first TP: its row, then what belongs to it
+    uint32_t id = 0, mine = 0;
+    float lse = 0.f, delta = 0.f;
+    const auto load_id = [&](int t0) {
+        if (tid < TP && t0 + tid < pairs) id = (uint32_t)idx[a.group_div.div(t0 + tid)];
+    };
+    const auto put_offsets = [&](int t0) {
+        if (tid < TP && t0 + tid < pairs) {
+            const uint32_t g = t0 + tid - a.group_div.div(t0 + tid) * a.s.group;
+            off[0][tid] = id * a.gq.unit + g * qhead;
+            off[1][tid] = id * a.gdout.unit + g * ghead;
         }
-        float p[G::VK], ds[G::VK];
+    };
+    u32x4 fly[2][kLoads];
+    constexpr int kStep = NT / kPieces;  // rows that one load of the work group covers
+    const int prow = tid / kPieces, pbyte = tid % kPieces * 16;  // this thread's place in them
+    const bool inside = G::kFull || pbyte < row_bytes;
+    const char* qp = qb + (inside ? pbyte : 0);
+    const char* gp = gb + (inside ? pbyte : 0);
+    const auto load_rows = [&](int t0) {
+        if (t0 + TP <= pairs) {
 #pragma unroll
-        for (int j = 0; j < G::VK; ++j) {
-            const float l2 = __shfl(lse2, G::key_of(j), kWave);
-            const float dj = __shfl(dl, G::key_of(j), kWave);
-            const bool on = G::key_of(j) < left;
-            p[j] = on ? fast_exp2(fmaf(s[j >> 2][j & 3], a.s.c, -l2)) : 0.f;
-            ds[j] = on ? p[j] * (dp[j >> 2][j & 3] - dj) : 0.f;
-            p[j] *= kProbScale<T>;
+            for (int i = 0; i < kLoads; ++i) {
+                const int p = i * kStep + prow;
+                fly[0][i] = *reinterpret_cast<const u32x4*>(qp + ((uint64_t)off[0][p] << a.gq.shift));
+                fly[1][i] =
+                    *reinterpret_cast<const u32x4*>(gp + ((uint64_t)off[1][p] << a.gdout.shift));
+            }
+        } else {
+            // pairs past the end read the first row and become 0
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int p = i * kStep + prow;
+                const bool in = t0 + p < pairs;
+                const u32x4 x = *reinterpret_cast<const u32x4*>(
+                    qp + (in ? (uint64_t)off[0][p] << a.gq.shift : 0));
+                const u32x4 y = *reinterpret_cast<const u32x4*>(
+                    gp + (in ? (uint64_t)off[1][p] << a.gdout.shift : 0));
+                fly[0][i] = in ? x : u32x4{0, 0, 0, 0};
+                fly[1][i] = in ? y : u32x4{0, 0, 0, 0};
+            }
         }
+        if (!inside) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) fly[0][i] = fly[1][i] = u32x4{0, 0, 0, 0};
+        }
+        mine = 0;
+        lse = -INFINITY;
+        delta = 0.f;
+        if (tid < TP && t0 + tid < pairs) {
+            const uint32_t e = a.group_div.div(t0 + tid), g = t0 + tid - e * a.s.group;
+            const int64_t at = (int64_t)id * a.s.hq + h * a.s.group + g;
+            mine = bits[e];
+            lse = a.lse[at];
+            delta = a.delta[at];
+        }
+    };
+    if (pairs > 0) {
+        load_id(0);
+        put_offsets(0);
+        __syncthreads();
+        load_rows(0);
+        load_id(TP);
+    }
+    for (int t0 = 0; t0 < pairs; t0 += TP) {
+        __syncthreads();  // the last tile's readers are done
+        const int put = G::stage_at(prow, pbyte);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int at = G::stage_more(put, i * kStep, 0);
+            *reinterpret_cast<u32x4*>(rows[0] + at) = fly[0][i];
+            *reinterpret_cast<u32x4*>(rows[1] + at) = fly[1][i];
+        }
+        if (tid < TP) {
+            lse_s[tid] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+            delta_s[tid] = delta;
+            bits_s[tid] = mine;
+        }
+        put_offsets(t0 + TP);
+        __syncthreads();
+        if (t0 + TP < pairs) {
+            load_rows(t0 + TP);
+            load_id(t0 + 2 * TP);
+        }
+        // S, P, dP and dS of this wavefront's 16 pairs
+        float pr[4], ds[4];
+        float wild = 0.f;
+        if (16 * w < TP) {
+            typename G::RowFrag f, key;
+            G::staged_row(rows[0], 16 * w + n, f);
+            G::staged_row(keys[0], n, key);
+            const f32x4 s = G::dot(f, key, f32x4{0, 0, 0, 0});
+            G::staged_row(rows[1], 16 * w + n, f);
+            G::staged_row(keys[1], n, key);
+            const f32x4 dp = G::dot(f, key, f32x4{0, 0, 0, 0});
+            const f32x4 l2 = *reinterpret_cast<const f32x4*>(lse_s + 16 * w + 4 * quad);
+            const f32x4 dl = *reinterpret_cast<const f32x4*>(delta_s + 16 * w + 4 * quad);
+            const u32x4 sees = *reinterpret_cast<const u32x4*>(bits_s + 16 * w + 4 * quad);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                // 0 times any score: NaN if one is not finite, which it cannot
+                // be where the pair's q or dout row holds an infinity or NaN
+                wild = fmaf(s[r], 0.f, wild);
+                wild = fmaf(dp[r], 0.f, wild);
+                const bool on = sees[r] >> n & 1;
+                pr[r] = on ? fast_exp2(fmaf(s[r], a.s.c, -l2[r])) : 0.f;
+                ds[r] = on ? pr[r] * (dp[r] - dl[r]) : 0.f;
+                pr[r] *= kProbScale<T>;
+            }
+        }
+        float fix = 1.f;
         if constexpr (half) {
+            if (16 * w < TP) {
+                float mx = 0.f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) mx = fmaxf(mx, fabsf(ds[r]));
+                mx = quad_max(mx);
+                if (quad == 0) most[w][n] = mx;
+            }
+            __syncthreads();
             float mx = 0.f;
 #pragma unroll
-            for (int j = 0; j < G::VK; ++j) mx = fmaxf(mx, fabsf(ds[j]));
-            const float f = hs.admit(quad_max(mx));
-            if (__any(f != 1.f)) G::scale_acc(dk, f);
+            for (int i = 0; i < TP / 16; ++i) mx = fmaxf(mx, most[i][n]);
+            fix = hs.admit(mx);
 #pragma unroll
-            for (int j = 0; j < G::VK; ++j) ds[j] *= hs.s;
+            for (int r = 0; r < 4; ++r) ds[r] *= hs.s;
         }
-        typename G::Probs pp, pd;
-        G::pack_probs(p, pp);
-        G::pack_probs(ds, pd);
+        if (16 * w < TP) {
+            char* at = weights[0] + n * kPitch + (16 * w + 4 * quad) * (int)sizeof(T);
+            char* ap = weights[1] + n * kPitch + (16 * w + 4 * quad) * (int)sizeof(T);
+            if constexpr (G::k16) {
+                *reinterpret_cast<u32x2*>(at) = u32x2{pack2<T>(ds[0], ds[1]), pack2<T>(ds[2], ds[3])};
+                *reinterpret_cast<u32x2*>(ap) = u32x2{pack2<T>(pr[0], pr[1]), pack2<T>(pr[2], pr[3])};
+            } else {
+                *reinterpret_cast<f32x4*>(at) = f32x4{ds[0], ds[1], ds[2], ds[3]};
+                *reinterpret_cast<f32x4*>(ap) = f32x4{pr[0], pr[1], pr[2], pr[3]};
+            }
+            const bool any = __any(wild != 0.f);
+            if (lane == 0) wild_s[w] = any;
+        }
+        __syncthreads();
+        // this wavefront's output: dk from q and dS (w even), dv from dout
+        // and P (w odd), half w / 2 of the head dimension
+        bool tame = true;
 #pragma unroll
-        for (int u = 0; u < G::U; ++u) {
-            typename G::VBlock c;
+        for (int i = 0; i < TP / 16; ++i) tame = tame && wild_s[i] == 0;
+        if constexpr (half) {
+            if ((w & 1) == 0 && __any(fix != 1.f)) {
 #pragma unroll
-            for (int j = 0; j < G::VK; ++j) {
-                const uint32_t off = __shfl(go, G::key_of(j), kWave);
-                G::load_chunk(gb + ((uint64_t)off << a.gdout.shift), u, row_bytes, c.w[j]);
-                if (G::key_of(j) >= left) {
+                for (int i = 0; i < kSets; ++i)
 #pragma unroll
-                    for (int i = 0; i < G::VW; ++i) c.w[j][i] = 0;
+                    for (int c = 0; c < G::kPerWord; ++c) acc[i][c] *= fix;
+            }
+        }
+        const char* x = rows[w & 1];
+        const char* y = weights[w & 1] + n * kPitch;
+        // this lane's word of its first pair and set; opaque, so that the
+        // tile's addresses are made again in each round instead of held in
+        // registers throughout
+        int w0 = G::stage_at(G::VK * quad, (w >> 1) * (G::kRowBytes / 2) + 4 * n);
+        asm volatile("" : "+v"(w0));
+        const auto word_at = [&](int st, int j, int i) {
+            if constexpr (G::KT == 32)  // whose multiples do not move the exchange
+                return *reinterpret_cast<const uint32_t*>(x + st * 32 * G::kRowBytes +
+                                                          G::stage_more(w0, j, 64 * i));
+            return *reinterpret_cast<const uint32_t*>(x + G::stage_more(w0, G::KT * st + j, 64 * i));
+        };
+        // product st: the pairs KT*st + VK*quad + j
+        const auto probs_at = [&](int st) {
+            const u32x4 b = *reinterpret_cast<const u32x4*>(
+                y + (G::KT * st + G::VK * quad) * (int)sizeof(T));
+            return typename G::Probs{{b[0], b[1], b[2], b[3]}};
+        };
+        if (tame) {
+#pragma unroll (G::k16 ? 1 : kSteps)
+            for (int st = 0; st < kSteps; ++st) {
+                const typename G::Probs pb = probs_at(st);
+#pragma unroll
+                for (int i = 0; i < kSets; ++i) {
+                    uint32_t word[G::VK];
+#pragma unroll
+                    for (int j = 0; j < G::VK; ++j)
+                        word[j] = word_at(st, j, i);
+                    G::accumulate_word(word, pb, acc[i]);
                 }
             }
-            G::accumulate(c, pp, u, dv);
+        } else {
+            // one key at a time, with the pairs that are not its own as 0
+#pragma unroll 1
+            for (int st = 0; st < kSteps; ++st) {
+                const typename G::Probs pb = probs_at(st);
+                const int p0 = G::KT * st + G::VK * quad;
 #pragma unroll
-            for (int j = 0; j < G::VK; ++j) {
-                const uint32_t off = __shfl(qo, G::key_of(j), kWave);
-                G::load_chunk(qb + ((uint64_t)off << a.gq.shift), u, row_bytes, c.w[j]);
-                if (G::key_of(j) >= left) {
+                for (int i = 0; i < kSets; ++i) {
+                    uint32_t word[G::VK];
 #pragma unroll
-                    for (int i = 0; i < G::VW; ++i) c.w[j][i] = 0;
+                    for (int j = 0; j < G::VK; ++j) word[j] = word_at(st, j, i);
+                    G::accumulate_word_seen(
+                        word, pb, kColBlock, n,
+                        [&](int key, int j) { return bits_s[p0 + j] >> key & 1; }, acc[i]);
                 }
             }
-            G::accumulate(c, pd, u, dk);
         }
     }
-    float fk = a.s.scale;
-    if constexpr (half) fk /= hs.s;
-    const float fv = 1.f / kProbScale<T>;
-    // the 16 columns are alike: column r stores register r
-    char* krow = a.dk.base + pc.row * a.dk.row + h * a.dk.head;
-    char* vrow = a.dv.base + pc.row * a.dv.row + h * a.dv.head;
-    float* part =
-        pc.slot < 0 ? nullptr : a.part_kv + ((int64_t)pc.slot * a.s.hkv + h) * 2 * a.s.dim;
+    if (col >= a.ncols) return;
+    float f = (w & 1) ? 1.f / kProbScale<T> : a.s.scale;
+    if constexpr (half) f = (w & 1) ? f : f / hs.s;
+    const AttnRows& out = (w & 1) ? a.dv : a.dk;
+    constexpr int kRun = 4 * G::kPerWord;  // values next to each other in a lane's result
 #pragma unroll
-    for (int u = 0; u < G::U; ++u)
+    for (int i = 0; i < kSets; ++i) {
+        const int d = (w >> 1) * (G::kDim / 2) + i * 16 * G::kPerWord + kRun * quad;
+        if (!G::kFull && d >= a.s.dim) continue;
+        float z[kRun];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            if (n != r) continue;
-            if (part) {
-                G::store_part(dk, u, r, fk, part, a.s.dim);
-                G::store_part(dv, u, r, fv, part + a.s.dim, a.s.dim);
-            } else {
-                G::store_out(dk, u, r, fk, krow, row_bytes);
-                G::store_out(dv, u, r, fv, vrow, row_bytes);
-            }
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < G::kPerWord; ++c) z[G::kPerWord * r + c] = acc[i][c][r] * f;
+        if (pc.slot >= 0) {
+            float* part = a.part_kv +
+                          ((((int64_t)pc.slot * a.s.hkv + h) * kColBlock + n) * 2 + (w & 1)) * a.s.dim;
+#pragma unroll
+            for (int r = 0; r < kRun; r += 4)
+                *reinterpret_cast<f32x4*>(part + d + r) = f32x4{z[r], z[r + 1], z[r + 2], z[r + 3]};
+        } else {
+            char* at = out.base + col * out.row + h * out.head + d * (int)sizeof(T);
+            if constexpr (G::k16)
+                *reinterpret_cast<u32x4*>(at) = u32x4{pack2<T>(z[0], z[1]), pack2<T>(z[2], z[3]),
+                                                      pack2<T>(z[4], z[5]), pack2<T>(z[6], z[7])};
+            else
+                *reinterpret_cast<f32x4*>(at) = f32x4{z[0], z[1], z[2], z[3]};
         }
+    }
 }
 
-// The rows of more than one piece: the sum of the pieces, in their order.
-// One wavefront per row, head and output (`outs` of them side by side).
+// The sums of rows (or blocks of columns) of more than one piece, in the
+// pieces' order. One wavefront per row, head and, for blocks, column and
+// output: `lines` results of dim values per head lie side by side.
 template <class T>
 __global__ __launch_bounds__(kWaves* kWave) void k_attn_join_sum(AttnSide side, const float* part,
-                                                                 int heads, int outs, int dim,
-                                                                 AttnRows out0, AttnRows out1) {
+                                                                 int heads, int lines, int dim,
+                                                                 int64_t nrows, AttnRows out0,
+                                                                 AttnRows out1) {
     const int lane = lane_id();
     const int64_t unit = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
-    if (unit >= side.nsplits * heads * outs) return;
-    const int64_t sp = unit / (heads * outs);
-    const int ho = (int)(unit - sp * heads * outs);
-    const int h = ho / outs;
+    const int64_t per = (int64_t)heads * lines;
+    if (unit >= side.nsplits * per) return;
+    const int64_t sp = unit / per, hl = unit - sp * per;
+    const int h = (int)(hl / lines), line = (int)(hl - (int64_t)h * lines);
     const AttnSplit s = side.splits[sp];
+    const int64_t row = lines == 1 ? s.row : (int64_t)s.row * kColBlock + line / 2;
+    if (row >= nrows) return;
     float x[SPGEMM_ATTENTION_MAX_HEAD_DIM / kWave] = {};
     for (int i = 0; i < s.count; ++i) {
-        const float* src = part + ((int64_t)(s.slot + i) * heads * outs + ho) * dim;
+        const float* src = part + ((int64_t)(s.slot + i) * per + hl) * dim;
 #pragma unroll
         for (int j = 0; j < SPGEMM_ATTENTION_MAX_HEAD_DIM / kWave; ++j)
             if (j * kWave + lane < dim) x[j] += src[j * kWave + lane];
     }
-    const AttnRows& o = ho - h * outs ? out1 : out0;
-    T* dst = reinterpret_cast<T*>(o.base + s.row * o.row + h * o.head);
+    const AttnRows& o = line & 1 ? out1 : out0;
+    T* dst = reinterpret_cast<T*>(o.base + row * o.row + h * o.head);
 #pragma unroll
     for (int j = 0; j < SPGEMM_ATTENTION_MAX_HEAD_DIM / kWave; ++j)
         if (j * kWave + lane < dim) dst[j * kWave + lane] = (T)x[j];
 }
 
 template <class T>
-void join_sum(const AttnSide& side, const float* part, int heads, int outs, int dim,
-              const AttnRows& out0, const AttnRows& out1, hipStream_t st) {
+void join_sum(const AttnSide& side, const float* part, int heads, int lines, int dim,
+              int64_t nrows, const AttnRows& out0, const AttnRows& out1, hipStream_t st) {
     if (side.nsplits == 0) return;
     hipLaunchKernelGGL(k_attn_join_sum<T>,
-                       dim3(grid_1d(ceil_div(side.nsplits * heads * outs, kWaves))),
-                       dim3(kWaves * kWave), 0, st, side, part, heads, outs, dim, out0, out1);
+                       dim3(grid_1d(ceil_div(side.nsplits * heads * lines, kWaves))),
+                       dim3(kWaves * kWave), 0, st, side, part, heads, lines, dim, nrows, out0,
+                       out1);
     SG_LAUNCH_CHECK();
 }
 
@@ -301,21 +565,23 @@ void attention_backward(const BackwardArgs& a, hipStream_t st) {
     with_type(a.s.type, a.s.dim, [&](auto tag) {
         using Tag = decltype(tag);
         using T = typename Tag::Elem;
-        const int64_t rows = a.rows.npieces * a.s.hkv * a.s.mtiles;
-        if (rows > 0) {
+        if (a.rows.npieces > 0) {
+            const int64_t heads = (int64_t)a.s.hkv * a.s.mtiles;
+            const int each = pieces_per_wave(a.rows.npieces * heads);
+            const int64_t groups = ceil_div(a.rows.npieces, kWaves * each);
             auto run = k_attn_grad_q<typename Tag::Geo, T>;
-            hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(ceil_div(rows, kWaves)))),
-                               dim3(kWaves * kWave), 0, st, a);
+            hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(groups * heads))), dim3(kWaves * kWave),
+                               0, st, a, each, groups);
             SG_LAUNCH_CHECK();
-            join_sum<T>(a.rows, a.part_q, a.s.hq, 1, a.s.dim, a.dq, a.dq, st);
+            join_sum<T>(a.rows, a.part_q, a.s.hq, 1, a.s.dim, a.rows.n, a.dq, a.dq, st);
         }
-        const int64_t cols = a.cols.npieces * a.s.hkv;
+        const int64_t cols = xcd_grid(a.cols.npieces) * a.s.hkv;
         if (cols > 0) {
             auto run = k_attn_grad_kv<typename Tag::Geo, T>;
-            hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(ceil_div(cols, kWaves)))),
-                               dim3(kWaves * kWave), 0, st, a);
+            hipLaunchKernelGGL(run, dim3(grid_1d(cols)), dim3(kKvWaves * kWave), 0, st,
+                               a);
             SG_LAUNCH_CHECK();
-            join_sum<T>(a.cols, a.part_kv, a.s.hkv, 2, a.s.dim, a.dk, a.dv, st);
+            join_sum<T>(a.cols, a.part_kv, a.s.hkv, 2 * kColBlock, a.s.dim, a.ncols, a.dk, a.dv, st);
         }
     });
 }

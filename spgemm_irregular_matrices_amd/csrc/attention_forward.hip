@@ -5,25 +5,23 @@ namespace sg {
 
 namespace {
 
-constexpr int kWaves = 4;  // wavefronts per work group; each has a piece of its own
+constexpr int kWaves = 4;
 
-// Half precision keeps only 2^-24 absolutely: probabilities are held times
-// 2^14 there, so that the many small ones of a long row keep their 11 bits
-// (the largest is 2^14, a quarter of the type's range). The sum carries the
-// same factor.
-template <class T>
-constexpr float kProbShift = std::is_same<T, _Float16>::value ? 14.f : 0.f;
-
-// One wavefront: the 16 query heads [16*mt, 16*mt+16) of a key head's group
-// against the piece's keys, one tile of KT gathered keys after another.
+// One wavefront: 16 query heads [16*mt, 16*mt+16) of a key head's group
+// against `each` pieces in turn. The tiles of all its pieces form one stream,
+// so that a short row costs no idle trip to memory: while a tile is computed
+// the next one's key and value rows are under way (K into the registers that
+// the scores freed, V into those that the second product freed) and the
+// indices of the one after that.
 template <class G, class T>
-__global__ __launch_bounds__(kWaves* kWave) void k_attn_forward(ForwardArgs a) {
+__global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_forward(ForwardArgs a, int each,
+                                                                int64_t groups) {
     const int lane = lane_id();
-    const int64_t unit = xcd_block() * kWaves + threadIdx.x / kWave;
-    const int64_t npieces = a.side.npieces;
-    if (unit >= npieces * a.s.hkv * a.s.mtiles) return;
-    const int hm = (int)(unit / npieces);  // key head and group of 16 query heads
-    const AttnPiece pc = a.side.pieces[unit - (int64_t)hm * npieces];
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t block = xcd_block();
+    const int hm = (int)(block / groups);  // key head and 16 query heads
+    if (hm >= a.s.hkv * a.s.mtiles) return;
+    const int64_t u0 = (block - hm * groups) * kWaves * each + w;
     const int h = hm / a.s.mtiles, mt = hm - h * a.s.mtiles;
     const int n = lane & 15;  // this lane's query head in the tile
     const int g = 16 * mt + n;
@@ -31,88 +29,120 @@ __global__ __launch_bounds__(kWaves* kWave) void k_attn_forward(ForwardArgs a) {
     const int hq = h * a.s.group + g;
     const int row_bytes = a.s.dim * (int)sizeof(T);
 
-    typename G::RowFrag q;
-    G::zero_row(q);
-    if (has) G::load_row(a.q.base + pc.row * a.q.row + hq * a.q.head, row_bytes, q);
-    typename G::Acc o;
-    G::zero_acc(o);
-    float m = -INFINITY, l = 0.f;  // l: this lane's keys only, until the end
+    PieceStream st(a.side, u0, kWaves, each);
+    for (uint64_t e = st.empty; e; e &= e - 1) {
+        const int row = st.row(__builtin_ctzll(e));
+        if (!has) continue;
+        typename G::Acc zero;
+        G::zero_acc(zero);
+        char* out = a.out.base + row * a.out.row + hq * a.out.head;
+#pragma unroll
+        for (int u = 0; u < G::U; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) G::store_out(zero, u, r, 0.f, out, row_bytes);
+        if (a.lse && lane < 16) a.lse[(int64_t)row * a.s.hq + hq] = -INFINITY;
+    }
+    if (!st.todo) return;
 
     const char* kb = a.k.base + h * a.k.head;
     const char* vb = a.v.base + h * a.v.head;
-    const int32_t* idx = a.side.idx + pc.first;
-    for (int t0 = 0; t0 < pc.len; t0 += G::KT) {
-        const int left = pc.len - t0;
-        // lanes past the end repeat the last entry: every address is one the row names
-        const uint32_t id = (uint32_t)idx[t0 + min(lane & (G::KT - 1), left - 1)];
-        const uint32_t ko = id * a.k.unit, vo = id * a.v.unit;
+    typename G::RowFrag q, k[G::KSUB];
+    typename G::VBlock v[G::U];
+    const auto load_q = [&](int i) {
+        G::zero_row(q);
+        if (has)
+            G::load_row(a.q.base + st.row(i) * a.q.row + hq * a.q.head, row_bytes, q);
+    };
+    const auto load_k = [&](uint32_t id) {
+        const uint32_t off = id * a.k.unit;
+#pragma unroll
+        for (int b = 0; b < G::KSUB; ++b)
+            G::load_row(kb + ((uint64_t)(uint32_t)__shfl(off, 16 * b + n, kWave) << a.k.shift),
+                        row_bytes, k[b]);
+    };
+    const auto load_v = [&](uint32_t id) {
+        const uint32_t off = id * a.v.unit;
+#pragma unroll
+        for (int j = 0; j < G::VK; ++j) {
+            const char* row = vb + ((uint64_t)(uint32_t)__shfl(off, G::key_of(j), kWave)
+                                    << a.v.shift);
+#pragma unroll
+            for (int u = 0; u < G::U; ++u) G::load_chunk(row, u, row_bytes, v[u].w[j]);
+        }
+    };
 
+    PieceStream::Cursor cur, ahead;  // ahead: the tile whose indices are loaded
+    st.open(cur);
+    uint32_t id = st.id(cur, G::KT);
+    load_q(cur.i);
+    load_k(id);
+    load_v(id);
+    ahead = cur;
+    st.next(ahead, G::KT);
+    if (ahead.more) id = st.id(ahead, G::KT);
+
+    typename G::Acc o;
+    G::zero_acc(o);
+    Softmax<G, T> sm;
+    while (true) {
+        const int left = cur.len - cur.t0;
+        const bool last = left <= G::KT, more = ahead.more;
         f32x4 s[G::KSUB];
 #pragma unroll
-        for (int b = 0; b < G::KSUB; ++b) {
-            const uint32_t off = __shfl(ko, 16 * b + n, kWave);
-            typename G::RowFrag k;
-            G::load_row(kb + ((uint64_t)off << a.k.shift), row_bytes, k);
-            s[b] = G::dot(k, q, f32x4{0, 0, 0, 0});
+        for (int b = 0; b < G::KSUB; ++b) s[b] = G::dot(k[b], q, f32x4{0, 0, 0, 0});
+        const uint32_t idn = id;
+        if (more) {
+            load_k(idn);
+            if (last) load_q(ahead.i);
         }
-        float p[G::VK], top = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < G::VK; ++j) {
-            p[j] = G::key_of(j) < left ? s[j >> 2][j & 3] * a.s.c : -INFINITY;
-            top = fmaxf(top, p[j]);
+        const PieceStream::Cursor after = ahead;
+        if (more) {
+            st.next(ahead, G::KT);
+            if (ahead.more) id = st.id(ahead, G::KT);
         }
-        const float mn = fmaxf(m, quad_max(top));
-        const float ms = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: weights 0, not NaN
-        const float fix = fast_exp2(m - ms);
-        m = mn;
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < G::VK; ++j) {
-            p[j] = fast_exp2(p[j] - (ms - kProbShift<T>));
-            sum += p[j];
-        }
-        l = l * fix + sum;
-        G::scale_acc(o, fix);
         typename G::Probs pr;
-        G::pack_probs(p, pr);
+        sm.step(s, left, a.s.c, o, pr);
+        if (left < G::KT) {
+            // 0 weight times what a repeated row holds may be NaN
 #pragma unroll
-        for (int u = 0; u < G::U; ++u) {
-            typename G::VBlock v;
+            for (int j = 0; j < G::VK; ++j)
+                if (G::key_of(j) >= left)
 #pragma unroll
-            for (int j = 0; j < G::VK; ++j) {
-                const uint32_t off = __shfl(vo, G::key_of(j), kWave);
-                G::load_chunk(vb + ((uint64_t)off << a.v.shift), u, row_bytes, v.w[j]);
-                if (G::key_of(j) >= left) {  // 0 weight times what the row holds may be NaN
+                    for (int u = 0; u < G::U; ++u)
 #pragma unroll
-                    for (int i = 0; i < G::VW; ++i) v.w[j][i] = 0;
+                        for (int i = 0; i < G::VW; ++i) v[u].w[j][i] = 0;
+        }
+#pragma unroll
+        for (int u = 0; u < G::U; ++u) G::accumulate(v[u], pr, u, o);
+        if (more) load_v(idn);
+        if (last) {
+            sm.finish();
+            const int row = st.row(cur.i), slot = st.slot(cur.i);
+            if (has && slot < 0) {
+                const float f = sm.factor();
+                char* out = a.out.base + row * a.out.row + hq * a.out.head;
+#pragma unroll
+                for (int u = 0; u < G::U; ++u)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) G::store_out(o, u, r, f, out, row_bytes);
+                if (a.lse && lane < 16) a.lse[(int64_t)row * a.s.hq + hq] = sm.lse();
+            } else if (has) {
+                const int64_t at = (int64_t)slot * a.s.hq + hq;
+                float* dst = a.part + at * a.s.dim;
+#pragma unroll
+                for (int u = 0; u < G::U; ++u)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) G::store_part(o, u, r, 1.f, dst, a.s.dim);
+                if (lane < 16) {
+                    a.part_ml[2 * at] = sm.m;
+                    a.part_ml[2 * at + 1] = sm.l;
                 }
             }
-            G::accumulate(v, pr, u, o);
+            if (!more) break;
+            G::zero_acc(o);
+            sm = Softmax<G, T>();
         }
-    }
-    l = quad_sum(l);
-    if (!has) return;
-    if (pc.slot < 0) {
-        const float f = l == 0.f ? 0.f : 1.f / l;
-        char* row = a.out.base + pc.row * a.out.row + hq * a.out.head;
-#pragma unroll
-        for (int u = 0; u < G::U; ++u)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) G::store_out(o, u, r, f, row, row_bytes);
-        if (a.lse && lane < 16)
-            a.lse[(int64_t)pc.row * a.s.hq + hq] =
-                l == 0.f ? -INFINITY : (m - kProbShift<T> + fast_log2(l)) * kLn2;
-    } else {
-        const int64_t at = (int64_t)pc.slot * a.s.hq + hq;
-        float* dst = a.part + at * a.s.dim;
-#pragma unroll
-        for (int u = 0; u < G::U; ++u)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) G::store_part(o, u, r, 1.f, dst, a.s.dim);
-        if (lane < 16) {
-            a.part_ml[2 * at] = m;
-            a.part_ml[2 * at + 1] = l;
-        }
+        cur = after;
     }
 }
 
@@ -155,13 +185,15 @@ __global__ __launch_bounds__(kWaves* kWave) void k_attn_join(ForwardArgs a) {
 }  // namespace
 
 void attention_forward(const ForwardArgs& a, hipStream_t st) {
-    const int64_t units = a.side.npieces * a.s.hkv * a.s.mtiles;
-    if (units == 0) return;
+    const int64_t heads = (int64_t)a.s.hkv * a.s.mtiles;
+    if (a.side.npieces == 0) return;
+    const int each = pieces_per_wave(a.side.npieces * heads);
+    const int64_t groups = ceil_div(a.side.npieces, kWaves * each);
     with_type(a.s.type, a.s.dim, [&](auto tag) {
         using Tag = decltype(tag);
         auto run = k_attn_forward<typename Tag::Geo, typename Tag::Elem>;
-        hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(ceil_div(units, kWaves)))),
-                           dim3(kWaves * kWave), 0, st, a);
+        hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(groups * heads))), dim3(kWaves * kWave), 0,
+                           st, a, each, groups);
         SG_LAUNCH_CHECK();
         if (a.side.nsplits > 0) {
             hipLaunchKernelGGL(k_attn_join<typename Tag::Elem>,

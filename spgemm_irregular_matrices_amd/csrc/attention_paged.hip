@@ -7,10 +7,6 @@ namespace {
 
 constexpr int kWaves = 4;
 
-// See attention_forward.hip: half-precision probabilities carry 2^14.
-template <class T>
-constexpr float kProbShift = std::is_same<T, _Float16>::value ? 14.f : 0.f;
-
 // One sequence of the batch, checked where it is read.
 struct Sequence {
     int64_t q0;      // its first new token's row
@@ -149,27 +145,13 @@ __global__ __launch_bounds__(kWaves* kWave) void k_paged(PagedArgs a, int32_t ti
                 G::accumulate(v, pr, u, o);
             } else {
                 // an infinity or NaN that some of the rows must not see: one
-                // token at a time, with what it does not see as 0 (the same sums
-                // in the same order, so the same bits as with finite values)
-                const typename G::Acc old = o;
-                for (int tt = first_row / a.s.group; tt <= most - before; ++tt) {
-                    typename G::VBlock seen;
-#pragma unroll
-                    for (int j = 0; j < G::VK; ++j)
-#pragma unroll
-                        for (int i = 0; i < G::VW; ++i)
-                            seen.w[j][i] =
-                                t0 + G::key_of(j) < before + tt ? v.w[j][i] : 0u;
-                    typename G::Acc x;
-#pragma unroll
-                    for (int c = 0; c < G::CHL; ++c) x.o[u][c] = old.o[u][c];
-                    G::accumulate(seen, pr, u, x);
-#pragma unroll
-                    for (int c = 0; c < G::CHL; ++c)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            o.o[u][c][r] = tt == t ? x.o[u][c][r] : o.o[u][c][r];
-                }
+                // token at a time
+                const int tok = first_row / a.s.group;
+                G::accumulate_seen(v, pr, u, most - before - tok + 1, t - tok,
+                                   [&](int i, int j) {
+                                       return t0 + G::key_of(j) < before + tok + i;
+                                   },
+                                   o);
             }
         }
     }

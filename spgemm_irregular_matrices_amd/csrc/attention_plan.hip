@@ -26,7 +26,7 @@ namespace {
 // those of 16 entries) and 1024.
 int64_t piece_length(int64_t nnz) {
     const int64_t want = ceil_div(ceil_div(nnz, 4096), 32) * 32;
-    return want < 128 ? 128 : want > 1024 ? 1024 : want;
+    return want < 32 ? 32 : want > 1024 ? 1024 : want;
 }
 
 struct RowPieces {
@@ -70,11 +70,6 @@ __global__ void k_fill_pieces(RowPieces rows, int64_t n, const int64_t* piece0,
     if (count > 1 && k == 0) splits[split0[row]] = {(int32_t)row, p.slot, (int32_t)count, 0};
 }
 
-__global__ void k_count_cols(const int32_t* col, int64_t nnz, int32_t* count) {
-    for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < nnz;
-         e += (int64_t)gridDim.x * blockDim.x)
-        atomicAdd(&count[col[e]], 1);
-}
 __global__ void k_entry_rows(const int64_t* rp, int64_t n, int64_t nnz, int32_t* row,
                              int32_t* entry) {
     const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -86,17 +81,48 @@ __global__ void k_gather(const int32_t* src, const int32_t* perm, int64_t n, int
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i < n) dst[i] = src[perm[i]];
 }
-struct LoadI32 {
-    const int32_t* p;
-    __device__ int64_t operator()(int64_t i) const { return p[i]; }
-};
-struct ColDigit {
+struct BlockDigit {
     const int32_t* col;
     const int32_t* entry;
     int shift;
     __device__ int operator()(int64_t i) const { return (col[entry[i]] >> shift) & 15; }
 };
 
+// Entries in the order (column block, row, place in the row). An entry
+// begins a new group where the block or the row changes, or the column does
+// not ascend: a group's columns differ, so 16 bits hold them.
+struct GroupStart {
+    const int32_t* col;
+    const int32_t* row;
+    const int32_t* entry;
+    __device__ int64_t operator()(int64_t i) const {
+        if (i == 0) return 1;
+        const int32_t e = entry[i], f = entry[i - 1];
+        return col[e] / kColBlock != col[f] / kColBlock || row[e] != row[f] || col[e] <= col[f];
+    }
+};
+__global__ void k_fill_groups(GroupStart g, int64_t nnz, const int64_t* group, int32_t* idx,
+                              uint16_t* bits) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= nnz || g(i) == 0) return;
+    uint32_t m = 0;
+    for (int64_t j = i; j < nnz && (j == i || g(j) == 0); ++j)
+        m |= 1u << (g.col[g.entry[j]] % kColBlock);
+    idx[group[i]] = g.row[g.entry[i]];
+    bits[group[i]] = (uint16_t)m;
+}
+// First group of every block, and the groups' number behind the last.
+__global__ void k_block_groups(const int32_t* col, const int32_t* entry, int64_t nnz,
+                               const int64_t* group, int64_t nblocks, int64_t* first) {
+    const int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (b > nblocks) return;
+    int64_t lo = 0, hi = nnz;  // first entry of block b or later
+    while (lo < hi) {
+        const int64_t mid = lo + ((hi - lo) >> 1);
+        if (col[entry[mid]] / kColBlock < b) lo = mid + 1; else hi = mid;
+    }
+    first[b] = group[lo];
+}
 
 AttnSide make_side(const char* name, const int64_t* rp, int64_t n, int64_t nnz, const int32_t* idx,
                    Arena& keep, Arena& tmp, hipStream_t st) {
@@ -156,38 +182,44 @@ int build_plan(spgemm_attention_plan p, const spgemm_csr* mask, bool backward, h
     copy<int32_t>(col, m.col, m.nnz, st);
     p->rows = make_side("rows", m.rp, m.n, m.nnz, col, p->ar, tmp, st);
     if (backward) {
-        int32_t* count = tmp.get<int32_t>("count", (size_t)m.m + 1);
-        int64_t* cp = tmp.get<int64_t>("colptr", (size_t)m.m + 1);
-        int32_t* trow = p->ar.get<int32_t>("trow", (size_t)m.nnz);
-        fill<int32_t>(count, m.m + 1, 0, st);
+        const int64_t nblocks = ceil_div(m.m, kColBlock);
+        int64_t* first = tmp.get<int64_t>("first", (size_t)nblocks + 1);
+        int32_t* gidx = p->ar.get<int32_t>("groups", (size_t)m.nnz);
+        uint16_t* gbits = p->ar.get<uint16_t>("bits", (size_t)m.nnz);
+        int64_t ngroups = 0;
         if (m.nnz > 0) {
-            hipLaunchKernelGGL(k_count_cols,
-                               dim3(grid_1d(std::min<int64_t>(ceil_div(m.nnz, 256), 8192))),
-                               dim3(256), 0, st, col, m.nnz, count);
-            SG_LAUNCH_CHECK();
-        }
-        scan_exclusive(LoadI32{count}, m.m, cp, tmp, st);
-        if (m.nnz > 0) {
-            // a stable radix sort of the entries by column, 4 bits a pass, so
-            // that the rows of a column ascend (and its sums have one order)
+            // a stable radix sort of the entries by column block, 4 bits a
+            // pass: rows ascend within a block, so its sums have one order
             const unsigned g = grid_1d(ceil_div(m.nnz, 256));
             int32_t* row = tmp.get<int32_t>("row", (size_t)m.nnz);
             int32_t* cur = tmp.get<int32_t>("cur", (size_t)m.nnz);
             int32_t* next = tmp.get<int32_t>("next", (size_t)m.nnz);
             int32_t* perm = tmp.get<int32_t>("perm", (size_t)m.nnz);
             int64_t* bins = tmp.get<int64_t>("bins", 17);
+            int64_t* group = tmp.get<int64_t>("group", (size_t)m.nnz + 1);
             hipLaunchKernelGGL(k_entry_rows, dim3(g), dim3(256), 0, st, m.rp, m.n, m.nnz, row, cur);
             SG_LAUNCH_CHECK();
-            for (int shift = 0; shift < 31 && (m.m - 1) >> shift > 0; shift += 4) {
-                partition(ColDigit{col, cur, shift}, m.nnz, 16, perm, nullptr, bins, tmp, st);
+            for (int shift = ilog2(kColBlock); shift < 31 && (m.m - 1) >> shift > 0; shift += 4) {
+                partition(BlockDigit{col, cur, shift}, m.nnz, 16, perm, nullptr, bins, tmp, st);
                 hipLaunchKernelGGL(k_gather, dim3(g), dim3(256), 0, st, cur, perm, m.nnz, next);
                 SG_LAUNCH_CHECK();
                 std::swap(cur, next);
             }
-            hipLaunchKernelGGL(k_gather, dim3(g), dim3(256), 0, st, row, cur, m.nnz, trow);
+            const GroupStart start{col, row, cur};
+            scan_exclusive(start, m.nnz, group, tmp, st);
+            hipLaunchKernelGGL(k_fill_groups, dim3(g), dim3(256), 0, st, start, m.nnz, group, gidx,
+                               gbits);
             SG_LAUNCH_CHECK();
+            hipLaunchKernelGGL(k_block_groups, dim3(grid_1d(ceil_div(nblocks + 1, 256))), dim3(256),
+                               0, st, col, cur, m.nnz, group, nblocks, first);
+            SG_LAUNCH_CHECK();
+            SG_HIP(hipMemcpyAsync(&ngroups, group + m.nnz, 8, hipMemcpyDeviceToHost, st));
+            SG_HIP(hipStreamSynchronize(st));
+        } else {
+            fill<int64_t>(first, nblocks + 1, 0, st);
         }
-        p->cols = make_side("cols", cp, m.m, m.nnz, trow, p->ar, tmp, st);
+        p->cols = make_side("cols", first, nblocks, ngroups, gidx, p->ar, tmp, st);
+        p->cols.bits = gbits;
     }
     SG_HIP(hipStreamSynchronize(st));  // before the temporary buffers go
     return SPGEMM_OK;
@@ -295,7 +327,7 @@ int64_t carve_backward(spgemm_attention_plan p, const AttnShape& s, void* ws, Ba
     Carver c{static_cast<char*>(ws)};
     a->delta = c.take((__int128)p->nrows * s.hq);
     a->part_q = c.take((__int128)p->rows.nslots * s.hq * s.dim);
-    a->part_kv = c.take((__int128)p->cols.nslots * s.hkv * 2 * s.dim);
+    a->part_kv = c.take((__int128)p->cols.nslots * s.hkv * kColBlock * 2 * s.dim);
     return c.used;
 }
 
@@ -453,6 +485,7 @@ SPGEMM_API int spgemm_attention_backward(spgemm_attention_plan p,
         a.s = make_shape(desc);
         a.rows = p->rows;
         a.cols = p->cols;
+        a.ncols = p->ncols;
         if (!rows_valid(q, p->nrows, a.s.hq, desc, false, &a.q) ||
             !rows_valid(k, p->ncols, a.s.hkv, desc, false, &a.krow) ||
             !rows_valid(v, p->ncols, a.s.hkv, desc, false, &a.vrow) ||

@@ -103,6 +103,7 @@ struct FastDiv {
 // FULL: the head dimension is DP itself, so that no chunk needs a check.
 template <class T, int DP, bool FULL>
 struct Tile {
+    static constexpr bool kFull = FULL;
     static constexpr bool k16 = sizeof(T) == 2;
     static constexpr int KT = k16 ? 32 : 16;     // keys per tile
     static constexpr int KSUB = KT / 16;         // 16-key results of S^T
@@ -203,15 +204,6 @@ struct Tile {
 #pragma unroll
             for (int c = 0; c < CHL; ++c) a.o[u][c] = f32x4{0, 0, 0, 0};
     }
-    // a += b in the lanes of `on`.
-    static __device__ __forceinline__ void add_acc(Acc& a, const Acc& b, bool on) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int c = 0; c < CHL; ++c)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) a.o[u][c][r] += on ? b.o[u][c][r] : 0.f;
-    }
     static __device__ __forceinline__ void scale_acc(Acc& a, float f) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -245,31 +237,135 @@ struct Tile {
         }
     }
 
-    // O^T += V^T P^T for chunk u.
-    static __device__ __forceinline__ void accumulate(const VBlock& v, const Probs& p, int u,
-                                                      Acc& a) {
+    // O^T += V^T P^T for word i of chunk u: the accumulators o[u][c] of the
+    // kPerWord values c that the word holds; w: the word of each of the
+    // lane's keys.
+    static constexpr int kPerWord = k16 ? 2 : 1;
+    static __device__ __forceinline__ void accumulate_word(const uint32_t (&w)[VK], const Probs& p,
+                                                           f32x4 (&o)[kPerWord]) {
         if constexpr (k16) {
             const u32x4 b{p.w[0], p.w[1], p.w[2], p.w[3]};
+            u32x4 lo, hi;
 #pragma unroll
-            for (int i = 0; i < VW; ++i) {
-                u32x4 lo, hi;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    lo[j] = __builtin_amdgcn_perm(v.w[2 * j + 1][i], v.w[2 * j][i], 0x05040100u);
-                    hi[j] = __builtin_amdgcn_perm(v.w[2 * j + 1][i], v.w[2 * j][i], 0x07060302u);
-                }
-                a.o[u][2 * i] = mfma32<T>(lo, b, a.o[u][2 * i]);
-                a.o[u][2 * i + 1] = mfma32<T>(hi, b, a.o[u][2 * i + 1]);
+            for (int j = 0; j < 4; ++j) {
+                lo[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x05040100u);
+                hi[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x07060302u);
             }
+            o[0] = mfma32<T>(lo, b, o[0]);
+            o[1] = mfma32<T>(hi, b, o[1]);
         } else {
 #pragma unroll
-            for (int c = 0; c < CHL; ++c)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    a.o[u][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                        __builtin_bit_cast(float, v.w[j][c]),
-                        __builtin_bit_cast(float, p.w[j]), a.o[u][c], 0, 0, 0);
+            for (int j = 0; j < 4; ++j)
+                o[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, w[j]),
+                                                            __builtin_bit_cast(float, p.w[j]),
+                                                            o[0], 0, 0, 0);
         }
+    }
+    static __device__ __forceinline__ void accumulate(const VBlock& v, const Probs& p, int u,
+                                                      Acc& a) {
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+            uint32_t w[VK];
+#pragma unroll
+            for (int j = 0; j < VK; ++j) w[j] = v.w[j][i];
+            f32x4 o[kPerWord];
+#pragma unroll
+            for (int c = 0; c < kPerWord; ++c) o[c] = a.o[u][kPerWord * i + c];
+            accumulate_word(w, p, o);
+#pragma unroll
+            for (int c = 0; c < kPerWord; ++c) a.o[u][kPerWord * i + c] = o[c];
+        }
+    }
+    // accumulate_word where a key may hold an infinity or a NaN and not every
+    // query sees every key: `times` passes, in each of which the keys that
+    // sees(pass, j) denies count as 0; a lane keeps the pass `mine`. The
+    // products and their order are the same, so finite keys give the same bits.
+    template <class Sees>
+    static __device__ __forceinline__ void accumulate_word_seen(const uint32_t (&w)[VK],
+                                                                const Probs& p, int times, int mine,
+                                                                Sees&& sees,
+                                                                f32x4 (&o)[kPerWord]) {
+        f32x4 old[kPerWord];
+#pragma unroll
+        for (int c = 0; c < kPerWord; ++c) old[c] = o[c];
+#pragma unroll 1
+        for (int t = 0; t < times; ++t) {
+            uint32_t x[VK];
+#pragma unroll
+            for (int j = 0; j < VK; ++j) x[j] = sees(t, j) ? w[j] : 0u;
+            f32x4 y[kPerWord];
+#pragma unroll
+            for (int c = 0; c < kPerWord; ++c) y[c] = old[c];
+            accumulate_word(x, p, y);
+#pragma unroll
+            for (int c = 0; c < kPerWord; ++c)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[c][r] = t == mine ? y[c][r] : o[c][r];
+        }
+    }
+    template <class Sees>
+    static __device__ __forceinline__ void accumulate_seen(const VBlock& v, const Probs& p, int u,
+                                                           int times, int mine, Sees&& sees,
+                                                           Acc& a) {
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+            uint32_t w[VK];
+#pragma unroll
+            for (int j = 0; j < VK; ++j) w[j] = v.w[j][i];
+            f32x4 o[kPerWord];
+#pragma unroll
+            for (int c = 0; c < kPerWord; ++c) o[c] = a.o[u][kPerWord * i + c];
+            accumulate_word_seen(w, p, times, mine, sees, o);
+#pragma unroll
+            for (int c = 0; c < kPerWord; ++c) a.o[u][kPerWord * i + c] = o[c];
+        }
+    }
+
+    // Rows staged in LDS, so that one trip to memory serves both operands.
+    // The 16-byte pieces of a row are exchanged by the bits b0.. of its
+    // number: by (b0, b1, b3, b2 ^ b4), which differs over 16 rows in
+    // sequence (the same piece of each is read at once) and in its upper two
+    // bits over every fourth and every eighth row (64 bytes of four such rows
+    // are); for rows of 128 bytes, two to a line of the banks, by (b1, b2, b3).
+    static constexpr int kDim = DP;
+    static constexpr int kRowBytes = DP * (int)sizeof(T);
+    static constexpr __device__ __forceinline__ int stage_x(int r) {
+        return kRowBytes < 256 ? ((r >> 1) & 7) << 4
+                               : ((r & 3) | ((r >> 3) & 1) << 2 | (((r >> 2) ^ (r >> 4)) & 1) << 3)
+                                     << 4;
+    }
+    static __device__ __forceinline__ int stage_at(int r, int byte) {
+        return r * kRowBytes + (byte ^ stage_x(r));
+    }
+    // stage_at(r | dr, byte | dbyte) from at = stage_at(r, byte), for constants
+    // that share no bit with r and byte (the exchange is linear in the bits).
+    static __device__ __forceinline__ int stage_more(int at, int dr, int dbyte) {
+        return (at ^ dbyte ^ stage_x(dr)) + dr * kRowBytes;
+    }
+    static __device__ __forceinline__ void stage_chunk(char* lds, int r, int u,
+                                                       const uint32_t (&w)[VW]) {
+        char* at = lds + stage_at(r, chunk_at(u));
+        if constexpr (VW == 4)
+            *reinterpret_cast<u32x4*>(at) = u32x4{w[0], w[1], w[2], w[3]};
+        else
+            *reinterpret_cast<u32x2*>(at) = u32x2{w[0], w[1]};
+    }
+    static __device__ __forceinline__ void staged_chunk(const char* lds, int r, int u,
+                                                        uint32_t (&w)[VW]) {
+        const char* at = lds + stage_at(r, chunk_at(u));
+        if constexpr (VW == 4) {
+            const u32x4 x = *reinterpret_cast<const u32x4*>(at);
+            w[0] = x[0]; w[1] = x[1]; w[2] = x[2]; w[3] = x[3];
+        } else {
+            const u32x2 x = *reinterpret_cast<const u32x2*>(at);
+            w[0] = x[0]; w[1] = x[1];
+        }
+    }
+    static __device__ __forceinline__ void staged_row(const char* lds, int r, RowFrag& f) {
+        const int at = stage_at(r, 16 * (lane_id() >> 4));
+#pragma unroll
+        for (int t = 0; t < QS; ++t)
+            f.w[t] = *reinterpret_cast<const u32x4*>(lds + stage_more(at, 0, 64 * t));
     }
 
     // Element index of the accumulator's first value in register r of chunk
@@ -306,6 +402,50 @@ struct Tile {
             *reinterpret_cast<f32x4*>(dst + at + c) =
                 f32x4{a.o[u][c][r] * f, a.o[u][c + 1][r] * f, a.o[u][c + 2][r] * f,
                       a.o[u][c + 3][r] * f};
+    }
+};
+
+// Half precision keeps only 2^-24 absolutely: probabilities are held times
+// 2^14 there, so that the many small ones of a long row keep their 11 bits
+// (the largest is 2^14, a quarter of the type's range). The sum carries the
+// same factor.
+template <class T>
+constexpr float kProbShift = std::is_same<T, _Float16>::value ? 14.f : 0.f;
+
+// The running maximum (base 2) and sum of a softmax, of this lane's query;
+// the sum covers this lane's keys only until finish().
+template <class G, class T>
+struct Softmax {
+    float m = -INFINITY, l = 0.f;
+
+    // Takes a tile's scores, of whose keys the first `limit` count, rescales
+    // what o holds, and leaves the weights.
+    __device__ __forceinline__ void step(const f32x4 (&s)[G::KSUB], int limit, float c,
+                                         typename G::Acc& o, typename G::Probs& out) {
+        float p[G::VK], top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < G::VK; ++j) {
+            p[j] = G::key_of(j) < limit ? s[j >> 2][j & 3] * c : -INFINITY;
+            top = fmaxf(top, p[j]);
+        }
+        const float mn = fmaxf(m, quad_max(top));
+        const float ms = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: weights 0, not NaN
+        const float fix = fast_exp2(m - ms);
+        m = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < G::VK; ++j) {
+            p[j] = fast_exp2(p[j] - (ms - kProbShift<T>));
+            sum += p[j];
+        }
+        l = l * fix + sum;
+        if (__any(fix != 1.f)) G::scale_acc(o, fix);
+        G::pack_probs(p, out);
+    }
+    __device__ __forceinline__ void finish() { l = quad_sum(l); }
+    __device__ __forceinline__ float factor() const { return l == 0.f ? 0.f : 1.f / l; }
+    __device__ __forceinline__ float lse() const {
+        return l == 0.f ? -INFINITY : (m - kProbShift<T> + fast_log2(l)) * kLn2;
     }
 };
 

@@ -44,7 +44,7 @@ struct InternalError : std::runtime_error {
 
 #define SG_LAUNCH_CHECK() SG_HIP(hipGetLastError())
 
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 inline int64_t floor_pow2(int64_t x) {
     int64_t p = 1;

@@ -155,6 +155,31 @@ def test_infinite_keys_and_values_in_seen_places():
         ref.check(lse, l, le, "lse")
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=str)
+@pytest.mark.parametrize("wild", [float("nan"), float("inf")])
+def test_gradients_of_wild_rows_stay_with_their_keys(dtype, wild):
+    """NaN or infinities in one row's q and dout reach only that row and the
+    keys it stores, not the neighbouring keys that share work with them."""
+    api = _api()
+    rng = np.random.default_rng(25)
+    rows = ref.mask([40, 3, 40, 40, 2, 40], 48, rng)
+    q, k, v, dout = (_rand(rng, s, dtype) for s in ((6, 4, 64), (48, 2, 64), (48, 2, 64), (6, 4, 64)))
+    with api.AttentionPlan(ref.csr(rows, 48), backward=True) as plan:
+        out, lse = plan.forward(q, k, v)
+        clean = plan.backward(dout, q, k, v, out, lse)
+        q[1], dout[4] = wild, wild
+        out, lse = plan.forward(q, k, v)
+        assert not torch.isfinite(out[1].float()).any()
+        dq, dk, dv = plan.backward(dout, q, k, v, out, lse)
+    mine = np.union1d(rows[1], rows[4])
+    rest = torch.from_numpy(np.setdiff1d(np.arange(48), mine)).cuda()
+    assert torch.equal(dk[rest], clean[1][rest]) and torch.equal(dv[rest], clean[2][rest])
+    for i in (0, 2, 3, 5):
+        assert torch.equal(dq[i], clean[0][i])
+    assert not torch.isfinite(dk[torch.from_numpy(rows[1]).cuda()].float()).any()
+    assert not torch.isfinite(dv[torch.from_numpy(rows[4]).cuda()].float()).any()
+
+
 @pytest.mark.parametrize("amount", [1e-6, 1.0, 3e4])
 def test_half_precision_gradients_of_any_size(amount):
     """Score gradients below and above what half precision holds."""
