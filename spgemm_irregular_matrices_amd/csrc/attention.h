@@ -105,7 +105,7 @@ struct PagedArgs {
     uint32_t k_shift = 0, v_shift = 0;
     int64_t k_head = 0, v_head = 0;  // bytes
     int64_t npages = 0;
-    FastDiv page_div;
+    FastDiv page_div, group_div;
     int64_t seqs = 0, tokens = 0, room = 0;  // room: entries of col
     const int64_t* rowptr = nullptr;
     const int32_t* col = nullptr;
@@ -119,6 +119,10 @@ struct PagedArgs {
     float* part_ml = nullptr;  // [piece][token][hq][2]
 };
 void paged_attention(const PagedArgs& a, hipStream_t st);
+// Whether a work group shares the keys of a sequence's `rows` rows (new
+// tokens times the query heads of a key head), and the rows of its tiles.
+bool paged_wide(int64_t rows);
+int paged_tile_rows(int dim, int64_t rows);
 
 // XCD x of the 8 gets every eighth work group; this gives each XCD a
 // contiguous eighth of the logical blocks, so that neighbouring pieces of one

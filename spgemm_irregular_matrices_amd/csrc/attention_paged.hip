@@ -32,14 +32,115 @@ __device__ __forceinline__ Sequence read_sequence(const PagedArgs& a, int64_t s)
     return x;
 }
 
-// One wavefront: 16 rows (neighbouring new tokens' query heads of one key
-// head, the heads of a token next to each other) against one piece of the
-// sequence's keys. A token whose keys all lie in the first piece is finished
-// here; the others leave their pieces to k_paged_join.
+// What a work group or wavefront has to do for a tile of `rows` rows of one
+// sequence (its new tokens' query heads of one key head, the heads of a token
+// next to each other) and one piece of its keys.
+struct TileJob {
+    Sequence sq;
+    int rows;    // of the whole sequence
+    int first;   // the tile's first row
+    int before;  // keys that the sequence's first new token sees
+    int k0, k1;  // the keys
+    bool idle;
+};
+__device__ __forceinline__ TileJob tile_job(const PagedArgs& a, int64_t s, int tile, int tile_rows,
+                                            int piece) {
+    TileJob j;
+    j.sq = read_sequence(a, s);
+    j.rows = j.sq.fresh * a.s.group;
+    j.first = tile * tile_rows;
+    j.idle = j.sq.none || j.first >= j.rows;
+    j.before = j.sq.length - j.sq.fresh + 1;
+    const int last = min(j.first + tile_rows, j.rows) - 1;
+    j.k0 = piece * a.piece;
+    j.k1 = min(j.k0 + a.piece, j.before + last / a.s.group);
+    return j;
+}
+
+// One row of a tile: its new token (of the sequence) and query head.
+struct TileRow {
+    bool has;
+    int t, hq;
+    int64_t token;
+};
+__device__ __forceinline__ TileRow tile_row(const PagedArgs& a, const TileJob& j, int row, int h) {
+    TileRow r;
+    r.has = row < j.rows;
+    const int x = min(row, j.rows - 1);
+    r.t = (int)a.group_div.div(x);
+    r.hq = h * a.s.group + x - r.t * a.s.group;
+    r.token = j.sq.q0 + r.t;
+    return r;
+}
+
+// NaN for one row of a sequence that breaks the rules, by the four lanes that
+// share it.
+template <class T>
+__device__ __forceinline__ void store_nan(const PagedArgs& a, const TileRow& r) {
+    if (!r.has) return;
+    T* out = reinterpret_cast<T*>(a.out.base + r.token * a.out.row + r.hq * a.out.head);
+    for (int d = lane_id() >> 4; d < a.s.dim; d += 4) out[d] = (T)NAN;
+    if (a.lse && lane_id() < 16) a.lse[r.token * a.s.hq + r.hq] = NAN;
+}
+
+// A row's result, finished if the first piece holds all keys that it sees,
+// otherwise as this piece's part of it.
 template <class G, class T>
-__global__ __launch_bounds__(kWaves* kWave) void k_paged(PagedArgs a, int32_t tiles) {
+__device__ __forceinline__ void store_row(const PagedArgs& a, const TileJob& j, const TileRow& r,
+                                          int piece, const typename G::Acc& o,
+                                          const Softmax<G, T>& sm) {
+    const int sees = j.before + r.t;
+    if (!r.has || sees <= j.k0) return;
+    const int row_bytes = a.s.dim * (int)sizeof(T);
+    const int64_t line = r.token * a.s.hq + r.hq;
+    if (sees <= a.piece) {
+        const float f = sm.factor();
+        char* out = a.out.base + r.token * a.out.row + r.hq * a.out.head;
+#pragma unroll
+        for (int u = 0; u < G::U; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) G::store_out(o, u, i, f, out, row_bytes);
+        if (a.lse && lane_id() < 16) a.lse[line] = sm.lse();
+    } else {
+        const int64_t at = (int64_t)piece * a.tokens * a.s.hq + line;
+        float* dst = a.part + at * a.s.dim;
+#pragma unroll
+        for (int u = 0; u < G::U; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) G::store_part(o, u, i, 1.f, dst, a.s.dim);
+        if (lane_id() < 16) {
+            a.part_ml[2 * at] = sm.m;
+            a.part_ml[2 * at + 1] = sm.l;
+        }
+    }
+}
+
+// O^T += V^T P^T for chunk u of a tile of keys. Where a row may not see every
+// key (`crosses`), 0 times an infinity or a NaN must not reach it.
+template <class G, int N, class Sees, class Row>
+__device__ __forceinline__ void add_values(typename G::VBlock& v,
+                                           const typename G::Probs (&pr)[N], int u, bool crosses,
+                                           int row_bytes, Sees&& sees, Row&& row,
+                                           typename G::Acc (&o)[N]) {
+    if (crosses) {
+        bool wild = false;
+#pragma unroll
+        for (int j = 0; j < G::VK; ++j) wild |= G::chunk_wild(v.w[j]);
+        if (__any(wild)) G::add_wild(v, pr, u, row_bytes, sees, row, o);
+    }
+#pragma unroll
+    for (int x = 0; x < N; ++x) G::accumulate(v, pr[x], u, o[x]);
+}
+
+// Few rows per sequence and key head: one wavefront takes 16 rows and one
+// piece of the keys, straight from memory. The next tile's rows are under way
+// while one is computed, as in the forward pass over a mask.
+template <class G, class T>
+__global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged(PagedArgs a,
+                                                                                 int32_t tiles) {
     const int lane = lane_id();
-    int64_t unit = xcd_block() * kWaves + threadIdx.x / kWave;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    int64_t unit = xcd_block() * kWaves + w;
     if (unit >= a.seqs * a.s.hkv * a.npieces * tiles) return;
     const int tile = (int)(unit % tiles);
     unit /= tiles;
@@ -47,137 +148,284 @@ __global__ __launch_bounds__(kWaves* kWave) void k_paged(PagedArgs a, int32_t ti
     unit /= a.npieces;
     const int64_t s = unit % a.seqs;
     const int h = (int)(unit / a.seqs);
-
-    const Sequence sq = read_sequence(a, s);
-    if (sq.none) return;
+    const TileJob job = tile_job(a, s, tile, 16, piece);
+    if (job.idle) return;
     const int n = lane & 15;
     const int row_bytes = a.s.dim * (int)sizeof(T);
-    const int first_row = 16 * tile;                 // of the sequence's fresh * group rows
-    const int rows = sq.fresh * a.s.group;
-    if (first_row >= rows) return;
-    const int row = first_row + n;
-    const bool has = row < rows;
-    const int t = min(row, rows - 1) / a.s.group, g = min(row, rows - 1) - t * a.s.group;
-    const int hq = h * a.s.group + g;
-    const int64_t token = sq.q0 + t;
-    char* out = a.out.base + token * a.out.row + hq * a.out.head;
-    if (sq.bad) {
-        if (piece == 0 && has) {
-            for (int d = lane >> 4; d < a.s.dim; d += 4) reinterpret_cast<T*>(out)[d] = (T)NAN;
-            if (a.lse && lane < 16) a.lse[token * a.s.hq + hq] = NAN;
-        }
+    const TileRow r = tile_row(a, job, job.first + n, h);
+    if (job.sq.bad) {
+        if (piece == 0) store_nan<T>(a, r);
         return;
     }
-    // keys this lane's token sees, and those that any row of the tile sees
-    const int before = sq.length - sq.fresh + 1;
-    const int sees = before + t;
-    const int least = before + first_row / a.s.group;
-    const int most = before + min(first_row + 15, rows - 1) / a.s.group;
-    const int k0 = piece * a.piece;
-    const int k1 = min(k0 + a.piece, most);
-    if (k0 >= k1) return;
+    if (job.k0 >= job.k1) return;
+    const int lo = __builtin_amdgcn_readfirstlane(r.t);
+    const int hi = __builtin_amdgcn_readlane(r.t, 15);
 
-    typename G::RowFrag q;
+    typename G::RowFrag q, k[G::KSUB];
+    typename G::VBlock v[G::U];
     G::zero_row(q);
-    if (has) G::load_row(a.q.base + token * a.q.row + hq * a.q.head, row_bytes, q);
-    typename G::Acc o;
-    G::zero_acc(o);
-    float m = -INFINITY, l = 0.f;
-    bool wrong = false;  // a page outside the cache
+    if (r.has) G::load_row(a.q.base + r.token * a.q.row + r.hq * a.q.head, row_bytes, q);
     const char* kb = a.k + h * a.k_head;
     const char* vb = a.v + h * a.v_head;
-    const int32_t* pages = a.col + sq.page0;
-    for (int t0 = k0; t0 < k1; t0 += G::KT) {
-        const int left = k1 - t0;
-        const uint32_t key = (uint32_t)(t0 + min(lane & (G::KT - 1), left - 1));
-        const uint32_t pg = a.page_div.div(key), slot = key - pg * a.page_div.d;
-        uint32_t id = (uint32_t)pages[pg];
-        if (id >= (uint64_t)a.npages) {
+    const int32_t* pages = a.col + job.sq.page0;
+    bool wrong = false;  // a page outside the cache
+    struct Place {
+        uint32_t id, slot;
+    };
+    // lanes past the piece's end repeat its last key
+    const auto place = [&](int t0) {
+        const uint32_t key = (uint32_t)min(t0 + (lane & (G::KT - 1)), job.k1 - 1);
+        const uint32_t pg = a.page_div.div(key);
+        return Place{(uint32_t)pages[pg], key - pg * a.page_div.d};
+    };
+    const auto checked = [&](Place& x) {
+        if (x.id >= (uint64_t)a.npages) {
             wrong = true;
-            id = 0;
+            x.id = 0;
         }
-        const uint32_t ko = id * a.k_page + slot * a.k_slot, vo = id * a.v_page + slot * a.v_slot;
+    };
+    const auto load_k = [&](const Place& x) {
+        const uint32_t off = x.id * a.k_page + x.slot * a.k_slot;
+#pragma unroll
+        for (int b = 0; b < G::KSUB; ++b)
+            G::load_row(kb + ((uint64_t)(uint32_t)__shfl(off, 16 * b + n, kWave) << a.k_shift),
+                        row_bytes, k[b]);
+    };
+    const auto load_v = [&](const Place& x) {
+        const uint32_t off = x.id * a.v_page + x.slot * a.v_slot;
+#pragma unroll
+        for (int j = 0; j < G::VK; ++j) {
+            const char* row =
+                vb + ((uint64_t)(uint32_t)__shfl(off, G::key_of(j), kWave) << a.v_shift);
+#pragma unroll
+            for (int u = 0; u < G::U; ++u) G::load_chunk(row, u, row_bytes, v[u].w[j]);
+        }
+    };
+    Place now = place(job.k0), here = now;  // here: of the tile that is computed
+    Place next = now;
+    if (job.k0 + G::KT < job.k1) next = place(job.k0 + G::KT);
+    checked(now);
+    load_k(now);
+    load_v(now);
+
+    typename G::Acc o[1];
+    G::zero_acc(o[0]);
+    Softmax<G, T> sm;
+    for (int t0 = job.k0; t0 < job.k1; t0 += G::KT) {
+        const int left = job.k1 - t0;
+        const bool more = left > G::KT;
         f32x4 sc[G::KSUB];
 #pragma unroll
-        for (int b = 0; b < G::KSUB; ++b) {
-            const uint32_t off = __shfl(ko, 16 * b + n, kWave);
-            typename G::RowFrag k;
-            G::load_row(kb + ((uint64_t)off << a.k_shift), row_bytes, k);
-            sc[b] = G::dot(k, q, f32x4{0, 0, 0, 0});
+        for (int b = 0; b < G::KSUB; ++b) sc[b] = G::dot(k[b], q, f32x4{0, 0, 0, 0});
+        here = now;
+        if (more) {
+            now = next;
+            checked(now);
+            load_k(now);
+            if (left > 2 * G::KT) next = place(t0 + 2 * G::KT);
         }
-        const int limit = min(left, sees - t0);
-        float p[G::VK], top = -INFINITY;
+        typename G::Probs pr[1];
+        sm.step(sc, min(left, job.before + r.t - t0), a.s.c, o[0], pr[0]);
+        if (left < G::KT) {
+            // 0 weight times what a repeated place holds may be NaN
 #pragma unroll
-        for (int j = 0; j < G::VK; ++j) {
-            p[j] = G::key_of(j) < limit ? sc[j >> 2][j & 3] * a.s.c : -INFINITY;
-            top = fmaxf(top, p[j]);
+            for (int j = 0; j < G::VK; ++j)
+                if (G::key_of(j) >= left)
+#pragma unroll
+                    for (int u = 0; u < G::U; ++u)
+#pragma unroll
+                        for (int i = 0; i < G::VW; ++i) v[u].w[j][i] = 0;
         }
-        const float mn = fmaxf(m, quad_max(top));
-        const float ms = mn == -INFINITY ? 0.f : mn;
-        const float fix = fast_exp2(m - ms);
-        m = mn;
-        float sum = 0.f;
+        const bool crosses = t0 + G::KT > job.before + lo;  // some row may not see some key
+        const auto sees = [&](int, int key) { return t0 + key < job.before + r.t; };
+        const auto row = [&](int key) {
+            const uint32_t off = __shfl(here.id * a.v_page + here.slot * a.v_slot, key, kWave);
+            const char* at = vb + ((uint64_t)off << a.v_shift);
+            return [at](int byte) { return *reinterpret_cast<const uint32_t*>(at + byte); };
+        };
 #pragma unroll
-        for (int j = 0; j < G::VK; ++j) {
-            p[j] = fast_exp2(p[j] - (ms - kProbShift<T>));
-            sum += p[j];
-        }
-        l = l * fix + sum;
-        G::scale_acc(o, fix);
-        typename G::Probs pr;
-        G::pack_probs(p, pr);
-        const bool crosses = t0 + G::KT > least;  // some row may not see some key
+        for (int u = 0; u < G::U; ++u)
+            add_values<G, 1>(v[u], pr, u, crosses, row_bytes, sees, row, o);
+        if (more) load_v(now);
+    }
+    sm.finish();
+    if (__any(wrong)) sm.l = NAN;
+    store_row<G, T>(a, job, r, piece, o[0], sm);
+}
+
+// Many rows: a work group of 4 wavefronts takes 4 * 16 * QB rows, a wavefront
+// 16 * QB of them, and BK keys at a time are shared in LDS. Each operand made
+// from the shared keys serves QB products.
+template <class G>
+struct Wide {
+    static constexpr int QB = G::kDim <= 128 ? 2 : 1;  // 16-row blocks per wavefront
+    static constexpr int BM = kWaves * 16 * QB;
+    static constexpr int BK = G::kRowBytes <= 256 ? 64 : 32;
+};
+
+template <class G, class T>
+__global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged_wide(
+    PagedArgs a, int32_t tiles) {
+    using W = Wide<G>;
+    constexpr int NT = kWaves * kWave, BK = W::BK, QB = W::QB;
+    constexpr int kPieces = G::kRowBytes / 16, kLoads = BK * kPieces / NT, kStep = NT / kPieces;
+    static_assert(BK * kPieces % NT == 0 && BK % G::KT == 0, "tile shape");
+    __shared__ __align__(16) char rows[2][BK * G::kRowBytes];  // k, v
+    __shared__ uint32_t off[2][BK];
+    __shared__ int wrong_s;
+    const int tid = threadIdx.x, lane = lane_id();
+    const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
+    int64_t unit = xcd_block();
+    if (unit >= a.seqs * a.s.hkv * a.npieces * tiles) return;
+    const int tile = tiles - 1 - (int)(unit % tiles);  // the longest first
+    unit /= tiles;
+    const int piece = (int)(unit % a.npieces);
+    unit /= a.npieces;
+    const int64_t s = unit % a.seqs;
+    const int h = (int)(unit / a.seqs);
+    const TileJob job = tile_job(a, s, tile, W::BM, piece);
+    if (job.idle) return;
+    const int n = lane & 15;
+    const int row_bytes = a.s.dim * (int)sizeof(T);
+    const int row0 = job.first + 16 * QB * w;  // this wavefront's first row
+    TileRow r[QB];
 #pragma unroll
-        for (int u = 0; u < G::U; ++u) {
-            typename G::VBlock v;
-            bool wild = false;
+    for (int b = 0; b < QB; ++b) r[b] = tile_row(a, job, row0 + 16 * b + n, h);
+    if (job.sq.bad) {
+        if (piece == 0)
 #pragma unroll
-            for (int j = 0; j < G::VK; ++j) {
-                const uint32_t off = __shfl(vo, G::key_of(j), kWave);
-                G::load_chunk(vb + ((uint64_t)off << a.v_shift), u, row_bytes, v.w[j]);
-                if (G::key_of(j) >= left) {  // 0 weight times what the place holds may be NaN
+            for (int b = 0; b < QB; ++b) store_nan<T>(a, r[b]);
+        return;
+    }
+    if (job.k0 >= job.k1) return;
+    if (tid == 0) wrong_s = 0;
+    // keys that some row of the wavefront sees (none: it only helps to load)
+    const int lo = __builtin_amdgcn_readfirstlane(r[0].t);
+    const int hi = __builtin_amdgcn_readlane(r[QB - 1].t, 15);
+    const int mine = row0 < job.rows ? min(job.k1, job.before + hi) : 0;
+
+    typename G::RowFrag q[QB];
+    typename G::Acc o[QB];
+    Softmax<G, T> sm[QB];
 #pragma unroll
-                    for (int i = 0; i < G::VW; ++i) v.w[j][i] = 0;
-                }
-                if (crosses) wild |= G::chunk_wild(v.w[j]);
+    for (int b = 0; b < QB; ++b) {
+        G::zero_row(q[b]);
+        G::zero_acc(o[b]);
+        if (r[b].has)
+            G::load_row(a.q.base + r[b].token * a.q.row + r[b].hq * a.q.head, row_bytes, q[b]);
+    }
+    const char* kb = a.k + h * a.k_head;
+    const char* vb = a.v + h * a.v_head;
+    const int32_t* pages = a.col + job.sq.page0;
+    // thread i < BK looks key i of a tile up
+    uint32_t id = 0;
+    const auto load_id = [&](int t0) {
+        if (tid < BK && t0 + tid < job.k1) id = (uint32_t)pages[a.page_div.div(t0 + tid)];
+    };
+    const auto put_offsets = [&](int t0) {
+        if (tid < BK && t0 + tid < job.k1) {
+            if (id >= (uint64_t)a.npages) {
+                wrong_s = 1;
+                id = 0;
             }
-            if (!crosses || !__any(wild)) {
-                G::accumulate(v, pr, u, o);
-            } else {
-                // an infinity or NaN that some of the rows must not see: one
-                // token at a time
-                const int tok = first_row / a.s.group;
-                G::accumulate_seen(v, pr, u, most - before - tok + 1, t - tok,
-                                   [&](int i, int j) {
-                                       return t0 + G::key_of(j) < before + tok + i;
-                                   },
-                                   o);
+            const uint32_t key = t0 + tid, slot = key - a.page_div.div(key) * a.page_div.d;
+            off[0][tid] = id * a.k_page + slot * a.k_slot;
+            off[1][tid] = id * a.v_page + slot * a.v_slot;
+        }
+    };
+    u32x4 fly[2][kLoads];
+    const int prow = tid / kPieces, pbyte = tid % kPieces * 16;
+    const bool inside = G::kFull || pbyte < row_bytes;
+    const char* kp = kb + (inside ? pbyte : 0);
+    const char* vp = vb + (inside ? pbyte : 0);
+    const auto load_rows = [&](int t0) {
+        const int left = job.k1 - t0;
+        if (left >= BK) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int p = i * kStep + prow;
+                fly[0][i] = *reinterpret_cast<const u32x4*>(kp + ((uint64_t)off[0][p] << a.k_shift));
+                fly[1][i] = *reinterpret_cast<const u32x4*>(vp + ((uint64_t)off[1][p] << a.v_shift));
+            }
+        } else {
+            // places past the end read the tile's first key and become 0
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int p = i * kStep + prow;
+                const bool in = p < left;
+                const u32x4 x = *reinterpret_cast<const u32x4*>(
+                    kp + ((uint64_t)off[0][in ? p : 0] << a.k_shift));
+                const u32x4 y = *reinterpret_cast<const u32x4*>(
+                    vp + ((uint64_t)off[1][in ? p : 0] << a.v_shift));
+                fly[0][i] = in ? x : u32x4{0, 0, 0, 0};
+                fly[1][i] = in ? y : u32x4{0, 0, 0, 0};
+            }
+        }
+        if (!inside) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) fly[0][i] = fly[1][i] = u32x4{0, 0, 0, 0};
+        }
+    };
+    load_id(job.k0);
+    __syncthreads();  // wrong_s
+    put_offsets(job.k0);
+    __syncthreads();
+    load_rows(job.k0);
+    load_id(job.k0 + BK);
+    for (int t0 = job.k0; t0 < job.k1; t0 += BK) {
+        __syncthreads();  // the last tile's readers are done
+        const int put = G::stage_at(prow, pbyte);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int at = G::stage_more(put, i * kStep, 0);
+            *reinterpret_cast<u32x4*>(rows[0] + at) = fly[0][i];
+            *reinterpret_cast<u32x4*>(rows[1] + at) = fly[1][i];
+        }
+        put_offsets(t0 + BK);
+        __syncthreads();
+        if (t0 + BK < job.k1) {
+            load_rows(t0 + BK);
+            load_id(t0 + 2 * BK);
+        }
+#pragma unroll 1
+        for (int t = t0; t < min(t0 + BK, mine); t += G::KT) {
+            const int at = t - t0;  // the tile's first staged row
+            f32x4 sc[QB][G::KSUB];
+#pragma unroll
+            for (int b = 0; b < G::KSUB; ++b) {
+                typename G::RowFrag k;
+                G::staged_row(rows[0], at + 16 * b + n, k);
+#pragma unroll
+                for (int x = 0; x < QB; ++x) sc[x][b] = G::dot(k, q[x], f32x4{0, 0, 0, 0});
+            }
+            typename G::Probs pr[QB];
+#pragma unroll
+            for (int x = 0; x < QB; ++x)
+                sm[x].step(sc[x], min(job.k1 - t, job.before + r[x].t - t), a.s.c, o[x], pr[x]);
+            const bool crosses = t + G::KT > job.before + lo;
+            const auto sees = [&](int x, int key) { return t + key < job.before + r[x].t; };
+            const auto row = [&](int key) {
+                const char* v = rows[1];
+                return [v, at, key](int byte) {
+                    return *reinterpret_cast<const uint32_t*>(v + G::stage_at(at + key, byte));
+                };
+            };
+#pragma unroll
+            for (int u = 0; u < G::U; ++u) {
+                typename G::VBlock v;
+#pragma unroll
+                for (int j = 0; j < G::VK; ++j) G::staged_chunk(rows[1], at + G::key_of(j), u, v.w[j]);
+                add_values<G, QB>(v, pr, u, crosses, row_bytes, sees, row, o);
             }
         }
     }
-    l = quad_sum(l);
-    if (__any(wrong)) l = NAN;
-    if (!has || sees <= k0) return;
-    if (sees <= a.piece) {
-        const float f = l == 0.f ? 0.f : 1.f / l;
+    if (row0 >= job.rows) return;
+    const bool wrong = wrong_s != 0;
 #pragma unroll
-        for (int u = 0; u < G::U; ++u)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) G::store_out(o, u, r, f, out, row_bytes);
-        if (a.lse && lane < 16)
-            a.lse[token * a.s.hq + hq] =
-                l == 0.f ? -INFINITY : (m - kProbShift<T> + fast_log2(l)) * kLn2;
-    } else {
-        const int64_t at = ((int64_t)piece * a.tokens + token) * a.s.hq + hq;
-        float* dst = a.part + at * a.s.dim;
-#pragma unroll
-        for (int u = 0; u < G::U; ++u)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) G::store_part(o, u, r, 1.f, dst, a.s.dim);
-        if (lane < 16) {
-            a.part_ml[2 * at] = m;
-            a.part_ml[2 * at + 1] = l;
-        }
+    for (int x = 0; x < QB; ++x) {
+        sm[x].finish();
+        if (wrong) sm[x].l = NAN;
+        store_row<G, T>(a, job, r[x], piece, o[x], sm[x]);
     }
 }
 
@@ -223,20 +471,36 @@ __global__ __launch_bounds__(kWaves* kWave) void k_paged_join(PagedArgs a) {
 
 }  // namespace
 
+bool paged_wide(int64_t rows) { return rows > 16; }
+
+int paged_tile_rows(int dim, int64_t rows) {
+    if (!paged_wide(rows)) return 16;
+    int bm = 0;
+    with_dim<float>(dim, [&](auto tag) { bm = Wide<typename decltype(tag)::Geo>::BM; });
+    return bm;
+}
+
 void paged_attention(const PagedArgs& a, hipStream_t st) {
-    const int64_t tiles = ceil_div((int64_t)a.max_new * a.s.group, 16);
+    const int64_t rows = (int64_t)a.max_new * a.s.group;
+    const int64_t tiles = ceil_div(rows, paged_tile_rows(a.s.dim, rows));
     if (a.seqs == 0 || a.tokens == 0 || tiles == 0) return;
-    if (tiles > 0x7fffffffLL) throw OverflowError("more rows per sequence than supported");
     const int64_t units = a.seqs * a.s.hkv * a.npieces * tiles;
     with_type(a.s.type, a.s.dim, [&](auto tag) {
         using Tag = decltype(tag);
-        auto run = k_paged<typename Tag::Geo, typename Tag::Elem>;
-        hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(ceil_div(units, kWaves)))),
-                           dim3(kWaves * kWave), 0, st, a, (int32_t)tiles);
+        using G = typename Tag::Geo;
+        using T = typename Tag::Elem;
+        if (paged_wide(rows)) {
+            auto run = k_paged_wide<G, T>;
+            hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(units))), dim3(kWaves * kWave), 0, st, a,
+                               (int32_t)tiles);
+        } else {
+            auto run = k_paged<G, T>;
+            hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(ceil_div(units, kWaves)))),
+                               dim3(kWaves * kWave), 0, st, a, (int32_t)tiles);
+        }
         SG_LAUNCH_CHECK();
         if (a.npieces > 1) {
-            hipLaunchKernelGGL(k_paged_join<typename Tag::Elem>,
-                               dim3(grid_1d(ceil_div(a.tokens * a.s.hq, kWaves))),
+            hipLaunchKernelGGL(k_paged_join<T>, dim3(grid_1d(ceil_div(a.tokens * a.s.hq, kWaves))),
                                dim3(kWaves * kWave), 0, st, a);
             SG_LAUNCH_CHECK();
         }

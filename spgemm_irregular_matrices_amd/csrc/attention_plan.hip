@@ -351,14 +351,19 @@ bool batch_sizes_fit(const spgemm_paged_batch* b, const spgemm_attention_desc* d
            b->tokens <= kMaxTokens && b->max_length <= kMaxTokens;
 }
 
-// Keys per piece. Few rows: the keys are cut until about 4096 wavefronts (16
-// per compute unit) have a piece each, of 64 keys at least.
+// Keys per piece. Where there are few rows the keys are cut: until about 4096
+// wavefronts (16 per compute unit) have a piece each, of 64 keys at least, or
+// where work groups share the keys, 1024 work groups one of 256 keys at least.
 void shape_pieces(PagedArgs* a) {
-    const int64_t tiles = ceil_div((int64_t)a->max_new * a->s.group, 16);
+    const int64_t rows = (int64_t)a->max_new * a->s.group;
+    const bool wide = paged_wide(rows);
+    const int64_t tiles = ceil_div(rows, paged_tile_rows(a->s.dim, rows));
     const int64_t units = std::max<int64_t>(a->seqs * a->s.hkv * tiles, 1);
-    const int64_t most = std::max<int64_t>(ceil_div(a->max_length, 64), 1);
-    const int64_t want = std::min(std::max<int64_t>(4096 / units, 1), most);
-    a->piece = (int32_t)std::max<int64_t>(ceil_div(ceil_div(a->max_length, want), 32) * 32, 32);
+    const int64_t most = std::max<int64_t>(ceil_div(a->max_length, wide ? 256 : 64), 1);
+    const int64_t want = std::min(std::max<int64_t>((wide ? 1024 : 4096) / units, 1), most);
+    const int64_t whole = wide ? 64 : 32;
+    a->piece = (int32_t)std::max<int64_t>(
+        ceil_div(ceil_div(a->max_length, want), whole) * whole, whole);
     a->npieces = (int32_t)std::max<int64_t>(ceil_div(a->max_length, a->piece), 1);
 }
 
@@ -570,6 +575,7 @@ SPGEMM_API int spgemm_paged_attention(const spgemm_attention_desc* desc, const s
         a.v_head = vs[2];
         a.npages = cache->npages;
         a.page_div = FastDiv((uint32_t)cache->page_size);
+        a.group_div = FastDiv((uint32_t)a.s.group);
         a.room = pg->nnz;
         a.rowptr = pg->rowptr;
         a.col = pg->col;

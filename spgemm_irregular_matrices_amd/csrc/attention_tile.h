@@ -71,14 +71,22 @@ __device__ __forceinline__ f32x4 mfma32(u32x4 a, u32x4 b, f32x4 c) {
                                                       __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// Largest / sum over the four lanes that hold one query (l%16 alike).
+// Largest / sum over the four lanes that hold one query (l%16 alike), by the
+// vector unit's exchanges of 16 and of 32 lanes.
+template <class Op>
+__device__ __forceinline__ float quad_reduce(float x, Op op) {
+    const uint32_t a = __builtin_bit_cast(uint32_t, x);
+    const auto h = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    x = op(__builtin_bit_cast(float, (uint32_t)h[0]), __builtin_bit_cast(float, (uint32_t)h[1]));
+    const uint32_t b = __builtin_bit_cast(uint32_t, x);
+    const auto f = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return op(__builtin_bit_cast(float, (uint32_t)f[0]), __builtin_bit_cast(float, (uint32_t)f[1]));
+}
 __device__ __forceinline__ float quad_max(float x) {
-    x = fmaxf(x, __shfl_xor(x, 16, kWave));
-    return fmaxf(x, __shfl_xor(x, 32, kWave));
+    return quad_reduce(x, [](float a, float b) { return fmaxf(a, b); });
 }
 __device__ __forceinline__ float quad_sum(float x) {
-    x += __shfl_xor(x, 16, kWave);
-    return x + __shfl_xor(x, 32, kWave);
+    return quad_reduce(x, [](float a, float b) { return a + b; });
 }
 
 // Unsigned division of n < 2^31 by a divisor fixed at launch: with
@@ -303,21 +311,66 @@ struct Tile {
                 for (int r = 0; r < 4; ++r) o[c][r] = t == mine ? y[c][r] : o[c][r];
         }
     }
-    template <class Sees>
-    static __device__ __forceinline__ void accumulate_seen(const VBlock& v, const Probs& p, int u,
-                                                           int times, int mine, Sees&& sees,
-                                                           Acc& a) {
+    // The weight that this lane's query gives to `key` of the tile.
+    static __device__ __forceinline__ float prob_of(const Probs& p, int key) {
+        const int j = (key & 3) + 4 * (key >> 4);
+        const int i = k16 ? j >> 1 : j;
+        const u32x4 all{p.w[0], p.w[1], p.w[2], p.w[3]};
+        const uint32_t mine = all[i];
+        const uint32_t w = __shfl(mine, 16 * ((key >> 2) & 3) + (lane_id() & 15), kWave);
+        if constexpr (k16) {
+            float x, y;
+            unpack2<T>(w, x, y);
+            return j & 1 ? y : x;
+        } else {
+            return __builtin_bit_cast(float, w);
+        }
+    }
+    // Chunk u of a value row holds infinities or NaN that not every query may
+    // see: these keys' chunks become 0 in v, and each is added on its own in
+    // the lanes whose query sees it. row(key): where the key's row lies.
+    template <class Sees, class Row, class A, int N>
+    static __device__ __forceinline__ void add_wild(VBlock& v, const Probs (&p)[N], int u,
+                                                    int row_bytes, Sees&& sees, Row&& row,
+                                                    A (&a)[N]) {
+        uint32_t keys = 0;
 #pragma unroll
-        for (int i = 0; i < VW; ++i) {
-            uint32_t w[VK];
+        for (int j = 0; j < VK; ++j) {
+            const uint64_t b = __ballot(chunk_wild(v.w[j]));
 #pragma unroll
-            for (int j = 0; j < VK; ++j) w[j] = v.w[j][i];
-            f32x4 o[kPerWord];
+            for (int x = 0; x < 4; ++x)
+                if (b >> (16 * x) & 0xffff) keys |= 1u << (4 * x + (j & 3) + 16 * (j >> 2));
+            if (b >> (lane_id() & 48) & 0xffff) {
 #pragma unroll
-            for (int c = 0; c < kPerWord; ++c) o[c] = a.o[u][kPerWord * i + c];
-            accumulate_word_seen(w, p, times, mine, sees, o);
+                for (int i = 0; i < VW; ++i) v.w[j][i] = 0;
+            }
+        }
+#pragma unroll 1
+        for (; keys; keys &= keys - 1) {
+            const int key = __builtin_ctz(keys);
+            const auto at = row(key);
 #pragma unroll
-            for (int c = 0; c < kPerWord; ++c) a.o[u][kPerWord * i + c] = o[c];
+            for (int x = 0; x < N; ++x) {
+                const float w = prob_of(p[x], key);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int byte = dim_of(u, r) * (int)sizeof(T);
+                    if (!sees(x, key) || (!FULL && byte >= row_bytes)) continue;
+#pragma unroll
+                    for (int i = 0; i < VW; ++i) {
+                        const uint32_t y = at(byte + 4 * i);
+                        if constexpr (k16) {
+                            float y0, y1;
+                            unpack2<T>(y, y0, y1);
+                            a[x].o[u][2 * i][r] = fmaf(w, y0, a[x].o[u][2 * i][r]);
+                            a[x].o[u][2 * i + 1][r] = fmaf(w, y1, a[x].o[u][2 * i + 1][r]);
+                        } else {
+                            a[x].o[u][i][r] =
+                                fmaf(w, __builtin_bit_cast(float, y), a[x].o[u][i][r]);
+                        }
+                    }
+                }
+            }
         }
     }
 
