@@ -66,6 +66,7 @@ struct AttnShape {
     int mtiles = 1;      // ceil(group / 16)
     float scale = 0.f;   // of the scores
     float c = 0.f;       // scale * log2(e)
+    float mag = 1.f;     // |c|, or 1 if that is 0: the factor that Softmax takes
 };
 
 struct ForwardArgs {

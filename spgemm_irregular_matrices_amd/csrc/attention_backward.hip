@@ -55,6 +55,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
     const int hq = h * a.s.group + g;
     const int row_bytes = a.s.dim * (int)sizeof(T);
     char* krows = stage[w];
+    const int rbase = G::row_base(0), cbase = G::chunk_base(0);
 
     PieceStream st(a.rows, u0, kWaves, each);
     for (uint64_t e = st.empty; e; e &= e - 1) {
@@ -138,7 +139,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
 #pragma unroll
                     for (int i = 0; i < G::VW; ++i) k[u].w[j][i] = 0;
                 }
-                G::stage_chunk(krows, G::key_of(j), u, k[u].w[j]);
+                G::stage_chunk(krows, cbase, j, u, k[u].w[j]);
             }
         wave_lds_sync();
         const uint32_t idn = id;
@@ -148,7 +149,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
         for (int b = 0; b < G::KSUB; ++b) {
             dp[b] = G::dot(v[b], dout, f32x4{0, 0, 0, 0});
             typename G::RowFrag x;
-            G::staged_row(krows, 16 * b + n, x);
+            G::staged_row(krows, rbase, 16 * b, x);
             s[b] = G::dot(x, q, f32x4{0, 0, 0, 0});
         }
         if (more) {
@@ -181,7 +182,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
         for (int u = 0; u < G::U; ++u) {
             typename G::VBlock x;
 #pragma unroll
-            for (int j = 0; j < G::VK; ++j) G::staged_chunk(krows, G::key_of(j), u, x.w[j]);
+            for (int j = 0; j < G::VK; ++j) G::staged_chunk(krows, cbase, 0, j, u, x.w[j]);
             G::accumulate(x, pr, u, o);
         }
         if (last) {
@@ -370,12 +371,13 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 1) void k_att
         float pr[4], ds[4];
         float wild = 0.f;
         if (16 * w < TP) {
+            const int rbase = G::row_base(0), mine_at = G::stage_at(16 * w + n, 16 * quad);
             typename G::RowFrag f, key;
-            G::staged_row(rows[0], 16 * w + n, f);
-            G::staged_row(keys[0], n, key);
+            G::staged_row(rows[0], mine_at, 0, f);
+            G::staged_row(keys[0], rbase, 0, key);
             const f32x4 s = G::dot(f, key, f32x4{0, 0, 0, 0});
-            G::staged_row(rows[1], 16 * w + n, f);
-            G::staged_row(keys[1], n, key);
+            G::staged_row(rows[1], mine_at, 0, f);
+            G::staged_row(keys[1], rbase, 0, key);
             const f32x4 dp = G::dot(f, key, f32x4{0, 0, 0, 0});
             const f32x4 l2 = *reinterpret_cast<const f32x4*>(lse_s + 16 * w + 4 * quad);
             const f32x4 dl = *reinterpret_cast<const f32x4*>(delta_s + 16 * w + 4 * quad);

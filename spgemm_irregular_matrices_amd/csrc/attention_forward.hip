@@ -52,6 +52,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
         G::zero_row(q);
         if (has)
             G::load_row(a.q.base + st.row(i) * a.q.row + hq * a.q.head, row_bytes, q);
+        G::sign_row(q, a.s.c);
     };
     const auto load_k = [&](uint32_t id) {
         const uint32_t off = id * a.k.unit;
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
             if (ahead.more) id = st.id(ahead, G::KT);
         }
         typename G::Probs pr;
-        sm.step(s, left, a.s.c, o, pr);
+        sm.step(s, left, a.s.mag, o, pr);
         if (left < G::KT) {
             // 0 weight times what a repeated row holds may be NaN
 #pragma unroll

@@ -165,6 +165,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
     typename G::VBlock v[G::U];
     G::zero_row(q);
     if (r.has) G::load_row(a.q.base + r.token * a.q.row + r.hq * a.q.head, row_bytes, q);
+    G::sign_row(q, a.s.c);
     const char* kb = a.k + h * a.k_head;
     const char* vb = a.v + h * a.v_head;
     const int32_t* pages = a.col + job.sq.page0;
@@ -225,7 +226,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
             if (left > 2 * G::KT) next = place(t0 + 2 * G::KT);
         }
         typename G::Probs pr[1];
-        sm.step(sc, min(left, job.before + r.t - t0), a.s.c, o[0], pr[0]);
+        sm.step(sc, min(left, job.before + r.t - t0), a.s.mag, o[0], pr[0]);
         if (left < G::KT) {
             // 0 weight times what a repeated place holds may be NaN
 #pragma unroll
@@ -313,6 +314,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
         G::zero_acc(o[b]);
         if (r[b].has)
             G::load_row(a.q.base + r[b].token * a.q.row + r[b].hq * a.q.head, row_bytes, q[b]);
+        G::sign_row(q[b], a.s.c);
     }
     const char* kb = a.k + h * a.k_head;
     const char* vb = a.v + h * a.v_head;
@@ -388,20 +390,23 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
             load_id(t0 + 2 * BK);
         }
 #pragma unroll 1
-        for (int t = t0; t < min(t0 + BK, mine); t += G::KT) {
-            const int at = t - t0;  // the tile's first staged row
+        for (int at = 0; at < BK; at += G::KT) {  // a tile's first staged row
+            const int t = t0 + at;
+            if (t >= mine) break;
+            const int rb = G::row_base(at), cb = G::chunk_base(at);
             f32x4 sc[QB][G::KSUB];
 #pragma unroll
             for (int b = 0; b < G::KSUB; ++b) {
                 typename G::RowFrag k;
-                G::staged_row(rows[0], at + 16 * b + n, k);
+                G::staged_row(rows[0], rb, 16 * b, k);
 #pragma unroll
                 for (int x = 0; x < QB; ++x) sc[x][b] = G::dot(k, q[x], f32x4{0, 0, 0, 0});
             }
             typename G::Probs pr[QB];
 #pragma unroll
             for (int x = 0; x < QB; ++x)
-                sm[x].step(sc[x], min(job.k1 - t, job.before + r[x].t - t), a.s.c, o[x], pr[x]);
+                sm[x].step(sc[x], min(job.k1, job.before + r[x].t) - t, a.s.mag,
+                           o[x], pr[x]);
             const bool crosses = t + G::KT > job.before + lo;
             const auto sees = [&](int x, int key) { return t + key < job.before + r[x].t; };
             const auto row = [&](int key) {
@@ -414,7 +419,8 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
             for (int u = 0; u < G::U; ++u) {
                 typename G::VBlock v;
 #pragma unroll
-                for (int j = 0; j < G::VK; ++j) G::staged_chunk(rows[1], at + G::key_of(j), u, v.w[j]);
+                for (int j = 0; j < G::VK; ++j)
+                    G::staged_chunk(rows[1], cb, 0, j, u, v.w[j]);
                 add_values<G, QB>(v, pr, u, crosses, row_bytes, sees, row, o);
             }
         }

@@ -249,6 +249,7 @@ AttnShape make_shape(const spgemm_attention_desc* d) {
     s.mtiles = (s.group + 15) / 16;
     s.scale = (float)d->scale;
     s.c = (float)(d->scale * 1.4426950408889634);
+    s.mag = s.c == 0.f ? 1.f : std::fabs(s.c);
     return s;
 }
 

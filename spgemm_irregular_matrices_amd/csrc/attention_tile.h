@@ -137,6 +137,13 @@ struct Tile {
                 f.w[t] = u32x4{0, 0, 0, 0};
         }
     }
+    // A query row for scores with the factor |c|, or 1 if c is 0 (see Softmax).
+    static __device__ __forceinline__ void sign_row(RowFrag& f, float c) {
+        if (c > 0.f) return;
+        const uint32_t flip = k16 ? 0x80008000u : 0x80000000u;
+#pragma unroll
+        for (int t = 0; t < QS; ++t) f.w[t] = c < 0.f ? f.w[t] ^ flip : u32x4{0, 0, 0, 0};
+    }
     static __device__ __forceinline__ void zero_row(RowFrag& f) {
 #pragma unroll
         for (int t = 0; t < QS; ++t) f.w[t] = u32x4{0, 0, 0, 0};
@@ -395,17 +402,32 @@ struct Tile {
     static __device__ __forceinline__ int stage_more(int at, int dr, int dbyte) {
         return (at ^ dbyte ^ stage_x(dr)) + dr * kRowBytes;
     }
-    static __device__ __forceinline__ void stage_chunk(char* lds, int r, int u,
+    // Where this lane's pieces of rows first + l % 16 and its chunks of rows
+    // first + key_of(j) begin, for a tile whose first row is `first`; dr: a
+    // constant, 0 or 16, more rows.
+    static __device__ __forceinline__ int row_base(int first) {
+        return stage_at(first + (lane_id() & 15), 16 * (lane_id() >> 4));
+    }
+    static __device__ __forceinline__ int chunk_base(int first) {
+        return stage_at(first + 4 * (lane_id() >> 4), chunk_at(0));
+    }
+    static __device__ __forceinline__ void staged_row(const char* lds, int base, int dr,
+                                                      RowFrag& f) {
+#pragma unroll
+        for (int t = 0; t < QS; ++t)
+            f.w[t] = *reinterpret_cast<const u32x4*>(lds + stage_more(base, dr, 64 * t));
+    }
+    static __device__ __forceinline__ void stage_chunk(char* lds, int base, int j, int u,
                                                        const uint32_t (&w)[VW]) {
-        char* at = lds + stage_at(r, chunk_at(u));
+        char* at = lds + stage_more(base, (j & 3) + 16 * (j >> 2), 64 * VW * u);
         if constexpr (VW == 4)
             *reinterpret_cast<u32x4*>(at) = u32x4{w[0], w[1], w[2], w[3]};
         else
             *reinterpret_cast<u32x2*>(at) = u32x2{w[0], w[1]};
     }
-    static __device__ __forceinline__ void staged_chunk(const char* lds, int r, int u,
-                                                        uint32_t (&w)[VW]) {
-        const char* at = lds + stage_at(r, chunk_at(u));
+    static __device__ __forceinline__ void staged_chunk(const char* lds, int base, int dr, int j,
+                                                        int u, uint32_t (&w)[VW]) {
+        const char* at = lds + stage_more(base, dr + (j & 3) + 16 * (j >> 2), 64 * VW * u);
         if constexpr (VW == 4) {
             const u32x4 x = *reinterpret_cast<const u32x4*>(at);
             w[0] = x[0]; w[1] = x[1]; w[2] = x[2]; w[3] = x[3];
@@ -413,12 +435,6 @@ struct Tile {
             const u32x2 x = *reinterpret_cast<const u32x2*>(at);
             w[0] = x[0]; w[1] = x[1];
         }
-    }
-    static __device__ __forceinline__ void staged_row(const char* lds, int r, RowFrag& f) {
-        const int at = stage_at(r, 16 * (lane_id() >> 4));
-#pragma unroll
-        for (int t = 0; t < QS; ++t)
-            f.w[t] = *reinterpret_cast<const u32x4*>(lds + stage_more(at, 0, 64 * t));
     }
 
     // Element index of the accumulator's first value in register r of chunk
@@ -471,24 +487,27 @@ template <class G, class T>
 struct Softmax {
     float m = -INFINITY, l = 0.f;
 
-    // Takes a tile's scores, of whose keys the first `limit` count, rescales
-    // what o holds, and leaves the weights.
+    // Takes a tile's scores before their factor c > 0 (a negative one's sign
+    // goes into q, and 0 makes q 0), of whose keys the first `limit` count,
+    // rescales what o holds, and leaves the weights.
     __device__ __forceinline__ void step(const f32x4 (&s)[G::KSUB], int limit, float c,
                                          typename G::Acc& o, typename G::Probs& out) {
         float p[G::VK], top = -INFINITY;
 #pragma unroll
         for (int j = 0; j < G::VK; ++j) {
-            p[j] = G::key_of(j) < limit ? s[j >> 2][j & 3] * c : -INFINITY;
+            p[j] = s[j >> 2][j & 3];
+            if (G::key_of(j) >= limit) p[j] = -INFINITY;
             top = fmaxf(top, p[j]);
         }
-        const float mn = fmaxf(m, quad_max(top));
+        const float mn = fmaxf(m, quad_max(top) * c);
         const float ms = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: weights 0, not NaN
         const float fix = fast_exp2(m - ms);
         m = mn;
+        const float base = kProbShift<T> - ms;
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < G::VK; ++j) {
-            p[j] = fast_exp2(p[j] - (ms - kProbShift<T>));
+            p[j] = fast_exp2(fmaf(p[j], c, base));
             sum += p[j];
         }
         l = l * fix + sum;
