@@ -86,50 +86,49 @@ __device__ __forceinline__ void store_nan(const PagedArgs& a, const TileRow& r) 
 // A row's result, finished if the first piece holds all keys that it sees,
 // otherwise as this piece's part of it.
 template <class G, class T>
+__device__ __forceinline__ void store_values(const typename G::Acc& o, float f, bool part,
+                                             char* at, int dim) {
+#pragma unroll
+    for (int u = 0; u < G::U; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (part)
+                G::store_part(o, u, i, f, reinterpret_cast<float*>(at), dim);
+            else
+                G::store_out(o, u, i, f, at, dim * (int)sizeof(T));
+        }
+}
+template <class G, class T>
+__device__ __forceinline__ void store_values(const typename G::AccB& o, float f, bool part,
+                                             char* at, int dim) {
+#pragma unroll
+    for (int b = 0; b < G::NB; ++b) {
+        const int d = 16 * b + 4 * (lane_id() >> 4);
+        if (!G::kFull && d >= dim) continue;
+        if (part)
+            *reinterpret_cast<f32x4*>(at + 4 * d) = o.o[b] * f;
+        else
+            G::store_four(o.o[b] * f, at + d * (int)sizeof(T));
+    }
+}
+template <class G, class T, class A>
 __device__ __forceinline__ void store_row(const PagedArgs& a, const TileJob& j, const TileRow& r,
-                                          int piece, const typename G::Acc& o,
-                                          const Softmax<G, T>& sm) {
+                                          int piece, const A& o, const Softmax<G, T>& sm) {
     const int sees = j.before + r.t;
     if (!r.has || sees <= j.k0) return;
-    const int row_bytes = a.s.dim * (int)sizeof(T);
     const int64_t line = r.token * a.s.hq + r.hq;
     if (sees <= a.piece) {
-        const float f = sm.factor();
-        char* out = a.out.base + r.token * a.out.row + r.hq * a.out.head;
-#pragma unroll
-        for (int u = 0; u < G::U; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) G::store_out(o, u, i, f, out, row_bytes);
+        store_values<G, T>(o, sm.factor(), false,
+                           a.out.base + r.token * a.out.row + r.hq * a.out.head, a.s.dim);
         if (a.lse && lane_id() < 16) a.lse[line] = sm.lse();
     } else {
         const int64_t at = (int64_t)piece * a.tokens * a.s.hq + line;
-        float* dst = a.part + at * a.s.dim;
-#pragma unroll
-        for (int u = 0; u < G::U; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) G::store_part(o, u, i, 1.f, dst, a.s.dim);
+        store_values<G, T>(o, 1.f, true, reinterpret_cast<char*>(a.part + at * a.s.dim), a.s.dim);
         if (lane_id() < 16) {
             a.part_ml[2 * at] = sm.m;
             a.part_ml[2 * at + 1] = sm.l;
         }
     }
-}
-
-// O^T += V^T P^T for chunk u of a tile of keys. Where a row may not see every
-// key (`crosses`), 0 times an infinity or a NaN must not reach it.
-template <class G, int N, class Sees, class Row>
-__device__ __forceinline__ void add_values(typename G::VBlock& v,
-                                           const typename G::Probs (&pr)[N], int u, bool crosses,
-                                           int row_bytes, Sees&& sees, Row&& row,
-                                           typename G::Acc (&o)[N]) {
-    if (crosses) {
-        bool wild = false;
-#pragma unroll
-        for (int j = 0; j < G::VK; ++j) wild |= G::chunk_wild(v.w[j]);
-        if (__any(wild)) G::add_wild(v, pr, u, row_bytes, sees, row, o);
-    }
-#pragma unroll
-    for (int x = 0; x < N; ++x) G::accumulate(v, pr[x], u, o[x]);
 }
 
 // Few rows per sequence and key head: one wavefront takes 16 rows and one
@@ -209,8 +208,8 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
     load_k(now);
     load_v(now);
 
-    typename G::Acc o[1];
-    G::zero_acc(o[0]);
+    typename G::Acc o;
+    G::zero_acc(o);
     Softmax<G, T> sm;
     for (int t0 = job.k0; t0 < job.k1; t0 += G::KT) {
         const int left = job.k1 - t0;
@@ -225,8 +224,8 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
             load_k(now);
             if (left > 2 * G::KT) next = place(t0 + 2 * G::KT);
         }
-        typename G::Probs pr[1];
-        sm.step(sc, min(left, job.before + r.t - t0), a.s.mag, o[0], pr[0]);
+        typename G::Probs pr;
+        sm.step(sc, min(left, job.before + r.t - t0), a.s.mag, o, pr);
         if (left < G::KT) {
             // 0 weight times what a repeated place holds may be NaN
 #pragma unroll
@@ -238,20 +237,37 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
                         for (int i = 0; i < G::VW; ++i) v[u].w[j][i] = 0;
         }
         const bool crosses = t0 + G::KT > job.before + lo;  // some row may not see some key
-        const auto sees = [&](int, int key) { return t0 + key < job.before + r.t; };
-        const auto row = [&](int key) {
-            const uint32_t off = __shfl(here.id * a.v_page + here.slot * a.v_slot, key, kWave);
-            const char* at = vb + ((uint64_t)off << a.v_shift);
-            return [at](int byte) { return *reinterpret_cast<const uint32_t*>(at + byte); };
-        };
 #pragma unroll
-        for (int u = 0; u < G::U; ++u)
-            add_values<G, 1>(v[u], pr, u, crosses, row_bytes, sees, row, o);
+        for (int u = 0; u < G::U; ++u) {
+            if (crosses) {
+                // a key that a row does not see must not reach it as 0 times
+                // an infinity or a NaN: such keys count as 0 here, and are
+                // added on their own in the lanes that see them
+                uint32_t keys = G::wild_keys(v[u]);
+                if (keys) {
+#pragma unroll
+                    for (int j = 0; j < G::VK; ++j)
+                        if (keys >> G::key_of(j) & 1)
+#pragma unroll
+                            for (int i = 0; i < G::VW; ++i) v[u].w[j][i] = 0;
+                }
+#pragma unroll 1
+                for (; keys; keys &= keys - 1) {
+                    const int key = __builtin_ctz(keys);
+                    const uint32_t off =
+                        __shfl(here.id * a.v_page + here.slot * a.v_slot, key, kWave);
+                    const float p = G::prob_of(pr, key);
+                    if (t0 + key < job.before + r.t)
+                        G::add_wild(vb + ((uint64_t)off << a.v_shift), p, u, row_bytes, o);
+                }
+            }
+            G::accumulate(v[u], pr, u, o);
+        }
         if (more) load_v(now);
     }
     sm.finish();
     if (__any(wrong)) sm.l = NAN;
-    store_row<G, T>(a, job, r, piece, o[0], sm);
+    store_row<G, T>(a, job, r, piece, o, sm);
 }
 
 // Many rows: a work group of 4 wavefronts takes 4 * 16 * QB rows, a wavefront
@@ -272,7 +288,8 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
     constexpr int kPieces = G::kRowBytes / 16, kLoads = BK * kPieces / NT, kStep = NT / kPieces;
     static_assert(BK * kPieces % NT == 0 && BK % G::KT == 0, "tile shape");
     __shared__ __align__(16) char rows[2][BK * G::kRowBytes];  // k, v
-    __shared__ uint32_t off[2][BK];
+    __shared__ uint32_t off[2][2][BK];       // of this tile and the next, k and v
+    __shared__ unsigned long long wild_s[2];  // keys whose value rows are not all finite
     __shared__ int wrong_s;
     const int tid = threadIdx.x, lane = lane_id();
     const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -299,19 +316,23 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
         return;
     }
     if (job.k0 >= job.k1) return;
-    if (tid == 0) wrong_s = 0;
+    if (tid == 0) {
+        wrong_s = 0;
+        wild_s[0] = 0;
+    }
     // keys that some row of the wavefront sees (none: it only helps to load)
     const int lo = __builtin_amdgcn_readfirstlane(r[0].t);
     const int hi = __builtin_amdgcn_readlane(r[QB - 1].t, 15);
     const int mine = row0 < job.rows ? min(job.k1, job.before + hi) : 0;
 
     typename G::RowFrag q[QB];
-    typename G::Acc o[QB];
+    typename G::AccB o[QB];
     Softmax<G, T> sm[QB];
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
         G::zero_row(q[b]);
-        G::zero_acc(o[b]);
+#pragma unroll
+        for (int i = 0; i < G::NB; ++i) o[b].o[i] = f32x4{0, 0, 0, 0};
         if (r[b].has)
             G::load_row(a.q.base + r[b].token * a.q.row + r[b].hq * a.q.head, row_bytes, q[b]);
         G::sign_row(q[b], a.s.c);
@@ -324,15 +345,15 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
     const auto load_id = [&](int t0) {
         if (tid < BK && t0 + tid < job.k1) id = (uint32_t)pages[a.page_div.div(t0 + tid)];
     };
-    const auto put_offsets = [&](int t0) {
+    const auto put_offsets = [&](int t0, int par) {
         if (tid < BK && t0 + tid < job.k1) {
             if (id >= (uint64_t)a.npages) {
                 wrong_s = 1;
                 id = 0;
             }
             const uint32_t key = t0 + tid, slot = key - a.page_div.div(key) * a.page_div.d;
-            off[0][tid] = id * a.k_page + slot * a.k_slot;
-            off[1][tid] = id * a.v_page + slot * a.v_slot;
+            off[par][0][tid] = id * a.k_page + slot * a.k_slot;
+            off[par][1][tid] = id * a.v_page + slot * a.v_slot;
         }
     };
     u32x4 fly[2][kLoads];
@@ -340,14 +361,14 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
     const bool inside = G::kFull || pbyte < row_bytes;
     const char* kp = kb + (inside ? pbyte : 0);
     const char* vp = vb + (inside ? pbyte : 0);
-    const auto load_rows = [&](int t0) {
+    const auto load_rows = [&](int t0, int par) {
         const int left = job.k1 - t0;
         if (left >= BK) {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 const int p = i * kStep + prow;
-                fly[0][i] = *reinterpret_cast<const u32x4*>(kp + ((uint64_t)off[0][p] << a.k_shift));
-                fly[1][i] = *reinterpret_cast<const u32x4*>(vp + ((uint64_t)off[1][p] << a.v_shift));
+                fly[0][i] = *reinterpret_cast<const u32x4*>(kp + ((uint64_t)off[par][0][p] << a.k_shift));
+                fly[1][i] = *reinterpret_cast<const u32x4*>(vp + ((uint64_t)off[par][1][p] << a.v_shift));
             }
         } else {
             // places past the end read the tile's first key and become 0
@@ -356,9 +377,9 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
                 const int p = i * kStep + prow;
                 const bool in = p < left;
                 const u32x4 x = *reinterpret_cast<const u32x4*>(
-                    kp + ((uint64_t)off[0][in ? p : 0] << a.k_shift));
+                    kp + ((uint64_t)off[par][0][in ? p : 0] << a.k_shift));
                 const u32x4 y = *reinterpret_cast<const u32x4*>(
-                    vp + ((uint64_t)off[1][in ? p : 0] << a.v_shift));
+                    vp + ((uint64_t)off[par][1][in ? p : 0] << a.v_shift));
                 fly[0][i] = in ? x : u32x4{0, 0, 0, 0};
                 fly[1][i] = in ? y : u32x4{0, 0, 0, 0};
             }
@@ -369,13 +390,30 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
         }
     };
     load_id(job.k0);
-    __syncthreads();  // wrong_s
-    put_offsets(job.k0);
+    __syncthreads();  // wrong_s, wild_s
+    put_offsets(job.k0, 0);
     __syncthreads();
-    load_rows(job.k0);
+    load_rows(job.k0, 0);
     load_id(job.k0 + BK);
-    for (int t0 = job.k0; t0 < job.k1; t0 += BK) {
+    int par = 0;
+    for (int t0 = job.k0; t0 < job.k1; t0 += BK, par ^= 1) {
         __syncthreads();  // the last tile's readers are done
+        if (t0 + BK > job.before + job.first / a.s.group) {
+            // some row may not see some key: a value row with an infinity or
+            // a NaN is staged as 0, so that 0 times it stays 0, and is added
+            // on its own below for the rows that see it
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const uint32_t x[4] = {fly[1][i][0], fly[1][i][1], fly[1][i][2], fly[1][i][3]};
+                const uint64_t b = __ballot(G::words_wild(x));
+                const int lane0 = lane / kPieces * kPieces;  // of this row's pieces
+                const uint64_t whole = kPieces == 64 ? ~0ull : (1ull << (kPieces & 63)) - 1;
+                if (b >> lane0 & whole) {
+                    fly[1][i] = u32x4{0, 0, 0, 0};
+                    if (lane == lane0) atomicOr(&wild_s[par], 1ull << (i * kStep + prow));
+                }
+            }
+        }
         const int put = G::stage_at(prow, pbyte);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
@@ -383,17 +421,19 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
             *reinterpret_cast<u32x4*>(rows[0] + at) = fly[0][i];
             *reinterpret_cast<u32x4*>(rows[1] + at) = fly[1][i];
         }
-        put_offsets(t0 + BK);
+        put_offsets(t0 + BK, par ^ 1);
         __syncthreads();
+        if (tid == 0) wild_s[par ^ 1] = 0;
         if (t0 + BK < job.k1) {
-            load_rows(t0 + BK);
+            load_rows(t0 + BK, par ^ 1);
             load_id(t0 + 2 * BK);
         }
+        const uint64_t wild = wild_s[par];
 #pragma unroll 1
         for (int at = 0; at < BK; at += G::KT) {  // a tile's first staged row
             const int t = t0 + at;
             if (t >= mine) break;
-            const int rb = G::row_base(at), cb = G::chunk_base(at);
+            const int rb = G::row_base(at), vbase = G::value_base(at);
             f32x4 sc[QB][G::KSUB];
 #pragma unroll
             for (int b = 0; b < G::KSUB; ++b) {
@@ -407,21 +447,28 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
             for (int x = 0; x < QB; ++x)
                 sm[x].step(sc[x], min(job.k1, job.before + r[x].t) - t, a.s.mag,
                            o[x], pr[x]);
-            const bool crosses = t + G::KT > job.before + lo;
-            const auto sees = [&](int x, int key) { return t + key < job.before + r[x].t; };
-            const auto row = [&](int key) {
-                const char* v = rows[1];
-                return [v, at, key](int byte) {
-                    return *reinterpret_cast<const uint32_t*>(v + G::stage_at(at + key, byte));
-                };
-            };
 #pragma unroll
-            for (int u = 0; u < G::U; ++u) {
-                typename G::VBlock v;
+            for (int b = 0; b < G::NB; ++b) {
+                const u32x4 v = G::value_frag(rows[1], vbase, b);
 #pragma unroll
-                for (int j = 0; j < G::VK; ++j)
-                    G::staged_chunk(rows[1], cb, 0, j, u, v.w[j]);
-                add_values<G, QB>(v, pr, u, crosses, row_bytes, sees, row, o);
+                for (int x = 0; x < QB; ++x) o[x].o[b] = G::add_block(v, pr[x], o[x].o[b]);
+            }
+            if (wild == 0) continue;
+#pragma unroll 1
+            for (int key = 0; key < G::KT; ++key) {
+                if (!(wild >> (at + key) & 1)) continue;
+                const char* row = vb + ((uint64_t)off[par][1][at + key] << a.v_shift);
+#pragma unroll
+                for (int x = 0; x < QB; ++x) {
+                    const float p = G::prob_of(pr[x], key);
+                    if (t + key >= job.before + r[x].t) continue;
+#pragma unroll
+                    for (int b = 0; b < G::NB; ++b) {
+                        const int d = 16 * b + 4 * (lane >> 4);
+                        if (G::kFull || d < a.s.dim)
+                            o[x].o[b] = G::add_four(row + d * (int)sizeof(T), p, o[x].o[b]);
+                    }
+                }
             }
         }
     }

@@ -226,11 +226,12 @@ struct Tile {
             for (int c = 0; c < CHL; ++c) a.o[u][c] *= f;
     }
 
-    // Whether a chunk holds an infinity or a NaN.
-    static __device__ __forceinline__ bool chunk_wild(const uint32_t (&w)[VW]) {
+    // Whether words of the type's values hold an infinity or a NaN.
+    template <int N>
+    static __device__ __forceinline__ bool words_wild(const uint32_t (&w)[N]) {
         bool wild = false;
 #pragma unroll
-        for (int i = 0; i < VW; ++i) {
+        for (int i = 0; i < N; ++i) {
             if constexpr (k16) {
                 constexpr uint32_t e = std::is_same<T, __bf16>::value ? 0x7f80u : 0x7c00u;
                 wild |= (w[i] & e) == e || ((w[i] >> 16) & e) == e;
@@ -239,6 +240,12 @@ struct Tile {
             }
         }
         return wild;
+    }
+
+    struct AccB;
+    static __device__ __forceinline__ void scale_acc(AccB& a, float f) {
+#pragma unroll
+        for (int b = 0; b < DP / 16; ++b) a.o[b] *= f;
     }
 
     // P^T from the lane's KT/4 probabilities (in key_of order), rounded to T.
@@ -333,52 +340,17 @@ struct Tile {
             return __builtin_bit_cast(float, w);
         }
     }
-    // Chunk u of a value row holds infinities or NaN that not every query may
-    // see: these keys' chunks become 0 in v, and each is added on its own in
-    // the lanes whose query sees it. row(key): where the key's row lies.
-    template <class Sees, class Row, class A, int N>
-    static __device__ __forceinline__ void add_wild(VBlock& v, const Probs (&p)[N], int u,
-                                                    int row_bytes, Sees&& sees, Row&& row,
-                                                    A (&a)[N]) {
+    // The keys (bits) whose chunk holds an infinity or a NaN.
+    static __device__ __forceinline__ uint32_t wild_keys(const VBlock& v) {
         uint32_t keys = 0;
 #pragma unroll
         for (int j = 0; j < VK; ++j) {
-            const uint64_t b = __ballot(chunk_wild(v.w[j]));
+            const uint64_t b = __ballot(words_wild(v.w[j]));
 #pragma unroll
             for (int x = 0; x < 4; ++x)
                 if (b >> (16 * x) & 0xffff) keys |= 1u << (4 * x + (j & 3) + 16 * (j >> 2));
-            if (b >> (lane_id() & 48) & 0xffff) {
-#pragma unroll
-                for (int i = 0; i < VW; ++i) v.w[j][i] = 0;
-            }
         }
-#pragma unroll 1
-        for (; keys; keys &= keys - 1) {
-            const int key = __builtin_ctz(keys);
-            const auto at = row(key);
-#pragma unroll
-            for (int x = 0; x < N; ++x) {
-                const float w = prob_of(p[x], key);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int byte = dim_of(u, r) * (int)sizeof(T);
-                    if (!sees(x, key) || (!FULL && byte >= row_bytes)) continue;
-#pragma unroll
-                    for (int i = 0; i < VW; ++i) {
-                        const uint32_t y = at(byte + 4 * i);
-                        if constexpr (k16) {
-                            float y0, y1;
-                            unpack2<T>(y, y0, y1);
-                            a[x].o[u][2 * i][r] = fmaf(w, y0, a[x].o[u][2 * i][r]);
-                            a[x].o[u][2 * i + 1][r] = fmaf(w, y1, a[x].o[u][2 * i + 1][r]);
-                        } else {
-                            a[x].o[u][i][r] =
-                                fmaf(w, __builtin_bit_cast(float, y), a[x].o[u][i][r]);
-                        }
-                    }
-                }
-            }
-        }
+        return keys;
     }
 
     // Rows staged in LDS, so that one trip to memory serves both operands.
@@ -437,6 +409,70 @@ struct Tile {
         }
     }
 
+    // V^T from LDS, by blocks of 16 indices of the head dimension: lane l has
+    // index 16 b + l%16 of its keys, turned over on the way by the transposing
+    // read (16 lanes name 4 rows of 16 values and each gets a column).
+    static constexpr int NB = DP / 16;
+    struct AccB { f32x4 o[NB]; };  // register r of block b: index 16 b + 4 (l/16) + r
+    static __device__ __forceinline__ int value_base(int first) {
+        const int l = lane_id() & 15, quad = lane_id() >> 4;
+        return k16 ? stage_at(first + 4 * quad + (l >> 2), 8 * (l & 3))
+                   : stage_at(first + 4 * quad, 4 * l);
+    }
+    static __device__ __forceinline__ u32x4 value_frag(const char* lds, int base, int b) {
+        if constexpr (k16) {
+            using s16x4 = short __attribute__((ext_vector_type(4)));
+            using lds_s16x4 = __attribute__((address_space(3))) s16x4;
+            const u32x2 lo = __builtin_bit_cast(
+                u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                           (lds_s16x4*)(lds + stage_more(base, 0, 32 * b))));
+            const u32x2 hi = __builtin_bit_cast(
+                u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                           (lds_s16x4*)(lds + stage_more(base, 16, 32 * b))));
+            return u32x4{lo[0], lo[1], hi[0], hi[1]};
+        } else {
+            u32x4 x;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                x[r] = *reinterpret_cast<const uint32_t*>(lds + stage_more(base, r, 64 * b));
+            return x;
+        }
+    }
+    static __device__ __forceinline__ f32x4 add_block(u32x4 v, const Probs& p, f32x4 o) {
+        if constexpr (k16) {
+            return mfma32<T>(v, u32x4{p.w[0], p.w[1], p.w[2], p.w[3]}, o);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                o = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, (uint32_t)v[r]),
+                                                         __builtin_bit_cast(float, p.w[r]), o, 0, 0,
+                                                         0);
+            return o;
+        }
+    }
+    // o += w times 4 values of type T.
+    static __device__ __forceinline__ f32x4 add_four(const char* at, float w, f32x4 o) {
+        if constexpr (k16) {
+            const u32x2 x = *reinterpret_cast<const u32x2*>(at);
+            float y[4];
+            unpack2<T>(x[0], y[0], y[1]);
+            unpack2<T>(x[1], y[2], y[3]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[r] = fmaf(w, y[r], o[r]);
+        } else {
+            const f32x4 y = *reinterpret_cast<const f32x4*>(at);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[r] = fmaf(w, y[r], o[r]);
+        }
+        return o;
+    }
+    static __device__ __forceinline__ void store_four(f32x4 v, char* at) {
+        if constexpr (k16)
+            *reinterpret_cast<u32x2*>(at) = u32x2{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])};
+        else
+            *reinterpret_cast<f32x4*>(at) = v;
+    }
+
     // Element index of the accumulator's first value in register r of chunk
     // u; the CHL values o[u][0..CHL)[r] follow one another.
     static __device__ __forceinline__ int dim_of(int u, int r) {
@@ -459,6 +495,27 @@ struct Tile {
         } else {
             *reinterpret_cast<f32x4*>(row + at) =
                 f32x4{a.o[u][0][r] * f, a.o[u][1][r] * f, a.o[u][2][r] * f, a.o[u][3][r] * f};
+        }
+    }
+    // Chunk u of the row at `row`, times w.
+    static __device__ __forceinline__ void add_wild(const char* row, float w, int u, int row_bytes,
+                                                    Acc& a) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int at = dim_of(u, r) * (int)sizeof(T);
+            if (!FULL && at >= row_bytes) continue;
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+                const uint32_t y = *reinterpret_cast<const uint32_t*>(row + at + 4 * i);
+                if constexpr (k16) {
+                    float y0, y1;
+                    unpack2<T>(y, y0, y1);
+                    a.o[u][2 * i][r] = fmaf(w, y0, a.o[u][2 * i][r]);
+                    a.o[u][2 * i + 1][r] = fmaf(w, y1, a.o[u][2 * i + 1][r]);
+                } else {
+                    a.o[u][i][r] = fmaf(w, __builtin_bit_cast(float, y), a.o[u][i][r]);
+                }
+            }
         }
     }
     // The same values as floats at dst (a row of the head dimension's floats).
@@ -490,8 +547,9 @@ struct Softmax {
     // Takes a tile's scores before their factor c > 0 (a negative one's sign
     // goes into q, and 0 makes q 0), of whose keys the first `limit` count,
     // rescales what o holds, and leaves the weights.
-    __device__ __forceinline__ void step(const f32x4 (&s)[G::KSUB], int limit, float c,
-                                         typename G::Acc& o, typename G::Probs& out) {
+    template <class A>
+    __device__ __forceinline__ void step(const f32x4 (&s)[G::KSUB], int limit, float c, A& o,
+                                         typename G::Probs& out) {
         float p[G::VK], top = -INFINITY;
 #pragma unroll
         for (int j = 0; j < G::VK; ++j) {
