@@ -75,51 +75,84 @@ def load():
     return _lib
 
 
+_codes = {}
+
+
 def _type_code(dtype) -> int:
-    import torch
-    codes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-    if dtype not in codes:
-        raise ValueError(f"attention takes bfloat16, float16 or float32 tensors, not {dtype}")
-    return codes[dtype]
+    code = _codes.get(dtype)
+    if code is None:
+        import torch
+        _codes.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+        code = _codes.get(dtype)
+        if code is None:
+            raise ValueError(f"attention takes bfloat16, float16 or float32 tensors, not {dtype}")
+    return code
 
 
-def _on_device(like, stream):
-    """A context with the tensor's device and the call's stream current."""
+class _Nothing:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_NOTHING = _Nothing()
+
+
+def _on_device(device, stream):
+    """A context with the tensors' device and the call's stream current."""
     import torch
-    if not like.is_cuda:
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
+    if device.type != "cuda":
         raise ValueError("attention needs tensors on the GPU")
-    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(like.device)
+    if torch.cuda.current_device() == device.index:
+        return _NOTHING
+    return torch.cuda.device(device)
 
 
-def _heads(name, t, rows, heads, like) -> Rows:
-    """A [rows, heads, head_dim] tensor as the library takes it."""
-    if t.dim() != 3 or (rows is not None and t.shape[0] != rows) or \
-            (heads is not None and t.shape[1] != heads) or t.shape[2] != like.shape[2]:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
-                         f"({rows if rows is not None else 'rows'}, "
-                         f"{heads if heads is not None else 'heads'}, {like.shape[2]})")
-    if t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on "
-                         f"{like.device}")
-    if t.numel() and t.shape[2] > 1 and t.stride(2) != 1:
+def _raw_stream(device) -> int | None:
+    """The device's current stream as the library takes it."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index) or None
+
+
+def _heads(name, t, rows, heads, dim, dtype, device) -> Rows:
+    """A [rows, heads, dim] tensor as the library takes it."""
+    s, st = t.shape, t.stride()
+    if len(s) != 3 or s[0] != rows or s[1] != heads or s[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(s)}, expected ({rows}, {heads}, {dim})")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {dtype} on {device}")
+    if st[2] != 1 and dim > 1 and t.numel():
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return Rows(t.data_ptr() if t.numel() else None, t.stride(0), t.stride(1))
+    return Rows(t.data_ptr(), st[0], st[1])
 
 
 def _flat(name, t, shape, dtype, device):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or \
-            not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
                          f"{device}")
 
 
-def _desc(q, hkv: int, scale) -> Desc:
-    hq, dim = q.shape[1], q.shape[2]
-    return Desc(_type_code(q.dtype), hq, hkv, dim, dim ** -0.5 if scale is None else float(scale))
+def _dims(q, k):
+    """(heads_q, heads_kv, dim, dtype, device) of a call."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError(f"q has shape {tuple(q.shape)} and k {tuple(k.shape)}, expected "
+                         "(rows, heads, dim)")
+    return q.shape[1], k.shape[1], q.shape[2], q.dtype, q.device
+
+
+def _scale(scale, dim) -> float:
+    return max(dim, 1) ** -0.5 if scale is None else float(scale)
 
 
 def _workspace(nbytes: int, device):
-    """(tensor, its 256-byte aligned address): the caching allocator's memory is 512-byte aligned."""
+    """A tensor of that many bytes and its address (the caching allocator's
+    memory is 512-byte aligned; the library asks for 256), or None twice."""
     import torch
     if nbytes == 0:
         return None, None
@@ -140,21 +173,18 @@ class AttentionPlan:
     def __init__(self, mask: DeviceCSR, backward: bool = False, stream=None):
         import torch
         lib = load()
-        for name, t, dtype, n in (("mask.rowptr", mask.rowptr, torch.int64, mask.nrows + 1),
-                                  ("mask.col", mask.col, torch.int32, mask.nnz)):
-            if not t.is_cuda:
-                raise ValueError("attention needs tensors on the GPU")
-            _flat(name, t, (n,), dtype, mask.rowptr.device)
         self._lib, self._h = lib, None
         self.nrows, self.ncols, self.nnz = mask.nrows, mask.ncols, mask.nnz
         self.device = mask.rowptr.device
-        h = ctypes.c_void_p()
-        s = _b.CSRStruct(mask.nrows, mask.ncols, mask.nnz, mask.rowptr.data_ptr(),
-                         mask.col.data_ptr() if mask.nnz else None, None)
-        with _on_device(mask.rowptr, stream):
+        self._sizes = {}  # workspace bytes by what they depend on
+        with _on_device(self.device, stream):
+            _flat("mask.rowptr", mask.rowptr, (mask.nrows + 1,), torch.int64, self.device)
+            _flat("mask.col", mask.col, (mask.nnz,), torch.int32, self.device)
+            h = ctypes.c_void_p()
+            s = _b.CSRStruct(mask.nrows, mask.ncols, mask.nnz, mask.rowptr.data_ptr(),
+                             _b._ptr(mask.col), None)
             _check(lib.spgemm_attention_plan_create(ctypes.byref(h), ctypes.byref(s),
-                                                    1 if backward else 0,
-                                                    _b._stream_handle(stream)),
+                                                    1 if backward else 0, _raw_stream(self.device)),
                    "spgemm_attention_plan_create")
         self._h = h
 
@@ -177,19 +207,22 @@ class AttentionPlan:
     def __exit__(self, *exc):
         self.close()
 
-    def _ready(self, q):
+    def _ready(self, device):
         if self._h is None:
             raise ValueError("the attention plan is closed")
-        if q.dim() != 3:
-            raise ValueError(f"q has shape {tuple(q.shape)}, expected (rows, heads, head_dim)")
-        if q.device != self.device:
-            raise ValueError(f"the plan is on {self.device}, q on {q.device}")
+        if device != self.device:
+            raise ValueError(f"the plan is on {self.device}, q on {device}")
 
     def _space(self, desc, backward):
-        n = ctypes.c_int64(0)
-        _check(self._lib.spgemm_attention_workspace(self._h, ctypes.byref(desc), backward,
-                                                    ctypes.byref(n)), "spgemm_attention_workspace")
-        return (*_workspace(n.value, self.device), n.value)
+        key = (desc.type, desc.heads_q, desc.heads_kv, desc.head_dim, backward)
+        n = self._sizes.get(key)
+        if n is None:
+            n = ctypes.c_int64(0)
+            _check(self._lib.spgemm_attention_workspace(self._h, ctypes.byref(desc), backward,
+                                                        ctypes.byref(n)),
+                   "spgemm_attention_workspace")
+            n = self._sizes[key] = n.value
+        return (*_workspace(n, self.device), n)
 
     def forward(self, q, k, v, scale=None, out=None, lse=None, stream=None):
         """(out, lse) for q [nrows, heads_q, dim] and k, v [ncols, heads_kv, dim].
@@ -197,24 +230,27 @@ class AttentionPlan:
         out has q's shape and type, lse is [nrows, heads_q] in float32. Either
         may be passed to be written into. scale defaults to dim ** -0.5."""
         import torch
-        self._ready(q)
-        qs = _heads("q", q, self.nrows, None, q)
-        ks = _heads("k", k, self.ncols, None, q)
-        vs = _heads("v", v, self.ncols, k.shape[1], q)
-        desc = _desc(q, k.shape[1], scale)
-        with _on_device(q, stream):
+        hq, hkv, dim, dtype, device = _dims(q, k)
+        self._ready(device)
+        nq, nk = self.nrows, self.ncols
+        ref = ctypes.byref
+        desc = Desc(_type_code(dtype), hq, hkv, dim, _scale(scale, dim))
+        with _on_device(device, stream):
             if out is None:
-                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                out = torch.empty(q.shape, dtype=dtype, device=device)
             if lse is None:
-                lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-            os = _heads("out", out, self.nrows, q.shape[1], q)
-            _flat("lse", lse, q.shape[:2], torch.float32, q.device)
-            _, ws, nbytes = space = self._space(desc, 0)
+                lse = torch.empty((nq, hq), dtype=torch.float32, device=device)
+            else:
+                _flat("lse", lse, (nq, hq), torch.float32, device)
+            rows = (_heads("q", q, nq, hq, dim, dtype, device),
+                    _heads("k", k, nk, hkv, dim, dtype, device),
+                    _heads("v", v, nk, hkv, dim, dtype, device),
+                    _heads("out", out, nq, hq, dim, dtype, device))
+            space, ws, nbytes = self._space(desc, 0)
             _check(self._lib.spgemm_attention_forward(
-                self._h, ctypes.byref(desc), ctypes.byref(qs), ctypes.byref(ks), ctypes.byref(vs),
-                ctypes.byref(os), _b._ptr(lse), ws, nbytes, _b._stream_handle(stream)),
+                self._h, ref(desc), ref(rows[0]), ref(rows[1]), ref(rows[2]), ref(rows[3]),
+                lse.data_ptr() or None, ws, nbytes, _raw_stream(device)),
                 "spgemm_attention_forward")
-            del space
         return out, lse
 
     def backward(self, dout, q, k, v, out, lse, scale=None, dq=None, dk=None, dv=None,
@@ -222,27 +258,29 @@ class AttentionPlan:
         """(dq, dk, dv), given dout and what ``forward`` returned. Gradients
         have their tensors' shapes and type, and are written, not added to."""
         import torch
-        self._ready(q)
-        hq, hkv = q.shape[1], k.shape[1] if k.dim() == 3 else None
-        qs = _heads("q", q, self.nrows, None, q)
-        ks = _heads("k", k, self.ncols, None, q)
-        vs = _heads("v", v, self.ncols, hkv, q)
-        os = _heads("out", out, self.nrows, hq, q)
-        gs = _heads("dout", dout, self.nrows, hq, q)
-        _flat("lse", lse, q.shape[:2], torch.float32, q.device)
-        desc = _desc(q, hkv, scale)
-        with _on_device(q, stream):
-            new = [torch.empty(x.shape, dtype=q.dtype, device=q.device) if g is None else g
-                   for g, x in ((dq, q), (dk, k), (dv, v))]
-            sinks = [_heads(n, g, x.shape[0], x.shape[1], q)
-                     for n, g, x in zip(("dq", "dk", "dv"), new, (q, k, v))]
-            _, ws, nbytes = space = self._space(desc, 1)
+        hq, hkv, dim, dtype, device = _dims(q, k)
+        self._ready(device)
+        nq, nk = self.nrows, self.ncols
+        ref = ctypes.byref
+        desc = Desc(_type_code(dtype), hq, hkv, dim, _scale(scale, dim))
+        with _on_device(device, stream):
+            _flat("lse", lse, (nq, hq), torch.float32, device)
+            if dq is None:
+                dq = torch.empty((nq, hq, dim), dtype=dtype, device=device)
+            if dk is None:
+                dk = torch.empty((nk, hkv, dim), dtype=dtype, device=device)
+            if dv is None:
+                dv = torch.empty((nk, hkv, dim), dtype=dtype, device=device)
+            rows = [_heads(name, t, n, h, dim, dtype, device) for name, t, n, h in (
+                ("q", q, nq, hq), ("k", k, nk, hkv), ("v", v, nk, hkv), ("out", out, nq, hq),
+                ("dout", dout, nq, hq), ("dq", dq, nq, hq), ("dk", dk, nk, hkv),
+                ("dv", dv, nk, hkv))]
+            space, ws, nbytes = self._space(desc, 1)
             _check(self._lib.spgemm_attention_backward(
-                self._h, ctypes.byref(desc), ctypes.byref(qs), ctypes.byref(ks), ctypes.byref(vs),
-                ctypes.byref(os), _b._ptr(lse), ctypes.byref(gs), *map(ctypes.byref, sinks), ws,
-                nbytes, _b._stream_handle(stream)), "spgemm_attention_backward")
-            del space
-        return tuple(new)
+                self._h, ref(desc), ref(rows[0]), ref(rows[1]), ref(rows[2]), ref(rows[3]),
+                lse.data_ptr() or None, ref(rows[4]), ref(rows[5]), ref(rows[6]), ref(rows[7]), ws,
+                nbytes, _raw_stream(device)), "spgemm_attention_backward")
+        return dq, dk, dv
 
 
 def paged_attention(q, k_cache, v_cache, pages: DeviceCSR, q_rowptr, lengths, max_q: int,
@@ -269,40 +307,42 @@ def paged_attention(q, k_cache, v_cache, pages: DeviceCSR, q_rowptr, lengths, ma
                          "twice (pages, slots, kv heads, dim)")
     tokens, hq, dim = q.shape
     npages, slots, hkv, _ = k_cache.shape
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != q.dtype or t.device != q.device:
-            raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {q.dtype} on {q.device}")
-        if t.numel() and dim > 1 and t.stride(3) != 1:
+    dtype, device, seqs = q.dtype, q.device, pages.nrows
+    ks, vs = k_cache.stride(), v_cache.stride()
+    for name, t, st in (("k_cache", k_cache, ks), ("v_cache", v_cache, vs)):
+        if t.dtype != dtype or t.device != device:
+            raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {dtype} on {device}")
+        if st[3] != 1 and dim > 1 and t.numel():
             raise ValueError(f"{name}'s last dimension must be contiguous")
     if pages.ncols != npages:
         raise ValueError(f"the page table names pages of a cache of {pages.ncols}, it has {npages}")
-    _flat("pages.rowptr", pages.rowptr, (pages.nrows + 1,), torch.int64, q.device)
-    _flat("pages.col", pages.col, (pages.nnz,), torch.int32, q.device)
-    _flat("q_rowptr", q_rowptr, (pages.nrows + 1,), torch.int64, q.device)
-    _flat("lengths", lengths, (pages.nrows,), torch.int64, q.device)
-    qs = _heads("q", q, tokens, None, q)
-    desc = _desc(q, hkv, scale)
-    table = _b.CSRStruct(pages.nrows, npages, pages.nnz, pages.rowptr.data_ptr(),
-                         _b._ptr(pages.col), None)
-    cache = PagedCache(_b._ptr(k_cache), _b._ptr(v_cache), npages, slots, *k_cache.stride()[:3],
-                       *v_cache.stride()[:3])
-    batch = PagedBatch(ctypes.pointer(table), q_rowptr.data_ptr(), _b._ptr(lengths), tokens,
-                       int(max_q), int(max_len))
-    with _on_device(q, stream):
+    desc = Desc(_type_code(dtype), hq, hkv, dim, _scale(scale, dim))
+    ref = ctypes.byref
+    with _on_device(device, stream):
+        nnz = pages.nnz
+        _flat("pages.rowptr", pages.rowptr, (seqs + 1,), torch.int64, device)
+        _flat("pages.col", pages.col, (nnz,), torch.int32, device)
+        _flat("q_rowptr", q_rowptr, (seqs + 1,), torch.int64, device)
+        _flat("lengths", lengths, (seqs,), torch.int64, device)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = torch.empty(q.shape, dtype=dtype, device=device)
         if lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        os = _heads("out", out, tokens, hq, q)
-        _flat("lse", lse, q.shape[:2], torch.float32, q.device)
+            lse = torch.empty((tokens, hq), dtype=torch.float32, device=device)
+        else:
+            _flat("lse", lse, (tokens, hq), torch.float32, device)
+        qs = _heads("q", q, tokens, hq, dim, dtype, device)
+        os = _heads("out", out, tokens, hq, dim, dtype, device)
+        table = _b.CSRStruct(seqs, npages, nnz, pages.rowptr.data_ptr(),
+                             pages.col.data_ptr() or None, None)
+        cache = PagedCache(k_cache.data_ptr() or None, v_cache.data_ptr() or None, npages, slots,
+                           ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
+        batch = PagedBatch(ctypes.pointer(table), q_rowptr.data_ptr(), lengths.data_ptr() or None,
+                           tokens, max_q, max_len)
         n = ctypes.c_int64(0)
-        _check(lib.spgemm_paged_attention_workspace(ctypes.byref(desc), ctypes.byref(batch),
-                                                    ctypes.byref(n)),
+        _check(lib.spgemm_paged_attention_workspace(ref(desc), ref(batch), ref(n)),
                "spgemm_paged_attention_workspace")
-        space, ws = _workspace(n.value, q.device)
+        space, ws = _workspace(n.value, device)
         _check(lib.spgemm_paged_attention(
-            ctypes.byref(desc), ctypes.byref(qs), ctypes.byref(cache), ctypes.byref(batch),
-            ctypes.byref(os), _b._ptr(lse), ws, n.value, _b._stream_handle(stream)),
-            "spgemm_paged_attention")
-        del space
+            ref(desc), ref(qs), ref(cache), ref(batch), ref(os), lse.data_ptr() or None, ws,
+            n.value, _raw_stream(device)), "spgemm_paged_attention")
     return out, lse

@@ -519,46 +519,39 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 1) void k_att
     }
 }
 
-// The sums of rows (or blocks of columns) of more than one piece, in the
-// pieces' order. One wavefront per row, head and, for blocks, column and
-// output: `lines` results of dim values per head lie side by side.
+// The sums of the rows, and of the blocks of columns, of more than one piece,
+// in the pieces' order: one wavefront per row and head of dq, and per
+// (column, output) of a block and head of dk and dv. A piece's results lie
+// side by side, `lines` of dim values per head (1, or 2 per column).
 template <class T>
-__global__ __launch_bounds__(kWaves* kWave) void k_attn_join_sum(AttnSide side, const float* part,
-                                                                 int heads, int lines, int dim,
-                                                                 int64_t nrows, AttnRows out0,
-                                                                 AttnRows out1) {
+__global__ __launch_bounds__(kWaves* kWave) void k_attn_join_sum(BackwardArgs a) {
     const int lane = lane_id();
-    const int64_t unit = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
+    int64_t unit = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
+    const int64_t row_units = a.rows.nsplits * a.s.hq;
+    const bool col_side = unit >= row_units;
+    if (col_side) unit -= row_units;
+    const AttnSide& side = col_side ? a.cols : a.rows;
+    const int heads = col_side ? a.s.hkv : a.s.hq, lines = col_side ? 2 * kColBlock : 1;
     const int64_t per = (int64_t)heads * lines;
     if (unit >= side.nsplits * per) return;
     const int64_t sp = unit / per, hl = unit - sp * per;
     const int h = (int)(hl / lines), line = (int)(hl - (int64_t)h * lines);
     const AttnSplit s = side.splits[sp];
-    const int64_t row = lines == 1 ? s.row : (int64_t)s.row * kColBlock + line / 2;
-    if (row >= nrows) return;
+    const int64_t row = col_side ? (int64_t)s.row * kColBlock + line / 2 : s.row;
+    if (col_side && row >= a.ncols) return;
+    const float* part = (col_side ? a.part_kv : a.part_q) + ((int64_t)s.slot * per + hl) * a.s.dim;
     float x[SPGEMM_ATTENTION_MAX_HEAD_DIM / kWave] = {};
     for (int i = 0; i < s.count; ++i) {
-        const float* src = part + ((int64_t)(s.slot + i) * per + hl) * dim;
+        const float* src = part + i * per * a.s.dim;
 #pragma unroll
         for (int j = 0; j < SPGEMM_ATTENTION_MAX_HEAD_DIM / kWave; ++j)
-            if (j * kWave + lane < dim) x[j] += src[j * kWave + lane];
+            if (j * kWave + lane < a.s.dim) x[j] += src[j * kWave + lane];
     }
-    const AttnRows& o = line & 1 ? out1 : out0;
+    const AttnRows& o = !col_side ? a.dq : line & 1 ? a.dv : a.dk;
     T* dst = reinterpret_cast<T*>(o.base + row * o.row + h * o.head);
 #pragma unroll
     for (int j = 0; j < SPGEMM_ATTENTION_MAX_HEAD_DIM / kWave; ++j)
-        if (j * kWave + lane < dim) dst[j * kWave + lane] = (T)x[j];
-}
-
-template <class T>
-void join_sum(const AttnSide& side, const float* part, int heads, int lines, int dim,
-              int64_t nrows, const AttnRows& out0, const AttnRows& out1, hipStream_t st) {
-    if (side.nsplits == 0) return;
-    hipLaunchKernelGGL(k_attn_join_sum<T>,
-                       dim3(grid_1d(ceil_div(side.nsplits * heads * lines, kWaves))),
-                       dim3(kWaves * kWave), 0, st, side, part, heads, lines, dim, nrows, out0,
-                       out1);
-    SG_LAUNCH_CHECK();
+        if (j * kWave + lane < a.s.dim) dst[j * kWave + lane] = (T)x[j];
 }
 
 }  // namespace
@@ -575,7 +568,6 @@ void attention_backward(const BackwardArgs& a, hipStream_t st) {
             hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(groups * heads))), dim3(kWaves * kWave),
                                0, st, a, each, groups);
             SG_LAUNCH_CHECK();
-            join_sum<T>(a.rows, a.part_q, a.s.hq, 1, a.s.dim, a.rows.n, a.dq, a.dq, st);
         }
         const int64_t cols = xcd_grid(a.cols.npieces) * a.s.hkv;
         if (cols > 0) {
@@ -583,7 +575,12 @@ void attention_backward(const BackwardArgs& a, hipStream_t st) {
             hipLaunchKernelGGL(run, dim3(grid_1d(cols)), dim3(kKvWaves * kWave), 0, st,
                                a);
             SG_LAUNCH_CHECK();
-            join_sum<T>(a.cols, a.part_kv, a.s.hkv, 2 * kColBlock, a.s.dim, a.ncols, a.dk, a.dv, st);
+        }
+        const int64_t joins = a.rows.nsplits * a.s.hq + a.cols.nsplits * a.s.hkv * 2 * kColBlock;
+        if (joins > 0) {
+            hipLaunchKernelGGL(k_attn_join_sum<T>, dim3(grid_1d(ceil_div(joins, kWaves))),
+                               dim3(kWaves * kWave), 0, st, a);
+            SG_LAUNCH_CHECK();
         }
     });
 }

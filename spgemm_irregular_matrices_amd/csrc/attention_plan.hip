@@ -20,14 +20,18 @@ struct spgemm_attention_plan_s {
 namespace {
 
 // ---------------------------------------------------------------- plan
-// Entries per piece. Long rows are cut so that the longest wavefront stays
-// near the mean one's work: about 4096 pieces over all entries, between 128
-// entries (a piece's fixed costs, its partial result among them, are about
-// those of 16 entries) and 1024.
-int64_t piece_length(int64_t nnz) {
-    const int64_t want = ceil_div(ceil_div(nnz, 4096), 32) * 32;
-    return want < 32 ? 32 : want > 1024 ? 1024 : want;
-}
+// Entries per piece. Long rows are cut so that the longest piece stays near
+// the mean one's work: about `pieces` of them over all entries (4096 where a
+// wavefront takes one, 1024 where a work group does), between `least` and
+// 1024 entries each.
+struct PieceRule {
+    int64_t pieces, least;
+    int64_t length(int64_t nnz) const {
+        const int64_t want = ceil_div(ceil_div(nnz, pieces), 32) * 32;
+        return want < least ? least : want > 1024 ? 1024 : want;
+    }
+};
+constexpr PieceRule kRowPieces{4096, 128}, kBlockPieces{1024, 32};
 
 struct RowPieces {
     const int64_t* rp;
@@ -124,14 +128,14 @@ __global__ void k_block_groups(const int32_t* col, const int32_t* entry, int64_t
     first[b] = group[lo];
 }
 
-AttnSide make_side(const char* name, const int64_t* rp, int64_t n, int64_t nnz, const int32_t* idx,
-                   Arena& keep, Arena& tmp, hipStream_t st) {
+AttnSide make_side(const char* name, const int64_t* rp, int64_t n, int64_t nnz, PieceRule rule,
+                   const int32_t* idx, Arena& keep, Arena& tmp, hipStream_t st) {
     AttnSide s;
     s.n = n;
     s.idx = idx;
     if (n == 0) return s;
     const std::string nm(name);
-    const RowPieces rows{rp, piece_length(nnz)};
+    const RowPieces rows{rp, rule.length(nnz)};
     int64_t* piece0 = tmp.get<int64_t>("piece0", (size_t)n + 1);
     int64_t* slot0 = tmp.get<int64_t>("slot0", (size_t)n + 1);
     int64_t* split0 = tmp.get<int64_t>("split0", (size_t)n + 1);
@@ -180,7 +184,7 @@ int build_plan(spgemm_attention_plan p, const spgemm_csr* mask, bool backward, h
     p->backward = backward;
     int32_t* col = p->ar.get<int32_t>("col", (size_t)m.nnz);
     copy<int32_t>(col, m.col, m.nnz, st);
-    p->rows = make_side("rows", m.rp, m.n, m.nnz, col, p->ar, tmp, st);
+    p->rows = make_side("rows", m.rp, m.n, m.nnz, kRowPieces, col, p->ar, tmp, st);
     if (backward) {
         const int64_t nblocks = ceil_div(m.m, kColBlock);
         int64_t* first = tmp.get<int64_t>("first", (size_t)nblocks + 1);
@@ -218,7 +222,7 @@ int build_plan(spgemm_attention_plan p, const spgemm_csr* mask, bool backward, h
         } else {
             fill<int64_t>(first, nblocks + 1, 0, st);
         }
-        p->cols = make_side("cols", first, nblocks, ngroups, gidx, p->ar, tmp, st);
+        p->cols = make_side("cols", first, nblocks, ngroups, kBlockPieces, gidx, p->ar, tmp, st);
         p->cols.bits = gbits;
     }
     SG_HIP(hipStreamSynchronize(st));  // before the temporary buffers go
@@ -361,7 +365,7 @@ void shape_pieces(PagedArgs* a) {
     const int64_t tiles = ceil_div(rows, paged_tile_rows(a->s.dim, rows));
     const int64_t units = std::max<int64_t>(a->seqs * a->s.hkv * tiles, 1);
     const int64_t most = std::max<int64_t>(ceil_div(a->max_length, wide ? 256 : 64), 1);
-    const int64_t want = std::min(std::max<int64_t>((wide ? 1024 : 4096) / units, 1), most);
+    const int64_t want = std::min(std::max<int64_t>((wide ? 512 : 4096) / units, 1), most);
     const int64_t whole = wide ? 64 : 32;
     a->piece = (int32_t)std::max<int64_t>(
         ceil_div(ceil_div(a->max_length, want), whole) * whole, whole);
