@@ -35,13 +35,13 @@ constexpr float kProbScale = std::is_same<T, _Float16>::value ? 0x1p14f : 1.f;
 
 // dq: one wavefront per piece of a row and 16 query heads of a key head, its
 // pieces' tiles in one stream as in the forward pass. S^T and dP^T = V dO^T
-// take the gathered rows as rows, dQ^T += K^T dS^T takes K as chunks: K rows
-// come from memory as chunks, a tile ahead, and are staged in the
+// take the gathered rows as rows, dQ^T += K^T dS^T takes K as chunks: all come
+// from memory as chunks, a tile ahead (see there), and are staged in the
 // wavefront's own LDS for the other layout.
 template <class G, class T>
 __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_grad_q(BackwardArgs a, int each,
                                                                int64_t groups) {
-    __shared__ __align__(16) char stage[kWaves][G::KT * G::kRowBytes];
+    __shared__ __align__(16) char stage[kWaves][2][G::KT * G::kRowBytes];
     const int lane = lane_id();
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t block = xcd_block();
@@ -54,7 +54,8 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
     const bool has = g < a.s.group;
     const int hq = h * a.s.group + g;
     const int row_bytes = a.s.dim * (int)sizeof(T);
-    char* krows = stage[w];
+    char* krows = stage[w][0];
+    char* vrows = stage[w][1];
     const int rbase = G::row_base(0), cbase = G::chunk_base(0);
 
     PieceStream st(a.rows, u0, kWaves, each);
@@ -72,8 +73,8 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
 
     const char* kb = a.k.base + h * a.k.head;
     const char* vb = a.v.base + h * a.v.head;
-    typename G::RowFrag q, dout, out, v[G::KSUB];
-    typename G::VBlock k[G::U];
+    typename G::RowFrag q, dout, out;
+    typename G::VBlock k[G::U], v[G::U];
     float lse = INFINITY;  // lanes without a head: weights 0
     const auto load_q = [&](int i) {
         const int row = st.row(i);
@@ -87,23 +88,18 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
             lse = a.lse[(int64_t)row * a.s.hq + hq];
         }
     };
-    const auto load_k = [&](uint32_t id) {
-        const uint32_t off = id * a.k.unit;
+    const auto load = [&](typename G::VBlock (&x)[G::U], const char* base, uint32_t off,
+                          uint32_t shift) {
 #pragma unroll
         for (int j = 0; j < G::VK; ++j) {
-            const char* row = kb + ((uint64_t)(uint32_t)__shfl(off, G::key_of(j), kWave)
-                                    << a.k.shift);
+            const char* row =
+                base + ((uint64_t)(uint32_t)__shfl(off, G::key_of(j), kWave) << shift);
 #pragma unroll
-            for (int u = 0; u < G::U; ++u) G::load_chunk(row, u, row_bytes, k[u].w[j]);
+            for (int u = 0; u < G::U; ++u) G::load_chunk(row, u, row_bytes, x[u].w[j]);
         }
     };
-    const auto load_v = [&](uint32_t id) {
-        const uint32_t off = id * a.v.unit;
-#pragma unroll
-        for (int b = 0; b < G::KSUB; ++b)
-            G::load_row(vb + ((uint64_t)(uint32_t)__shfl(off, 16 * b + n, kWave) << a.v.shift),
-                        row_bytes, v[b]);
-    };
+    const auto load_k = [&](uint32_t id) { load(k, kb, id * a.k.unit, a.k.shift); };
+    const auto load_v = [&](uint32_t id) { load(v, vb, id * a.v.unit, a.v.shift); };
 
     PieceStream::Cursor cur, ahead;
     st.open(cur);
@@ -130,32 +126,26 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
                 a.delta[(int64_t)st.row(cur.i) * a.s.hq + hq] = delta;
             fresh = false;
         }
+        if (left < G::KT) G::clear_past(k, left);
         wave_lds_sync();
-#pragma unroll
-        for (int j = 0; j < G::VK; ++j)
-#pragma unroll
-            for (int u = 0; u < G::U; ++u) {
-                if (G::key_of(j) >= left) {  // 0 times what a repeated row holds may be NaN
-#pragma unroll
-                    for (int i = 0; i < G::VW; ++i) k[u].w[j][i] = 0;
-                }
-                G::stage_chunk(krows, cbase, j, u, k[u].w[j]);
-            }
+        G::stage_tile(krows, cbase, k);
+        G::stage_tile(vrows, cbase, v);
         wave_lds_sync();
         const uint32_t idn = id;
-        if (more) load_k(idn);
+        if (more) {
+            load_k(idn);
+            load_v(idn);
+        }
         f32x4 s[G::KSUB], dp[G::KSUB];
 #pragma unroll
         for (int b = 0; b < G::KSUB; ++b) {
-            dp[b] = G::dot(v[b], dout, f32x4{0, 0, 0, 0});
             typename G::RowFrag x;
             G::staged_row(krows, rbase, 16 * b, x);
             s[b] = G::dot(x, q, f32x4{0, 0, 0, 0});
+            G::staged_row(vrows, rbase, 16 * b, x);
+            dp[b] = G::dot(x, dout, f32x4{0, 0, 0, 0});
         }
-        if (more) {
-            load_v(idn);
-            if (last) load_q(ahead.i);
-        }
+        if (more && last) load_q(ahead.i);
         const PieceStream::Cursor after = ahead;
         if (more) {
             st.next(ahead, G::KT);

@@ -10,14 +10,18 @@ constexpr int kWaves = 4;
 // One wavefront: 16 query heads [16*mt, 16*mt+16) of a key head's group
 // against `each` pieces in turn. The tiles of all its pieces form one stream,
 // so that a short row costs no idle trip to memory: while a tile is computed
-// the next one's key and value rows are under way (K into the registers that
-// the scores freed, V into those that the second product freed) and the
-// indices of the one after that.
+// the next one's key and value rows are under way and the indices of the one
+// after that. All rows are loaded as chunks, 16 lanes to a row: loaded as rows
+// (a lane to a row) each lane's 16 bytes are an access of their own to the
+// first-level cache, four times as many, and that rate is what bound this
+// kernel. K takes the other layout through the wavefront's own LDS.
 template <class G, class T>
 __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_forward(ForwardArgs a, int each,
                                                                 int64_t groups) {
+    __shared__ __align__(16) char stage[kWaves][G::KT * G::kRowBytes];
     const int lane = lane_id();
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    char* krows = stage[w];
     const int64_t block = xcd_block();
     const int hm = (int)(block / groups);  // key head and 16 query heads
     if (hm >= a.s.hkv * a.s.mtiles) return;
@@ -46,31 +50,27 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
 
     const char* kb = a.k.base + h * a.k.head;
     const char* vb = a.v.base + h * a.v.head;
-    typename G::RowFrag q, k[G::KSUB];
-    typename G::VBlock v[G::U];
+    const int rbase = G::row_base(0), cbase = G::chunk_base(0);
+    typename G::RowFrag q;
+    typename G::VBlock k[G::U], v[G::U];
     const auto load_q = [&](int i) {
         G::zero_row(q);
         if (has)
             G::load_row(a.q.base + st.row(i) * a.q.row + hq * a.q.head, row_bytes, q);
         G::sign_row(q, a.s.c);
     };
-    const auto load_k = [&](uint32_t id) {
-        const uint32_t off = id * a.k.unit;
-#pragma unroll
-        for (int b = 0; b < G::KSUB; ++b)
-            G::load_row(kb + ((uint64_t)(uint32_t)__shfl(off, 16 * b + n, kWave) << a.k.shift),
-                        row_bytes, k[b]);
-    };
-    const auto load_v = [&](uint32_t id) {
-        const uint32_t off = id * a.v.unit;
+    const auto load = [&](typename G::VBlock (&x)[G::U], const char* base, uint32_t off,
+                          uint32_t shift) {
 #pragma unroll
         for (int j = 0; j < G::VK; ++j) {
-            const char* row = vb + ((uint64_t)(uint32_t)__shfl(off, G::key_of(j), kWave)
-                                    << a.v.shift);
+            const char* row =
+                base + ((uint64_t)(uint32_t)__shfl(off, G::key_of(j), kWave) << shift);
 #pragma unroll
-            for (int u = 0; u < G::U; ++u) G::load_chunk(row, u, row_bytes, v[u].w[j]);
+            for (int u = 0; u < G::U; ++u) G::load_chunk(row, u, row_bytes, x[u].w[j]);
         }
     };
+    const auto load_k = [&](uint32_t id) { load(k, kb, id * a.k.unit, a.k.shift); };
+    const auto load_v = [&](uint32_t id) { load(v, vb, id * a.v.unit, a.v.shift); };
 
     PieceStream::Cursor cur, ahead;  // ahead: the tile whose indices are loaded
     st.open(cur);
@@ -88,14 +88,19 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
     while (true) {
         const int left = cur.len - cur.t0;
         const bool last = left <= G::KT, more = ahead.more;
+        wave_lds_sync();
+        G::stage_tile(krows, cbase, k);
+        wave_lds_sync();
+        const uint32_t idn = id;
+        if (more) load_k(idn);
         f32x4 s[G::KSUB];
 #pragma unroll
-        for (int b = 0; b < G::KSUB; ++b) s[b] = G::dot(k[b], q, f32x4{0, 0, 0, 0});
-        const uint32_t idn = id;
-        if (more) {
-            load_k(idn);
-            if (last) load_q(ahead.i);
+        for (int b = 0; b < G::KSUB; ++b) {
+            typename G::RowFrag x;
+            G::staged_row(krows, rbase, 16 * b, x);
+            s[b] = G::dot(x, q, f32x4{0, 0, 0, 0});
         }
+        if (more && last) load_q(ahead.i);
         const PieceStream::Cursor after = ahead;
         if (more) {
             st.next(ahead, G::KT);
@@ -103,16 +108,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
         }
         typename G::Probs pr;
         sm.step(s, left, a.s.mag, o, pr);
-        if (left < G::KT) {
-            // 0 weight times what a repeated row holds may be NaN
-#pragma unroll
-            for (int j = 0; j < G::VK; ++j)
-                if (G::key_of(j) >= left)
-#pragma unroll
-                    for (int u = 0; u < G::U; ++u)
-#pragma unroll
-                        for (int i = 0; i < G::VW; ++i) v[u].w[j][i] = 0;
-        }
+        if (left < G::KT) G::clear_past(v, left);
 #pragma unroll
         for (int u = 0; u < G::U; ++u) G::accumulate(v[u], pr, u, o);
         if (more) load_v(idn);

@@ -137,8 +137,11 @@ __device__ __forceinline__ void store_row(const PagedArgs& a, const TileJob& j, 
 template <class G, class T>
 __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged(PagedArgs a,
                                                                                  int32_t tiles) {
+    __shared__ __align__(16) char stage[kWaves][G::KT * G::kRowBytes];
     const int lane = lane_id();
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    char* krows = stage[w];
+    const int rbase = G::row_base(0), cbase = G::chunk_base(0);
     int64_t unit = xcd_block() * kWaves + w;
     if (unit >= a.seqs * a.s.hkv * a.npieces * tiles) return;
     const int tile = (int)(unit % tiles);
@@ -160,8 +163,8 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
     const int lo = __builtin_amdgcn_readfirstlane(r.t);
     const int hi = __builtin_amdgcn_readlane(r.t, 15);
 
-    typename G::RowFrag q, k[G::KSUB];
-    typename G::VBlock v[G::U];
+    typename G::RowFrag q;
+    typename G::VBlock k[G::U], v[G::U];
     G::zero_row(q);
     if (r.has) G::load_row(a.q.base + r.token * a.q.row + r.hq * a.q.head, row_bytes, q);
     G::sign_row(q, a.s.c);
@@ -184,22 +187,21 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
             x.id = 0;
         }
     };
-    const auto load_k = [&](const Place& x) {
-        const uint32_t off = x.id * a.k_page + x.slot * a.k_slot;
-#pragma unroll
-        for (int b = 0; b < G::KSUB; ++b)
-            G::load_row(kb + ((uint64_t)(uint32_t)__shfl(off, 16 * b + n, kWave) << a.k_shift),
-                        row_bytes, k[b]);
-    };
-    const auto load_v = [&](const Place& x) {
-        const uint32_t off = x.id * a.v_page + x.slot * a.v_slot;
+    const auto load = [&](typename G::VBlock (&x)[G::U], const char* base, uint32_t off,
+                          uint32_t shift) {
 #pragma unroll
         for (int j = 0; j < G::VK; ++j) {
             const char* row =
-                vb + ((uint64_t)(uint32_t)__shfl(off, G::key_of(j), kWave) << a.v_shift);
+                base + ((uint64_t)(uint32_t)__shfl(off, G::key_of(j), kWave) << shift);
 #pragma unroll
-            for (int u = 0; u < G::U; ++u) G::load_chunk(row, u, row_bytes, v[u].w[j]);
+            for (int u = 0; u < G::U; ++u) G::load_chunk(row, u, row_bytes, x[u].w[j]);
         }
+    };
+    const auto load_k = [&](const Place& x) {
+        load(k, kb, x.id * a.k_page + x.slot * a.k_slot, a.k_shift);
+    };
+    const auto load_v = [&](const Place& x) {
+        load(v, vb, x.id * a.v_page + x.slot * a.v_slot, a.v_shift);
     };
     Place now = place(job.k0), here = now;  // here: of the tile that is computed
     Place next = now;
@@ -214,9 +216,9 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
     for (int t0 = job.k0; t0 < job.k1; t0 += G::KT) {
         const int left = job.k1 - t0;
         const bool more = left > G::KT;
-        f32x4 sc[G::KSUB];
-#pragma unroll
-        for (int b = 0; b < G::KSUB; ++b) sc[b] = G::dot(k[b], q, f32x4{0, 0, 0, 0});
+        wave_lds_sync();
+        G::stage_tile(krows, cbase, k);
+        wave_lds_sync();
         here = now;
         if (more) {
             now = next;
@@ -224,18 +226,16 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
             load_k(now);
             if (left > 2 * G::KT) next = place(t0 + 2 * G::KT);
         }
+        f32x4 sc[G::KSUB];
+#pragma unroll
+        for (int b = 0; b < G::KSUB; ++b) {
+            typename G::RowFrag x;
+            G::staged_row(krows, rbase, 16 * b, x);
+            sc[b] = G::dot(x, q, f32x4{0, 0, 0, 0});
+        }
         typename G::Probs pr;
         sm.step(sc, min(left, job.before + r.t - t0), a.s.mag, o, pr);
-        if (left < G::KT) {
-            // 0 weight times what a repeated place holds may be NaN
-#pragma unroll
-            for (int j = 0; j < G::VK; ++j)
-                if (G::key_of(j) >= left)
-#pragma unroll
-                    for (int u = 0; u < G::U; ++u)
-#pragma unroll
-                        for (int i = 0; i < G::VW; ++i) v[u].w[j][i] = 0;
-        }
+        if (left < G::KT) G::clear_past(v, left);
         const bool crosses = t0 + G::KT > job.before + lo;  // some row may not see some key
 #pragma unroll
         for (int u = 0; u < G::U; ++u) {

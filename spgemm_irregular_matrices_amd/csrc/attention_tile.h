@@ -397,6 +397,24 @@ struct Tile {
         else
             *reinterpret_cast<u32x2*>(at) = u32x2{w[0], w[1]};
     }
+    // The lane's chunks of a tile's rows.
+    static __device__ __forceinline__ void stage_tile(char* lds, int base, const VBlock (&x)[U]) {
+#pragma unroll
+        for (int j = 0; j < VK; ++j)
+#pragma unroll
+            for (int u = 0; u < U; ++u) stage_chunk(lds, base, j, u, x[u].w[j]);
+    }
+    // Its keys from the `left`-th on as 0: 0 weight times what the row that
+    // they repeat holds may be NaN.
+    static __device__ __forceinline__ void clear_past(VBlock (&x)[U], int left) {
+#pragma unroll
+        for (int j = 0; j < VK; ++j)
+            if (key_of(j) >= left)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < VW; ++i) x[u].w[j][i] = 0;
+    }
     static __device__ __forceinline__ void staged_chunk(const char* lds, int base, int dr, int j,
                                                         int u, uint32_t (&w)[VW]) {
         const char* at = lds + stage_more(base, dr + (j & 3) + 16 * (j >> 2), 64 * VW * u);
