@@ -28,14 +28,15 @@ struct AttnSplit {
 
 // One direction of the mask, cut into pieces.
 struct AttnSide {
-    int64_t n = 0;          // rows
+    int64_t n = 0;          // rows, or blocks of rows
     int64_t npieces = 0;
     int64_t nslots = 0;
     int64_t nsplits = 0;
     const AttnPiece* pieces = nullptr;
     const AttnSplit* splits = nullptr;
     const int32_t* idx = nullptr;  // the entries' columns
-    const uint16_t* bits = nullptr;  // see kColBlock
+    const uint16_t* bits = nullptr;  // see kColBlock and kRowBlock; null for single rows
+    int block = 1;                   // rows per block
 };
 
 // The transposed mask, by blocks of 16 columns: an entry of block b is a row
@@ -44,6 +45,10 @@ struct AttnSide {
 // rows ascend; a row comes again where it stores a column twice, or columns
 // out of order.
 constexpr int kColBlock = 16;
+// The mask by blocks of 4 rows, in the same manner: an entry is a column with
+// the set of the block's rows that store it, so that one trip for its key and
+// value rows serves up to 4 rows, and 4 short rows share a tile.
+constexpr int kRowBlock = 4;
 
 // Rows of a gathered tensor. A row's offset is unit * (its index) << shift
 // bytes, so that it fits 32 bits before the shift; the strides of every
@@ -63,7 +68,7 @@ struct AttnRows {
 struct AttnShape {
     int type = 0;
     int hq = 0, hkv = 0, group = 0, dim = 0;
-    int mtiles = 1;      // ceil(group / 16)
+    int mtiles = 1;      // tiles of 16 queries per piece and key head (see AttnColumn)
     float scale = 0.f;   // of the scores
     float c = 0.f;       // scale * log2(e)
     float mag = 1.f;     // |c|, or 1 if that is 0: the factor that Softmax takes
@@ -72,11 +77,12 @@ struct AttnShape {
 struct ForwardArgs {
     AttnShape s;
     AttnSide side;
+    int64_t nrows = 0;
     AttnRows q, out;
     AttnGather k, v;
     float* lse = nullptr;      // may be null
-    float* part = nullptr;     // [slot][hq][dim] unnormalised outputs
-    float* part_ml = nullptr;  // [slot][hq][2]: maximum (base 2) and sum
+    float* part = nullptr;     // [slot][row of block][hq][dim] unnormalised outputs
+    float* part_ml = nullptr;  // [slot][row of block][hq][2]: maximum (base 2) and sum
 };
 void attention_forward(const ForwardArgs& a, hipStream_t st);
 
@@ -89,9 +95,9 @@ struct BackwardArgs {
     AttnRows krow, vrow;    // k and v, one row per column of the mask
     const float* lse = nullptr;
     float* delta = nullptr;    // [row][hq]
-    float* part_q = nullptr;   // [slot][hq][dim]
+    float* part_q = nullptr;   // [slot][row of block][hq][dim]
     float* part_kv = nullptr;  // [slot of cols][hkv][kColBlock][2][dim]
-    int64_t ncols = 0;
+    int64_t nrows = 0, ncols = 0;
     FastDiv group_div;
 };
 void attention_backward(const BackwardArgs& a, hipStream_t st);
@@ -149,16 +155,17 @@ inline int pieces_per_wave(int64_t units) {
 struct PieceStream {
     struct Cursor {
         int i, t0, len;
-        const int32_t* idx;
+        uint64_t first;
         bool more;
     };
     AttnPiece mine{};
     uint64_t empty, todo;
     const int32_t* idx;
+    const uint16_t* bits;
 
     __device__ __forceinline__ PieceStream(const AttnSide& side, int64_t first, int stride,
                                            int each)
-        : idx(side.idx) {
+        : idx(side.idx), bits(side.bits) {
         const int64_t u = first + (int64_t)lane_id() * stride;
         const bool there = lane_id() < each && u < side.npieces;
         if (there) mine = side.pieces[u];
@@ -180,16 +187,56 @@ struct PieceStream {
         c.len = lane_value(mine.len, c.i);
         const uint32_t lo = (uint32_t)lane_value((int)(mine.first & 0xffffffff), c.i);
         const uint32_t hi = (uint32_t)lane_value((int)(mine.first >> 32), c.i);
-        c.idx = idx + ((uint64_t)hi << 32 | lo);
+        c.first = (uint64_t)hi << 32 | lo;
     }
     __device__ __forceinline__ void next(Cursor& c, int tile) {
         c.t0 += tile;
         if (c.t0 >= c.len) open(c);
     }
-    // This lane's index of the tile. Lanes past the piece's end repeat its
-    // last entry: every address made from one is a row that the piece names.
-    static __device__ __forceinline__ uint32_t id(const Cursor& c, int tile) {
-        return (uint32_t)c.idx[min(c.t0 + (lane_id() & (tile - 1)), c.len - 1)];
+    // This lane's entry of the tile. Lanes past the piece's end repeat its
+    // last one: every address made from an index is a row that the piece
+    // names. Their bits are 0.
+    struct Entry {
+        uint32_t id, bits;
+    };
+    template <bool SHARED>
+    __device__ __forceinline__ Entry entry(const Cursor& c, int tile) const {
+        const int at = c.t0 + (lane_id() & (tile - 1));
+        const uint64_t e = c.first + min(at, c.len - 1);
+        Entry x{(uint32_t)idx[e], 0};
+        if constexpr (SHARED) x.bits = at < c.len ? bits[e] : 0;
+        return x;
+    }
+};
+
+// Which query this lane (and the three that share l % 16) has in tile mt of a
+// piece: 16 query heads of one row, or with blocks of rows the query heads of
+// block / mtiles rows of the block.
+struct AttnColumn {
+    bool has;
+    int rr, hq;  // row of the block, query head
+    __device__ __forceinline__ AttnColumn(const AttnShape& s, int block, int h, int mt) {
+        const int n = lane_id() & 15;
+        if (block == 1) {
+            rr = 0;
+            hq = h * s.group + 16 * mt + n;
+            has = 16 * mt + n < s.group;
+        } else {
+            const int rows = block / s.mtiles, r = n / s.group;
+            rr = mt * rows + r;
+            hq = h * s.group + n - r * s.group;
+            has = r < rows;
+        }
+    }
+    // The keys of a tile that the column's row stores, from each lane's bits.
+    __device__ __forceinline__ Seen seen(uint32_t bits) const {
+        uint32_t all = 0;
+#pragma unroll
+        for (int r = 0; r < kRowBlock; ++r) {
+            const uint32_t b = (uint32_t)__ballot(bits >> r & 1);
+            all = rr == r ? b : all;
+        }
+        return Seen::keys(all);
     }
 };
 

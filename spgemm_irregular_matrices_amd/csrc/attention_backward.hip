@@ -38,9 +38,9 @@ constexpr float kProbScale = std::is_same<T, _Float16>::value ? 0x1p14f : 1.f;
 // take the gathered rows as rows, dQ^T += K^T dS^T takes K as chunks: all come
 // from memory as chunks, a tile ahead (see there), and are staged in the
 // wavefront's own LDS for the other layout.
-template <class G, class T>
-__global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_grad_q(BackwardArgs a, int each,
-                                                               int64_t groups) {
+template <class G, class T, bool SHARED>
+__global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_grad_q(
+    BackwardArgs a, int each, int64_t groups) {
     __shared__ __align__(16) char stage[kWaves][2][G::KT * G::kRowBytes];
     const int lane = lane_id();
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -49,25 +49,26 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
     if (hm >= a.s.hkv * a.s.mtiles) return;
     const int64_t u0 = (block - hm * groups) * kWaves * each + w;
     const int h = hm / a.s.mtiles, mt = hm - h * a.s.mtiles;
-    const int n = lane & 15;
-    const int g = 16 * mt + n;
-    const bool has = g < a.s.group;
-    const int hq = h * a.s.group + g;
+    const int block_rows = SHARED ? kRowBlock : 1;
+    const AttnColumn me(a.s, block_rows, h, mt);
     const int row_bytes = a.s.dim * (int)sizeof(T);
+    const auto row_of = [&](int row) { return (int64_t)row * block_rows + me.rr; };
+    const auto here = [&](int64_t row) { return me.has && (!SHARED || row < a.nrows); };
     char* krows = stage[w][0];
     char* vrows = stage[w][1];
     const int rbase = G::row_base(0), cbase = G::chunk_base(0);
 
     PieceStream st(a.rows, u0, kWaves, each);
     for (uint64_t e = st.empty; e; e &= e - 1) {
-        if (!has) continue;
+        const int64_t row = row_of(st.row(__builtin_ctzll(e)));
+        if (!here(row)) continue;
         typename G::Acc zero;
         G::zero_acc(zero);
-        char* row = a.dq.base + st.row(__builtin_ctzll(e)) * a.dq.row + hq * a.dq.head;
+        char* dst = a.dq.base + row * a.dq.row + me.hq * a.dq.head;
 #pragma unroll
         for (int u = 0; u < G::U; ++u)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) G::store_out(zero, u, r, 0.f, row, row_bytes);
+            for (int r = 0; r < 4; ++r) G::store_out(zero, u, r, 0.f, dst, row_bytes);
     }
     if (!st.todo) return;
 
@@ -77,15 +78,15 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
     typename G::VBlock k[G::U], v[G::U];
     float lse = INFINITY;  // lanes without a head: weights 0
     const auto load_q = [&](int i) {
-        const int row = st.row(i);
+        const int64_t row = row_of(st.row(i));
         G::zero_row(q);
         G::zero_row(dout);
         G::zero_row(out);
-        if (has) {
-            G::load_row(a.q.base + row * a.q.row + hq * a.q.head, row_bytes, q);
-            G::load_row(a.dout.base + row * a.dout.row + hq * a.dout.head, row_bytes, dout);
-            G::load_row(a.out.base + row * a.out.row + hq * a.out.head, row_bytes, out);
-            lse = a.lse[(int64_t)row * a.s.hq + hq];
+        if (here(row)) {
+            G::load_row(a.q.base + row * a.q.row + me.hq * a.q.head, row_bytes, q);
+            G::load_row(a.dout.base + row * a.dout.row + me.hq * a.dout.head, row_bytes, dout);
+            G::load_row(a.out.base + row * a.out.row + me.hq * a.out.head, row_bytes, out);
+            lse = a.lse[row * a.s.hq + me.hq];
         }
     };
     const auto load = [&](typename G::VBlock (&x)[G::U], const char* base, uint32_t off,
@@ -103,13 +104,13 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
 
     PieceStream::Cursor cur, ahead;
     st.open(cur);
-    uint32_t id = st.id(cur, G::KT);
+    PieceStream::Entry now = st.entry<SHARED>(cur, G::KT), next;
     load_q(cur.i);
-    load_k(id);
-    load_v(id);
+    load_k(now.id);
+    load_v(now.id);
     ahead = cur;
     st.next(ahead, G::KT);
-    if (ahead.more) id = st.id(ahead, G::KT);
+    if (ahead.more) next = st.entry<SHARED>(ahead, G::KT);
 
     typename G::Acc o;
     G::zero_acc(o);
@@ -122,8 +123,8 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
         if (fresh) {
             delta = quad_sum(G::dot_lane(dout, out));
             lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
-            if (has && lane < 16 && st.lead(cur.i))
-                a.delta[(int64_t)st.row(cur.i) * a.s.hq + hq] = delta;
+            const int64_t row = row_of(st.row(cur.i));
+            if (here(row) && lane < 16 && st.lead(cur.i)) a.delta[row * a.s.hq + me.hq] = delta;
             fresh = false;
         }
         if (left < G::KT) G::clear_past(k, left);
@@ -131,10 +132,10 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
         G::stage_tile(krows, cbase, k);
         G::stage_tile(vrows, cbase, v);
         wave_lds_sync();
-        const uint32_t idn = id;
+        const PieceStream::Entry then = next;
         if (more) {
-            load_k(idn);
-            load_v(idn);
+            load_k(then.id);
+            load_v(then.id);
         }
         f32x4 s[G::KSUB], dp[G::KSUB];
 #pragma unroll
@@ -149,13 +150,19 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
         const PieceStream::Cursor after = ahead;
         if (more) {
             st.next(ahead, G::KT);
-            if (ahead.more) id = st.id(ahead, G::KT);
+            if (ahead.more) next = st.entry<SHARED>(ahead, G::KT);
+        }
+        const Seen seen = SHARED ? me.seen(now.bits) : Seen::first(left);
+        float wild = 0.f;  // a NaN where a key's row may not be finite (see k_attn_grad_kv)
+        if constexpr (SHARED) {
+#pragma unroll
+            for (int j = 0; j < G::VK; ++j) wild = fmaf(s[j >> 2][j & 3], 0.f, wild);
         }
         float ds[G::VK];
 #pragma unroll
         for (int j = 0; j < G::VK; ++j) {
             const float p = fast_exp2(fmaf(s[j >> 2][j & 3], a.s.c, -lse2));
-            ds[j] = G::key_of(j) < left ? p * (dp[j >> 2][j & 3] - delta) : 0.f;
+            ds[j] = seen.pick(j, p * (dp[j >> 2][j & 3] - delta), 0.f);
         }
         if constexpr (std::is_same<T, _Float16>::value) {
             float mx = 0.f;
@@ -173,20 +180,32 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
             typename G::VBlock x;
 #pragma unroll
             for (int j = 0; j < G::VK; ++j) G::staged_chunk(krows, cbase, 0, j, u, x.w[j]);
+            if constexpr (SHARED) {
+                if (__any(wild != 0.f))
+                    G::add_wild_keys(
+                        x, pr, u, row_bytes,
+                        [&](int key) {
+                            const uint32_t off = __shfl(now.id * a.k.unit, key, kWave);
+                            return kb + ((uint64_t)off << a.k.shift);
+                        },
+                        [&](int key) { return __shfl(now.bits, key, kWave) >> me.rr & 1; }, o);
+            }
             G::accumulate(x, pr, u, o);
         }
         if (last) {
             float f = a.s.scale;
             if constexpr (std::is_same<T, _Float16>::value) f /= hs.s;
-            const int row = st.row(cur.i), slot = st.slot(cur.i);
-            if (has && slot < 0) {
-                char* dst = a.dq.base + row * a.dq.row + hq * a.dq.head;
+            const int slot = st.slot(cur.i);
+            const int64_t row = row_of(st.row(cur.i));
+            if (here(row) && slot < 0) {
+                char* dst = a.dq.base + row * a.dq.row + me.hq * a.dq.head;
 #pragma unroll
                 for (int u = 0; u < G::U; ++u)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) G::store_out(o, u, r, f, dst, row_bytes);
-            } else if (has) {
-                float* dst = a.part_q + ((int64_t)slot * a.s.hq + hq) * a.s.dim;
+            } else if (here(row)) {
+                float* dst =
+                    a.part_q + (((int64_t)slot * block_rows + me.rr) * a.s.hq + me.hq) * a.s.dim;
 #pragma unroll
                 for (int u = 0; u < G::U; ++u)
 #pragma unroll
@@ -198,6 +217,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
             fresh = true;
         }
         cur = after;
+        now = then;
     }
 }
 
@@ -510,25 +530,25 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 1) void k_att
 }
 
 // The sums of the rows, and of the blocks of columns, of more than one piece,
-// in the pieces' order: one wavefront per row and head of dq, and per
-// (column, output) of a block and head of dk and dv. A piece's results lie
-// side by side, `lines` of dim values per head (1, or 2 per column).
+// in the pieces' order: one wavefront per row and head of dq, and per head,
+// column and output of dk and dv. A piece's results lie side by side.
 template <class T>
 __global__ __launch_bounds__(kWaves* kWave) void k_attn_join_sum(BackwardArgs a) {
     const int lane = lane_id();
     int64_t unit = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
-    const int64_t row_units = a.rows.nsplits * a.s.hq;
+    const int64_t row_units = a.rows.nsplits * a.rows.block * a.s.hq;
     const bool col_side = unit >= row_units;
     if (col_side) unit -= row_units;
     const AttnSide& side = col_side ? a.cols : a.rows;
-    const int heads = col_side ? a.s.hkv : a.s.hq, lines = col_side ? 2 * kColBlock : 1;
-    const int64_t per = (int64_t)heads * lines;
+    const int64_t per = col_side ? (int64_t)a.s.hkv * 2 * kColBlock : (int64_t)side.block * a.s.hq;
     if (unit >= side.nsplits * per) return;
     const int64_t sp = unit / per, hl = unit - sp * per;
-    const int h = (int)(hl / lines), line = (int)(hl - (int64_t)h * lines);
     const AttnSplit s = side.splits[sp];
-    const int64_t row = col_side ? (int64_t)s.row * kColBlock + line / 2 : s.row;
-    if (col_side && row >= a.ncols) return;
+    const int line = (int)(hl % (2 * kColBlock));
+    const int h = (int)(col_side ? hl / (2 * kColBlock) : hl % a.s.hq);
+    const int64_t row = col_side ? (int64_t)s.row * kColBlock + line / 2
+                                 : (int64_t)s.row * side.block + hl / a.s.hq;
+    if (row >= (col_side ? a.ncols : a.nrows)) return;
     const float* part = (col_side ? a.part_kv : a.part_q) + ((int64_t)s.slot * per + hl) * a.s.dim;
     float x[SPGEMM_ATTENTION_MAX_HEAD_DIM / kWave] = {};
     for (int i = 0; i < s.count; ++i) {
@@ -554,7 +574,8 @@ void attention_backward(const BackwardArgs& a, hipStream_t st) {
             const int64_t heads = (int64_t)a.s.hkv * a.s.mtiles;
             const int each = pieces_per_wave(a.rows.npieces * heads);
             const int64_t groups = ceil_div(a.rows.npieces, kWaves * each);
-            auto run = k_attn_grad_q<typename Tag::Geo, T>;
+            auto run = a.rows.block > 1 ? k_attn_grad_q<typename Tag::Geo, T, true>
+                                        : k_attn_grad_q<typename Tag::Geo, T, false>;
             hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(groups * heads))), dim3(kWaves * kWave),
                                0, st, a, each, groups);
             SG_LAUNCH_CHECK();
@@ -566,7 +587,7 @@ void attention_backward(const BackwardArgs& a, hipStream_t st) {
                                a);
             SG_LAUNCH_CHECK();
         }
-        const int64_t joins = a.rows.nsplits * a.s.hq + a.cols.nsplits * a.s.hkv * 2 * kColBlock;
+        const int64_t joins = a.rows.nsplits * a.rows.block * a.s.hq + a.cols.nsplits * a.s.hkv * 2 * kColBlock;
         if (joins > 0) {
             hipLaunchKernelGGL(k_attn_join_sum<T>, dim3(grid_1d(ceil_div(joins, kWaves))),
                                dim3(kWaves * kWave), 0, st, a);

@@ -15,7 +15,9 @@ constexpr int kWaves = 4;
 // (a lane to a row) each lane's 16 bytes are an access of their own to the
 // first-level cache, four times as many, and that rate is what bound this
 // kernel. K takes the other layout through the wavefront's own LDS.
-template <class G, class T>
+// With SHARED a piece belongs to a block of rows: the tile's queries are heads
+// of several rows, and each sees the keys that its row stores.
+template <class G, class T, bool SHARED>
 __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_forward(ForwardArgs a, int each,
                                                                 int64_t groups) {
     __shared__ __align__(16) char stage[kWaves][G::KT * G::kRowBytes];
@@ -27,24 +29,24 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
     if (hm >= a.s.hkv * a.s.mtiles) return;
     const int64_t u0 = (block - hm * groups) * kWaves * each + w;
     const int h = hm / a.s.mtiles, mt = hm - h * a.s.mtiles;
-    const int n = lane & 15;  // this lane's query head in the tile
-    const int g = 16 * mt + n;
-    const bool has = g < a.s.group;
-    const int hq = h * a.s.group + g;
+    const int block_rows = SHARED ? kRowBlock : 1;
+    const AttnColumn me(a.s, block_rows, h, mt);
     const int row_bytes = a.s.dim * (int)sizeof(T);
+    const auto row_of = [&](int row) { return (int64_t)row * block_rows + me.rr; };
+    const auto here = [&](int64_t row) { return me.has && (!SHARED || row < a.nrows); };
 
     PieceStream st(a.side, u0, kWaves, each);
     for (uint64_t e = st.empty; e; e &= e - 1) {
-        const int row = st.row(__builtin_ctzll(e));
-        if (!has) continue;
+        const int64_t row = row_of(st.row(__builtin_ctzll(e)));
+        if (!here(row)) continue;
         typename G::Acc zero;
         G::zero_acc(zero);
-        char* out = a.out.base + row * a.out.row + hq * a.out.head;
+        char* out = a.out.base + row * a.out.row + me.hq * a.out.head;
 #pragma unroll
         for (int u = 0; u < G::U; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r) G::store_out(zero, u, r, 0.f, out, row_bytes);
-        if (a.lse && lane < 16) a.lse[(int64_t)row * a.s.hq + hq] = -INFINITY;
+        if (a.lse && lane < 16) a.lse[row * a.s.hq + me.hq] = -INFINITY;
     }
     if (!st.todo) return;
 
@@ -55,8 +57,8 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
     typename G::VBlock k[G::U], v[G::U];
     const auto load_q = [&](int i) {
         G::zero_row(q);
-        if (has)
-            G::load_row(a.q.base + st.row(i) * a.q.row + hq * a.q.head, row_bytes, q);
+        const int64_t row = row_of(st.row(i));
+        if (here(row)) G::load_row(a.q.base + row * a.q.row + me.hq * a.q.head, row_bytes, q);
         G::sign_row(q, a.s.c);
     };
     const auto load = [&](typename G::VBlock (&x)[G::U], const char* base, uint32_t off,
@@ -72,15 +74,15 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
     const auto load_k = [&](uint32_t id) { load(k, kb, id * a.k.unit, a.k.shift); };
     const auto load_v = [&](uint32_t id) { load(v, vb, id * a.v.unit, a.v.shift); };
 
-    PieceStream::Cursor cur, ahead;  // ahead: the tile whose indices are loaded
+    PieceStream::Cursor cur, ahead;  // ahead: the tile whose entries are loaded
     st.open(cur);
-    uint32_t id = st.id(cur, G::KT);
+    PieceStream::Entry now = st.entry<SHARED>(cur, G::KT), next;
     load_q(cur.i);
-    load_k(id);
-    load_v(id);
+    load_k(now.id);
+    load_v(now.id);
     ahead = cur;
     st.next(ahead, G::KT);
-    if (ahead.more) id = st.id(ahead, G::KT);
+    if (ahead.more) next = st.entry<SHARED>(ahead, G::KT);
 
     typename G::Acc o;
     G::zero_acc(o);
@@ -91,8 +93,8 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
         wave_lds_sync();
         G::stage_tile(krows, cbase, k);
         wave_lds_sync();
-        const uint32_t idn = id;
-        if (more) load_k(idn);
+        const PieceStream::Entry then = next;
+        if (more) load_k(then.id);
         f32x4 s[G::KSUB];
 #pragma unroll
         for (int b = 0; b < G::KSUB; ++b) {
@@ -104,27 +106,46 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
         const PieceStream::Cursor after = ahead;
         if (more) {
             st.next(ahead, G::KT);
-            if (ahead.more) id = st.id(ahead, G::KT);
+            if (ahead.more) next = st.entry<SHARED>(ahead, G::KT);
         }
         typename G::Probs pr;
-        sm.step(s, left, a.s.mag, o, pr);
+        const Seen seen = SHARED ? me.seen(now.bits) : Seen::first(left);
+        sm.step(s, seen, a.s.mag, o, pr);
         if (left < G::KT) G::clear_past(v, left);
 #pragma unroll
-        for (int u = 0; u < G::U; ++u) G::accumulate(v[u], pr, u, o);
-        if (more) load_v(idn);
+        for (int u = 0; u < G::U; ++u) {
+            if constexpr (SHARED) {
+                // a key that a row does not store must not reach it as 0
+                // times an infinity or a NaN
+                float z = 0.f;
+#pragma unroll
+                for (int j = 0; j < G::VK; ++j) z = G::chunk_zero(v[u].w[j], z);
+                if (__any(z != 0.f))
+                    G::add_wild_keys(
+                        v[u], pr, u, row_bytes,
+                        [&](int key) {
+                            const uint32_t off = __shfl(now.id * a.v.unit, key, kWave);
+                            return vb + ((uint64_t)off << a.v.shift);
+                        },
+                        [&](int key) { return __shfl(now.bits, key, kWave) >> me.rr & 1; }, o);
+            }
+            G::accumulate(v[u], pr, u, o);
+        }
+        if (more) load_v(then.id);
         if (last) {
             sm.finish();
-            const int row = st.row(cur.i), slot = st.slot(cur.i);
-            if (has && slot < 0) {
+            const int slot = st.slot(cur.i);
+            const int64_t row = row_of(st.row(cur.i));
+            if (here(row) && slot < 0) {
                 const float f = sm.factor();
-                char* out = a.out.base + row * a.out.row + hq * a.out.head;
+                char* out = a.out.base + row * a.out.row + me.hq * a.out.head;
 #pragma unroll
                 for (int u = 0; u < G::U; ++u)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) G::store_out(o, u, r, f, out, row_bytes);
-                if (a.lse && lane < 16) a.lse[(int64_t)row * a.s.hq + hq] = sm.lse();
-            } else if (has) {
-                const int64_t at = (int64_t)slot * a.s.hq + hq;
+                if (a.lse && lane < 16) a.lse[row * a.s.hq + me.hq] = sm.lse();
+            } else if (here(row)) {
+                const int64_t at = ((int64_t)slot * block_rows + me.rr) * a.s.hq + me.hq;
                 float* dst = a.part + at * a.s.dim;
 #pragma unroll
                 for (int u = 0; u < G::U; ++u)
@@ -140,6 +161,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
             sm = Softmax<G, T>();
         }
         cur = after;
+        now = then;
     }
 }
 
@@ -149,19 +171,23 @@ template <class T>
 __global__ __launch_bounds__(kWaves* kWave) void k_attn_join(ForwardArgs a) {
     const int lane = lane_id();
     const int64_t unit = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
-    if (unit >= a.side.nsplits * a.s.hq) return;
-    const int64_t sp = unit / a.s.hq;
-    const int hq = (int)(unit - sp * a.s.hq);
+    const int64_t lines = (int64_t)a.side.block * a.s.hq;
+    if (unit >= a.side.nsplits * lines) return;
+    const int64_t sp = unit / lines, line = unit - sp * lines;
     const AttnSplit s = a.side.splits[sp];
+    const int64_t row = (int64_t)s.row * a.side.block + line / a.s.hq;
+    const int hq = (int)(line % a.s.hq);
+    if (row >= a.nrows) return;
+    const int64_t first = (int64_t)s.slot * lines + line;
     float m = -INFINITY;
     for (int i = lane; i < s.count; i += kWave)
-        m = fmaxf(m, a.part_ml[2 * ((int64_t)(s.slot + i) * a.s.hq + hq)]);
+        m = fmaxf(m, a.part_ml[2 * (first + i * lines)]);
 #pragma unroll
     for (int d = kWave / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, kWave));
     const float ms = m == -INFINITY ? 0.f : m;
     float l = 0.f, o[SPGEMM_ATTENTION_MAX_HEAD_DIM / kWave] = {};
     for (int i = 0; i < s.count; ++i) {
-        const int64_t at = (int64_t)(s.slot + i) * a.s.hq + hq;
+        const int64_t at = first + i * lines;
         const float w = fast_exp2(a.part_ml[2 * at] - ms);
         l += a.part_ml[2 * at + 1] * w;
         const float* src = a.part + at * a.s.dim;
@@ -170,12 +196,12 @@ __global__ __launch_bounds__(kWaves* kWave) void k_attn_join(ForwardArgs a) {
             if (j * kWave + lane < a.s.dim) o[j] += src[j * kWave + lane] * w;
     }
     const float f = l == 0.f ? 0.f : 1.f / l;
-    T* dst = reinterpret_cast<T*>(a.out.base + s.row * a.out.row + hq * a.out.head);
+    T* dst = reinterpret_cast<T*>(a.out.base + row * a.out.row + hq * a.out.head);
 #pragma unroll
     for (int j = 0; j < SPGEMM_ATTENTION_MAX_HEAD_DIM / kWave; ++j)
         if (j * kWave + lane < a.s.dim) dst[j * kWave + lane] = (T)(o[j] * f);
     if (a.lse && lane == 0)
-        a.lse[(int64_t)s.row * a.s.hq + hq] =
+        a.lse[row * a.s.hq + hq] =
             l == 0.f ? -INFINITY : (m - kProbShift<T> + fast_log2(l)) * kLn2;
 }
 
@@ -188,13 +214,14 @@ void attention_forward(const ForwardArgs& a, hipStream_t st) {
     const int64_t groups = ceil_div(a.side.npieces, kWaves * each);
     with_type(a.s.type, a.s.dim, [&](auto tag) {
         using Tag = decltype(tag);
-        auto run = k_attn_forward<typename Tag::Geo, typename Tag::Elem>;
+        auto run = a.side.block > 1 ? k_attn_forward<typename Tag::Geo, typename Tag::Elem, true>
+                                    : k_attn_forward<typename Tag::Geo, typename Tag::Elem, false>;
         hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(groups * heads))), dim3(kWaves * kWave), 0,
                            st, a, each, groups);
         SG_LAUNCH_CHECK();
         if (a.side.nsplits > 0) {
             hipLaunchKernelGGL(k_attn_join<typename Tag::Elem>,
-                               dim3(grid_1d(ceil_div(a.side.nsplits * a.s.hq, kWaves))),
+                               dim3(grid_1d(ceil_div(a.side.nsplits * a.side.block * a.s.hq, kWaves))),
                                dim3(kWaves * kWave), 0, st, a);
             SG_LAUNCH_CHECK();
         }

@@ -234,32 +234,26 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
             sc[b] = G::dot(x, q, f32x4{0, 0, 0, 0});
         }
         typename G::Probs pr;
-        sm.step(sc, min(left, job.before + r.t - t0), a.s.mag, o, pr);
+        sm.step(sc, Seen::first(min(left, job.before + r.t - t0)), a.s.mag, o, pr);
         if (left < G::KT) G::clear_past(v, left);
         const bool crosses = t0 + G::KT > job.before + lo;  // some row may not see some key
 #pragma unroll
         for (int u = 0; u < G::U; ++u) {
             if (crosses) {
                 // a key that a row does not see must not reach it as 0 times
-                // an infinity or a NaN: such keys count as 0 here, and are
-                // added on their own in the lanes that see them
-                uint32_t keys = G::wild_keys(v[u]);
-                if (keys) {
+                // an infinity or a NaN
+                float z = 0.f;
 #pragma unroll
-                    for (int j = 0; j < G::VK; ++j)
-                        if (keys >> G::key_of(j) & 1)
-#pragma unroll
-                            for (int i = 0; i < G::VW; ++i) v[u].w[j][i] = 0;
-                }
-#pragma unroll 1
-                for (; keys; keys &= keys - 1) {
-                    const int key = __builtin_ctz(keys);
-                    const uint32_t off =
-                        __shfl(here.id * a.v_page + here.slot * a.v_slot, key, kWave);
-                    const float p = G::prob_of(pr, key);
-                    if (t0 + key < job.before + r.t)
-                        G::add_wild(vb + ((uint64_t)off << a.v_shift), p, u, row_bytes, o);
-                }
+                for (int j = 0; j < G::VK; ++j) z = G::chunk_zero(v[u].w[j], z);
+                if (__any(z != 0.f))
+                    G::add_wild_keys(
+                        v[u], pr, u, row_bytes,
+                        [&](int key) {
+                            const uint32_t off =
+                                __shfl(here.id * a.v_page + here.slot * a.v_slot, key, kWave);
+                            return vb + ((uint64_t)off << a.v_shift);
+                        },
+                        [&](int key) { return t0 + key < job.before + r.t; }, o);
             }
             G::accumulate(v[u], pr, u, o);
         }
@@ -445,8 +439,8 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
             typename G::Probs pr[QB];
 #pragma unroll
             for (int x = 0; x < QB; ++x)
-                sm[x].step(sc[x], min(job.k1, job.before + r[x].t) - t, a.s.mag,
-                           o[x], pr[x]);
+                sm[x].step(sc[x], Seen::first(min(job.k1, job.before + r[x].t) - t), a.s.mag, o[x],
+                           pr[x]);
 #pragma unroll
             for (int b = 0; b < G::NB; ++b) {
                 const u32x4 v = G::value_frag(rows[1], vbase, b);

@@ -13,7 +13,10 @@ struct spgemm_attention_plan_s {
     int device = 0;
     int64_t nrows = 0, ncols = 0, nnz = 0;
     bool backward = false;
-    AttnSide rows, cols;
+    AttnSide rows;    // single rows
+    AttnSide blocks;  // blocks of rows, if built (n > 0)
+    bool overlap = false;  // the blocks' entries are at most half of the rows'
+    AttnSide cols;
     Arena ar;  // pieces, splits and entries of both sides; never changed after creation
 };
 
@@ -74,12 +77,13 @@ __global__ void k_fill_pieces(RowPieces rows, int64_t n, const int64_t* piece0,
     if (count > 1 && k == 0) splits[split0[row]] = {(int32_t)row, p.slot, (int32_t)count, 0};
 }
 
-__global__ void k_entry_rows(const int64_t* rp, int64_t n, int64_t nnz, int32_t* row,
-                             int32_t* entry) {
+__global__ void k_entry_rows(const int64_t* rp, int64_t n, int64_t nnz, int32_t* row) {
     const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (e >= nnz) return;
-    row[e] = (int32_t)upper_index(rp, int64_t(0), n, e);
-    entry[e] = (int32_t)e;
+    if (e < nnz) row[e] = (int32_t)upper_index(rp, int64_t(0), n, e);
+}
+__global__ void k_iota(int32_t* x, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < n) x[i] = (int32_t)i;
 }
 __global__ void k_gather(const int32_t* src, const int32_t* perm, int64_t n, int32_t* dst) {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -128,6 +132,64 @@ __global__ void k_block_groups(const int32_t* col, const int32_t* entry, int64_t
     first[b] = group[lo];
 }
 
+// First entry from lo on, before hi, of a row with ascending columns that is
+// not below c.
+__device__ __forceinline__ int64_t lower_index(const int32_t* col, int64_t lo, int64_t hi,
+                                               int32_t c) {
+    while (lo < hi) {
+        const int64_t mid = lo + ((hi - lo) >> 1);
+        if (col[mid] < c) lo = mid + 1; else hi = mid;
+    }
+    return lo;
+}
+
+// lead[e] = 1 if no earlier row of entry e's block stores its column; *flag is
+// set where a row's columns do not ascend.
+__global__ void k_block_leaders(const int64_t* rp, const int32_t* col, const int32_t* row,
+                                int64_t nnz, int32_t* lead, int* flag) {
+    const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (e >= nnz) return;
+    const int32_t r = row[e], c = col[e];
+    if (e > rp[r] && col[e - 1] >= c) *flag = 1;  // (every writer writes the same)
+    int32_t is = 1;
+    for (int32_t x = r / kRowBlock * kRowBlock; x < r && is; ++x) {
+        const int64_t end = rp[x + 1], at = lower_index(col, rp[x], end, c);
+        if (at < end && col[at] == c) is = 0;
+    }
+    lead[e] = is;
+}
+// The blocks' entries in the order of their columns. before[e]: leaders among
+// the entries below e; a leader's place is its block's first plus the number
+// of the block's leaders with smaller columns.
+__global__ void k_block_entries(const int64_t* rp, int64_t n, const int32_t* col,
+                                const int32_t* row, int64_t nnz, const int32_t* lead,
+                                const int64_t* before, int32_t* idx, uint16_t* bits) {
+    const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (e >= nnz || !lead[e]) return;
+    const int32_t c = col[e];
+    const int64_t r0 = row[e] / kRowBlock * kRowBlock;
+    int64_t place = before[rp[r0]];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kRowBlock; ++i) {
+        if (r0 + i >= n) break;
+        const int64_t b = rp[r0 + i], end = rp[r0 + i + 1], at = lower_index(col, b, end, c);
+        place += before[at] - before[b];
+        if (at < end && col[at] == c) m |= 1u << i;
+    }
+    idx[place] = c;
+    bits[place] = (uint16_t)m;
+}
+__global__ void k_block_starts(const int64_t* rp, int64_t n, const int64_t* before, int64_t nblocks,
+                               int64_t* first) {
+    const int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (b <= nblocks) first[b] = before[rp[b * kRowBlock < n ? b * kRowBlock : n]];
+}
+struct LoadI32 {
+    const int32_t* p;
+    __device__ int64_t operator()(int64_t i) const { return p[i]; }
+};
+
 AttnSide make_side(const char* name, const int64_t* rp, int64_t n, int64_t nnz, PieceRule rule,
                    const int32_t* idx, Arena& keep, Arena& tmp, hipStream_t st) {
     AttnSide s;
@@ -163,6 +225,88 @@ AttnSide make_side(const char* name, const int64_t* rp, int64_t n, int64_t nnz, 
     return s;
 }
 
+// Blocks of 4 rows, where they serve: the rows are short (they share tiles) or
+// store the same columns (they share keys), and their columns ascend (else
+// the blocks stay unbuilt and single rows do).
+bool blocks_serve(int64_t n, int64_t nnz, int64_t entries) {
+    return nnz < 64 * n || entries <= nnz / 4 * 3;
+}
+void build_blocks(spgemm_attention_plan p, const DevCSR& m, const int32_t* col, const int32_t* row,
+                  Arena& tmp, hipStream_t st) {
+    const unsigned g = grid_1d(ceil_div(m.nnz, 256));
+    const int64_t nblocks = ceil_div(m.n, kRowBlock);
+    int32_t* lead = tmp.get<int32_t>("lead", (size_t)m.nnz);
+    int64_t* before = tmp.get<int64_t>("before", (size_t)m.nnz + 1);
+    int* flag = tmp.get<int>("flag", 1);
+    fill<int>(flag, 1, 0, st);
+    hipLaunchKernelGGL(k_block_leaders, dim3(g), dim3(256), 0, st, m.rp, col, row, m.nnz, lead,
+                       flag);
+    SG_LAUNCH_CHECK();
+    scan_exclusive(LoadI32{lead}, m.nnz, before, tmp, st);
+    int unsorted = 0;
+    int64_t entries = 0;
+    SG_HIP(hipMemcpyAsync(&unsorted, flag, sizeof(int), hipMemcpyDeviceToHost, st));
+    SG_HIP(hipMemcpyAsync(&entries, before + m.nnz, 8, hipMemcpyDeviceToHost, st));
+    SG_HIP(hipStreamSynchronize(st));
+    if (unsorted || !blocks_serve(m.n, m.nnz, entries)) return;
+    int32_t* idx = p->ar.get<int32_t>("block_idx", (size_t)entries);
+    uint16_t* bits = p->ar.get<uint16_t>("block_bits", (size_t)entries);
+    int64_t* first = tmp.get<int64_t>("block_first", (size_t)nblocks + 1);
+    hipLaunchKernelGGL(k_block_entries, dim3(g), dim3(256), 0, st, m.rp, m.n, col, row, m.nnz, lead,
+                       before, idx, bits);
+    SG_LAUNCH_CHECK();
+    hipLaunchKernelGGL(k_block_starts, dim3(grid_1d(ceil_div(nblocks + 1, 256))), dim3(256), 0, st,
+                       m.rp, m.n, before, nblocks, first);
+    SG_LAUNCH_CHECK();
+    p->blocks = make_side("blocks", first, nblocks, entries, kRowPieces, idx, p->ar, tmp, st);
+    p->blocks.bits = bits;
+    p->blocks.block = kRowBlock;
+    p->overlap = entries <= m.nnz / 2;
+}
+
+// The transposed mask by blocks of columns.
+void build_cols(spgemm_attention_plan p, const DevCSR& m, const int32_t* col, const int32_t* row,
+                Arena& tmp, hipStream_t st) {
+    const int64_t nblocks = ceil_div(m.m, kColBlock);
+    int64_t* first = tmp.get<int64_t>("first", (size_t)nblocks + 1);
+    int32_t* gidx = p->ar.get<int32_t>("groups", (size_t)m.nnz);
+    uint16_t* gbits = p->ar.get<uint16_t>("bits", (size_t)m.nnz);
+    int64_t ngroups = 0;
+    if (m.nnz > 0) {
+        // a stable radix sort of the entries by column block, 4 bits a pass:
+        // rows ascend within a block, so its sums have one order
+        const unsigned g = grid_1d(ceil_div(m.nnz, 256));
+        int32_t* cur = tmp.get<int32_t>("cur", (size_t)m.nnz);
+        int32_t* next = tmp.get<int32_t>("next", (size_t)m.nnz);
+        int32_t* perm = tmp.get<int32_t>("perm", (size_t)m.nnz);
+        int64_t* bins = tmp.get<int64_t>("bins", 17);
+        int64_t* group = tmp.get<int64_t>("group", (size_t)m.nnz + 1);
+        hipLaunchKernelGGL(k_iota, dim3(g), dim3(256), 0, st, cur, m.nnz);
+        SG_LAUNCH_CHECK();
+        for (int shift = ilog2(kColBlock); shift < 31 && (m.m - 1) >> shift > 0; shift += 4) {
+            partition(BlockDigit{col, cur, shift}, m.nnz, 16, perm, nullptr, bins, tmp, st);
+            hipLaunchKernelGGL(k_gather, dim3(g), dim3(256), 0, st, cur, perm, m.nnz, next);
+            SG_LAUNCH_CHECK();
+            std::swap(cur, next);
+        }
+        const GroupStart start{col, row, cur};
+        scan_exclusive(start, m.nnz, group, tmp, st);
+        hipLaunchKernelGGL(k_fill_groups, dim3(g), dim3(256), 0, st, start, m.nnz, group, gidx,
+                           gbits);
+        SG_LAUNCH_CHECK();
+        hipLaunchKernelGGL(k_block_groups, dim3(grid_1d(ceil_div(nblocks + 1, 256))), dim3(256), 0,
+                           st, col, cur, m.nnz, group, nblocks, first);
+        SG_LAUNCH_CHECK();
+        SG_HIP(hipMemcpyAsync(&ngroups, group + m.nnz, 8, hipMemcpyDeviceToHost, st));
+        SG_HIP(hipStreamSynchronize(st));
+    } else {
+        fill<int64_t>(first, nblocks + 1, 0, st);
+    }
+    p->cols = make_side("cols", first, nblocks, ngroups, kBlockPieces, gidx, p->ar, tmp, st);
+    p->cols.bits = gbits;
+    p->cols.block = kColBlock;
+}
+
 int build_plan(spgemm_attention_plan p, const spgemm_csr* mask, bool backward, hipStream_t st) {
     Arena tmp;
     DevCSR m;
@@ -184,49 +328,25 @@ int build_plan(spgemm_attention_plan p, const spgemm_csr* mask, bool backward, h
     p->backward = backward;
     int32_t* col = p->ar.get<int32_t>("col", (size_t)m.nnz);
     copy<int32_t>(col, m.col, m.nnz, st);
-    p->rows = make_side("rows", m.rp, m.n, m.nnz, kRowPieces, col, p->ar, tmp, st);
-    if (backward) {
-        const int64_t nblocks = ceil_div(m.m, kColBlock);
-        int64_t* first = tmp.get<int64_t>("first", (size_t)nblocks + 1);
-        int32_t* gidx = p->ar.get<int32_t>("groups", (size_t)m.nnz);
-        uint16_t* gbits = p->ar.get<uint16_t>("bits", (size_t)m.nnz);
-        int64_t ngroups = 0;
-        if (m.nnz > 0) {
-            // a stable radix sort of the entries by column block, 4 bits a
-            // pass: rows ascend within a block, so its sums have one order
-            const unsigned g = grid_1d(ceil_div(m.nnz, 256));
-            int32_t* row = tmp.get<int32_t>("row", (size_t)m.nnz);
-            int32_t* cur = tmp.get<int32_t>("cur", (size_t)m.nnz);
-            int32_t* next = tmp.get<int32_t>("next", (size_t)m.nnz);
-            int32_t* perm = tmp.get<int32_t>("perm", (size_t)m.nnz);
-            int64_t* bins = tmp.get<int64_t>("bins", 17);
-            int64_t* group = tmp.get<int64_t>("group", (size_t)m.nnz + 1);
-            hipLaunchKernelGGL(k_entry_rows, dim3(g), dim3(256), 0, st, m.rp, m.n, m.nnz, row, cur);
-            SG_LAUNCH_CHECK();
-            for (int shift = ilog2(kColBlock); shift < 31 && (m.m - 1) >> shift > 0; shift += 4) {
-                partition(BlockDigit{col, cur, shift}, m.nnz, 16, perm, nullptr, bins, tmp, st);
-                hipLaunchKernelGGL(k_gather, dim3(g), dim3(256), 0, st, cur, perm, m.nnz, next);
-                SG_LAUNCH_CHECK();
-                std::swap(cur, next);
-            }
-            const GroupStart start{col, row, cur};
-            scan_exclusive(start, m.nnz, group, tmp, st);
-            hipLaunchKernelGGL(k_fill_groups, dim3(g), dim3(256), 0, st, start, m.nnz, group, gidx,
-                               gbits);
-            SG_LAUNCH_CHECK();
-            hipLaunchKernelGGL(k_block_groups, dim3(grid_1d(ceil_div(nblocks + 1, 256))), dim3(256),
-                               0, st, col, cur, m.nnz, group, nblocks, first);
-            SG_LAUNCH_CHECK();
-            SG_HIP(hipMemcpyAsync(&ngroups, group + m.nnz, 8, hipMemcpyDeviceToHost, st));
-            SG_HIP(hipStreamSynchronize(st));
-        } else {
-            fill<int64_t>(first, nblocks + 1, 0, st);
-        }
-        p->cols = make_side("cols", first, nblocks, ngroups, kBlockPieces, gidx, p->ar, tmp, st);
-        p->cols.bits = gbits;
+    int32_t* row = tmp.get<int32_t>("row", (size_t)m.nnz);
+    if (m.nnz > 0) {
+        hipLaunchKernelGGL(k_entry_rows, dim3(grid_1d(ceil_div(m.nnz, 256))), dim3(256), 0, st,
+                           m.rp, m.n, m.nnz, row);
+        SG_LAUNCH_CHECK();
     }
+    p->rows = make_side("rows", m.rp, m.n, m.nnz, kRowPieces, col, p->ar, tmp, st);
+    if (m.nnz > 0) build_blocks(p, m, col, row, tmp, st);
+    if (backward) build_cols(p, m, col, row, tmp, st);
     SG_HIP(hipStreamSynchronize(st));  // before the temporary buffers go
     return SPGEMM_OK;
+}
+
+// The rows' side for a call, and its tiles of 16 queries: blocks of 4 rows
+// where their queries fill one tile, or two that mostly see the same keys.
+const AttnSide& row_side(spgemm_attention_plan p, AttnShape* s) {
+    const bool blocks = p->blocks.n > 0 && (s->group <= 4 || (s->group <= 8 && p->overlap));
+    s->mtiles = blocks ? (s->group <= 4 ? 1 : 2) : (s->group + 15) / 16;
+    return blocks ? p->blocks : p->rows;
 }
 
 // ---------------------------------------------------------------- checks
@@ -250,7 +370,6 @@ AttnShape make_shape(const spgemm_attention_desc* d) {
     s.hkv = d->heads_kv;
     s.group = s.hq / s.hkv;
     s.dim = d->head_dim;
-    s.mtiles = (s.group + 15) / 16;
     s.scale = (float)d->scale;
     s.c = (float)(d->scale * 1.4426950408889634);
     s.mag = s.c == 0.f ? 1.f : std::fabs(s.c);
@@ -322,16 +441,18 @@ struct Carver {
     }
 };
 
-int64_t carve_forward(spgemm_attention_plan p, const AttnShape& s, void* ws, ForwardArgs* a) {
+int64_t carve_forward(spgemm_attention_plan p, AttnShape s, void* ws, ForwardArgs* a) {
+    const AttnSide& side = row_side(p, &s);
     Carver c{static_cast<char*>(ws)};
-    a->part = c.take((__int128)p->rows.nslots * s.hq * s.dim);
-    a->part_ml = c.take((__int128)p->rows.nslots * s.hq * 2);
+    a->part = c.take((__int128)side.nslots * side.block * s.hq * s.dim);
+    a->part_ml = c.take((__int128)side.nslots * side.block * s.hq * 2);
     return c.used;
 }
-int64_t carve_backward(spgemm_attention_plan p, const AttnShape& s, void* ws, BackwardArgs* a) {
+int64_t carve_backward(spgemm_attention_plan p, AttnShape s, void* ws, BackwardArgs* a) {
+    const AttnSide& side = row_side(p, &s);
     Carver c{static_cast<char*>(ws)};
     a->delta = c.take((__int128)p->nrows * s.hq);
-    a->part_q = c.take((__int128)p->rows.nslots * s.hq * s.dim);
+    a->part_q = c.take((__int128)side.nslots * side.block * s.hq * s.dim);
     a->part_kv = c.take((__int128)p->cols.nslots * s.hkv * kColBlock * 2 * s.dim);
     return c.used;
 }
@@ -463,7 +584,8 @@ SPGEMM_API int spgemm_attention_forward(spgemm_attention_plan p, const spgemm_at
     return guarded([&]() -> int {
         ForwardArgs a;
         a.s = make_shape(desc);
-        a.side = p->rows;
+        a.side = row_side(p, &a.s);
+        a.nrows = p->nrows;
         AttnRows kr, vr;
         if (!rows_valid(q, p->nrows, a.s.hq, desc, false, &a.q) ||
             !rows_valid(k, p->ncols, a.s.hkv, desc, false, &kr) ||
@@ -493,7 +615,8 @@ SPGEMM_API int spgemm_attention_backward(spgemm_attention_plan p,
     return guarded([&]() -> int {
         BackwardArgs a;
         a.s = make_shape(desc);
-        a.rows = p->rows;
+        a.rows = row_side(p, &a.s);
+        a.nrows = p->nrows;
         a.cols = p->cols;
         a.ncols = p->ncols;
         if (!rows_valid(q, p->nrows, a.s.hq, desc, false, &a.q) ||

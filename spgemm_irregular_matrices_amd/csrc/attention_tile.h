@@ -340,6 +340,43 @@ struct Tile {
             return __builtin_bit_cast(float, w);
         }
     }
+    // O^T += V^T P^T for chunk u where v holds infinities or NaN and not every
+    // query sees every key: such keys count as 0 in the product and are added
+    // on their own in the lanes whose query sees them. row(key): a pointer to
+    // the key's row, sees(key): whether this lane's query does.
+    template <class Row, class Sees>
+    static __device__ __forceinline__ void add_wild_keys(VBlock& v, const Probs& p, int u,
+                                                         int row_bytes, Row&& row, Sees&& sees,
+                                                         Acc& a) {
+        uint32_t keys = wild_keys(v);
+#pragma unroll
+        for (int j = 0; j < VK; ++j)
+            if (keys >> key_of(j) & 1)
+#pragma unroll
+                for (int i = 0; i < VW; ++i) v.w[j][i] = 0;
+#pragma unroll 1
+        for (; keys; keys &= keys - 1) {
+            const int key = __builtin_ctz(keys);
+            const char* at = row(key);
+            const float w = prob_of(p, key);
+            if (sees(key)) add_wild(at, w, u, row_bytes, a);
+        }
+    }
+    // Not 0 (a NaN) if the chunk holds an infinity or a NaN: 0 times all of it.
+    static __device__ __forceinline__ float chunk_zero(const uint32_t (&w)[VW], float z) {
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+            if constexpr (std::is_same<T, __bf16>::value)
+                z = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w[i]),
+                                                    bf16x2{(__bf16)0.f, (__bf16)0.f}, z, false);
+            else if constexpr (k16)
+                z = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w[i]),
+                                           f16x2{(_Float16)0.f, (_Float16)0.f}, z, false);
+            else
+                z = fmaf(__builtin_bit_cast(float, w[i]), 0.f, z);
+        }
+        return z;
+    }
     // The keys (bits) whose chunk holds an infinity or a NaN.
     static __device__ __forceinline__ uint32_t wild_keys(const VBlock& v) {
         uint32_t keys = 0;
@@ -556,6 +593,26 @@ struct Tile {
 template <class T>
 constexpr float kProbShift = std::is_same<T, _Float16>::value ? 14.f : 0.f;
 
+// The keys of a tile that this lane's query sees: bit (j & 3) + 16 * (j >> 2)
+// for the lane's j-th key.
+struct Seen {
+    uint32_t bits;
+    // from a tile's keys as bits 0 to 31
+    static __device__ __forceinline__ Seen keys(uint32_t all) {
+        return {all >> (4 * (lane_id() >> 4))};
+    }
+    static __device__ __forceinline__ Seen first(int n) {
+        return keys(n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1);
+    }
+    // x if the lane's j-th key is seen, else y (by bits: whatever x holds)
+    __device__ __forceinline__ float pick(int j, float x, float y) const {
+        const int at = (j & 3) + 16 * (j >> 2);
+        const uint32_t on = (uint32_t)((int32_t)(bits << (31 - at)) >> 31);
+        return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & on) |
+                                             (__builtin_bit_cast(uint32_t, y) & ~on));
+    }
+};
+
 // The running maximum (base 2) and sum of a softmax, of this lane's query;
 // the sum covers this lane's keys only until finish().
 template <class G, class T>
@@ -563,16 +620,15 @@ struct Softmax {
     float m = -INFINITY, l = 0.f;
 
     // Takes a tile's scores before their factor c > 0 (a negative one's sign
-    // goes into q, and 0 makes q 0), of whose keys the first `limit` count,
-    // rescales what o holds, and leaves the weights.
+    // goes into q, and 0 makes q 0), of whose keys those count that `seen`
+    // names (see Seen), rescales what o holds, and leaves the weights.
     template <class A>
-    __device__ __forceinline__ void step(const f32x4 (&s)[G::KSUB], int limit, float c, A& o,
+    __device__ __forceinline__ void step(const f32x4 (&s)[G::KSUB], Seen seen, float c, A& o,
                                          typename G::Probs& out) {
         float p[G::VK], top = -INFINITY;
 #pragma unroll
         for (int j = 0; j < G::VK; ++j) {
-            p[j] = s[j >> 2][j & 3];
-            if (G::key_of(j) >= limit) p[j] = -INFINITY;
+            p[j] = seen.pick(j, s[j >> 2][j & 3], -INFINITY);
             top = fmaxf(top, p[j]);
         }
         const float mn = fmaxf(m, quad_max(top) * c);

@@ -78,6 +78,44 @@ def test_head_layouts(dtype, hq, hkv):
     _check_both(rows, q, k, v, dout, 301, 0.125)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=str)
+@pytest.mark.parametrize("hq,hkv,kind", [(1, 1, "short"), (8, 2, "short"), (3, 1, "band"), (16, 2, "band"),
+                                         (5, 1, "band"), (18, 2, "band"), (2, 1, "long"), (4, 1, "hub")])
+def test_rows_that_share_work(dtype, hq, hkv, kind):
+    """Ascending rows, four of which share tiles: short ones, neighbours in a
+    band (with wild values in keys that only some of the four see), long ones
+    without common columns, and one long row among empty ones."""
+    rng = np.random.default_rng(hq * 10 + len(kind))
+    nk = 700
+    if kind == "short":
+        rows = [np.sort(r) for r in ref.mask([0, 3, 0, 40, 17, 1, 1, 2, 0, 0, 0, 0, 33, 32, 31, 5, 6], nk, rng)]
+    elif kind == "band":
+        rows = [np.arange(max(0, i - 150), i + 1) for i in range(203)]
+        nk = 203
+    elif kind == "long":
+        rows = [np.arange(i % 4, nk, 4) for i in range(9)]
+    else:
+        rows = [np.arange(nk) if i == 6 else np.zeros(0, int) for i in range(14)]
+    nq = len(rows)
+    q, k, v, dout = (_rand(rng, s, dtype) for s in ((nq, hq, 64), (nk, hkv, 64), (nk, hkv, 64), (nq, hq, 64)))
+    _check_both(rows, q, k, v, dout, nk, 0.125)
+    # a NaN key and an infinite value reach the rows that store them and no others
+    api = _api()
+    bad = 2 if kind != "short" else int(rows[3][7])
+    with api.AttentionPlan(ref.csr(rows, nk), backward=True) as plan:
+        out, lse = plan.forward(q, k, v)
+        clean = (out, lse, *plan.backward(dout, q, k, v, out, lse))
+        k[bad], v[bad] = float("nan"), float("inf")
+        out, lse = plan.forward(q, k, v)
+        got = (out, lse, plan.backward(dout, q, k, v, out, lse)[0])
+    has = torch.tensor([bad in set(r.tolist()) for r in rows]).cuda()
+    assert has.any() and (kind == "hub" or not has.all())
+    for a, b in zip(got, clean):
+        assert torch.equal(a[~has], b[~has])
+        assert not torch.isfinite(a[has].float()).any() if a.dim() == 2 else \
+            not torch.isfinite(a[has].float()).all(2).any()
+
+
 def test_float_head_dim_of_four():
     rng = np.random.default_rng(4)
     rows, q, k, v, dout = _case(rng, F32, 4, 2, 1)
