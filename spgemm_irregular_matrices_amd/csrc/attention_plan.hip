@@ -23,18 +23,21 @@ struct spgemm_attention_plan_s {
 namespace {
 
 // ---------------------------------------------------------------- plan
-// Entries per piece. Long rows are cut so that the longest piece stays near
-// the mean one's work: about `pieces` of them over all entries (4096 where a
-// wavefront takes one, 1024 where a work group does), between `least` and
-// 1024 entries each.
+// Entries per piece. Rows are cut where they are longer than twice the mean, so
+// that rows of about one length stay whole (a cut one's pieces are written and
+// joined in floats), or longer than all entries spread over the chip: then
+// the longest would end last. (`share` entries of every piece's worth: with
+// some 4 key heads, 512 wavefronts' or 192 work groups' share each.)
 struct PieceRule {
-    int64_t pieces, least;
-    int64_t length(int64_t nnz) const {
-        const int64_t want = ceil_div(ceil_div(nnz, pieces), 32) * 32;
+    int64_t share, least;
+    int64_t length(int64_t n, int64_t entries) const {
+        const int64_t twice = ceil_div(2 * entries, n < 1 ? 1 : n);
+        int64_t want = std::min(twice, ceil_div(entries, share));
+        want = ceil_div(want, 32) * 32;
         return want < least ? least : want > 1024 ? 1024 : want;
     }
 };
-constexpr PieceRule kRowPieces{4096, 128}, kBlockPieces{1024, 32};
+constexpr PieceRule kRowPieces{512, 128}, kBlockPieces{192, 32};
 
 struct RowPieces {
     const int64_t* rp;
@@ -197,7 +200,7 @@ AttnSide make_side(const char* name, const int64_t* rp, int64_t n, int64_t nnz, 
     s.idx = idx;
     if (n == 0) return s;
     const std::string nm(name);
-    const RowPieces rows{rp, rule.length(nnz)};
+    const RowPieces rows{rp, rule.length(n, nnz)};
     int64_t* piece0 = tmp.get<int64_t>("piece0", (size_t)n + 1);
     int64_t* slot0 = tmp.get<int64_t>("slot0", (size_t)n + 1);
     int64_t* split0 = tmp.get<int64_t>("split0", (size_t)n + 1);
@@ -229,7 +232,7 @@ AttnSide make_side(const char* name, const int64_t* rp, int64_t n, int64_t nnz, 
 // store the same columns (they share keys), and their columns ascend (else
 // the blocks stay unbuilt and single rows do).
 bool blocks_serve(int64_t n, int64_t nnz, int64_t entries) {
-    return nnz < 64 * n || entries <= nnz / 4 * 3;
+    return nnz < 192 * n || entries <= nnz / 4 * 3;
 }
 void build_blocks(spgemm_attention_plan p, const DevCSR& m, const int32_t* col, const int32_t* row,
                   Arena& tmp, hipStream_t st) {
