@@ -480,16 +480,22 @@ bool batch_sizes_fit(const spgemm_paged_batch* b, const spgemm_attention_desc* d
            b->tokens <= kMaxTokens && b->max_length <= kMaxTokens;
 }
 
-// Keys per piece. Where there are few rows the keys are cut: until about 4096
-// wavefronts (16 per compute unit) have a piece each, of 64 keys at least, or
-// where work groups share the keys, 1024 work groups one of 256 keys at least.
+// Keys per piece. Where there are few rows the keys are cut: for wavefronts
+// with keys of their own until 4096 (16 per compute unit) have a piece of at
+// least 64 keys each; for work groups that share keys, of which a compute unit
+// holds two (one from 129 values per head on), until there are as many as the
+// chip holds, with at least 256 keys each: their pieces cost more to join. The
+// rows of ragged chunks are counted by the tokens.
 void shape_pieces(PagedArgs* a) {
     const int64_t rows = (int64_t)a->max_new * a->s.group;
     const bool wide = paged_wide(rows);
-    const int64_t tiles = ceil_div(rows, paged_tile_rows(a->s.dim, rows));
-    const int64_t units = std::max<int64_t>(a->seqs * a->s.hkv * tiles, 1);
+    const int64_t tile = paged_tile_rows(a->s.dim, rows);
+    const int64_t tiles = std::min(a->seqs * ceil_div(rows, tile),
+                                   a->seqs + a->tokens * a->s.group / tile);
+    const int64_t units = std::max<int64_t>(a->s.hkv * tiles, 1);
     const int64_t most = std::max<int64_t>(ceil_div(a->max_length, wide ? 256 : 64), 1);
-    const int64_t want = std::min(std::max<int64_t>((wide ? 512 : 4096) / units, 1), most);
+    const int64_t target = !wide ? 4096 : a->s.dim <= 128 ? 512 : 256;
+    const int64_t want = std::min(std::max<int64_t>(target / units, 1), most);
     const int64_t whole = wide ? 64 : 32;
     a->piece = (int32_t)std::max<int64_t>(
         ceil_div(ceil_div(a->max_length, want), whole) * whole, whole);
