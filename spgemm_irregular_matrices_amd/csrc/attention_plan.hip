@@ -1,6 +1,7 @@
 // Plans of attention over a CSR mask, argument checks, and the C ABI of
 // include/spgemm_attention.h.
 #include <cmath>
+#include <memory>
 #include <new>
 
 #include "attention.h"
@@ -17,7 +18,12 @@ struct spgemm_attention_plan_s {
     AttnSide blocks;  // blocks of rows, if built (n > 0)
     bool overlap = false;  // the blocks' entries are at most half of the rows'
     AttnSide cols;
-    Arena ar;  // pieces, splits and entries of both sides; never changed after creation
+    void* slab = nullptr;  // what ar's buffers lie in, if not in allocations of their own
+    Arena ar;              // pieces, splits and entries; never changed after creation
+    ~spgemm_attention_plan_s() {
+        ar.release();
+        if (slab) (void)hipFree(slab);
+    }
 };
 
 namespace {
@@ -310,8 +316,55 @@ void build_cols(spgemm_attention_plan p, const DevCSR& m, const int32_t* col, co
     p->cols.block = kColBlock;
 }
 
-int build_plan(spgemm_attention_plan p, const spgemm_csr* mask, bool backward, hipStream_t st) {
+// Device memory given back with the scope.
+struct Slab {
+    void* p = nullptr;
+    explicit Slab(size_t bytes) {
+        if (hipMalloc(&p, bytes) != hipSuccess) {
+            (void)hipGetLastError();
+            throw OomError("attention plan");
+        }
+    }
+    ~Slab() {
+        if (p) (void)hipFree(p);
+    }
+};
+
+// Bytes that cover a plan's buffers, and those used while it is made: each is
+// carved out of one allocation, because allocating and freeing two dozen
+// buffers takes longer than the kernels do. A mask so large that the bounds
+// are far from the need gets allocations one by one instead.
+constexpr int64_t kSlabMost = int64_t(1) << 30;
+int64_t kept_bytes(int64_t n, int64_t m, int64_t nnz, bool backward) {
+    const int64_t row_cuts = nnz / kRowPieces.least + 1, col_cuts = nnz / kBlockPieces.least + 1;
+    int64_t b = 10 * nnz + sizeof(AttnPiece) * (n + n / kRowBlock + 1 + 2 * row_cuts) +
+                2 * sizeof(AttnSplit) * row_cuts;
+    if (backward)
+        b += 6 * nnz + sizeof(AttnPiece) * (m / kColBlock + 1 + col_cuts) +
+             sizeof(AttnSplit) * col_cuts;
+    return b + (int64_t(16) << 10);
+}
+int64_t temporary_bytes(int64_t n, int64_t m, int64_t nnz, bool backward) {
+    return (backward ? 37 : 17) * nnz + 40 * n + (backward ? 3 * m : 0) + (int64_t(256) << 10);
+}
+
+int build_plan(spgemm_attention_plan p, const spgemm_csr* mask, bool backward, bool slabs,
+               hipStream_t st) {
+    const int64_t n = mask->nrows, cols = mask->ncols, nnz = mask->nnz;
+    const int64_t kept = kept_bytes(n, cols, nnz, backward);
+    const int64_t used = temporary_bytes(n, cols, nnz, backward);
     Arena tmp;
+    std::unique_ptr<Slab> slab;
+    if (slabs && used <= kSlabMost) {
+        slab = std::make_unique<Slab>((size_t)used);
+        tmp.use_region(slab->p, (size_t)used);
+        if (hipMalloc(&p->slab, (size_t)kept) != hipSuccess) {
+            (void)hipGetLastError();
+            p->slab = nullptr;
+            throw OomError("attention plan");
+        }
+        p->ar.use_region(p->slab, (size_t)kept);
+    }
     DevCSR m;
     m.n = mask->nrows;
     m.m = mask->ncols;
@@ -552,9 +605,21 @@ SPGEMM_API int spgemm_attention_plan_create(spgemm_attention_plan* out, const sp
         return SPGEMM_ERR_OVERFLOW;
     spgemm_attention_plan p = nullptr;
     const int rc = guarded([&]() -> int {
-        p = new spgemm_attention_plan_s();
-        SG_HIP(hipGetDevice(&p->device));
-        return build_plan(p, mask, backward != 0, (hipStream_t)stream);
+        int device = 0;
+        SG_HIP(hipGetDevice(&device));
+        for (const bool slabs : {true, false}) {
+            delete p;
+            p = nullptr;
+            p = new spgemm_attention_plan_s();
+            p->device = device;
+            try {
+                return build_plan(p, mask, backward != 0, slabs, (hipStream_t)stream);
+            } catch (const ScratchError&) {
+                // the bounds of the slabs fell short: once more without them
+                SG_HIP(hipStreamSynchronize((hipStream_t)stream));
+            }
+        }
+        return SPGEMM_ERR_INTERNAL;
     });
     if (rc != SPGEMM_OK) {
         if (p) (void)hipStreamSynchronize((hipStream_t)stream);
