@@ -71,6 +71,7 @@ struct AttnShape {
     int mtiles = 1;      // tiles of 16 queries per piece and key head (see AttnColumn)
     float scale = 0.f;   // of the scores
     float c = 0.f;       // scale * log2(e)
+    float c_low = 0.f;   // and what c rounds off
     float mag = 1.f;     // |c|, or 1 if that is 0: the factor that Softmax takes
 };
 

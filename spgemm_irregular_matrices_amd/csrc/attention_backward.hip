@@ -115,14 +115,14 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
     typename G::Acc o;
     G::zero_acc(o);
     HalfScale hs;
-    float lse2 = 0.f, delta = 0.f;
+    float seen_lse = 0.f, delta = 0.f;  // of the piece that is computed
     bool fresh = true;  // first tile of its piece
     while (true) {
         const int left = cur.len - cur.t0;
         const bool last = left <= G::KT, more = ahead.more;
         if (fresh) {
             delta = quad_sum(G::dot_lane(dout, out));
-            lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
+            seen_lse = lse;
             const int64_t row = row_of(st.row(cur.i));
             if (here(row) && lane < 16 && st.lead(cur.i)) a.delta[row * a.s.hq + me.hq] = delta;
             fresh = false;
@@ -161,7 +161,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
         float ds[G::VK];
 #pragma unroll
         for (int j = 0; j < G::VK; ++j) {
-            const float p = fast_exp2(fmaf(s[j >> 2][j & 3], a.s.c, -lse2));
+            const float p = weight<T>(s[j >> 2][j & 3], a.s.c, a.s.c_low, seen_lse);
             ds[j] = seen.pick(j, p * (dp[j >> 2][j & 3] - delta), 0.f);
         }
         if constexpr (std::is_same<T, _Float16>::value) {
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 1) void k_att
             *reinterpret_cast<u32x4*>(rows[1] + at) = fly[1][i];
         }
         if (tid < TP) {
-            lse_s[tid] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+            lse_s[tid] = lse;
             delta_s[tid] = delta;
             bits_s[tid] = mine;
         }
@@ -399,7 +399,7 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 1) void k_att
                 wild = fmaf(s[r], 0.f, wild);
                 wild = fmaf(dp[r], 0.f, wild);
                 const bool on = sees[r] >> n & 1;
-                pr[r] = on ? fast_exp2(fmaf(s[r], a.s.c, -l2[r])) : 0.f;
+                pr[r] = on ? weight<T>(s[r], a.s.c, a.s.c_low, l2[r]) : 0.f;
                 ds[r] = on ? pr[r] * (dp[r] - dl[r]) : 0.f;
                 pr[r] *= kProbScale<T>;
             }

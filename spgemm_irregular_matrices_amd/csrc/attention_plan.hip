@@ -428,6 +428,7 @@ AttnShape make_shape(const spgemm_attention_desc* d) {
     s.dim = d->head_dim;
     s.scale = (float)d->scale;
     s.c = (float)(d->scale * 1.4426950408889634);
+    s.c_low = (float)(d->scale * 1.4426950408889634 - (double)s.c);
     s.mag = s.c == 0.f ? 1.f : std::fabs(s.c);
     return s;
 }

@@ -34,6 +34,7 @@ using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2eLow = (float)(1.44269504088896340736 - (double)kLog2e);
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // exp2 and log2 of the vector unit (1 ulp; results below the smallest normal
@@ -87,6 +88,22 @@ __device__ __forceinline__ float quad_max(float x) {
 }
 __device__ __forceinline__ float quad_sum(float x) {
     return quad_reduce(x, [](float a, float b) { return a + b; });
+}
+
+// exp(scale * s - lse), with c + c_low = scale * log2(e). In single precision
+// the roundings of c and of lse * log2(e), which would weigh |lse| times a
+// rounding, are carried along; in the 16-bit types they are far below the
+// weight's own rounding. An infinite lse (no row, or one that sees nothing)
+// gives 0.
+template <class T>
+__device__ __forceinline__ float weight(float s, float c, float c_low, float lse) {
+    const float a = lse == -INFINITY ? INFINITY : lse * kLog2e;
+    float x = fmaf(s, c, -a);
+    if constexpr (sizeof(T) == 4) {
+        const float low = fmaf(lse, kLog2eLow, fmaf(lse, kLog2e, -a));
+        x += a == INFINITY ? 0.f : fmaf(s, c_low, -low);
+    }
+    return fast_exp2(x);
 }
 
 // Unsigned division of n < 2^31 by a divisor fixed at launch: with

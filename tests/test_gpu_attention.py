@@ -150,6 +150,38 @@ def test_long_rows_and_columns(dtype):
     _check_both(rows, q, k, v, dout, nk, 0.125)
 
 
+def test_many_entries():
+    """33 million entries, more than the plan carves its buffers out of one
+    allocation for: every row sees every key, so sums over the dense product
+    give the results."""
+    api = _api()
+    n, d = 5760, 8
+    from spgemm_irregular_matrices_amd import binding
+    rowptr = torch.arange(n + 1, device="cuda") * n
+    col = torch.arange(n, device="cuda", dtype=torch.int32).repeat(n)
+    rng = np.random.default_rng(26)
+    q, k, v, dout = (_rand(rng, (n, 1, d), F32) for _ in range(4))
+    with api.AttentionPlan(binding.DeviceCSR(n, n, rowptr, col, None), backward=True) as plan:
+        out, lse = plan.forward(q, k, v, scale=0.3)
+        grads = plan.backward(dout, q, k, v, out, lse, scale=0.3)
+    Q, K, V, D = (x[:, 0].double().cpu() for x in (q, k, v, dout))
+    s = 0.3 * Q @ K.T
+    p = torch.softmax(s, 1)
+    O = p @ V
+    dp = D @ V.T
+    ds = p * (dp - (D * O).sum(1, keepdim=True))
+    # sums of 5760 terms in floats, each with a weight off by a few roundings:
+    # (5760 + 64) * 2^-24 of the sums of magnitudes
+    f = 6000 * 2.0 ** -24
+    mag = p * (dp.abs() + D.abs() @ V.abs().T)
+    for got, want, size in ((out, O, p @ V.abs()), (lse[..., None], torch.logsumexp(s, 1)[:, None],
+                             torch.full((n, 1), 20.0)),
+                            (grads[0], 0.3 * ds @ K, 0.3 * mag @ K.abs()),
+                            (grads[1], 0.3 * ds.T @ Q, 0.3 * mag.T @ Q.abs()),
+                            (grads[2], p.T @ D, p.T @ D.abs())):
+        assert ((got[:, 0].double().cpu() - want).abs() <= f * size).all()
+
+
 @pytest.mark.parametrize("nq,nk", [(0, 5), (5, 0), (0, 0), (1, 1)])
 def test_empty_shapes(nq, nk):
     api = _api()
