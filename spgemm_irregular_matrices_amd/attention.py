@@ -120,16 +120,23 @@ def _raw_stream(device) -> int | None:
     return torch._C._cuda_getCurrentRawStream(device.index) or None
 
 
-def _heads(name, t, rows, heads, dim, dtype, device) -> Rows:
-    """A [rows, heads, dim] tensor as the library takes it."""
-    s, st = t.shape, t.stride()
-    if len(s) != 3 or s[0] != rows or s[1] != heads or s[2] != dim:
-        raise ValueError(f"{name} has shape {tuple(s)}, expected ({rows}, {heads}, {dim})")
-    if t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {dtype} on {device}")
-    if st[2] != 1 and dim > 1 and t.numel():
+def _heads(name, t, shape, dtype, device) -> Rows:
+    """A [rows, heads, dim] tensor of that shape as the library takes it."""
+    st = t.stride()
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} is {tuple(t.shape)}, {t.dtype} on {t.device}, expected "
+                         f"{tuple(shape)}, {dtype} on {device}")
+    if st[2] != 1 and shape[2] > 1 and t.numel():
         raise ValueError(f"{name}'s last dimension must be contiguous")
     return Rows(t.data_ptr(), st[0], st[1])
+
+
+def _new(like, shape):
+    """A new contiguous tensor of `like`'s shape, type and device (the shorter call if it can be)."""
+    import torch
+    if like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=like.dtype, device=like.device)
 
 
 def _flat(name, t, shape, dtype, device):
@@ -139,11 +146,11 @@ def _flat(name, t, shape, dtype, device):
 
 
 def _dims(q, k):
-    """(heads_q, heads_kv, dim, dtype, device) of a call."""
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError(f"q has shape {tuple(q.shape)} and k {tuple(k.shape)}, expected "
-                         "(rows, heads, dim)")
-    return q.shape[1], k.shape[1], q.shape[2], q.dtype, q.device
+    """(heads_q, heads_kv, dim) of a call."""
+    a, b = q.shape, k.shape
+    if len(a) != 3 or len(b) != 3:
+        raise ValueError(f"q has shape {tuple(a)} and k {tuple(b)}, expected (rows, heads, dim)")
+    return a[1], b[1], a[2]
 
 
 def _scale(scale, dim) -> float:
@@ -230,27 +237,27 @@ class AttentionPlan:
         out has q's shape and type, lse is [nrows, heads_q] in float32. Either
         may be passed to be written into. scale defaults to dim ** -0.5."""
         import torch
-        hq, hkv, dim, dtype, device = _dims(q, k)
+        hq, hkv, dim = _dims(q, k)
+        dtype, device = q.dtype, q.device
         self._ready(device)
-        nq, nk = self.nrows, self.ncols
+        big, small, line = (self.nrows, hq, dim), (self.ncols, hkv, dim), (self.nrows, hq)
         ref = ctypes.byref
         desc = Desc(_type_code(dtype), hq, hkv, dim, _scale(scale, dim))
+        qs = _heads("q", q, big, dtype, device)
+        ks = _heads("k", k, small, dtype, device)
+        vs = _heads("v", v, small, dtype, device)
         with _on_device(device, stream):
             if out is None:
-                out = torch.empty(q.shape, dtype=dtype, device=device)
+                out = _new(q, big)
             if lse is None:
-                lse = torch.empty((nq, hq), dtype=torch.float32, device=device)
+                lse = torch.empty(line, dtype=torch.float32, device=device)
             else:
-                _flat("lse", lse, (nq, hq), torch.float32, device)
-            rows = (_heads("q", q, nq, hq, dim, dtype, device),
-                    _heads("k", k, nk, hkv, dim, dtype, device),
-                    _heads("v", v, nk, hkv, dim, dtype, device),
-                    _heads("out", out, nq, hq, dim, dtype, device))
+                _flat("lse", lse, line, torch.float32, device)
+            os = _heads("out", out, big, dtype, device)
             space, ws, nbytes = self._space(desc, 0)
             _check(self._lib.spgemm_attention_forward(
-                self._h, ref(desc), ref(rows[0]), ref(rows[1]), ref(rows[2]), ref(rows[3]),
-                lse.data_ptr() or None, ws, nbytes, _raw_stream(device)),
-                "spgemm_attention_forward")
+                self._h, ref(desc), ref(qs), ref(ks), ref(vs), ref(os), lse.data_ptr() or None, ws,
+                nbytes, _raw_stream(device)), "spgemm_attention_forward")
         return out, lse
 
     def backward(self, dout, q, k, v, out, lse, scale=None, dq=None, dk=None, dv=None,
@@ -258,28 +265,33 @@ class AttentionPlan:
         """(dq, dk, dv), given dout and what ``forward`` returned. Gradients
         have their tensors' shapes and type, and are written, not added to."""
         import torch
-        hq, hkv, dim, dtype, device = _dims(q, k)
+        hq, hkv, dim = _dims(q, k)
+        dtype, device = q.dtype, q.device
         self._ready(device)
-        nq, nk = self.nrows, self.ncols
+        big, small = (self.nrows, hq, dim), (self.ncols, hkv, dim)
         ref = ctypes.byref
         desc = Desc(_type_code(dtype), hq, hkv, dim, _scale(scale, dim))
+        _flat("lse", lse, (self.nrows, hq), torch.float32, device)
+        qs = _heads("q", q, big, dtype, device)
+        ks = _heads("k", k, small, dtype, device)
+        vs = _heads("v", v, small, dtype, device)
+        os = _heads("out", out, big, dtype, device)
+        gs = _heads("dout", dout, big, dtype, device)
         with _on_device(device, stream):
-            _flat("lse", lse, (nq, hq), torch.float32, device)
             if dq is None:
-                dq = torch.empty((nq, hq, dim), dtype=dtype, device=device)
+                dq = _new(q, big)
             if dk is None:
-                dk = torch.empty((nk, hkv, dim), dtype=dtype, device=device)
+                dk = _new(k, small)
             if dv is None:
-                dv = torch.empty((nk, hkv, dim), dtype=dtype, device=device)
-            rows = [_heads(name, t, n, h, dim, dtype, device) for name, t, n, h in (
-                ("q", q, nq, hq), ("k", k, nk, hkv), ("v", v, nk, hkv), ("out", out, nq, hq),
-                ("dout", dout, nq, hq), ("dq", dq, nq, hq), ("dk", dk, nk, hkv),
-                ("dv", dv, nk, hkv))]
+                dv = _new(v, small)
+            dqs = _heads("dq", dq, big, dtype, device)
+            dks = _heads("dk", dk, small, dtype, device)
+            dvs = _heads("dv", dv, small, dtype, device)
             space, ws, nbytes = self._space(desc, 1)
             _check(self._lib.spgemm_attention_backward(
-                self._h, ref(desc), ref(rows[0]), ref(rows[1]), ref(rows[2]), ref(rows[3]),
-                lse.data_ptr() or None, ref(rows[4]), ref(rows[5]), ref(rows[6]), ref(rows[7]), ws,
-                nbytes, _raw_stream(device)), "spgemm_attention_backward")
+                self._h, ref(desc), ref(qs), ref(ks), ref(vs), ref(os), lse.data_ptr() or None,
+                ref(gs), ref(dqs), ref(dks), ref(dvs), ws, nbytes, _raw_stream(device)),
+                "spgemm_attention_backward")
         return dq, dk, dv
 
 
@@ -325,13 +337,13 @@ def paged_attention(q, k_cache, v_cache, pages: DeviceCSR, q_rowptr, lengths, ma
         _flat("q_rowptr", q_rowptr, (seqs + 1,), torch.int64, device)
         _flat("lengths", lengths, (seqs,), torch.int64, device)
         if out is None:
-            out = torch.empty(q.shape, dtype=dtype, device=device)
+            out = _new(q, q.shape)
         if lse is None:
             lse = torch.empty((tokens, hq), dtype=torch.float32, device=device)
         else:
             _flat("lse", lse, (tokens, hq), torch.float32, device)
-        qs = _heads("q", q, tokens, hq, dim, dtype, device)
-        os = _heads("out", out, tokens, hq, dim, dtype, device)
+        qs = _heads("q", q, q.shape, dtype, device)
+        os = _heads("out", out, q.shape, dtype, device)
         table = _b.CSRStruct(seqs, npages, nnz, pages.rowptr.data_ptr(),
                              pages.col.data_ptr() or None, None)
         cache = PagedCache(k_cache.data_ptr() or None, v_cache.data_ptr() or None, npages, slots,

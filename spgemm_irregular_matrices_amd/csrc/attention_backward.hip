@@ -534,7 +534,6 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 1) void k_att
 // column and output of dk and dv. A piece's results lie side by side.
 template <class T>
 __global__ __launch_bounds__(kWaves* kWave) void k_attn_join_sum(BackwardArgs a) {
-    const int lane = lane_id();
     int64_t unit = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
     const int64_t row_units = a.rows.nsplits * a.rows.block * a.s.hq;
     const bool col_side = unit >= row_units;
@@ -550,18 +549,9 @@ __global__ __launch_bounds__(kWaves* kWave) void k_attn_join_sum(BackwardArgs a)
                                  : (int64_t)s.row * side.block + hl / a.s.hq;
     if (row >= (col_side ? a.ncols : a.nrows)) return;
     const float* part = (col_side ? a.part_kv : a.part_q) + ((int64_t)s.slot * per + hl) * a.s.dim;
-    float x[SPGEMM_ATTENTION_MAX_HEAD_DIM / kWave] = {};
-    for (int i = 0; i < s.count; ++i) {
-        const float* src = part + i * per * a.s.dim;
-#pragma unroll
-        for (int j = 0; j < SPGEMM_ATTENTION_MAX_HEAD_DIM / kWave; ++j)
-            if (j * kWave + lane < a.s.dim) x[j] += src[j * kWave + lane];
-    }
     const AttnRows& o = !col_side ? a.dq : line & 1 ? a.dv : a.dk;
-    T* dst = reinterpret_cast<T*>(o.base + row * o.row + h * o.head);
-#pragma unroll
-    for (int j = 0; j < SPGEMM_ATTENTION_MAX_HEAD_DIM / kWave; ++j)
-        if (j * kWave + lane < a.s.dim) dst[j * kWave + lane] = (T)x[j];
+    JoinedRow(part, per * a.s.dim, s.count, a.s.dim, [](int) { return 1.f; })
+        .store<T>(o.base + row * o.row + h * o.head, 1.f, a.s.dim);
 }
 
 }  // namespace

@@ -492,26 +492,13 @@ __global__ __launch_bounds__(kWaves* kWave) void k_paged_join(PagedArgs a) {
     if (sees <= a.piece) return;
     const int count = (sees + a.piece - 1) / a.piece;
     const int64_t step = a.tokens * a.s.hq;
-    float m = -INFINITY;
-    for (int i = lane; i < count; i += kWave) m = fmaxf(m, a.part_ml[2 * (i * step + unit)]);
-#pragma unroll
-    for (int d = kWave / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, kWave));
-    const float ms = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[SPGEMM_ATTENTION_MAX_HEAD_DIM / kWave] = {};
-    for (int i = 0; i < count; ++i) {
-        const int64_t at = i * step + unit;
-        const float w = fast_exp2(a.part_ml[2 * at] - ms);
-        l += a.part_ml[2 * at + 1] * w;
-        const float* src = a.part + at * a.s.dim;
-#pragma unroll
-        for (int j = 0; j < SPGEMM_ATTENTION_MAX_HEAD_DIM / kWave; ++j)
-            if (j * kWave + lane < a.s.dim) o[j] += src[j * kWave + lane] * w;
-    }
-    const float f = l == 0.f ? 0.f : 1.f / l;
-    T* dst = reinterpret_cast<T*>(a.out.base + token * a.out.row + hq * a.out.head);
-#pragma unroll
-    for (int j = 0; j < SPGEMM_ATTENTION_MAX_HEAD_DIM / kWave; ++j)
-        if (j * kWave + lane < a.s.dim) dst[j * kWave + lane] = (T)(o[j] * f);
+    const float* ml = a.part_ml + 2 * unit;
+    float m, l;
+    join_sums(ml, step, count, m, l);
+    const JoinedRow o(a.part + unit * a.s.dim, step * a.s.dim, count, a.s.dim,
+                      [&](int i) { return fast_exp2(ml[2 * i * step] - m); });
+    o.store<T>(a.out.base + token * a.out.row + hq * a.out.head, l == 0.f ? 0.f : 1.f / l,
+               a.s.dim);
     if (a.lse && lane == 0)
         a.lse[unit] = l == 0.f ? -INFINITY : (m - kProbShift<T> + fast_log2(l)) * kLn2;
 }

@@ -670,6 +670,62 @@ struct Softmax {
     }
 };
 
+// Joins `count` partial results of dim floats, `step` floats apart, by one
+// wavefront: the four rows of 16 lanes take every fourth piece, four values a
+// lane, so that a long chain of pieces is a quarter as long and its loads
+// wide; they are added up at the end, in the same order every time.
+struct JoinedRow {
+    static constexpr int kParts = 4;  // of 64 values
+    f32x4 x[kParts];
+    // weight(i): the factor of piece i
+    template <class Weight>
+    __device__ __forceinline__ JoinedRow(const float* part, int64_t step, int count, int dim,
+                                         Weight&& weight) {
+        const int at = 4 * (lane_id() & 15);
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) x[j] = f32x4{0, 0, 0, 0};
+#pragma unroll 2
+        for (int i = lane_id() >> 4; i < count; i += 4) {
+            const float w = weight(i);
+            const float* src = part + i * step;
+#pragma unroll
+            for (int j = 0; j < kParts; ++j)
+                if (64 * j + at < dim)
+                    x[j] += *reinterpret_cast<const f32x4*>(src + 64 * j + at) * w;
+        }
+#pragma unroll
+        for (int j = 0; j < kParts; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[j][r] = quad_sum(x[j][r]);
+    }
+    // The values times f, rounded to T.
+    template <class T>
+    __device__ __forceinline__ void store(char* row, float f, int dim) const {
+        const int j = lane_id() >> 4, at = 64 * j + 4 * (lane_id() & 15);
+        if (at >= dim) return;
+        const f32x4 y = (j == 0 ? x[0] : j == 1 ? x[1] : j == 2 ? x[2] : x[3]) * f;
+        if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<u32x2*>(row + 2 * at) = u32x2{pack2<T>(y[0], y[1]),
+                                                            pack2<T>(y[2], y[3])};
+        else
+            *reinterpret_cast<f32x4*>(row + 4 * at) = y;
+    }
+};
+// The largest maximum and the sum of softmax partials (maximum, sum) `step`
+// pairs apart, by one wavefront.
+__device__ __forceinline__ void join_sums(const float* ml, int64_t step, int count, float& m,
+                                          float& l) {
+    m = -INFINITY;
+    for (int i = lane_id(); i < count; i += kWave) m = fmaxf(m, ml[2 * i * step]);
+#pragma unroll
+    for (int d = kWave / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, kWave));
+    m = m == -INFINITY ? 0.f : m;
+    l = 0.f;
+    for (int i = lane_id(); i < count; i += kWave)
+        l += ml[2 * i * step + 1] * fast_exp2(ml[2 * i * step] - m);
+    l = wave_reduce_sum(l);
+}
+
 // Calls f(Tag<T, DP, FULL>) for the run-time element type and head dimension.
 template <class T, int DP, bool FULL>
 struct TileTag {
