@@ -22,7 +22,9 @@
  *     data[t * stride_row + h * stride_head + x]. Strides count elements, are
  *     not negative, and together with `data` keep every row 16-byte aligned;
  *     head_dim * (bytes of the type) is a multiple of 16 too. Rows of an
- *     output tensor must not overlap. Anything else is INVALID_ARG.
+ *     output tensor must not overlap. Anything else is INVALID_ARG. (That an
+ *     output shares no memory with another tensor of the call is the caller's
+ *     to see to.)
  *   - Types: bfloat16, IEEE half or float for every tensor of a call alike;
  *     log-sum-exps are always float, [rows, heads_q] without gaps. Scores,
  *     softmax statistics and all sums are held in 32 bits. The probabilities
@@ -30,6 +32,9 @@
  *     type before they enter the second product, results once at the end.
  *   - Calls with the same arguments give the same bits: no sum depends on
  *     the order in which work groups run.
+ *   - An infinity or a NaN reaches the results whose formula has it, and no
+ *     others: not those of a row that does not store the key that holds it,
+ *     nor of a token that may not see it.
  *   - Attention calls neither allocate nor wait: they are asynchronous on
  *     `stream`, take their workspace from the caller, and may be captured
  *     into a HIP graph. A workspace belongs to one call at a time; two
@@ -74,7 +79,8 @@ typedef struct spgemm_attention_plan_s* spgemm_attention_plan;
 /* Create a plan for one mask: checks it, copies its columns, cuts its long
  * rows into pieces of similar work and, if `backward` is not 0, does the same
  * for its transpose. mask->val is not read and may be NULL. Columns need not
- * be sorted; a column that a row stores twice counts as two keys. The mask's
+ * be sorted (but only rows whose columns ascend can share work with their
+ * neighbours); a column that a row stores twice counts as two keys. The mask's
  * arrays are not used after the call, which blocks until the plan is ready.
  * A plan never changes afterwards: any number of calls, on any streams, may
  * use it at once, and it must outlive them and the graphs that captured

@@ -707,6 +707,31 @@ def test_tensor_refusals():
     long.close()
 
 
+def test_offsets_that_do_not_fit_are_refused():
+    """Rows so far apart that no power of two fits their offsets into 32 bits
+    (checked before any kernel runs: nothing of them is read)."""
+    api = _api()
+    lib = api.load()
+    plan = api.AttentionPlan(ref.csr([np.array([0, 2]), np.array([1])], 3), backward=True)
+    one = torch.zeros(8, 64, dtype=BF16, device="cuda")
+    far = (1 << 36) + 8
+    d = api.Desc(0, 1, 1, 64, 1.0)
+    near, wide = api.Rows(one.data_ptr(), 64, 64), api.Rows(one.data_ptr(), far, 64)
+    lse = torch.zeros(2, device="cuda")
+    space = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+    at = lambda *x: [ctypes.byref(y) for y in x]  # noqa: E731
+    tail = (space.data_ptr(), 1 << 16, None)
+    assert lib.spgemm_attention_forward(plan._h, *at(d, near, wide, near, near), None, *tail) == -4
+    assert lib.spgemm_attention_forward(plan._h, *at(d, near, near, wide, near), None, *tail) == -4
+    grads = at(near, near, near, near)
+    for q, dout in ((wide, near), (near, wide)):
+        assert lib.spgemm_attention_backward(plan._h, *at(d, q, near, near, near), lse.data_ptr(),
+                                             ctypes.byref(dout), *grads[:3], *tail) == -4
+    assert lib.spgemm_attention_forward(plan._h, *at(d, near, near, near, near), None, *tail) == 0
+    torch.cuda.synchronize()
+    plan.close()
+
+
 def test_paged_refusals():
     rng = np.random.default_rng(39)
     c = _paged_case(rng, BF16, 64, 4, 2, 16, [(20, 1), (5, 2)])
