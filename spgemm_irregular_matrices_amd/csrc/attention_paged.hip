@@ -318,6 +318,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
     const int lo = __builtin_amdgcn_readfirstlane(r[0].t);
     const int hi = __builtin_amdgcn_readlane(r[QB - 1].t, 15);
     const int mine = row0 < job.rows ? min(job.k1, job.before + hi) : 0;
+    const int full = min(job.k1, job.before + lo);  // that all of them see
 
     typename G::RowFrag q[QB];
     typename G::AccB o[QB];
@@ -436,11 +437,23 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
 #pragma unroll
                 for (int x = 0; x < QB; ++x) sc[x][b] = G::dot(k, q[x], f32x4{0, 0, 0, 0});
             }
-            typename G::Probs pr[QB];
+            if (t + G::KT > full) {  // some row does not see some key
 #pragma unroll
-            for (int x = 0; x < QB; ++x)
-                sm[x].step(sc[x], Seen::first(min(job.k1, job.before + r[x].t) - t), a.s.mag, o[x],
-                           pr[x]);
+                for (int x = 0; x < QB; ++x)
+                    sm[x].hide(sc[x], Seen::first(min(job.k1, job.before + r[x].t) - t));
+            }
+            typename G::Probs pr[QB];
+            float fix[QB];
+            bool moved = false;
+#pragma unroll
+            for (int x = 0; x < QB; ++x) {
+                fix[x] = sm[x].weigh(sc[x], a.s.mag, pr[x]);
+                moved |= fix[x] != 1.f;
+            }
+            if (__any(moved)) {
+#pragma unroll
+                for (int x = 0; x < QB; ++x) G::scale_acc(o[x], fix[x]);
+            }
 #pragma unroll
             for (int b = 0; b < G::NB; ++b) {
                 const u32x4 v = G::value_frag(rows[1], vbase, b);

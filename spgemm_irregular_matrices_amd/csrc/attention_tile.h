@@ -637,17 +637,13 @@ struct Softmax {
     float m = -INFINITY, l = 0.f;
 
     // Takes a tile's scores before their factor c > 0 (a negative one's sign
-    // goes into q, and 0 makes q 0), of whose keys those count that `seen`
-    // names (see Seen), rescales what o holds, and leaves the weights.
-    template <class A>
-    __device__ __forceinline__ void step(const f32x4 (&s)[G::KSUB], Seen seen, float c, A& o,
-                                         typename G::Probs& out) {
-        float p[G::VK], top = -INFINITY;
+    // goes into q, and 0 makes q 0; -infinity for a key that does not count)
+    // and leaves the weights; returns the factor of what was summed before.
+    __device__ __forceinline__ float weigh(const f32x4 (&s)[G::KSUB], float c,
+                                           typename G::Probs& out) {
+        float p[G::VK], top = s[0][0];
 #pragma unroll
-        for (int j = 0; j < G::VK; ++j) {
-            p[j] = seen.pick(j, s[j >> 2][j & 3], -INFINITY);
-            top = fmaxf(top, p[j]);
-        }
+        for (int j = 1; j < G::VK; ++j) top = fmaxf(top, s[j >> 2][j & 3]);
         const float mn = fmaxf(m, quad_max(top) * c);
         const float ms = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: weights 0, not NaN
         const float fix = fast_exp2(m - ms);
@@ -656,12 +652,24 @@ struct Softmax {
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < G::VK; ++j) {
-            p[j] = fast_exp2(fmaf(p[j], c, base));
+            p[j] = fast_exp2(fmaf(s[j >> 2][j & 3], c, base));
             sum += p[j];
         }
         l = l * fix + sum;
-        if (__any(fix != 1.f)) G::scale_acc(o, fix);
         G::pack_probs(p, out);
+        return fix;
+    }
+    // weigh() of the keys that are seen, and o rescaled.
+    __device__ __forceinline__ void step(f32x4 (&s)[G::KSUB], Seen seen, float c,
+                                         typename G::Acc& o, typename G::Probs& out) {
+        hide(s, seen);
+        const float fix = weigh(s, c, out);
+        if (__any(fix != 1.f)) G::scale_acc(o, fix);
+    }
+    static __device__ __forceinline__ void hide(f32x4 (&s)[G::KSUB], Seen seen) {
+#pragma unroll
+        for (int j = 0; j < G::VK; ++j)
+            s[j >> 2][j & 3] = seen.pick(j, s[j >> 2][j & 3], -INFINITY);
     }
     __device__ __forceinline__ void finish() { l = quad_sum(l); }
     __device__ __forceinline__ float factor() const { return l == 0.f ? 0.f : 1.f / l; }
