@@ -95,12 +95,12 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
         wave_lds_sync();
         const PieceStream::Entry then = next;
         if (more) load_k(then.id);
-        f32x4 s[G::KSUB];
+        f32x4 s[1][G::KSUB];
 #pragma unroll
         for (int b = 0; b < G::KSUB; ++b) {
             typename G::RowFrag x;
             G::staged_row(krows, rbase, 16 * b, x);
-            s[b] = G::dot(x, q, f32x4{0, 0, 0, 0});
+            s[0][b] = G::dot(x, q, f32x4{0, 0, 0, 0});
         }
         if (more && last) load_q(ahead.i);
         const PieceStream::Cursor after = ahead;
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
             st.next(ahead, G::KT);
             if (ahead.more) next = st.entry<SHARED>(ahead, G::KT);
         }
-        typename G::Probs pr;
+        typename G::Probs pr[1];
         const Seen seen = SHARED ? me.seen(now.bits) : Seen::first(left);
         sm.step(s, seen, a.s.mag, o, pr);
         if (left < G::KT) G::clear_past(v, left);
@@ -122,14 +122,14 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
                 for (int j = 0; j < G::VK; ++j) z = G::chunk_zero(v[u].w[j], z);
                 if (__any(z != 0.f))
                     G::add_wild_keys(
-                        v[u], pr, u, row_bytes,
+                        v[u], pr[0], u, row_bytes,
                         [&](int key) {
                             const uint32_t off = __shfl(now.id * a.v.unit, key, kWave);
                             return vb + ((uint64_t)off << a.v.shift);
                         },
                         [&](int key) { return __shfl(now.bits, key, kWave) >> me.rr & 1; }, o);
             }
-            G::accumulate(v[u], pr, u, o);
+            G::accumulate(v[u], pr[0], u, o);
         }
         if (more) load_v(then.id);
         if (last) {

@@ -226,14 +226,14 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
             load_k(now);
             if (left > 2 * G::KT) next = place(t0 + 2 * G::KT);
         }
-        f32x4 sc[G::KSUB];
+        f32x4 sc[1][G::KSUB];
 #pragma unroll
         for (int b = 0; b < G::KSUB; ++b) {
             typename G::RowFrag x;
             G::staged_row(krows, rbase, 16 * b, x);
-            sc[b] = G::dot(x, q, f32x4{0, 0, 0, 0});
+            sc[0][b] = G::dot(x, q, f32x4{0, 0, 0, 0});
         }
-        typename G::Probs pr;
+        typename G::Probs pr[1];
         sm.step(sc, Seen::first(min(left, job.before + r.t - t0)), a.s.mag, o, pr);
         if (left < G::KT) G::clear_past(v, left);
         const bool crosses = t0 + G::KT > job.before + lo;  // some row may not see some key
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
                 for (int j = 0; j < G::VK; ++j) z = G::chunk_zero(v[u].w[j], z);
                 if (__any(z != 0.f))
                     G::add_wild_keys(
-                        v[u], pr, u, row_bytes,
+                        v[u], pr[0], u, row_bytes,
                         [&](int key) {
                             const uint32_t off =
                                 __shfl(here.id * a.v_page + here.slot * a.v_slot, key, kWave);
@@ -255,7 +255,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
                         },
                         [&](int key) { return t0 + key < job.before + r.t; }, o);
             }
-            G::accumulate(v[u], pr, u, o);
+            G::accumulate(v[u], pr[0], u, o);
         }
         if (more) load_v(now);
     }
@@ -267,20 +267,25 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
 // Many rows: a work group of 4 wavefronts takes 4 * 16 * QB rows, a wavefront
 // 16 * QB of them, and BK keys at a time are shared in LDS. Each operand made
 // from the shared keys serves QB products.
-template <class G>
+template <class G, class T>
 struct Wide {
     static constexpr int QB = G::kDim <= 128 ? 2 : 1;  // 16-row blocks per wavefront
     static constexpr int BM = kWaves * 16 * QB;
     static constexpr int BK = G::kRowBytes <= 256 ? 64 : 32;
+    // Tiles of keys per step of the softmax. Two share its reductions, its
+    // rescale and the branches: chunks of 2048 over 32768 keys, 32 heads,
+    // 1650 -> 1500 us, 64-wide heads 236 -> 181 us. Single precision has no
+    // registers for a second tile (174 -> 200 us, spilled).
+    static constexpr int NS = sizeof(T) == 2 && BK > G::KT ? 2 : 1;
 };
 
 template <class G, class T>
 __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged_wide(
     PagedArgs a, int32_t tiles) {
-    using W = Wide<G>;
-    constexpr int NT = kWaves * kWave, BK = W::BK, QB = W::QB;
+    using W = Wide<G, T>;
+    constexpr int NT = kWaves * kWave, BK = W::BK, QB = W::QB, NS = W::NS;
     constexpr int kPieces = G::kRowBytes / 16, kLoads = BK * kPieces / NT, kStep = NT / kPieces;
-    static_assert(BK * kPieces % NT == 0 && BK % G::KT == 0, "tile shape");
+    static_assert(BK * kPieces % NT == 0 && BK % (NS * G::KT) == 0, "tile shape");
     __shared__ __align__(16) char rows[2][BK * G::kRowBytes];  // k, v
     __shared__ uint32_t off[2][2][BK];       // of this tile and the next, k and v
     __shared__ unsigned long long wild_s[2];  // keys whose value rows are not all finite
@@ -425,24 +430,31 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
         }
         const uint64_t wild = wild_s[par];
 #pragma unroll 1
-        for (int at = 0; at < BK; at += G::KT) {  // a tile's first staged row
+        for (int at = 0; at < BK; at += NS * G::KT) {  // the first staged row of NS tiles
             const int t = t0 + at;
             if (t >= mine) break;
-            const int rb = G::row_base(at), vbase = G::value_base(at);
-            f32x4 sc[QB][G::KSUB];
+            f32x4 sc[QB][NS][G::KSUB];
 #pragma unroll
-            for (int b = 0; b < G::KSUB; ++b) {
-                typename G::RowFrag k;
-                G::staged_row(rows[0], rb, 16 * b, k);
+            for (int i = 0; i < NS; ++i) {
+                const int rb = G::row_base(at + i * G::KT);
 #pragma unroll
-                for (int x = 0; x < QB; ++x) sc[x][b] = G::dot(k, q[x], f32x4{0, 0, 0, 0});
+                for (int b = 0; b < G::KSUB; ++b) {
+                    typename G::RowFrag k;
+                    G::staged_row(rows[0], rb, 16 * b, k);
+#pragma unroll
+                    for (int x = 0; x < QB; ++x)
+                        sc[x][i][b] = G::dot(k, q[x], f32x4{0, 0, 0, 0});
+                }
             }
-            if (t + G::KT > full) {  // some row does not see some key
+            if (t + NS * G::KT > full) {  // some row does not see some key
 #pragma unroll
                 for (int x = 0; x < QB; ++x)
-                    sm[x].hide(sc[x], Seen::first(min(job.k1, job.before + r[x].t) - t));
+#pragma unroll
+                    for (int i = 0; i < NS; ++i)
+                        sm[x].hide(sc[x][i], Seen::first(min(job.k1, job.before + r[x].t) - t -
+                                                         i * G::KT));
             }
-            typename G::Probs pr[QB];
+            typename G::Probs pr[QB][NS];
             float fix[QB];
             bool moved = false;
 #pragma unroll
@@ -455,25 +467,33 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
                 for (int x = 0; x < QB; ++x) G::scale_acc(o[x], fix[x]);
             }
 #pragma unroll
-            for (int b = 0; b < G::NB; ++b) {
-                const u32x4 v = G::value_frag(rows[1], vbase, b);
+            for (int i = 0; i < NS; ++i) {
+                const int vbase = G::value_base(at + i * G::KT);
 #pragma unroll
-                for (int x = 0; x < QB; ++x) o[x].o[b] = G::add_block(v, pr[x], o[x].o[b]);
+                for (int b = 0; b < G::NB; ++b) {
+                    const u32x4 v = G::value_frag(rows[1], vbase, b);
+#pragma unroll
+                    for (int x = 0; x < QB; ++x) o[x].o[b] = G::add_block(v, pr[x][i], o[x].o[b]);
+                }
             }
             if (wild == 0) continue;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const int first = at + i * G::KT;
 #pragma unroll 1
-            for (int key = 0; key < G::KT; ++key) {
-                if (!(wild >> (at + key) & 1)) continue;
-                const char* row = vb + ((uint64_t)off[par][1][at + key] << a.v_shift);
+                for (int key = 0; key < G::KT; ++key) {
+                    if (!(wild >> (first + key) & 1)) continue;
+                    const char* row = vb + ((uint64_t)off[par][1][first + key] << a.v_shift);
 #pragma unroll
-                for (int x = 0; x < QB; ++x) {
-                    const float p = G::prob_of(pr[x], key);
-                    if (t + key >= job.before + r[x].t) continue;
+                    for (int x = 0; x < QB; ++x) {
+                        const float p = G::prob_of(pr[x][i], key);
+                        if (t0 + first + key >= job.before + r[x].t) continue;
 #pragma unroll
-                    for (int b = 0; b < G::NB; ++b) {
-                        const int d = 16 * b + 4 * (lane >> 4);
-                        if (G::kFull || d < a.s.dim)
-                            o[x].o[b] = G::add_four(row + d * (int)sizeof(T), p, o[x].o[b]);
+                        for (int b = 0; b < G::NB; ++b) {
+                            const int d = 16 * b + 4 * (lane >> 4);
+                            if (G::kFull || d < a.s.dim)
+                                o[x].o[b] = G::add_four(row + d * (int)sizeof(T), p, o[x].o[b]);
+                        }
                     }
                 }
             }
@@ -523,7 +543,7 @@ bool paged_wide(int64_t rows) { return rows > 16; }
 int paged_tile_rows(int dim, int64_t rows) {
     if (!paged_wide(rows)) return 16;
     int bm = 0;
-    with_dim<float>(dim, [&](auto tag) { bm = Wide<typename decltype(tag)::Geo>::BM; });
+    with_dim<float>(dim, [&](auto tag) { bm = Wide<typename decltype(tag)::Geo, float>::BM; });
     return bm;
 }
 

@@ -636,14 +636,17 @@ template <class G, class T>
 struct Softmax {
     float m = -INFINITY, l = 0.f;
 
-    // Takes a tile's scores before their factor c > 0 (a negative one's sign
+    // Takes NS tiles' scores before their factor c > 0 (a negative one's sign
     // goes into q, and 0 makes q 0; -infinity for a key that does not count)
     // and leaves the weights; returns the factor of what was summed before.
-    __device__ __forceinline__ float weigh(const f32x4 (&s)[G::KSUB], float c,
-                                           typename G::Probs& out) {
-        float p[G::VK], top = s[0][0];
+    template <int NS>
+    __device__ __forceinline__ float weigh(const f32x4 (&s)[NS][G::KSUB], float c,
+                                           typename G::Probs (&out)[NS]) {
+        float top = s[0][0][0];
 #pragma unroll
-        for (int j = 1; j < G::VK; ++j) top = fmaxf(top, s[j >> 2][j & 3]);
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+            for (int j = 0; j < G::VK; ++j) top = fmaxf(top, s[i][j >> 2][j & 3]);
         const float mn = fmaxf(m, quad_max(top) * c);
         const float ms = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: weights 0, not NaN
         const float fix = fast_exp2(m - ms);
@@ -651,18 +654,22 @@ struct Softmax {
         const float base = kProbShift<T> - ms;
         float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < G::VK; ++j) {
-            p[j] = fast_exp2(fmaf(s[j >> 2][j & 3], c, base));
-            sum += p[j];
+        for (int i = 0; i < NS; ++i) {
+            float p[G::VK];
+#pragma unroll
+            for (int j = 0; j < G::VK; ++j) {
+                p[j] = fast_exp2(fmaf(s[i][j >> 2][j & 3], c, base));
+                sum += p[j];
+            }
+            G::pack_probs(p, out[i]);
         }
         l = l * fix + sum;
-        G::pack_probs(p, out);
         return fix;
     }
-    // weigh() of the keys that are seen, and o rescaled.
-    __device__ __forceinline__ void step(f32x4 (&s)[G::KSUB], Seen seen, float c,
-                                         typename G::Acc& o, typename G::Probs& out) {
-        hide(s, seen);
+    // weigh() of one tile's keys that are seen, and o rescaled.
+    __device__ __forceinline__ void step(f32x4 (&s)[1][G::KSUB], Seen seen, float c,
+                                         typename G::Acc& o, typename G::Probs (&out)[1]) {
+        hide(s[0], seen);
         const float fix = weigh(s, c, out);
         if (__any(fix != 1.f)) G::scale_acc(o, fix);
     }
