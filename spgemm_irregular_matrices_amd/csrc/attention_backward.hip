@@ -243,7 +243,7 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 1) void k_att
     constexpr int kPieces = G::kRowBytes / 16;        // 16-byte pieces of a row
     constexpr int kLoads = TP * kPieces / NT;         // of each tensor per thread
     constexpr int kPitch = TP * (int)sizeof(T) + 16;  // bytes between keys of P and dS
-    constexpr int kSets = G::kDim / 2 / (16 * G::kPerWord);  // 16-row results per wavefront
+    constexpr int kSets = G::kDim / 32;               // 16-index results per wavefront
     constexpr int kSteps = TP / G::KT;                // products over G::KT pairs each
     static_assert(TP * kPieces % NT == 0 && kSets >= 1, "tile shape");
     __shared__ __align__(16) char rows[2][TP * G::kRowBytes];  // q, dout
@@ -279,11 +279,9 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 1) void k_att
         for (int t = 0; t < G::QS; ++t)
             *reinterpret_cast<u32x4*>(keys[w] + G::stage_at(n, 64 * t + 16 * quad)) = f.w[t];
     }
-    f32x4 acc[kSets][G::kPerWord];
+    f32x4 acc[kSets];
 #pragma unroll
-    for (int i = 0; i < kSets; ++i)
-#pragma unroll
-        for (int c = 0; c < G::kPerWord; ++c) acc[i][c] = f32x4{0, 0, 0, 0};
+    for (int i = 0; i < kSets; ++i) acc[i] = f32x4{0, 0, 0, 0};
     HalfScale hs;
     const char* qb = a.gq.base + (int64_t)h * a.s.group * a.gq.head;
     const char* gb = a.gdout.base + (int64_t)h * a.s.group * a.gdout.head;
@@ -443,57 +441,58 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 1) void k_att
         if constexpr (half) {
             if ((w & 1) == 0 && __any(fix != 1.f)) {
 #pragma unroll
-                for (int i = 0; i < kSets; ++i)
-#pragma unroll
-                    for (int c = 0; c < G::kPerWord; ++c) acc[i][c] *= fix;
+                for (int i = 0; i < kSets; ++i) acc[i] *= fix;
             }
         }
         const char* x = rows[w & 1];
         const char* y = weights[w & 1] + n * kPitch;
-        // this lane's word of its first pair and set; opaque, so that the
-        // tile's addresses are made again in each round instead of held in
-        // registers throughout
-        int w0 = G::stage_at(G::VK * quad, (w >> 1) * (G::kRowBytes / 2) + 4 * n);
-        asm volatile("" : "+v"(w0));
-        const auto word_at = [&](int st, int j, int i) {
-            if constexpr (G::KT == 32)  // whose multiples do not move the exchange
-                return *reinterpret_cast<const uint32_t*>(x + st * 32 * G::kRowBytes +
-                                                          G::stage_more(w0, j, 64 * i));
-            return *reinterpret_cast<const uint32_t*>(x + G::stage_more(w0, G::KT * st + j, 64 * i));
-        };
-        // product st: the pairs KT*st + VK*quad + j
+        const int half_at = (w >> 1) * (G::kRowBytes / 2);
+        // of the pairs G::KT * st + G::key_of(j)
         const auto probs_at = [&](int st) {
-            const u32x4 b = *reinterpret_cast<const u32x4*>(
-                y + (G::KT * st + G::VK * quad) * (int)sizeof(T));
-            return typename G::Probs{{b[0], b[1], b[2], b[3]}};
+            const char* at = y + (G::KT * st + 4 * quad) * (int)sizeof(T);
+            if constexpr (G::k16) {
+                const u32x2 lo = *reinterpret_cast<const u32x2*>(at);
+                const u32x2 hi = *reinterpret_cast<const u32x2*>(at + 16 * sizeof(T));
+                return typename G::Probs{{lo[0], lo[1], hi[0], hi[1]}};
+            } else {
+                const u32x4 b = *reinterpret_cast<const u32x4*>(at);
+                return typename G::Probs{{b[0], b[1], b[2], b[3]}};
+            }
         };
+        // opaque, so that the tile's addresses are made again in each round
+        // instead of held in registers throughout
+        int base0 = G::value_base(0) ^ half_at;
+        asm volatile("" : "+v"(base0));
         if (tame) {
 #pragma unroll (G::k16 ? 1 : kSteps)
             for (int st = 0; st < kSteps; ++st) {
+                const int base = G::stage_more(base0, G::KT * st, 0);
                 const typename G::Probs pb = probs_at(st);
 #pragma unroll
-                for (int i = 0; i < kSets; ++i) {
-                    uint32_t word[G::VK];
-#pragma unroll
-                    for (int j = 0; j < G::VK; ++j)
-                        word[j] = word_at(st, j, i);
-                    G::accumulate_word(word, pb, acc[i]);
-                }
+                for (int i = 0; i < kSets; ++i)
+                    acc[i] = G::add_block(G::value_frag(x, base, i), pb, acc[i]);
             }
         } else {
-            // one key at a time, with the pairs that are not its own as 0
+            // key by key, with the pairs that do not have it as 0; the products
+            // and their order are the same, so other keys get the same bits
 #pragma unroll 1
             for (int st = 0; st < kSteps; ++st) {
+                const int base = G::stage_more(base0, G::KT * st, 0);
                 const typename G::Probs pb = probs_at(st);
-                const int p0 = G::KT * st + G::VK * quad;
+                uint32_t has[G::VK];
+#pragma unroll
+                for (int j = 0; j < G::VK; ++j) has[j] = bits_s[G::KT * st + G::key_of(j)];
 #pragma unroll
                 for (int i = 0; i < kSets; ++i) {
-                    uint32_t word[G::VK];
+                    const u32x4 all = G::value_frag(x, base, i);
+                    const f32x4 old = acc[i];
+#pragma unroll 1
+                    for (int key = 0; key < kColBlock; ++key) {
+                        const f32x4 z = G::add_block(
+                            G::keep(all, [&](int j) { return has[j] >> key & 1; }), pb, old);
 #pragma unroll
-                    for (int j = 0; j < G::VK; ++j) word[j] = word_at(st, j, i);
-                    G::accumulate_word_seen(
-                        word, pb, kColBlock, n,
-                        [&](int key, int j) { return bits_s[p0 + j] >> key & 1; }, acc[i]);
+                        for (int r = 0; r < 4; ++r) acc[i][r] = key == n ? z[r] : acc[i][r];
+                    }
                 }
             }
         }
@@ -502,29 +501,17 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 1) void k_att
     float f = (w & 1) ? 1.f / kProbScale<T> : a.s.scale;
     if constexpr (half) f = (w & 1) ? f : f / hs.s;
     const AttnRows& out = (w & 1) ? a.dv : a.dk;
-    constexpr int kRun = 4 * G::kPerWord;  // values next to each other in a lane's result
 #pragma unroll
     for (int i = 0; i < kSets; ++i) {
-        const int d = (w >> 1) * (G::kDim / 2) + i * 16 * G::kPerWord + kRun * quad;
+        const int d = (w >> 1) * (G::kDim / 2) + 16 * i + 4 * quad;
         if (!G::kFull && d >= a.s.dim) continue;
-        float z[kRun];
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int c = 0; c < G::kPerWord; ++c) z[G::kPerWord * r + c] = acc[i][c][r] * f;
+        const f32x4 z = acc[i] * f;
         if (pc.slot >= 0) {
             float* part = a.part_kv +
                           ((((int64_t)pc.slot * a.s.hkv + h) * kColBlock + n) * 2 + (w & 1)) * a.s.dim;
-#pragma unroll
-            for (int r = 0; r < kRun; r += 4)
-                *reinterpret_cast<f32x4*>(part + d + r) = f32x4{z[r], z[r + 1], z[r + 2], z[r + 3]};
+            *reinterpret_cast<f32x4*>(part + d) = z;
         } else {
-            char* at = out.base + col * out.row + h * out.head + d * (int)sizeof(T);
-            if constexpr (G::k16)
-                *reinterpret_cast<u32x4*>(at) = u32x4{pack2<T>(z[0], z[1]), pack2<T>(z[2], z[3]),
-                                                      pack2<T>(z[4], z[5]), pack2<T>(z[6], z[7])};
-            else
-                *reinterpret_cast<f32x4*>(at) = f32x4{z[0], z[1], z[2], z[3]};
+            G::store_four(z, out.base + col * out.row + h * out.head + d * (int)sizeof(T));
         }
     }
 }

@@ -315,33 +315,6 @@ struct Tile {
             for (int c = 0; c < kPerWord; ++c) a.o[u][kPerWord * i + c] = o[c];
         }
     }
-    // accumulate_word where a key may hold an infinity or a NaN and not every
-    // query sees every key: `times` passes, in each of which the keys that
-    // sees(pass, j) denies count as 0; a lane keeps the pass `mine`. The
-    // products and their order are the same, so finite keys give the same bits.
-    template <class Sees>
-    static __device__ __forceinline__ void accumulate_word_seen(const uint32_t (&w)[VK],
-                                                                const Probs& p, int times, int mine,
-                                                                Sees&& sees,
-                                                                f32x4 (&o)[kPerWord]) {
-        f32x4 old[kPerWord];
-#pragma unroll
-        for (int c = 0; c < kPerWord; ++c) old[c] = o[c];
-#pragma unroll 1
-        for (int t = 0; t < times; ++t) {
-            uint32_t x[VK];
-#pragma unroll
-            for (int j = 0; j < VK; ++j) x[j] = sees(t, j) ? w[j] : 0u;
-            f32x4 y[kPerWord];
-#pragma unroll
-            for (int c = 0; c < kPerWord; ++c) y[c] = old[c];
-            accumulate_word(x, p, y);
-#pragma unroll
-            for (int c = 0; c < kPerWord; ++c)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[c][r] = t == mine ? y[c][r] : o[c][r];
-        }
-    }
     // The weight that this lane's query gives to `key` of the tile.
     static __device__ __forceinline__ float prob_of(const Probs& p, int key) {
         const int j = (key & 3) + 4 * (key >> 4);
@@ -509,6 +482,18 @@ struct Tile {
                 x[r] = *reinterpret_cast<const uint32_t*>(lds + stage_more(base, r, 64 * b));
             return x;
         }
+    }
+    // v with 0 in place of the lane's keys j that on(j) denies.
+    template <class On>
+    static __device__ __forceinline__ u32x4 keep(u32x4 v, On&& on) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (k16)
+                v[i] &= (on(2 * i) ? 0xffffu : 0u) | (on(2 * i + 1) ? 0xffff0000u : 0u);
+            else
+                v[i] = on(i) ? v[i] : 0u;
+        }
+        return v;
     }
     static __device__ __forceinline__ f32x4 add_block(u32x4 v, const Probs& p, f32x4 o) {
         if constexpr (k16) {
