@@ -17,7 +17,8 @@ struct spgemm_attention_plan_s {
     AttnSide rows;    // single rows
     AttnSide blocks;  // blocks of rows, if built (n > 0)
     bool overlap = false;  // the blocks' entries are at most half of the rows'
-    AttnSide cols;
+    AttnSide cols;    // blocks of 16 columns
+    AttnSide cut_cols;  // the same in shorter pieces, for few key heads
     void* slab = nullptr;  // what ar's buffers lie in, if not in allocations of their own
     Arena ar;              // pieces, splits and entries; never changed after creation
     ~spgemm_attention_plan_s() {
@@ -43,7 +44,7 @@ struct PieceRule {
         return want < least ? least : want > 1024 ? 1024 : want;
     }
 };
-constexpr PieceRule kRowPieces{512, 64}, kBlockPieces{192, 32};
+constexpr PieceRule kRowPieces{512, 64}, kBlockPieces{192, 32}, kShortPieces{1024, 32};
 
 struct RowPieces {
     const int64_t* rp;
@@ -314,6 +315,13 @@ void build_cols(spgemm_attention_plan p, const DevCSR& m, const int32_t* col, co
     p->cols = make_side("cols", first, nblocks, ngroups, kBlockPieces, gidx, p->ar, tmp, st);
     p->cols.bits = gbits;
     p->cols.block = kColBlock;
+    p->cut_cols = p->cols;
+    if (kShortPieces.length(nblocks, ngroups) < kBlockPieces.length(nblocks, ngroups)) {
+        p->cut_cols = make_side("cut_cols", first, nblocks, ngroups, kShortPieces, gidx, p->ar,
+                                tmp, st);
+        p->cut_cols.bits = gbits;
+        p->cut_cols.block = kColBlock;
+    }
 }
 
 // Device memory given back with the scope.
@@ -340,8 +348,8 @@ int64_t kept_bytes(int64_t n, int64_t m, int64_t nnz, bool backward) {
     int64_t b = 10 * nnz + sizeof(AttnPiece) * (n + n / kRowBlock + 1 + 2 * row_cuts) +
                 2 * sizeof(AttnSplit) * row_cuts;
     if (backward)
-        b += 6 * nnz + sizeof(AttnPiece) * (m / kColBlock + 1 + col_cuts) +
-             sizeof(AttnSplit) * col_cuts;
+        b += 6 * nnz + 2 * sizeof(AttnPiece) * (m / kColBlock + 1 + col_cuts) +
+             2 * sizeof(AttnSplit) * col_cuts;
     return b + (int64_t(16) << 10);
 }
 int64_t temporary_bytes(int64_t n, int64_t m, int64_t nnz, bool backward) {
@@ -403,6 +411,16 @@ const AttnSide& row_side(spgemm_attention_plan p, AttnShape* s) {
     const bool blocks = p->blocks.n > 0 && (s->group <= 4 || (s->group <= 8 && p->overlap));
     s->mtiles = blocks ? (s->group <= 4 ? 1 : 2) : (s->group + 15) / 16;
     return blocks ? p->blocks : p->rows;
+}
+
+// The columns' side for a call: in shorter pieces where the others' work groups,
+// one for each of the key heads, are not the three or four per compute unit that
+// the chip holds at once (a mask of 1500 x 4000 with 200 entries to a row, heads
+// of 128: with 16 query heads on 2 key heads 394 -> 284 us; with 8 on 8, and
+// work groups enough, short pieces take 279 us for 263, as their sums go
+// through memory).
+const AttnSide& col_side(spgemm_attention_plan p, int hkv) {
+    return p->cols.npieces * hkv <= 1024 ? p->cut_cols : p->cols;
 }
 
 // ---------------------------------------------------------------- checks
@@ -510,7 +528,7 @@ int64_t carve_backward(spgemm_attention_plan p, AttnShape s, void* ws, BackwardA
     Carver c{static_cast<char*>(ws)};
     a->delta = c.take((__int128)p->nrows * s.hq);
     a->part_q = c.take((__int128)side.nslots * side.block * s.hq * s.dim);
-    a->part_kv = c.take((__int128)p->cols.nslots * s.hkv * kColBlock * 2 * s.dim);
+    a->part_kv = c.take((__int128)col_side(p, s.hkv).nslots * s.hkv * kColBlock * 2 * s.dim);
     return c.used;
 }
 
@@ -696,7 +714,7 @@ SPGEMM_API int spgemm_attention_backward(spgemm_attention_plan p,
         a.s = make_shape(desc);
         a.rows = row_side(p, &a.s);
         a.nrows = p->nrows;
-        a.cols = p->cols;
+        a.cols = col_side(p, a.s.hkv);
         a.ncols = p->ncols;
         if (!rows_valid(q, p->nrows, a.s.hq, desc, false, &a.q) ||
             !rows_valid(k, p->ncols, a.s.hkv, desc, false, &a.krow) ||
