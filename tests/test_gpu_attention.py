@@ -150,6 +150,15 @@ def test_long_rows_and_columns(dtype):
     _check_both(rows, q, k, v, dout, nk, 0.125)
 
 
+@pytest.mark.parametrize("dtype,hkv", [(BF16, 2), (F16, 1), (F16, 8), (F32, 2), (F32, 8)], ids=str)
+def test_long_columns_and_head_counts(dtype, hkv):
+    """2500 rows on 100 columns: blocks of columns that are cut finer for few
+    key heads than for many."""
+    rng = np.random.default_rng(hkv)
+    rows, q, k, v, dout = _case(rng, dtype, 16, hkv, hkv, nk=100, lengths=[30] * 2500)
+    _check_both(rows, q, k, v, dout, 100, 0.25)
+
+
 def test_many_entries():
     """33 million entries, more than the plan carves its buffers out of one
     allocation for: every row sees every key, so sums over the dense product
