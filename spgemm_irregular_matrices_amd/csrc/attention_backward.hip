@@ -226,18 +226,30 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
 // piece's entries, kTilePairs at a time; the other operand of S and dP is the
 // block's 16 k (or v) rows, and an entry's bits say which of the 16 scores
 // are the mask's. A tile's q and dout rows come from memory once, a tile ahead
-// of their use, and are shared in LDS. Each wavefront makes S, P, dP and dS of
-// 16 pairs (of TP / 16 wavefronts' worth), and after these are exchanged in
-// LDS too, one output (dv from dout and P, dk from q and dS) of one half of
-// the head dimension: that keeps the accumulators at an eighth of the
-// output each, where one wavefront with both outputs would need over 256
-// registers with a tile under way.
+// of their use, and are shared in LDS. S and dP of a tile are spread over the
+// wavefronts: 16 pairs each for tiles of 64, S and dP apart for tiles of 32, and
+// by halves of the head dimension too for tiles of 16 (with rows of 512 and
+// 1024 bytes these tiles let two work groups share a unit; in single precision,
+// where the products take longest, two wavefronts with all of S and dP took
+// 1260 us for 1150 with 128 values a head and, in tiles of 32, 1775 for 1390
+// with 256). After P and dS are exchanged in LDS too, each wavefront makes one
+// output (dv from dout and P, dk from q and dS) of one half of the head
+// dimension: that keeps the accumulators at an eighth of the output each, where
+// one wavefront with both outputs would need over 256 registers with a tile
+// under way. The rows are turned over for it by transposing reads; as words
+// that a byte permutation sorts it took a fifth more vector instructions (heads
+// of 256 values: 620 -> 586 us).
+// What bounds it is the gather where q and dout of the key head's group do not
+// fit a 4 MB L2: 16384 rows of 4 heads, 524288 entries without overlap, 8.6 GB
+// in 1060 us, of which 7.6 GB come from the last-level cache. Where they fit,
+// the four barriers per tile, with three or four work groups to a unit: 1000 rows
+// of 8 heads of 64, 1.2 GB in 237 us.
 constexpr int kKvWaves = 4;
 template <class G>
-constexpr int kTilePairs = G::kRowBytes <= 256 ? 64 : 32;
+constexpr int kTilePairs = G::kRowBytes <= 256 ? 64 : G::kRowBytes <= 512 ? 32 : 16;
 
 template <class G, class T>
-__global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 1) void k_attn_grad_kv(BackwardArgs a) {
+__global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 2) void k_attn_grad_kv(BackwardArgs a) {
     constexpr bool half = std::is_same<T, _Float16>::value;
     constexpr int TP = kTilePairs<G>, NT = kKvWaves * kWave;
     constexpr int kPieces = G::kRowBytes / 16;        // 16-byte pieces of a row
@@ -245,6 +257,8 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 1) void k_att
     constexpr int kPitch = TP * (int)sizeof(T) + 16;  // bytes between keys of P and dS
     constexpr int kSets = G::kDim / 32;               // 16-index results per wavefront
     constexpr int kSteps = TP / G::KT;                // products over G::KT pairs each
+    constexpr int kBlocks = TP / 16;                  // of 16 pairs, each S and dP of
+    constexpr int kParts = kKvWaves / kBlocks;        // so many wavefronts
     static_assert(TP * kPieces % NT == 0 && kSets >= 1, "tile shape");
     __shared__ __align__(16) char rows[2][TP * G::kRowBytes];  // q, dout
     __shared__ __align__(16) char weights[2][kColBlock * kPitch];  // dS, P: [key][pair]
@@ -254,6 +268,7 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 1) void k_att
     __shared__ __align__(16) uint32_t bits_s[TP];
     __shared__ float most[kKvWaves][kColBlock];
     __shared__ int wild_s[kKvWaves];
+    __shared__ __align__(16) f32x4 part_s[kParts > 1 ? kKvWaves : 1][kWave];
 
     const int tid = threadIdx.x, lane = lane_id();
     const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -375,18 +390,33 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 1) void k_att
             load_rows(t0 + TP);
             load_id(t0 + 2 * TP);
         }
-        // S, P, dP and dS of this wavefront's 16 pairs
+        // S, P, dP and dS of 16 pairs: by one wavefront, or S by one and dP by
+        // another, or of halves of the head dimension by four
+        const int blk = w % kBlocks, part = w / kBlocks;
+        f32x4 s{0, 0, 0, 0}, dp{0, 0, 0, 0};
+        {
+            int mine_at = G::stage_at(16 * blk + n, 16 * quad), rbase = G::row_base(0);
+            if constexpr (kParts == 1) {
+                s = G::template dot_staged<G::QS>(rows[0], mine_at, keys[0], rbase);
+                dp = G::template dot_staged<G::QS>(rows[1], mine_at, keys[1], rbase);
+            } else {
+                const int skip = kParts == 4 ? (part >> 1) * (G::kRowBytes / 2) : 0;
+                s = G::template dot_staged<2 * G::QS / kParts>(rows[part & 1], mine_at ^ skip,
+                                                               keys[part & 1], rbase ^ skip);
+                part_s[w][lane] = s;
+                __syncthreads();
+                if (part == 0) {
+                    dp = part_s[kBlocks + blk][lane];
+                    if constexpr (kParts == 4) {
+                        s += part_s[2 * kBlocks + blk][lane];
+                        dp += part_s[3 * kBlocks + blk][lane];
+                    }
+                }
+            }
+        }
         float pr[4], ds[4];
         float wild = 0.f;
         if (16 * w < TP) {
-            const int rbase = G::row_base(0), mine_at = G::stage_at(16 * w + n, 16 * quad);
-            typename G::RowFrag f, key;
-            G::staged_row(rows[0], mine_at, 0, f);
-            G::staged_row(keys[0], rbase, 0, key);
-            const f32x4 s = G::dot(f, key, f32x4{0, 0, 0, 0});
-            G::staged_row(rows[1], mine_at, 0, f);
-            G::staged_row(keys[1], rbase, 0, key);
-            const f32x4 dp = G::dot(f, key, f32x4{0, 0, 0, 0});
             const f32x4 l2 = *reinterpret_cast<const f32x4*>(lse_s + 16 * w + 4 * quad);
             const f32x4 dl = *reinterpret_cast<const f32x4*>(delta_s + 16 * w + 4 * quad);
             const u32x4 sees = *reinterpret_cast<const u32x4*>(bits_s + 16 * w + 4 * quad);

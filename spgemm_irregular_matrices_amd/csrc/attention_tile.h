@@ -187,20 +187,22 @@ struct Tile {
         return x;
     }
 
-    // c + A B^T over the head dimension.
+    // c + A B^T over the head dimension, and over 64 bytes of it.
+    static __device__ __forceinline__ f32x4 dot_step(u32x4 a, u32x4 b, f32x4 c) {
+        if constexpr (k16) {
+            return mfma32<T>(a, b, c);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                c = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, (uint32_t)a[j]),
+                                                         __builtin_bit_cast(float, (uint32_t)b[j]),
+                                                         c, 0, 0, 0);
+            return c;
+        }
+    }
     static __device__ __forceinline__ f32x4 dot(const RowFrag& a, const RowFrag& b, f32x4 c) {
 #pragma unroll
-        for (int t = 0; t < QS; ++t) {
-            if constexpr (k16) {
-                c = mfma32<T>(a.w[t], b.w[t], c);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    c = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                        __builtin_bit_cast(float, (uint32_t)a.w[t][j]),
-                        __builtin_bit_cast(float, (uint32_t)b.w[t][j]), c, 0, 0, 0);
-            }
-        }
+        for (int t = 0; t < QS; ++t) c = dot_step(a.w[t], b.w[t], c);
         return c;
     }
 
@@ -415,6 +417,17 @@ struct Tile {
 #pragma unroll
         for (int t = 0; t < QS; ++t)
             f.w[t] = *reinterpret_cast<const u32x4*>(lds + stage_more(base, dr, 64 * t));
+    }
+    // dot() of two staged rows, of STEPS steps of 64 bytes from the bases on.
+    template <int STEPS>
+    static __device__ __forceinline__ f32x4 dot_staged(const char* a, int abase, const char* b,
+                                                       int bbase) {
+        f32x4 c{0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < STEPS; ++t)
+            c = dot_step(*reinterpret_cast<const u32x4*>(a + stage_more(abase, 0, 64 * t)),
+                         *reinterpret_cast<const u32x4*>(b + stage_more(bbase, 0, 64 * t)), c);
+        return c;
     }
     static __device__ __forceinline__ void stage_chunk(char* lds, int base, int j, int u,
                                                        const uint32_t (&w)[VW]) {
