@@ -129,8 +129,8 @@ struct PagedArgs {
 void paged_attention(const PagedArgs& a, hipStream_t st);
 // Whether a work group shares the keys of a sequence's `rows` rows (new
 // tokens times the query heads of a key head), and the rows of its tiles.
-bool paged_wide(int64_t rows);
-int paged_tile_rows(int dim, int64_t rows);
+bool paged_wide(const AttnShape& s, int64_t rows);
+int paged_tile_rows(const AttnShape& s, int64_t rows);
 
 // XCD x of the 8 gets every eighth work group; this gives each XCD a
 // contiguous eighth of the logical blocks, so that neighbouring pieces of one

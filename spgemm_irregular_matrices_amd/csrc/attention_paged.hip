@@ -133,7 +133,9 @@ __device__ __forceinline__ void store_row(const PagedArgs& a, const TileJob& j, 
 
 // Few rows per sequence and key head: one wavefront takes 16 rows and one
 // piece of the keys, straight from memory. The next tile's rows are under way
-// while one is computed, as in the forward pass over a mask.
+// while one is computed, as in the forward pass over a mask. Bound by memory:
+// the next token of 64 sequences of 8.5 K tokens on average, 8 key heads of
+// 128, reads 2.2 GB in 492 us (4.5 TB/s; a large copy moves 4.9).
 template <class G, class T>
 __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged(PagedArgs a,
                                                                                  int32_t tiles) {
@@ -266,7 +268,10 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
 
 // Many rows: a work group of 4 wavefronts takes 4 * 16 * QB rows, a wavefront
 // 16 * QB of them, and BK keys at a time are shared in LDS. Each operand made
-// from the shared keys serves QB products.
+// from the shared keys serves QB products. 2596 new tokens of two sequences, 46 K tokens together, 32 heads of 128:
+// 1.2 TFLOP in 1500 us, 800 TFLOP/s. The vector unit's softmax and the matrix
+// units are 45 % and 35 % busy, which with two wavefronts to a SIMD (256
+// registers each) hide each other only in part.
 template <class G, class T>
 struct Wide {
     static constexpr int QB = G::kDim <= 128 ? 2 : 1;  // 16-row blocks per wavefront
@@ -538,10 +543,19 @@ __global__ __launch_bounds__(kWaves* kWave) void k_paged_join(PagedArgs a) {
 
 }  // namespace
 
-bool paged_wide(int64_t rows) { return rows > 16; }
+// 16 sequences of 4.2 K tokens on average, 4 key heads, bf16 of 128 values a
+// head: 20 rows 56 us by single wavefronts, 49 us shared (16 rows: 57 and 49, but
+// with 64 values 28 and 32). The shared tiles are of 128 rows whatever is there
+// (64 from 129 values on), which costs more where products take longer: 256
+// values 88 and 110 us at 20 rows, 113 and 114 at 48, 151 and 117 at 64; single
+// precision 97 and 186 at 20, 232 and 309 at 96 (64 values: 179 and 176).
+bool paged_wide(const AttnShape& s, int64_t rows) {
+    return rows > (s.type == SPGEMM_TYPE_F32 ? 96 : s.dim > 128 ? 48 : 16);
+}
 
-int paged_tile_rows(int dim, int64_t rows) {
-    if (!paged_wide(rows)) return 16;
+int paged_tile_rows(const AttnShape& s, int64_t rows) {
+    if (!paged_wide(s, rows)) return 16;
+    const int dim = s.dim;
     int bm = 0;
     with_dim<float>(dim, [&](auto tag) { bm = Wide<typename decltype(tag)::Geo, float>::BM; });
     return bm;
@@ -549,14 +563,14 @@ int paged_tile_rows(int dim, int64_t rows) {
 
 void paged_attention(const PagedArgs& a, hipStream_t st) {
     const int64_t rows = (int64_t)a.max_new * a.s.group;
-    const int64_t tiles = ceil_div(rows, paged_tile_rows(a.s.dim, rows));
+    const int64_t tiles = ceil_div(rows, paged_tile_rows(a.s, rows));
     if (a.seqs == 0 || a.tokens == 0 || tiles == 0) return;
     const int64_t units = a.seqs * a.s.hkv * a.npieces * tiles;
     with_type(a.s.type, a.s.dim, [&](auto tag) {
         using Tag = decltype(tag);
         using G = typename Tag::Geo;
         using T = typename Tag::Elem;
-        if (paged_wide(rows)) {
+        if (paged_wide(a.s, rows)) {
             auto run = k_paged_wide<G, T>;
             hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(units))), dim3(kWaves * kWave), 0, st, a,
                                (int32_t)tiles);

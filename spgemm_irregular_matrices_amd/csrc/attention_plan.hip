@@ -552,25 +552,30 @@ bool batch_sizes_fit(const spgemm_paged_batch* b, const spgemm_attention_desc* d
            b->tokens <= kMaxTokens && b->max_length <= kMaxTokens;
 }
 
-// Keys per piece. Where there are few rows the keys are cut: for wavefronts
-// with keys of their own until 4096 (16 per compute unit) have a piece of at
-// least 64 keys each; for work groups that share keys, of which a compute unit
-// holds two (one from 129 values per head on), until there are as many as the
-// chip holds, with at least 256 keys each: their pieces cost more to join.
+// Keys per piece. Where there are few rows the keys are cut until there are as
+// many wavefronts with keys of their own, or work groups that share keys, as the
+// chip holds at once: of the first eight to a compute unit (four from 129 values
+// per head on), with at least 64 keys each, of the second two (one), with at
+// least 256 keys each, as their pieces cost more to join. (Twice as many of the
+// first are no better loaded and have twice the pieces to join: the next token
+// of 64 sequences of 8.5 K tokens, 64 heads on 8, 503 us for 468; of 16
+// sequences, 16 heads of 256 on 2, 93 us for 52 with four times as many. Half as
+// many take 534 us of the former.)
 // Twice as many where the batch's chunks differ and are of several tiles, for
 // then its texts differ too, and the longest would end last (16 chunks of up
 // to 128 tokens, 7 heads of 64: 88 -> 64 us; 8 chunks of up to 8 tokens, one
 // tile each, take 55 us, and 64 us if cut so).
 void shape_pieces(PagedArgs* a) {
     const int64_t rows = (int64_t)a->max_new * a->s.group;
-    const bool wide = paged_wide(rows);
-    const int64_t tile = paged_tile_rows(a->s.dim, rows);
+    const bool wide = paged_wide(a->s, rows);
+    const int64_t tile = paged_tile_rows(a->s, rows);
     const int64_t whole_tiles = a->seqs * ceil_div(rows, tile);
     const int64_t tiles = std::min(whole_tiles, a->seqs + a->tokens * a->s.group / tile);
     const bool ragged = rows > tile && a->tokens * 4 < a->seqs * a->max_new * 3;
     const int64_t units = std::max<int64_t>(a->s.hkv * tiles, 1);
     const int64_t most = std::max<int64_t>(ceil_div(a->max_length, wide ? 256 : 64), 1);
-    const int64_t target = !wide ? 4096 : (a->s.dim <= 128 ? 512 : 256) * (ragged ? 2 : 1);
+    const int64_t target =
+        (a->s.dim <= 128 ? 2 : 1) * (!wide ? 1024 : ragged ? 512 : 256);
     const int64_t want = std::min(std::max<int64_t>(target / units, 1), most);
     const int64_t step = wide ? 64 : 32;
     a->piece = (int32_t)std::max<int64_t>(
