@@ -135,7 +135,7 @@ __device__ __forceinline__ void store_row(const PagedArgs& a, const TileJob& j, 
 // piece of the keys, straight from memory. The next tile's rows are under way
 // while one is computed, as in the forward pass over a mask. Bound by memory:
 // the next token of 64 sequences of 8.5 K tokens on average, 8 key heads of
-// 128, reads 2.2 GB in 492 us (4.5 TB/s; a large copy moves 4.9).
+// 128, reads 2.2 GB in 468 us with the join (4.7 TB/s; a large copy moves 4.9).
 template <class G, class T>
 __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged(PagedArgs a,
                                                                                  int32_t tiles) {

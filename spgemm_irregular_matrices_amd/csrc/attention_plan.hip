@@ -237,7 +237,8 @@ AttnSide make_side(const char* name, const int64_t* rp, int64_t n, int64_t nnz, 
 
 // Blocks of 4 rows, where they serve: the rows are short (they share tiles) or
 // store the same columns (they share keys), and their columns ascend (else
-// the blocks stay unbuilt and single rows do).
+// the blocks stay unbuilt and single rows do). 4 heads to a key head, 8192 rows of
+// 128 spread keys: 159 us by blocks and 172 by rows; of 256 keys 277 by either.
 bool blocks_serve(int64_t n, int64_t nnz, int64_t entries) {
     return nnz < 192 * n || entries <= nnz / 4 * 3;
 }
@@ -407,6 +408,10 @@ int build_plan(spgemm_attention_plan p, const spgemm_csr* mask, bool backward, b
 
 // The rows' side for a call, and its tiles of 16 queries: blocks of 4 rows
 // where their queries fill one tile, or two that mostly see the same keys.
+// bf16, 128 values a head, by blocks and by single rows: 4 query heads to a key
+// head, 509 K entries of 16384 rows by a power law 270 and 318 us, a window of
+// 256 48 and 132 us, 8192 rows of 24 spread keys 53 and 61 us; 8 heads, a window
+// of 256 88 and 136 us, but 8192 rows of 64 spread keys 184 and 119 us.
 const AttnSide& row_side(spgemm_attention_plan p, AttnShape* s) {
     const bool blocks = p->blocks.n > 0 && (s->group <= 4 || (s->group <= 8 && p->overlap));
     s->mtiles = blocks ? (s->group <= 4 ? 1 : 2) : (s->group + 15) / 16;
@@ -563,7 +568,7 @@ bool batch_sizes_fit(const spgemm_paged_batch* b, const spgemm_attention_desc* d
 // many take 534 us of the former.)
 // Twice as many where the batch's chunks differ and are of several tiles, for
 // then its texts differ too, and the longest would end last (16 chunks of up
-// to 128 tokens, 7 heads of 64: 88 -> 64 us; 8 chunks of up to 8 tokens, one
+// to 128 tokens, 7 heads of 64: 88 -> 59 us; 8 chunks of up to 8 tokens, one
 // tile each, take 55 us, and 64 us if cut so).
 void shape_pieces(PagedArgs* a) {
     const int64_t rows = (int64_t)a->max_new * a->s.group;
@@ -574,8 +579,7 @@ void shape_pieces(PagedArgs* a) {
     const bool ragged = rows > tile && a->tokens * 4 < a->seqs * a->max_new * 3;
     const int64_t units = std::max<int64_t>(a->s.hkv * tiles, 1);
     const int64_t most = std::max<int64_t>(ceil_div(a->max_length, wide ? 256 : 64), 1);
-    const int64_t target =
-        (a->s.dim <= 128 ? 2 : 1) * (!wide ? 1024 : ragged ? 512 : 256);
+    const int64_t target = (a->s.dim <= 128 ? 2 : 1) * (!wide ? 1024 : ragged ? 512 : 256);
     const int64_t want = std::min(std::max<int64_t>(target / units, 1), most);
     const int64_t step = wide ? 64 : 32;
     a->piece = (int32_t)std::max<int64_t>(

@@ -542,6 +542,30 @@ def test_paged_later_tokens_reach_nothing(dtype, wild):
     assert not torch.isfinite(out[before:20]).all(2).any()
 
 
+@pytest.mark.parametrize("new", [8, 24, 120])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=str)
+@pytest.mark.parametrize("d", [64, 128, 200])
+def test_paged_chunk_sizes(dtype, d, new):
+    """Chunks of 16 to 240 rows to a key head, in the tiles of single wavefronts
+    and of work groups; then a wild key and value that only later tokens see."""
+    rng = np.random.default_rng(d + new)
+    seqs = [(40 + new, new), (new, new), (310, max(1, new // 3)), (3, 1)]
+    c = _paged_case(rng, dtype, d, 4, 2, 16, seqs)
+    clean = _paged_run(c)
+    _paged_check(c, seqs, d ** -0.5, *clean)
+    at = 40 + new // 2  # seen by the first sequence's tokens from new // 2 on
+    page = int(c["table"].col[at // 16])
+    c["k"][page, at % 16], c["v"][page, at % 16] = float("nan"), float("inf")
+    got = _paged_run(c)
+    sees = torch.zeros(len(c["q"]), dtype=torch.bool, device="cuda")
+    sees[new // 2:new] = True
+    tokens = sum(m for _, m in seqs)
+    for a, b in zip(got, clean):
+        assert torch.equal(a[:tokens][~sees[:tokens]], b[:tokens][~sees[:tokens]])
+    assert not torch.isfinite(got[0][sees].float()).any()
+    assert not torch.isfinite(got[1][sees]).any()
+
+
 def test_paged_equals_lower_triangular_mask():
     """Used together: a text read in chunks over the cache gives what one call
     over a lower triangular mask gives, to the roundings of the two."""
