@@ -122,7 +122,9 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
         const int left = cur.len - cur.t0;
         const bool last = left <= G::KT, more = ahead.more;
         if (fresh) {
-            delta = quad_sum(G::dot_lane(dout, out));
+            // summed as dP is, so that a row's only key, whose value is `out`,
+            // has dS = 0 to the last bit
+            delta = G::dot_own(out, dout);
             seen_lse = lse;
             const int64_t row = row_of(st.row(cur.i));
             if (here(row) && lane < 16 && st.lead(cur.i)) a.delta[row * a.s.hq + me.hq] = delta;
@@ -145,7 +147,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
             G::staged_row(krows, rbase, 16 * b, x);
             s[b] = G::dot(x, q, f32x4{0, 0, 0, 0});
             G::staged_row(vrows, rbase, 16 * b, x);
-            dp[b] = G::dot(x, dout, f32x4{0, 0, 0, 0});
+            dp[b] = G::dot_halves(x, dout);
         }
         if (more && last) load_q(ahead.i);
         const PieceStream::Cursor after = ahead;

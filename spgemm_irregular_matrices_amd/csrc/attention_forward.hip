@@ -138,7 +138,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
         }
         if (more) load_v(then.id);
         if (last) {
-            sm.finish();
+            sm.finish(a.s.mag);
             const int slot = st.slot(cur.i);
             const int64_t row = row_of(st.row(cur.i));
             if (here(row) && slot < 0) {

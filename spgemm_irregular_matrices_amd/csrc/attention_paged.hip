@@ -261,7 +261,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
         }
         if (more) load_v(now);
     }
-    sm.finish();
+    sm.finish(a.s.mag);
     if (__any(wrong)) sm.l = NAN;
     store_row<G, T>(a, job, r, piece, o, sm);
 }
@@ -508,7 +508,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
     const bool wrong = wrong_s != 0;
 #pragma unroll
     for (int x = 0; x < QB; ++x) {
-        sm[x].finish();
+        sm[x].finish(a.s.mag);
         if (wrong) sm[x].l = NAN;
         store_row<G, T>(a, job, r[x], piece, o[x], sm[x]);
     }

@@ -166,27 +166,6 @@ struct Tile {
         for (int t = 0; t < QS; ++t) f.w[t] = u32x4{0, 0, 0, 0};
     }
 
-    // This lane's share of the products a[i] * b[i].
-    static __device__ __forceinline__ float dot_lane(const RowFrag& a, const RowFrag& b) {
-        float x = 0.f;
-#pragma unroll
-        for (int t = 0; t < QS; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (k16) {
-                    float a0, a1, b0, b1;
-                    unpack2<T>(a.w[t][i], a0, a1);
-                    unpack2<T>(b.w[t][i], b0, b1);
-                    x = fmaf(a0, b0, x);
-                    x = fmaf(a1, b1, x);
-                } else {
-                    x = fmaf(__builtin_bit_cast(float, (uint32_t)a.w[t][i]),
-                             __builtin_bit_cast(float, (uint32_t)b.w[t][i]), x);
-                }
-            }
-        return x;
-    }
-
     // c + A B^T over the head dimension, and over 64 bytes of it.
     static __device__ __forceinline__ f32x4 dot_step(u32x4 a, u32x4 b, f32x4 c) {
         if constexpr (k16) {
@@ -204,6 +183,24 @@ struct Tile {
 #pragma unroll
         for (int t = 0; t < QS; ++t) c = dot_step(a.w[t], b.w[t], c);
         return c;
+    }
+    // A B^T with the bits that the column pass gets, which takes rows of 1024
+    // bytes by halves.
+    static __device__ __forceinline__ f32x4 dot_halves(const RowFrag& a, const RowFrag& b) {
+        f32x4 c[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+        for (int t = 0; t < QS; ++t) {
+            const int half = kRowBytes == 1024 && t >= QS / 2;
+            c[half] = dot_step(a.w[t], b.w[t], c[half]);
+        }
+        return kRowBytes == 1024 ? c[0] + c[1] : c[0];
+    }
+    // a . b of this lane's own row, summed as dot_halves() sums it.
+    static __device__ __forceinline__ float dot_own(const RowFrag& a, const RowFrag& b) {
+        const f32x4 all = dot_halves(a, b);
+        const int n = lane_id() & 15;
+        const float lo = n & 1 ? all[1] : all[0], hi = n & 1 ? all[3] : all[2];
+        return __shfl(n & 2 ? hi : lo, 16 * (n >> 2) + n, kWave);
     }
 
     // The position in the tile of this lane's j-th key of P^T and V.
@@ -632,7 +629,7 @@ struct Seen {
 // the sum covers this lane's keys only until finish().
 template <class G, class T>
 struct Softmax {
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f;  // m: see weigh()
 
     // Takes NS tiles' scores before their factor c > 0 (a negative one's sign
     // goes into q, and 0 makes q 0; -infinity for a key that does not count)
@@ -645,9 +642,13 @@ struct Softmax {
         for (int i = 0; i < NS; ++i)
 #pragma unroll
             for (int j = 0; j < G::VK; ++j) top = fmaxf(top, s[i][j >> 2][j & 3]);
-        const float mn = fmaxf(m, quad_max(top) * c);
+        // Single precision keeps m before its factor until finish(): the
+        // largest weight is 1 to the last bit then, and a row's only key gives
+        // its value unchanged. 16 bits round that difference away.
+        constexpr bool late = sizeof(T) == 4;
+        const float mn = fmaxf(m, late ? quad_max(top) : quad_max(top) * c);
         const float ms = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: weights 0, not NaN
-        const float fix = fast_exp2(m - ms);
+        const float fix = fast_exp2(late ? (m - ms) * c : m - ms);
         m = mn;
         const float base = kProbShift<T> - ms;
         float sum = 0.f;
@@ -656,7 +657,8 @@ struct Softmax {
             float p[G::VK];
 #pragma unroll
             for (int j = 0; j < G::VK; ++j) {
-                p[j] = fast_exp2(fmaf(s[i][j >> 2][j & 3], c, base));
+                const float x = s[i][j >> 2][j & 3];
+                p[j] = fast_exp2(late ? (x - ms) * c : fmaf(x, c, base));
                 sum += p[j];
             }
             G::pack_probs(p, out[i]);
@@ -676,7 +678,10 @@ struct Softmax {
         for (int j = 0; j < G::VK; ++j)
             s[j >> 2][j & 3] = seen.pick(j, s[j >> 2][j & 3], -INFINITY);
     }
-    __device__ __forceinline__ void finish() { l = quad_sum(l); }
+    __device__ __forceinline__ void finish(float c) {
+        l = quad_sum(l);
+        if (sizeof(T) == 4) m *= c;
+    }
     __device__ __forceinline__ float factor() const { return l == 0.f ? 0.f : 1.f / l; }
     __device__ __forceinline__ float lse() const {
         return l == 0.f ? -INFINITY : (m - kProbShift<T> + fast_log2(l)) * kLn2;

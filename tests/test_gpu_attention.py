@@ -343,6 +343,25 @@ def test_offsets_past_32_bits():
     assert not dk[rest].any() and not dv[rest].any()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=str)
+@pytest.mark.parametrize("d", [40, 64, 128, 200, 256])
+def test_only_keys_have_no_gradient(dtype, d):
+    """A row with one key: o is its value, and dq and dk are 0, to the last bit."""
+    rng = np.random.default_rng(d)
+    nq, nk = 37, 50
+    q, dout = (_rand(rng, (nq, 4, d), dtype) for _ in range(2))
+    k, v = (_rand(rng, (nk, 2, d), dtype) for _ in range(2))
+    rows = [np.array([rng.integers(nk)]) for _ in range(nq)]
+    api = _api()
+    with api.AttentionPlan(ref.csr(rows, nk), backward=True) as plan:
+        out, lse = plan.forward(q, k, v)
+        dq, dk, dv = plan.backward(dout, q, k, v, out, lse)
+    seen = torch.from_numpy(np.concatenate(rows)).cuda()
+    assert torch.equal(out, v[seen].repeat_interleave(2, 1))
+    assert not dq.any() and not dk.any()
+    assert dv[seen].any()
+
+
 def test_same_bits_every_time():
     api = _api()
     rng = np.random.default_rng(21)
