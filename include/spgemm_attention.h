@@ -180,8 +180,9 @@ SPGEMM_API int spgemm_paged_attention_workspace(const spgemm_attention_desc* des
  * npages), gets NaN in those of its first max_new rows that exist (a page
  * that only some of its tokens need: in those tokens' rows at least); no
  * memory outside the arrays is touched. `lse` may be NULL. Errors:
- * INVALID_ARG, OVERFLOW (as spgemm_attention_forward; max_length or sequences
- * over 2^30, or 2^31 - 1 or more pairs of token and query head), HIP. */
+ * INVALID_ARG, OVERFLOW (as spgemm_attention_forward; tokens, max_length or
+ * the page size over 2^30, 2^30 or more sequences, more than 2^31 - 128 pairs
+ * of token and query head, 2^31 or more pages or entries of their table), HIP. */
 SPGEMM_API int spgemm_paged_attention(const spgemm_attention_desc* desc, const spgemm_rows* q,
                                       const spgemm_paged_cache* cache,
                                       const spgemm_paged_batch* batch, const spgemm_rows* out,

@@ -130,6 +130,7 @@ void paged_attention(const PagedArgs& a, hipStream_t st);
 // Whether a work group shares the keys of a sequence's `rows` rows (new
 // tokens times the query heads of a key head), and the rows of its tiles.
 bool paged_wide(const AttnShape& s, int64_t rows);
+constexpr int kPagedTileMost = 128;
 int paged_tile_rows(const AttnShape& s, int64_t rows);
 
 // XCD x of the 8 gets every eighth work group; this gives each XCD a

@@ -276,6 +276,7 @@ template <class G, class T>
 struct Wide {
     static constexpr int QB = G::kDim <= 128 ? 2 : 1;  // 16-row blocks per wavefront
     static constexpr int BM = kWaves * 16 * QB;
+    static_assert(BM <= kPagedTileMost, "the limit of rows counts on it");
     static constexpr int BK = G::kRowBytes <= 256 ? 64 : 32;
     // Tiles of keys per step of the softmax. Two share its reductions, its
     // rescale and the branches: chunks of 2048 over 32768 keys, 32 heads,

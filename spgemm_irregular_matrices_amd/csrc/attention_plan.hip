@@ -552,9 +552,11 @@ bool batch_sizes_valid(const spgemm_paged_batch* b) {
            b->max_length >= 0;
 }
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
+// A tile's rows are counted in 32 bits, those of its last one past the end too.
+constexpr int64_t kMaxPairs = (int64_t(1) << 31) - kPagedTileMost;
 bool batch_sizes_fit(const spgemm_paged_batch* b, const spgemm_attention_desc* d) {
-    return b->pages->nrows < kMaxTokens && b->tokens * d->heads_q < 0x7fffffffLL &&
-           b->tokens <= kMaxTokens && b->max_length <= kMaxTokens;
+    return b->pages->nrows < kMaxTokens && b->tokens <= kMaxTokens &&
+           b->max_length <= kMaxTokens && b->tokens * d->heads_q <= kMaxPairs;
 }
 
 // Keys per piece. Where there are few rows the keys are cut until there are as

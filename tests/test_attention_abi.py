@@ -99,3 +99,20 @@ def test_no_gpu_call_fails_loudly():
     cache = torch.zeros(1, 16, 1, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         attention.paged_attention(q, cache, cache, mask, torch.tensor([0, 1]), torch.tensor([1]), 1, 1)
+
+
+def test_paged_sizes_at_their_limits():
+    """A tile of up to 128 rows begins inside the last sequence's rows, so its end fits 32 bits
+    only up to 2^31 - 128 pairs of token and query head; larger products must not wrap around."""
+    d = attention.Desc(0, 8, 8, 128, 0.1)
+    most = (2 ** 31 - 128) // 8
+    assert _paged_bytes(d, tokens=most, max_length=32) == (0, 0)
+    for tokens in (most + 1, 2 ** 28, 2 ** 61, 2 ** 61 + 1, 2 ** 63 - 1):
+        assert _paged_bytes(d, tokens=tokens, max_length=32)[0] == -4, tokens
+    many = attention.Desc(0, 65536, 1, 128, 0.1)
+    for tokens in (2 ** 15, 2 ** 47, 2 ** 48, 2 ** 48 + 1):
+        assert _paged_bytes(many, tokens=tokens, max_length=32)[0] == -4, tokens
+    one = attention.Desc(0, 1, 1, 128, 0.1)
+    assert _paged_bytes(one, tokens=2 ** 30, max_new=2 ** 30, max_length=2 ** 30)[0] == 0
+    for tokens in (2 ** 30 + 1, 2 ** 62):
+        assert _paged_bytes(one, tokens=tokens, max_length=32)[0] == -4, tokens
