@@ -440,35 +440,55 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
             const int t = t0 + at;
             if (t >= mine) break;
             f32x4 sc[QB][NS][G::KSUB];
+            const auto scores = [&](int at) {
 #pragma unroll
-            for (int i = 0; i < NS; ++i) {
-                const int rb = G::row_base(at + i * G::KT);
+                for (int i = 0; i < NS; ++i) {
+                    const int rb = G::row_base(at + i * G::KT);
 #pragma unroll
-                for (int b = 0; b < G::KSUB; ++b) {
-                    typename G::RowFrag k;
-                    G::staged_row(rows[0], rb, 16 * b, k);
+                    for (int b = 0; b < G::KSUB; ++b) {
+                        typename G::RowFrag k;
+                        G::staged_row(rows[0], rb, 16 * b, k);
+#pragma unroll
+                        for (int x = 0; x < QB; ++x)
+                            sc[x][i][b] = G::dot(k, q[x], f32x4{0, 0, 0, 0});
+                    }
+                }
+                if (t + NS * G::KT > full) {  // some row does not see some key
 #pragma unroll
                     for (int x = 0; x < QB; ++x)
-                        sc[x][i][b] = G::dot(k, q[x], f32x4{0, 0, 0, 0});
+#pragma unroll
+                        for (int i = 0; i < NS; ++i)
+                            sm[x].hide(sc[x][i], Seen::first(min(job.k1, job.before + r[x].t) - t -
+                                                             i * G::KT));
                 }
-            }
-            if (t + NS * G::KT > full) {  // some row does not see some key
-#pragma unroll
-                for (int x = 0; x < QB; ++x)
-#pragma unroll
-                    for (int i = 0; i < NS; ++i)
-                        sm[x].hide(sc[x][i], Seen::first(min(job.k1, job.before + r[x].t) - t -
-                                                         i * G::KT));
-            }
+            };
+            scores(at);
             typename G::Probs pr[QB][NS];
-            float fix[QB];
-            bool moved = false;
+            float fix[QB], old[QB];
+            bool moved = false, far = false;
 #pragma unroll
             for (int x = 0; x < QB; ++x) {
-                fix[x] = sm[x].weigh(sc[x], a.s.mag, pr[x]);
+                bool one;
+                old[x] = sm[x].l;
+                fix[x] = sm[x].template weigh<false>(sc[x], a.s.mag, pr[x], one);
                 moved |= fix[x] != 1.f;
+                far |= one;
             }
-            if (__any(moved)) {
+            if (__any(moved || far)) {
+                if (__any(far)) {
+                    // Hardly ever, so the scores are made again; from 128 values on
+                    // they look like others to the compiler, which would keep
+                    // them through every step in registers that are not there.
+                    // (Asked before the exponentials, which it keeps from
+                    // running beside each other, the branch took 1494 -> 1524
+                    // us for chunks of 2048 over 32768 keys.)
+                    int again = at;
+                    if constexpr (G::kDim > 64) asm volatile("" : "+s"(again));
+                    scores(again);
+#pragma unroll
+                    for (int x = 0; x < QB; ++x)
+                        sm[x].weigh_far(sc[x], a.s.mag, old[x], fix[x], pr[x]);
+                }
 #pragma unroll
                 for (int x = 0; x < QB; ++x) G::scale_acc(o[x], fix[x]);
             }

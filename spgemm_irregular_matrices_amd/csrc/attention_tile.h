@@ -629,27 +629,35 @@ struct Seen {
 // the sum covers this lane's keys only until finish().
 template <class G, class T>
 struct Softmax {
-    float m = -INFINITY, l = 0.f;  // m: see weigh()
+    // Single precision keeps m before its factor until finish(): the largest
+    // weight is 1 to the last bit then, and a row's only key gives its value
+    // unchanged. 16 bits round that difference away, unless m is far from 0:
+    // from 2^13 on its own rounding, up to 2^-24 of it, is not small beside a
+    // weight's, and from about 2^24 on 2 to the power of that rounding, which
+    // is what the largest weight becomes, passes the types' ranges at either
+    // end. There the products are rounded as the maximum's was, which makes it 1
+    // again and takes two instructions a weight for one.
+    static constexpr bool kLate = sizeof(T) == 4;
+    static constexpr float kFar = 8192.f;
+    float m = -INFINITY, l = 0.f;
 
     // Takes NS tiles' scores before their factor c > 0 (a negative one's sign
     // goes into q, and 0 makes q 0; -infinity for a key that does not count)
     // and leaves the weights; returns the factor of what was summed before.
-    template <int NS>
+    // far: whether this lane's query is so; without EXACT it is left at that.
+    template <bool EXACT, int NS>
     __device__ __forceinline__ float weigh(const f32x4 (&s)[NS][G::KSUB], float c,
-                                           typename G::Probs (&out)[NS]) {
+                                           typename G::Probs (&out)[NS], bool& far) {
         float top = s[0][0][0];
 #pragma unroll
         for (int i = 0; i < NS; ++i)
 #pragma unroll
             for (int j = 0; j < G::VK; ++j) top = fmaxf(top, s[i][j >> 2][j & 3]);
-        // Single precision keeps m before its factor until finish(): the
-        // largest weight is 1 to the last bit then, and a row's only key gives
-        // its value unchanged. 16 bits round that difference away.
-        constexpr bool late = sizeof(T) == 4;
-        const float mn = fmaxf(m, late ? quad_max(top) : quad_max(top) * c);
+        const float mn = fmaxf(m, kLate ? quad_max(top) : quad_max(top) * c);
         const float ms = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: weights 0, not NaN
-        const float fix = fast_exp2(late ? (m - ms) * c : m - ms);
+        const float fix = fast_exp2(kLate ? (m - ms) * c : m - ms);
         m = mn;
+        far = !kLate && fabsf(ms) >= kFar;
         const float base = kProbShift<T> - ms;
         float sum = 0.f;
 #pragma unroll
@@ -658,7 +666,19 @@ struct Softmax {
 #pragma unroll
             for (int j = 0; j < G::VK; ++j) {
                 const float x = s[i][j >> 2][j & 3];
-                p[j] = fast_exp2(late ? (x - ms) * c : fmaf(x, c, base));
+                p[j] = kLate ? (x - ms) * c : fmaf(x, c, base);
+            }
+            if (EXACT && __builtin_expect(__any(far), 0)) {
+#pragma clang fp contract(off)
+#pragma unroll
+                for (int j = 0; j < G::VK; ++j) {
+                    const float apart = s[i][j >> 2][j & 3] * c - ms + kProbShift<T>;
+                    p[j] = far ? apart : p[j];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < G::VK; ++j) {
+                p[j] = fast_exp2(p[j]);
                 sum += p[j];
             }
             G::pack_probs(p, out[i]);
@@ -666,11 +686,23 @@ struct Softmax {
         l = l * fix + sum;
         return fix;
     }
+    // After weigh<false> where some query was far: its weights EXACT, from the
+    // scores that it had (other queries' results keep their bits). old: l before.
+    template <int NS>
+    __device__ __forceinline__ void weigh_far(const f32x4 (&s)[NS][G::KSUB], float c, float old,
+                                              float fix, typename G::Probs (&out)[NS]) {
+        const float near = l;
+        bool far;
+        l = old * fix;
+        (void)weigh<true>(s, c, out, far);
+        l = far ? l : near;
+    }
     // weigh() of one tile's keys that are seen, and o rescaled.
     __device__ __forceinline__ void step(f32x4 (&s)[1][G::KSUB], Seen seen, float c,
                                          typename G::Acc& o, typename G::Probs (&out)[1]) {
         hide(s[0], seen);
-        const float fix = weigh(s, c, out);
+        bool far;
+        const float fix = weigh<true>(s, c, out, far);
         if (__any(fix != 1.f)) G::scale_acc(o, fix);
     }
     static __device__ __forceinline__ void hide(f32x4 (&s)[G::KSUB], Seen seen) {
