@@ -116,7 +116,9 @@ SPGEMM_API int spgemm_attention_forward(spgemm_attention_plan plan,
 
 /* Gradients of a scalar with respect to q, k and v, given its gradient dout
  * with respect to o, and o and lse as the forward call left them. The
- * probabilities are recomputed from q, k and lse:
+ * probabilities are recomputed from q, k and lse (a float: of scores past 10^4
+ * its rounding, 2^-24 of it, is the larger part of a probability's relative
+ * error; none is taken as more than 1):
  *
  *   delta_i = dout_i . o_i          ds_ij = p_ij (dout_i . v_j - delta_i)
  *   dq_i = scale * sum_{j in M_i} ds_ij k_j

@@ -92,9 +92,11 @@ __device__ __forceinline__ float quad_sum(float x) {
 
 // exp(scale * s - lse), with c + c_low = scale * log2(e). In single precision
 // the roundings of c and of lse * log2(e), which would weigh |lse| times a
-// rounding, are carried along; in the 16-bit types they are far below the
-// weight's own rounding. An infinite lse (no row, or one that sees nothing)
-// gives 0.
+// rounding, are carried along; in the 16-bit types they are below the weight's
+// own rounding unless |lse| passes 2^13. lse's rounding remains, |lse| times
+// 2^-24, which of large scores is more than 1: a weight above 1 is taken as 1, so
+// that none passes its type's range (minimum() keeps a NaN). An infinite lse (no
+// row, or one that sees nothing) gives 0.
 template <class T>
 __device__ __forceinline__ float weight(float s, float c, float c_low, float lse) {
     const float a = lse == -INFINITY ? INFINITY : lse * kLog2e;
@@ -103,7 +105,7 @@ __device__ __forceinline__ float weight(float s, float c, float c_low, float lse
         const float low = fmaf(lse, kLog2eLow, fmaf(lse, kLog2e, -a));
         x += a == INFINITY ? 0.f : fmaf(s, c_low, -low);
     }
-    return fast_exp2(x);
+    return __builtin_elementwise_minimum(fast_exp2(x), 1.f);
 }
 
 // Unsigned division of n < 2^31 by a divisor fixed at launch: with

@@ -107,3 +107,33 @@ def test_large_scores_leave_other_rows_alone(dtype, new):
             keep = torch.arange(len(x), device="cuda") != 1
             assert torch.equal(x[keep], y[keep]) and not torch.equal(x[1], y[1])
             assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("dtype,amount", [x for x in SIZES if x != (F16, 2.0 ** 15)], ids=str)
+@pytest.mark.parametrize("d", [64, 128, 200])
+def test_gradients_of_scores_of_any_size(dtype, amount, d):
+    """A weight is exp(s - lse) of two floats, so that of large scores its error passes 1; but it
+    is at most 1. So |dv_j| <= sum_i |dout_i| (n terms summed in floats, one rounding to the type),
+    and a row's only key has dS = p (dP - delta) = p * 0 = 0."""
+    api = _api()
+    rng = np.random.default_rng(d)
+    rows = ref.mask([1, 1, 1, 1, 0, 5, 200, 40, 33, 0, 64, 65, 3, 2, 17], 250, rng)
+    alone = np.arange(250, 254)  # keys 250 to 253: seen by one row each, which sees nothing else
+    rows[:4] = [np.array([j]) for j in alone]
+    q, k = _signs(rng, (len(rows), 4, d), amount, dtype), _signs(rng, (254, 2, d), 8 * amount, dtype)
+    v, dout = _rand(rng, (254, 2, d), dtype), _rand(rng, (len(rows), 4, d), dtype)
+    with api.AttentionPlan(ref.csr(rows, 254), backward=True) as plan:
+        out, lse = plan.forward(q, k, v, scale=1.0)
+        dq, dk, dv = plan.backward(dout, q, k, v, out, lse, scale=1.0)
+    assert torch.isfinite(dv).all()
+    for x in (dq, dk):
+        # one key's dS k is up to |dP - delta| * 8 amount, in half precision 20 * 8 * 2^10 for
+        # instance, past its largest of 65504: infinities are that type's results there
+        assert not torch.isnan(x).any() and (dtype == F16 or torch.isfinite(x).all())
+    assert not dq[:4].any() and not dk[250:].any()
+    most = np.zeros(v.shape)
+    for i, cols in enumerate(rows):
+        for h in range(4):
+            np.add.at(most[:, h // 2], cols, np.abs(ref.f64(dout)[i, h]))
+    n = sum(len(r) for r in rows) * 2
+    assert (np.abs(ref.f64(dv)) <= most * (1 + ref.U[dtype] + n * ref.E)).all()
