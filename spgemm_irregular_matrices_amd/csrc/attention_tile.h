@@ -156,12 +156,29 @@ struct Tile {
                 f.w[t] = u32x4{0, 0, 0, 0};
         }
     }
-    // A query row for scores with the factor |c|, or 1 if c is 0 (see Softmax).
+    // A query row for scores with the factor |c|, or 1 if c is 0 (see Softmax):
+    // 0 times each value then, which is NaN for an infinity or a NaN.
     static __device__ __forceinline__ void sign_row(RowFrag& f, float c) {
-        if (c > 0.f) return;
-        const uint32_t flip = k16 ? 0x80008000u : 0x80000000u;
+        if (__builtin_expect(c > 0.f, 1)) return;
+        if (c < 0.f) {
+            const uint32_t flip = k16 ? 0x80008000u : 0x80000000u;
 #pragma unroll
-        for (int t = 0; t < QS; ++t) f.w[t] = c < 0.f ? f.w[t] ^ flip : u32x4{0, 0, 0, 0};
+            for (int t = 0; t < QS; ++t) f.w[t] ^= flip;
+        } else {
+#pragma unroll
+            for (int t = 0; t < QS; ++t)
+                f.w[t] = u32x4{times0(f.w[t][0]), times0(f.w[t][1]), times0(f.w[t][2]),
+                               times0(f.w[t][3])};
+        }
+    }
+    static __device__ __forceinline__ uint32_t times0(uint32_t w) {
+        if constexpr (k16) {
+            float a, b;
+            unpack2<T>(w, a, b);
+            return pack2<T>(a * 0.f, b * 0.f);
+        } else {
+            return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, w) * 0.f);
+        }
     }
     static __device__ __forceinline__ void zero_row(RowFrag& f) {
 #pragma unroll

@@ -137,3 +137,26 @@ def test_gradients_of_scores_of_any_size(dtype, amount, d):
             np.add.at(most[:, h // 2], cols, np.abs(ref.f64(dout)[i, h]))
     n = sum(len(r) for r in rows) * 2
     assert (np.abs(ref.f64(dv)) <= most * (1 + ref.U[dtype] + n * ref.E)).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=str)
+@pytest.mark.parametrize("wild", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("new", [2, 40])
+def test_scale_of_zero_keeps_wild_queries(dtype, wild, new):
+    """0 times a score that is not a number is not a number: such a query's row is NaN (to a
+    NaN sum belongs a NaN), and others are the mean of their values."""
+    api = _api()
+    rng = np.random.default_rng(new)
+    rows = ref.mask([3, 17, 40, 33, 1, 2, 60, 5], 60, rng)
+    q, k, v = (_rand(rng, s, dtype) for s in ((8, 4, 64), (60, 2, 64), (60, 2, 64)))
+    c = _paged_case(rng, dtype, 64, 4, 2, 16, [(100, new)], pad=0)
+    with api.AttentionPlan(ref.csr(rows, 60)) as plan:
+        clean = plan.forward(q, k, v, scale=0.0), _paged_run(c, scale=0.0)
+        q[1, 2, 5], c["q"][1, 2, 5] = wild, wild
+        got = plan.forward(q, k, v, scale=0.0), _paged_run(c, scale=0.0)
+    for a, b in zip(clean, got):
+        for x, y in zip(a, b):
+            keep = torch.ones(x.shape[:2], dtype=torch.bool, device="cuda")
+            keep[1, 2] = False
+            assert torch.equal(x[keep], y[keep]) and torch.isfinite(x).all()
+            assert torch.isnan(y[1, 2]).all()
