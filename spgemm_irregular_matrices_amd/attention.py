@@ -6,7 +6,8 @@ Argument marshalling only, as in ``binding``: outputs and workspaces are torch
 tensors, every step runs in the HIP library's kernels. All tensors of a call
 are on one device; the call runs on ``stream`` (default: that device's current
 stream), which the tensors it allocates then belong to. Nothing here waits for
-the GPU, except making and closing a plan.
+the GPU, except making and closing a plan. Calls are not recorded by autograd:
+while it records, tensors that require gradients are refused.
 """
 from __future__ import annotations
 
@@ -153,6 +154,15 @@ def _dims(q, k):
     return a[1], b[1], a[2]
 
 
+def _unrecorded(*tensors):
+    """Autograd does not see the library's calls: a result would be cut off from its inputs."""
+    import torch
+    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+        raise ValueError("attention calls are not recorded by autograd: call them under "
+                         "torch.no_grad(), or from a torch.autograd.Function of forward and "
+                         "backward, for tensors that require gradients")
+
+
 def _scale(scale, dim) -> float:
     return max(dim, 1) ** -0.5 if scale is None else float(scale)
 
@@ -238,6 +248,7 @@ class AttentionPlan:
         may be passed to be written into. scale defaults to dim ** -0.5."""
         import torch
         hq, hkv, dim = _dims(q, k)
+        _unrecorded(q, k, v)
         dtype, device = q.dtype, q.device
         self._ready(device)
         big, small, line = (self.nrows, hq, dim), (self.ncols, hkv, dim), (self.nrows, hq)
@@ -266,6 +277,7 @@ class AttentionPlan:
         have their tensors' shapes and type, and are written, not added to."""
         import torch
         hq, hkv, dim = _dims(q, k)
+        _unrecorded(dout, q, k, v, out)
         dtype, device = q.dtype, q.device
         self._ready(device)
         big, small = (self.nrows, hq, dim), (self.ncols, hkv, dim)
@@ -317,6 +329,7 @@ def paged_attention(q, k_cache, v_cache, pages: DeviceCSR, q_rowptr, lengths, ma
         raise ValueError(f"q {tuple(q.shape)}, k_cache {tuple(k_cache.shape)} and v_cache "
                          f"{tuple(v_cache.shape)} do not fit: expected (tokens, heads, dim) and "
                          "twice (pages, slots, kv heads, dim)")
+    _unrecorded(q, k_cache, v_cache)
     tokens, hq, dim = q.shape
     npages, slots, hkv, _ = k_cache.shape
     dtype, device, seqs = q.dtype, q.device, pages.nrows

@@ -160,3 +160,33 @@ def test_scale_of_zero_keeps_wild_queries(dtype, wild, new):
             keep[1, 2] = False
             assert torch.equal(x[keep], y[keep]) and torch.isfinite(x).all()
             assert torch.isnan(y[1, 2]).all()
+
+
+def test_a_function_of_autograd():
+    """forward and backward in a user's autograd Function: leaves get the gradients of the calls."""
+    api = _api()
+    rng = np.random.default_rng(41)
+    rows = [np.arange(max(0, i - 9), i + 1) for i in range(40)]
+    q, k, v = (_rand(rng, s, F32) for s in ((40, 4, 64), (40, 2, 64), (40, 2, 64)))
+    dout = _rand(rng, q.shape, F32)
+    with api.AttentionPlan(ref.csr(rows, 40), backward=True) as plan:
+
+        class Attention(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, v):
+                out, lse = plan.forward(q, k, v)
+                ctx.save_for_backward(q, k, v, out, lse)
+                return out
+
+            @staticmethod
+            def backward(ctx, dout):
+                return plan.backward(dout.contiguous(), *ctx.saved_tensors)
+
+        out, lse = plan.forward(q, k, v)
+        want = plan.backward(2 * dout, q, k, v, out, lse)
+        leaves = [x.clone().requires_grad_() for x in (q, k, v)]
+        with pytest.raises(ValueError):
+            plan.forward(*leaves)
+        (2 * dout * Attention.apply(*leaves)).sum().backward()
+    for x, g in zip(leaves, want):
+        assert torch.equal(x.grad, g)
