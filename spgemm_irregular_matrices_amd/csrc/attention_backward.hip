@@ -418,7 +418,7 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 2) void k_att
                 }
             }
         }
-        float pr[4], ds[4];
+        float pr[4] = {}, ds[4] = {};  // (wavefronts without a block scale and drop these)
         float wild = 0.f;
         if (16 * w < TP) {
             const f32x4 l2 = *reinterpret_cast<const f32x4*>(lse_s + 16 * w + 4 * quad);

@@ -163,7 +163,6 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
     }
     if (job.k0 >= job.k1) return;
     const int lo = __builtin_amdgcn_readfirstlane(r.t);
-    const int hi = __builtin_amdgcn_readlane(r.t, 15);
 
     typename G::RowFrag q;
     typename G::VBlock k[G::U], v[G::U];

@@ -142,7 +142,7 @@ struct Tile {
 
     struct RowFrag { u32x4 w[QS]; };        // a row as A or B operand of S^T
     struct Acc { f32x4 o[U][CHL]; };        // O^T
-    struct Probs { uint32_t w[k16 ? 4 : 4]; };  // P^T as B operand (floats' bits if T is float)
+    struct Probs { uint32_t w[4]; };        // P^T as B operand (floats' bits if T is float)
     struct VBlock { uint32_t w[VK][VW]; };  // one V chunk of the lane's keys
 
     // The 16-byte pieces 4*t + l/16 of a row; pieces from row_bytes on are 0.
