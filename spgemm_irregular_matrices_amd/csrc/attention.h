@@ -133,14 +133,28 @@ bool paged_wide(const AttnShape& s, int64_t rows);
 constexpr int kPagedTileMost = 128;
 int paged_tile_rows(const AttnShape& s, int64_t rows);
 
+// The grid of at least that many work groups, which kernels number along x, then
+// y. A launch whose lanes along one axis pass 2^32 runs without those past it and
+// without an error.
+inline dim3 grid_2d(int64_t blocks) {
+    constexpr int64_t most = int64_t(1) << 22;  // of up to 512 lanes
+    if (blocks <= most) return dim3(grid_1d(blocks));
+    const int64_t y = ceil_div(blocks, most);
+    if (y > 65535) throw OverflowError("grid size exceeds the HIP limit");
+    return dim3((unsigned)most, (unsigned)y);
+}
+__device__ __forceinline__ int64_t grid_block() {
+    return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+}
+
 // XCD x of the 8 gets every eighth work group; this gives each XCD a
 // contiguous eighth of the logical blocks, so that neighbouring pieces of one
 // head, which gather the same key rows, meet in one XCD's L2.
 constexpr int kXcds = 8;
 inline int64_t xcd_grid(int64_t blocks) { return ceil_div(blocks, kXcds) * kXcds; }
 __device__ __forceinline__ int64_t xcd_block() {
-    const uint32_t per = gridDim.x / kXcds;
-    return (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+    const int64_t per = (int64_t)gridDim.x / kXcds * gridDim.y;
+    return (int64_t)(blockIdx.x % kXcds) * per + grid_block() / kXcds;
 }
 
 // Pieces that one wavefront takes in turn: enough to hide the first trip to

@@ -279,9 +279,10 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 2) void k_att
     // every XCD has an eighth of each head's pieces, and all are at one head
     // at a time: what they gather of it together stays in the last-level cache
     const uint32_t per = (uint32_t)ceil_div(a.cols.npieces, kXcds);
-    const int h = (int)(blockIdx.x / kXcds / per);
-    const int64_t piece = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds % per;
-    if (piece >= a.cols.npieces) return;
+    const uint32_t turn = (uint32_t)(grid_block() / kXcds);  // (2^32 would write 2^42 bytes)
+    const int h = (int)(turn / per);
+    const int64_t piece = (int64_t)(blockIdx.x % kXcds) * per + turn % per;
+    if (h >= a.s.hkv || piece >= a.cols.npieces) return;
     const AttnPiece pc = a.cols.pieces[piece];
     const int n = lane & 15, quad = lane >> 4;
     const int64_t col = (int64_t)pc.row * kColBlock + n;  // this lane's key
@@ -555,7 +556,7 @@ __global__ __launch_bounds__(kKvWaves* kWave, G::kDim <= 128 ? 3 : 2) void k_att
 // column and output of dk and dv. A piece's results lie side by side.
 template <class T>
 __global__ __launch_bounds__(kWaves* kWave) void k_attn_join_sum(BackwardArgs a) {
-    int64_t unit = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
+    int64_t unit = grid_block() * kWaves + threadIdx.x / kWave;
     const int64_t row_units = a.rows.nsplits * a.rows.block * a.s.hq;
     const bool col_side = unit >= row_units;
     if (col_side) unit -= row_units;
@@ -587,20 +588,20 @@ void attention_backward(const BackwardArgs& a, hipStream_t st) {
             const int64_t groups = ceil_div(a.rows.npieces, kWaves * each);
             auto run = a.rows.block > 1 ? k_attn_grad_q<typename Tag::Geo, T, true>
                                         : k_attn_grad_q<typename Tag::Geo, T, false>;
-            hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(groups * heads))), dim3(kWaves * kWave),
+            hipLaunchKernelGGL(run, grid_2d(xcd_grid(groups * heads)), dim3(kWaves * kWave),
                                0, st, a, each, groups);
             SG_LAUNCH_CHECK();
         }
         const int64_t cols = xcd_grid(a.cols.npieces) * a.s.hkv;
         if (cols > 0) {
             auto run = k_attn_grad_kv<typename Tag::Geo, T>;
-            hipLaunchKernelGGL(run, dim3(grid_1d(cols)), dim3(kKvWaves * kWave), 0, st, a);
+            hipLaunchKernelGGL(run, grid_2d(cols), dim3(kKvWaves * kWave), 0, st, a);
             SG_LAUNCH_CHECK();
         }
         const int64_t joins = a.rows.nsplits * a.rows.block * a.s.hq +
                               a.cols.nsplits * a.s.hkv * 2 * kColBlock;
         if (joins > 0) {
-            hipLaunchKernelGGL(k_attn_join_sum<T>, dim3(grid_1d(ceil_div(joins, kWaves))),
+            hipLaunchKernelGGL(k_attn_join_sum<T>, grid_2d(ceil_div(joins, kWaves)),
                                dim3(kWaves * kWave), 0, st, a);
             SG_LAUNCH_CHECK();
         }

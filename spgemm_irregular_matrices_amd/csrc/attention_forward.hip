@@ -176,7 +176,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_
 template <class T>
 __global__ __launch_bounds__(kWaves* kWave) void k_attn_join(ForwardArgs a) {
     const int lane = lane_id();
-    const int64_t unit = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
+    const int64_t unit = grid_block() * kWaves + threadIdx.x / kWave;
     const int64_t lines = (int64_t)a.side.block * a.s.hq;
     if (unit >= a.side.nsplits * lines) return;
     const int64_t sp = unit / lines, line = unit - sp * lines;
@@ -206,12 +206,12 @@ void attention_forward(const ForwardArgs& a, hipStream_t st) {
         using Tag = decltype(tag);
         auto run = a.side.block > 1 ? k_attn_forward<typename Tag::Geo, typename Tag::Elem, true>
                                     : k_attn_forward<typename Tag::Geo, typename Tag::Elem, false>;
-        hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(groups * heads))), dim3(kWaves * kWave), 0,
+        hipLaunchKernelGGL(run, grid_2d(xcd_grid(groups * heads)), dim3(kWaves * kWave), 0,
                            st, a, each, groups);
         SG_LAUNCH_CHECK();
         if (a.side.nsplits > 0) {
             hipLaunchKernelGGL(k_attn_join<typename Tag::Elem>,
-                               dim3(grid_1d(ceil_div(a.side.nsplits * a.side.block * a.s.hq, kWaves))),
+                               grid_2d(ceil_div(a.side.nsplits * a.side.block * a.s.hq, kWaves)),
                                dim3(kWaves * kWave), 0, st, a);
             SG_LAUNCH_CHECK();
         }

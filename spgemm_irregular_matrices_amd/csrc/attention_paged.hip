@@ -538,7 +538,7 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
 template <class T>
 __global__ __launch_bounds__(kWaves* kWave) void k_paged_join(PagedArgs a) {
     const int lane = lane_id();
-    const int64_t unit = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
+    const int64_t unit = grid_block() * kWaves + threadIdx.x / kWave;
     if (unit >= a.tokens * a.s.hq) return;
     const int64_t token = unit / a.s.hq;
     const int hq = (int)(unit - token * a.s.hq);
@@ -592,16 +592,16 @@ void paged_attention(const PagedArgs& a, hipStream_t st) {
         using T = typename Tag::Elem;
         if (paged_wide(a.s, rows)) {
             auto run = k_paged_wide<G, T>;
-            hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(units))), dim3(kWaves * kWave), 0, st, a,
+            hipLaunchKernelGGL(run, grid_2d(xcd_grid(units)), dim3(kWaves * kWave), 0, st, a,
                                (int32_t)tiles);
         } else {
             auto run = k_paged<G, T>;
-            hipLaunchKernelGGL(run, dim3(grid_1d(xcd_grid(ceil_div(units, kWaves)))),
+            hipLaunchKernelGGL(run, grid_2d(xcd_grid(ceil_div(units, kWaves))),
                                dim3(kWaves * kWave), 0, st, a, (int32_t)tiles);
         }
         SG_LAUNCH_CHECK();
         if (a.npieces > 1) {
-            hipLaunchKernelGGL(k_paged_join<T>, dim3(grid_1d(ceil_div(a.tokens * a.s.hq, kWaves))),
+            hipLaunchKernelGGL(k_paged_join<T>, grid_2d(ceil_div(a.tokens * a.s.hq, kWaves)),
                                dim3(kWaves * kWave), 0, st, a);
             SG_LAUNCH_CHECK();
         }
