@@ -464,23 +464,27 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
             scores(at);
             typename G::Probs pr[QB][NS];
             float fix[QB], old[QB];
+            // Queries whose scores are far from 0 (see Softmax) get their
+            // weights again, after those of the others: asked before the
+            // exponentials, which it keeps from running beside each other,
+            // the branch took 1494 -> 1524 us for chunks of 2048 over 32768
+            // keys. Padded widths have no registers for that (192 values:
+            // 9190 us asked before, 10297 after).
+            constexpr bool kAgain = G::kFull;
             bool moved = false, far = false;
 #pragma unroll
             for (int x = 0; x < QB; ++x) {
                 bool one;
                 old[x] = sm[x].l;
-                fix[x] = sm[x].template weigh<false>(sc[x], a.s.mag, pr[x], one);
+                fix[x] = sm[x].template weigh<!kAgain>(sc[x], a.s.mag, pr[x], one);
                 moved |= fix[x] != 1.f;
-                far |= one;
+                far |= kAgain && one;
             }
             if (__any(moved || far)) {
                 if (__any(far)) {
                     // Hardly ever, so the scores are made again; from 128 values on
                     // they look like others to the compiler, which would keep
                     // them through every step in registers that are not there.
-                    // (Asked before the exponentials, which it keeps from
-                    // running beside each other, the branch took 1494 -> 1524
-                    // us for chunks of 2048 over 32768 keys.)
                     int again = at;
                     if constexpr (G::kDim > 64) asm volatile("" : "+s"(again));
                     scores(again);
