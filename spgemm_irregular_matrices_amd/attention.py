@@ -154,10 +154,11 @@ def _dims(q, k):
     return a[1], b[1], a[2]
 
 
-def _unrecorded(*tensors):
-    """Autograd does not see the library's calls: a result would be cut off from its inputs."""
+def _unrecorded():
+    """For tensors that require gradients: autograd does not see the library's
+    calls, and a result would be cut off from its inputs."""
     import torch
-    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+    if torch.is_grad_enabled():
         raise ValueError("attention calls are not recorded by autograd: call them under "
                          "torch.no_grad(), or from a torch.autograd.Function of forward and "
                          "backward, for tensors that require gradients")
@@ -248,7 +249,8 @@ class AttentionPlan:
         may be passed to be written into. scale defaults to dim ** -0.5."""
         import torch
         hq, hkv, dim = _dims(q, k)
-        _unrecorded(q, k, v)
+        if q.requires_grad or k.requires_grad or v.requires_grad:
+            _unrecorded()
         dtype, device = q.dtype, q.device
         self._ready(device)
         big, small, line = (self.nrows, hq, dim), (self.ncols, hkv, dim), (self.nrows, hq)
@@ -277,7 +279,9 @@ class AttentionPlan:
         have their tensors' shapes and type, and are written, not added to."""
         import torch
         hq, hkv, dim = _dims(q, k)
-        _unrecorded(dout, q, k, v, out)
+        if (q.requires_grad or k.requires_grad or v.requires_grad or dout.requires_grad
+                or out.requires_grad):
+            _unrecorded()
         dtype, device = q.dtype, q.device
         self._ready(device)
         big, small = (self.nrows, hq, dim), (self.ncols, hkv, dim)
@@ -329,7 +333,8 @@ def paged_attention(q, k_cache, v_cache, pages: DeviceCSR, q_rowptr, lengths, ma
         raise ValueError(f"q {tuple(q.shape)}, k_cache {tuple(k_cache.shape)} and v_cache "
                          f"{tuple(v_cache.shape)} do not fit: expected (tokens, heads, dim) and "
                          "twice (pages, slots, kv heads, dim)")
-    _unrecorded(q, k_cache, v_cache)
+    if q.requires_grad or k_cache.requires_grad or v_cache.requires_grad:
+        _unrecorded()
     tokens, hq, dim = q.shape
     npages, slots, hkv, _ = k_cache.shape
     dtype, device, seqs = q.dtype, q.device, pages.nrows
