@@ -31,6 +31,16 @@ def test_paged_many_tiles():
     assert (out[96:] == 7).all()
 
 
+def test_paged_many_sequences():
+    """300000 sequences and 64 key heads, most without tokens: 4.8 million work groups."""
+    rng = np.random.default_rng(65)
+    seqs = [(70, 1), (128, 1), (33, 1), (100, 1)]
+    c = _padded(_paged_case(rng, BF16, 8, 64, 64, 16, seqs), seqs, 300000, 7)
+    out, lse = _paged_run(c, out=torch.full_like(c["q"], 7.0))
+    _paged_check(c, seqs, 8 ** -0.5, out, lse)
+    assert (out[4:] == 7).all()
+
+
 def test_paged_join_of_many_rows():
     """2^20 + 3 rows of 64 heads, most of no sequence, and texts of two pieces."""
     rng = np.random.default_rng(62)
