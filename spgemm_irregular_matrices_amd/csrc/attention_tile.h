@@ -655,13 +655,14 @@ struct Softmax {
     // Single precision keeps m before its factor until finish(): the largest
     // weight is 1 to the last bit then, and a row's only key gives its value
     // unchanged. 16 bits round that difference away, unless m is far from 0:
-    // from 2^13 on its own rounding, up to 2^-24 of it, is not small beside a
-    // weight's, and from about 2^24 on 2 to the power of that rounding, which
-    // is what the largest weight becomes, passes the types' ranges at either
-    // end. There the products are rounded as the maximum's was, which makes it 1
-    // again and takes two instructions a weight for one.
+    // from 2^12 on its own rounding, and that of the shift minus it, up to
+    // 2^-24 of it each, are not small beside a weight's, and from about 2^24 on 2
+    // to the power of them, which is what the largest weight becomes, passes the
+    // types' ranges at either end. There the products are rounded as the
+    // maximum's was, which makes it 1 again and takes two instructions a weight
+    // for one.
     static constexpr bool kLate = sizeof(T) == 4;
-    static constexpr float kFar = 8192.f;
+    static constexpr float kFar = 4096.f;
     float m = -INFINITY, l = 0.f;
 
     // Takes NS tiles' scores before their factor c > 0 (a negative one's sign

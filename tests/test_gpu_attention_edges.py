@@ -90,6 +90,28 @@ def test_paged_scores_of_any_size(dtype, amount, d, new):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=str)
+@pytest.mark.parametrize("amount", [1, 3, 8, 11, 16, 60, 200])
+def test_only_keys_of_any_score(dtype, amount):
+    """A row with one key gives its value unchanged: below 2^12 the maximum's rounding and that of its
+    difference to the shift are up to 2^-13 each, so that the weight is off by up to 2^-12 log 2, under
+    half a step of half precision and of the quotient; from there on it is 1."""
+    api = _api()
+    rng = np.random.default_rng(amount)
+    n, d = 600, 64
+    q, k, v = (_rand(rng, (n, h, d), dtype, s) for h, s in ((4, amount * 4), (2, amount * 4), (2, 1)))
+    at = rng.permutation(n)
+    with api.AttentionPlan(ref.csr([np.array([j]) for j in at], n)) as plan:
+        out, _ = plan.forward(q, k, v, scale=0.4)
+    assert torch.equal(out, v[torch.from_numpy(at).cuda()].repeat_interleave(2, 1))
+    c = _paged_case(rng, dtype, d, 4, 2, 16, [(1, 1)] * 50)
+    c["q"].mul_(amount * 4)
+    c["k"].mul_(amount * 4)
+    out, _ = _paged_run(c, scale=0.4)
+    want = torch.stack([x[1, 0] for x in c["keys"]]).cuda().repeat_interleave(2, 1)
+    assert torch.equal(out[:50], want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=str)
 @pytest.mark.parametrize("new", [3, 40])
 def test_large_scores_leave_other_rows_alone(dtype, new):
     """Rows that share tiles with one of huge scores keep their bits."""
