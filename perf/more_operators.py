@@ -245,12 +245,16 @@ def prepare(case, seed):
                 st |= {"k": kv[:, :hkv], "v": kv[:, hkv:]}
             st |= {"k_out": torch.zeros(tokens, hkv, d, dtype=dtype, device="cuda"), "v_out": torch.zeros(tokens, hkv, d, dtype=dtype, device="cuda")}
     if own:
-        from spgemm_irregular_matrices_amd import binding, cache, latent
+        from spgemm_irregular_matrices_amd import binding
 
         st["table"] = binding.DeviceCSR(case["seqs"], pool, st["rowptr"], st["pages"], None)
         if op in ("latent", "expanded"):
+            from spgemm_irregular_matrices_amd import latent
+
             st["call"] = latent.latent_attention if op == "latent" else latent.latent_attention_expanded
         else:
+            from spgemm_irregular_matrices_amd import cache
+
             st["store"] = cache.QuantizedCache(st["k_codes"], st["k_scales"], st["v_codes"], st["v_scales"], form)
     return st
 
