@@ -127,6 +127,8 @@ struct PagedArgs {
     float* part_ml = nullptr;  // [piece][token][hq][2]
 };
 void paged_attention(const PagedArgs& a, hipStream_t st);
+// Joins the pieces of every token and query head (npieces > 1).
+void paged_join(const PagedArgs& a, hipStream_t st);
 // Whether a work group shares the keys of a sequence's `rows` rows (new
 // tokens times the query heads of a key head), and the rows of its tiles.
 bool paged_wide(const AttnShape& s, int64_t rows);

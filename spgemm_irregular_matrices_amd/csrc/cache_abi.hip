@@ -1,0 +1,212 @@
+// Argument checks and the C ABI of include/spgemm_cache.h.
+#include "attention_checks.h"
+#include "mx.h"
+
+using namespace sg;
+
+namespace {
+
+// ---------------------------------------------------------------- batches
+// What every call over a paged cache checks of its batch and cache: OK with
+// *empty set where there is nothing to do.
+int paged_checks(const spgemm_paged_batch* b, const AttnShape& s, int64_t npages, int64_t page_size,
+                 PagedArgs* a, bool* empty) {
+    const spgemm_csr* pg = b->pages;
+    if (pg->nnz < 0 || npages < 0 || page_size < 1 || pg->ncols != npages)
+        return SPGEMM_ERR_INVALID_ARG;
+    if (pg->nnz > 0x7fffffffLL || npages > 0x7fffffffLL || page_size > kMaxTokens)
+        return SPGEMM_ERR_OVERFLOW;
+    *empty = a->seqs == 0 || a->tokens == 0 || a->max_new == 0;
+    if (*empty) return SPGEMM_OK;
+    if (!pg->rowptr || (pg->nnz > 0 && !pg->col) || !b->q_rowptr || !b->lengths)
+        return SPGEMM_ERR_INVALID_ARG;
+    a->npages = npages;
+    a->page_div = FastDiv((uint32_t)page_size);
+    a->group_div = FastDiv((uint32_t)s.group);
+    a->room = pg->nnz;
+    a->rowptr = pg->rowptr;
+    a->col = pg->col;
+    a->q_rowptr = b->q_rowptr;
+    a->lengths = b->lengths;
+    return SPGEMM_OK;
+}
+
+void batch_shape(const spgemm_paged_batch* b, const AttnShape& s, PagedArgs* a) {
+    a->s = s;
+    a->seqs = b->pages->nrows;
+    a->tokens = b->tokens;
+    a->max_new = (int32_t)std::min(b->max_new, b->tokens);
+    a->max_length = (int32_t)b->max_length;
+}
+
+// Pieces of the keys, so that `target` units (wavefronts with keys of their own,
+// or work groups) are there, with at least `least` keys and a multiple of
+// `step` keys each.
+void cut_pieces(PagedArgs* a, int64_t tile, int64_t target, int64_t least, int64_t step) {
+    const int64_t rows = (int64_t)a->max_new * a->s.group;
+    const int64_t whole_tiles = a->seqs * ceil_div(rows, tile);
+    const int64_t tiles = std::min(whole_tiles, a->seqs + a->tokens * a->s.group / tile);
+    const int64_t units = std::max<int64_t>(a->s.hkv * tiles, 1);
+    const int64_t most = std::max<int64_t>(ceil_div(a->max_length, least), 1);
+    const int64_t want = std::min(std::max<int64_t>(target / units, 1), most);
+    a->piece = (int32_t)std::max<int64_t>(
+        ceil_div(ceil_div(a->max_length, want), step) * step, step);
+    a->npieces = (int32_t)std::max<int64_t>(ceil_div(a->max_length, a->piece), 1);
+}
+
+int64_t carve_parts(void* ws, PagedArgs* a) {
+    Carver c{static_cast<char*>(ws)};
+    if (a->npieces > 1) {
+        const __int128 rows = (__int128)a->npieces * a->tokens * a->s.hq;
+        a->part = c.take(rows * a->s.dim);
+        a->part_ml = c.take(rows * 2);
+    }
+    return c.used;
+}
+
+// ---------------------------------------------------------------- quantised
+bool mx_desc_valid(const spgemm_attention_desc* d) {
+    return desc_valid(d) && d->head_dim % SPGEMM_MX_BLOCK == 0;
+}
+
+// One tensor of bytes: its strides in units of 1 << shift. align: of data and
+// strides.
+int mx_bytes(const spgemm_mx_bytes& x, const spgemm_mx_cache* cache, int heads, int align,
+             const char** base, int64_t* head, uint32_t* page, uint32_t* slot, uint32_t* shift) {
+    const int64_t counts[2] = {cache->npages, cache->page_size};
+    const auto bytes = [&](int64_t stride, int64_t n) -> int64_t {
+        if (n <= 1) return 0;
+        return stride < 0 || stride > kMaxStride || stride % align != 0 ? -1 : stride;
+    };
+    const int64_t s[3] = {bytes(x.stride_page, counts[0]), bytes(x.stride_slot, counts[1]),
+                          bytes(x.stride_head, heads)};
+    if (s[0] < 0 || s[1] < 0 || s[2] < 0) return SPGEMM_ERR_INVALID_ARG;
+    *base = static_cast<const char*>(x.data);
+    if (cache->npages > 0 && (!*base || reinterpret_cast<uintptr_t>(*base) % align != 0))
+        return SPGEMM_ERR_INVALID_ARG;
+    if (!gather_unit(s, counts, 2, shift)) return SPGEMM_ERR_OVERFLOW;
+    *page = (uint32_t)(s[0] >> *shift);
+    *slot = (uint32_t)(s[1] >> *shift);
+    *head = s[2];
+    return SPGEMM_OK;
+}
+
+int mx_cache(const spgemm_mx_cache* c, const AttnShape& s, MxArgs* a) {
+    a->format = c->format;
+    const char *ks = nullptr, *vs = nullptr;
+    int rc = mx_bytes(c->k_codes, c, s.hkv, 16, &a->k, &a->k_head, &a->k_page, &a->k_slot, &a->k_shift);
+    if (rc == SPGEMM_OK)
+        rc = mx_bytes(c->v_codes, c, s.hkv, 16, &a->v, &a->v_head, &a->v_page, &a->v_slot, &a->v_shift);
+    if (rc == SPGEMM_OK)
+        rc = mx_bytes(c->k_scales, c, s.hkv, 1, &ks, &a->ks_head, &a->ks_page, &a->ks_slot,
+                      &a->ks_shift);
+    if (rc == SPGEMM_OK)
+        rc = mx_bytes(c->v_scales, c, s.hkv, 1, &vs, &a->vs_head, &a->vs_page, &a->vs_slot,
+                      &a->vs_shift);
+    a->ks = reinterpret_cast<const uint8_t*>(ks);
+    a->vs = reinterpret_cast<const uint8_t*>(vs);
+    return rc;
+}
+
+bool mx_format_valid(const spgemm_mx_cache* c) {
+    return c && (c->format == SPGEMM_MX_E4M3 || c->format == SPGEMM_MX_E2M1) && c->reserved == 0;
+}
+
+// Writing and reading: everything but the direction.
+template <class Run>
+int mx_rows(const spgemm_attention_desc* desc, const spgemm_rows* k, const spgemm_rows* v,
+            const spgemm_mx_cache* cache, const spgemm_paged_batch* batch, bool output, Run&& run) {
+    if (!desc || !batch_sizes_valid(batch) || !mx_format_valid(cache)) return SPGEMM_ERR_INVALID_ARG;
+    spgemm_attention_desc d = *desc;
+    d.heads_q = d.heads_kv;
+    d.scale = 0.;
+    if (!mx_desc_valid(&d)) return SPGEMM_ERR_INVALID_ARG;
+    if (!batch_sizes_fit(batch, &d)) return SPGEMM_ERR_OVERFLOW;
+    return guarded([&]() -> int {
+        MxRowsArgs a;
+        batch_shape(batch, make_shape(&d), &a);
+        if (!rows_valid(k, a.tokens, a.s.hkv, &d, output, &a.rk) ||
+            !rows_valid(v, a.tokens, a.s.hkv, &d, output, &a.rv))
+            return SPGEMM_ERR_INVALID_ARG;
+        bool empty = false;
+        int rc = paged_checks(batch, a.s, cache->npages, cache->page_size, &a, &empty);
+        if (rc != SPGEMM_OK || empty) return rc;
+        rc = mx_cache(cache, a.s, &a);
+        if (rc != SPGEMM_OK) return rc;
+        run(a);
+        return SPGEMM_OK;
+    });
+}
+
+// Keys per piece, as for a cache of 16-bit values.
+void mx_pieces(PagedArgs* a, int format) {
+    const int64_t rows = (int64_t)a->max_new * a->s.group;
+    const int64_t tile = mx_tile_rows(a->s, format, rows);
+    const int64_t each = a->s.dim <= 128 ? 2 : 1;
+    if (mx_wide(a->s, format, rows)) {
+        const bool ragged = rows > tile && a->tokens * 4 < a->seqs * a->max_new * 3;
+        cut_pieces(a, tile, each * (ragged ? 512 : 256), 256, 64);
+    } else {
+        cut_pieces(a, tile, each * 1024, 64, 32);
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+SPGEMM_API int spgemm_mx_write(const spgemm_attention_desc* desc, const spgemm_rows* k,
+                               const spgemm_rows* v, const spgemm_mx_cache* cache,
+                               const spgemm_paged_batch* batch, void* stream) {
+    return mx_rows(desc, k, v, cache, batch, false,
+                   [&](const MxRowsArgs& a) { mx_write(a, (hipStream_t)stream); });
+}
+
+SPGEMM_API int spgemm_mx_read(const spgemm_attention_desc* desc, const spgemm_mx_cache* cache,
+                              const spgemm_paged_batch* batch, const spgemm_rows* k,
+                              const spgemm_rows* v, void* stream) {
+    return mx_rows(desc, k, v, cache, batch, true,
+                   [&](const MxRowsArgs& a) { mx_read(a, (hipStream_t)stream); });
+}
+
+SPGEMM_API int spgemm_mx_attention_workspace(const spgemm_attention_desc* desc,
+                                             const spgemm_paged_batch* batch, int64_t* bytes) {
+    if (!mx_desc_valid(desc) || !batch_sizes_valid(batch) || !bytes) return SPGEMM_ERR_INVALID_ARG;
+    if (!batch_sizes_fit(batch, desc)) return SPGEMM_ERR_OVERFLOW;
+    return guarded([&]() -> int {
+        MxArgs a;
+        batch_shape(batch, make_shape(desc), &a);
+        mx_pieces(&a, 0);
+        *bytes = carve_parts(nullptr, &a);
+        return SPGEMM_OK;
+    });
+}
+
+SPGEMM_API int spgemm_mx_attention(const spgemm_attention_desc* desc, const spgemm_rows* q,
+                                   const spgemm_mx_cache* cache, const spgemm_paged_batch* batch,
+                                   const spgemm_rows* out, float* lse, void* workspace,
+                                   int64_t workspace_bytes, void* stream) {
+    if (!mx_desc_valid(desc) || !batch_sizes_valid(batch) || !mx_format_valid(cache))
+        return SPGEMM_ERR_INVALID_ARG;
+    if (!batch_sizes_fit(batch, desc)) return SPGEMM_ERR_OVERFLOW;
+    return guarded([&]() -> int {
+        MxArgs a;
+        batch_shape(batch, make_shape(desc), &a);
+        mx_pieces(&a, 0);
+        if (!rows_valid(q, a.tokens, a.s.hq, desc, false, &a.q) ||
+            !rows_valid(out, a.tokens, a.s.hq, desc, true, &a.out))
+            return SPGEMM_ERR_INVALID_ARG;
+        bool empty = false;
+        int rc = paged_checks(batch, a.s, cache->npages, cache->page_size, &a, &empty);
+        if (rc != SPGEMM_OK || empty) return rc;
+        rc = mx_cache(cache, a.s, &a);
+        if (rc != SPGEMM_OK) return rc;
+        a.lse = lse;
+        if (!workspace_valid(workspace, workspace_bytes, carve_parts(workspace, &a)))
+            return SPGEMM_ERR_INVALID_ARG;
+        mx_attention(a, (hipStream_t)stream);
+        return SPGEMM_OK;
+    });
+}
+
+}  // extern "C"
