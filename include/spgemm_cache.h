@@ -1,7 +1,8 @@
 /*
  * spgemm_cache.h -- C ABI of key/value caches that take less memory than
  * those of spgemm_attention.h, and of the attention that reads them, on the
- * MI355X (gfx950): paged caches in 8 or 4 bits a value.
+ * MI355X (gfx950): paged caches in 8 or 4 bits a value, and paged caches of
+ * one latent vector a token that all heads share.
  *
  * Conventions are those of spgemm_attention.h: its descriptions, batches,
  * page tables, alignment, checks of a batch on the device, infinities and
@@ -94,6 +95,79 @@ SPGEMM_API int spgemm_mx_attention(const spgemm_attention_desc* desc, const spge
                                    const spgemm_mx_cache* cache, const spgemm_paged_batch* batch,
                                    const spgemm_rows* out, float* lse, void* workspace,
                                    int64_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Latent caches. A token holds one vector c_j of latent_dim values and one
+ * r_j of rope_dim values (keys' part that depends on the position), next to
+ * each other, for all heads together.
+ * ------------------------------------------------------------------------ */
+#define SPGEMM_LATENT_MAX_DIM 512
+#define SPGEMM_LATENT_MAX_ROPE 64
+#define SPGEMM_LATENT_MAX_HEAD 128
+
+typedef struct {
+    int32_t type;        /* bfloat16 or half                                   */
+    int32_t heads;       /* at most 65536                                      */
+    int32_t latent_dim;  /* 32 to 512, a multiple of 32                        */
+    int32_t rope_dim;    /* 0 to 64, a multiple of 8                           */
+    int32_t key_dim;     /* the expanded form's values of a head's key beside the
+                            rope_dim ones and of its value: 16 to 128, multiples
+                            of 16; the absorbed form does not read them        */
+    int32_t value_dim;
+    double scale;        /* factor of the scores; magnitude below 1e30         */
+} spgemm_latent_desc;
+
+/* Value x of c (x < latent_dim) or r (x - latent_dim) in slot s of page p is at
+ * data[p * stride_page + s * stride_slot + x]; rows are 16-byte aligned. */
+typedef struct {
+    const void* data;
+    int64_t npages;
+    int64_t page_size;
+    int64_t stride_page;
+    int64_t stride_slot;
+} spgemm_latent_cache;
+
+/* Absorbed form: queries in the latents' space. For the batch's new tokens
+ * (rows and what they see as in spgemm_paged_attention) and every head,
+ *
+ *   s_j = scale * (q . [c_j, r_j])    o = sum_j softmax(s)_j c_j
+ *
+ * with q [tokens, heads, latent_dim + rope_dim] and out [tokens, heads,
+ * latent_dim]; lse (may be NULL) as there. Probabilities are rounded to the
+ * type before the second product, the result once. Errors and broken batches:
+ * as spgemm_paged_attention. */
+SPGEMM_API int spgemm_latent_attention_workspace(const spgemm_latent_desc* desc,
+                                                 const spgemm_paged_batch* batch, int64_t* bytes);
+SPGEMM_API int spgemm_latent_attention(const spgemm_latent_desc* desc, const spgemm_rows* q,
+                                       const spgemm_latent_cache* cache,
+                                       const spgemm_paged_batch* batch, const spgemm_rows* out,
+                                       float* lse, void* workspace, int64_t workspace_bytes,
+                                       void* stream);
+
+/* Expanded form: every head's keys and values are made from the latents,
+ *
+ *   k_hj = [W_k,h c_j, r_j]   v_hj = W_v,h c_j
+ *   s_j = scale * (q_h . k_hj)    o_h = sum_j softmax(s)_j v_hj
+ *
+ * with w_k [heads, key_dim, latent_dim] and w_v [heads, value_dim, latent_dim]
+ * given as spgemm_rows (row: the head, head: the key's or value's index), q
+ * [tokens, heads, key_dim + rope_dim] and out [tokens, heads, value_dim]. The
+ * products with the weights are kept in the workspace for every cached token of
+ * the batch, as two numbers of the type each (the rounded product, and what
+ * that leaves, rounded): that is for chunks of many new tokens; a few are the
+ * absorbed form's, with W_k and W_v multiplied into q and out. A product past
+ * the type's range is infinite. The workspace grows with min(room of the page table * page_size,
+ * sequences * max_length). Errors and broken batches: as
+ * spgemm_paged_attention; the workspace call needs the cache's page size. */
+SPGEMM_API int spgemm_latent_expanded_workspace(const spgemm_latent_desc* desc,
+                                                const spgemm_latent_cache* cache,
+                                                const spgemm_paged_batch* batch, int64_t* bytes);
+SPGEMM_API int spgemm_latent_expanded(const spgemm_latent_desc* desc, const spgemm_rows* q,
+                                      const spgemm_rows* w_k, const spgemm_rows* w_v,
+                                      const spgemm_latent_cache* cache,
+                                      const spgemm_paged_batch* batch, const spgemm_rows* out,
+                                      float* lse, void* workspace, int64_t workspace_bytes,
+                                      void* stream);
 
 #ifdef __cplusplus
 }

@@ -15,7 +15,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["setup.hip", "heavy.hip", "accum.hip", "direct.hip", "plan.hip",
            "attention_plan.hip", "attention_forward.hip", "attention_backward.hip",
-           "attention_paged.hip", "attention_mx.hip", "cache_mx.hip", "cache_abi.hip"]
+           "attention_paged.hip", "attention_mx.hip", "attention_latent.hip",
+           "cache_mx.hip", "cache_abi.hip"]
 ARCH = os.environ.get("SPGEMM_OFFLOAD_ARCH", "gfx950")
 
 

@@ -1,0 +1,923 @@
+// Attention over a paged cache of latent vectors, in the latents' space
+// (absorbed) or over keys and values that were made from them (expanded).
+#include "latent.h"
+
+namespace sg {
+
+namespace {
+
+// What places without a source read: as long as the longest row.
+__device__ const u32x4 g_zero[SPGEMM_LATENT_MAX_DIM / 8 + SPGEMM_LATENT_MAX_ROPE / 8] = {};
+
+typedef __attribute__((address_space(1))) const void GlobalBytes;
+typedef __attribute__((address_space(3))) void LdsBytes;
+
+// 16 bytes a lane from memory to LDS, lane after lane from `dst` on. (The
+// restricted parameters keep reads of other LDS buffers from waiting for it.)
+__device__ __forceinline__ void load_to_lds(const char* __restrict__ src, char* __restrict__ dst) {
+    __builtin_amdgcn_global_load_lds((GlobalBytes*)src, (LdsBytes*)dst, 16, 0, 0);
+}
+// Everything that load_to_lds() of this wavefront asked for is there.
+__device__ __forceinline__ void wait_for_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+
+// A tile's rows in LDS: plane after plane of 64 values (128 bytes) of KEYS rows,
+// which one load fills 8 rows at a time. A row's 16-byte pieces are exchanged
+// by bits of its number, so that one piece of 16 rows in sequence, and two of
+// every fourth row (the transposing read), fall on different banks.
+template <int KEYS>
+struct Planes {
+    static constexpr int kPlane = KEYS * 128;
+    static constexpr __device__ __forceinline__ int swap(int r) {
+        return ((r >> 3) & 1) | ((r >> 1) & 1) << 1 | ((r >> 2) & 1) << 2;
+    }
+    static __device__ __forceinline__ int at(int r, int byte) {
+        return (byte >> 7) * kPlane + r * 128 + ((byte & 127) ^ (swap(r) << 4));
+    }
+    // at(r | dr, byte | dbyte) from at(r, byte), for constants that share no bit
+    // with r (whose exchanged bits they are none of) and byte
+    static __device__ __forceinline__ int more(int base, int dr, int dbyte) {
+        return (base ^ (dbyte & 127)) + (dbyte >> 7) * kPlane + dr * 128;
+    }
+    // an operand of 16 rows: 16 bytes, of step t, of row first + l % 16
+    static __device__ __forceinline__ int row_base(int first) {
+        return at(first + (lane_id() & 15), 16 * (lane_id() >> 4));
+    }
+    static __device__ __forceinline__ u32x4 row(const char* lds, int base, int dr, int t) {
+        return *reinterpret_cast<const u32x4*>(lds + more(base, dr, 64 * t));
+    }
+    // 16 columns, block b's, of rows first + 4 (l / 16) + 0..3 and 16 more, turned over
+    static __device__ __forceinline__ int value_base(int first) {
+        const int l = lane_id() & 15, quad = lane_id() >> 4;
+        return at(first + 4 * quad + (l >> 2), 8 * (l & 3));
+    }
+    static __device__ __forceinline__ u32x4 value(const char* lds, int base, int b) {
+        using s16x4 = short __attribute__((ext_vector_type(4)));
+        using lds_s16x4 = __attribute__((address_space(3))) s16x4;
+        const u32x2 lo = __builtin_bit_cast(
+            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + more(base, 0, 32 * b))));
+        const u32x2 hi = __builtin_bit_cast(
+            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + more(base, 16, 32 * b))));
+        return u32x4{lo[0], lo[1], hi[0], hi[1]};
+    }
+};
+
+// This lane's rows of a tile: of blocks of 8 rows first, first + 1, ... row l / 8.
+// Their pages are looked up a tile ahead.
+template <class P, int BLOCKS>
+struct TileRows {
+    int row[BLOCKS];
+    uint32_t id[BLOCKS];
+    int byte[BLOCKS];  // of the 128 of a plane, that this lane's piece holds
+    bool wrong = false;
+    __device__ __forceinline__ explicit TileRows(int first) {
+#pragma unroll
+        for (int i = 0; i < BLOCKS; ++i) {
+            row[i] = 8 * (first + i) + (lane_id() >> 3);
+            byte[i] = 16 * ((lane_id() & 7) ^ P::swap(row[i]));
+            id[i] = 0;
+        }
+    }
+    __device__ __forceinline__ void look_up(const PagedArgs& a, const int32_t* pages, int t0, int k1) {
+#pragma unroll
+        for (int i = 0; i < BLOCKS; ++i)
+            if (t0 + row[i] < k1) id[i] = (uint32_t)pages[a.page_div.div(t0 + row[i])];
+    }
+    // The i-th row's latent row; null past the end.
+    __device__ __forceinline__ const char* latent(const PagedArgs& a, int t0, int k1, int i) {
+        const uint32_t key = t0 + row[i];
+        if ((int)key >= k1) return nullptr;
+        if (id[i] >= (uint64_t)a.npages) {
+            wrong = true;
+            id[i] = 0;
+        }
+        const uint32_t slot = key - a.page_div.div(key) * a.page_div.d;
+        return a.k + ((uint64_t)(id[i] * a.k_page + slot * a.k_slot) << a.k_shift);
+    }
+};
+
+// Step t of a query row as an operand: 16 bytes from byte `at` on, 0 past `end`,
+// with the sign of the scores' factor (0: see Softmax).
+template <class G>
+__device__ __forceinline__ u32x4 load_query(const LatentArgs& a, const TileRow& r, int at, int end) {
+    const char* row = a.q.base + r.token * a.q.row + r.hq * a.q.head;
+    u32x4 q{0, 0, 0, 0};
+    if (r.has && at < end) q = *reinterpret_cast<const u32x4*>(row + at);
+    if (a.s.c < 0.f) q ^= 0x80008000u;
+    if (a.s.c == 0.f) q = u32x4{G::times0(q[0]), G::times0(q[1]), G::times0(q[2]), G::times0(q[3])};
+    return q;
+}
+
+// Weights are taken relative to a reference that only moves when a score
+// passes it by more than 2^kSlack, which few tiles do: only then are sums
+// rescaled. Half precision, whose range is short at both ends, holds them times
+// 2^kShift. Products are rounded before the reference is subtracted, so that
+// the difference is exact and the reference's own weight 1 for scores of any
+// size.
+constexpr float kSlack = 8.f;
+template <class T>
+constexpr float kShift = std::is_same<T, _Float16>::value ? 7.f : 0.f;
+// Moves a query's reference if its keys' largest score asks for it (whatever other
+// queries ask for), and returns the factor of what was summed before.
+__device__ __forceinline__ float move(float& ref, float top) {
+    if (!(top > ref + kSlack)) return 1.f;
+    const float fix = fast_exp2(ref - top);
+    ref = top;
+    return fix;
+}
+__device__ __forceinline__ float weight_of(float s, float c, float ref, float shift) {
+#pragma clang fp contract(off)
+    const float x = s * c;
+    return fast_exp2((x - ref) + shift);
+}
+
+// Keys that not all rows of a work group see. An infinity or a NaN in one's value
+// must not reach a row that does not see it as 0 times it: in the tiles that
+// hold such keys those elements are made 0 in LDS, and at the end they are added
+// to the rows that see their keys, whose results are what the elements make of
+// them whatever the weights.
+template <int KEYS>
+struct Crossing {
+    static constexpr int kKeys = KEYS, kTiles = kPagedTileMost / KEYS + 2;
+    int from;  // the first such tile's first key
+    __device__ __forceinline__ Crossing(const TileJob& j, int first_token)
+        : from(j.k0 + max(j.before + first_token - j.k0, 0) / kKeys * kKeys) {}
+    // Clears such elements of the planes at `vals`; keeps their keys in `wild`.
+    template <class G, int THREADS>
+    static __device__ __forceinline__ void clear(char* vals, int planes, unsigned long long* wild) {
+#pragma unroll 1
+        for (int at = threadIdx.x; at < planes * kKeys * 8; at += THREADS) {
+            u32x4 x = *reinterpret_cast<const u32x4*>(vals + 16 * at);
+            const uint32_t words[4] = {x[0], x[1], x[2], x[3]};
+            if (!G::words_wild(words)) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t low[1] = {x[i] & 0xffffu}, high[1] = {x[i] & 0xffff0000u};
+                x[i] &= (G::words_wild(low) ? 0u : 0xffffu) | (G::words_wild(high) ? 0u : 0xffff0000u);
+            }
+            *reinterpret_cast<u32x4*>(vals + 16 * at) = x;
+            atomicOr(wild, 1ull << (at / 8 % kKeys));
+        }
+    }
+    // o plus the elements that are not finite of the keys below `sees` that were
+    // cleared; row(key): where the key's values of o begin.
+    template <class T, int NB, class Row>
+    __device__ __forceinline__ void add(const unsigned long long* wild, int sees, int dim, Row&& row,
+                                        f32x4 (&o)[NB]) const {
+#pragma unroll 1
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll 1
+            for (uint64_t m = wild[i]; m; m &= m - 1) {
+                const int key = from + kKeys * i + __builtin_ctzll(m);
+                if (key >= sees) break;
+                const char* at = row(key);
+                if (!at) break;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    if (16 * b + 4 * (lane_id() >> 4) >= dim) continue;
+                    const u32x2 x = *reinterpret_cast<const u32x2*>(at + 32 * b + 8 * (lane_id() >> 4));
+                    float y[4];
+                    unpack2<T>(x[0], y[0], y[1]);
+                    unpack2<T>(x[1], y[2], y[3]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[b][j] += __builtin_isfinite(y[j]) ? 0.f : y[j];
+                }
+            }
+    }
+};
+
+// ---------------------------------------------------------------- absorbed
+// Keys of up to DK and values of up to DV elements, a value the first part of its
+// key. NW wavefronts, in pairs: a pair takes 32 rows, each of the two half of a
+// tile's keys for the scores and half of the columns for the result.
+template <class T, int DK, int DV, int NW_>
+struct AbsorbedGeo : Tile<T, 64, true> {
+    static constexpr int kKeys = 64;
+    static constexpr int QS = DK / 32, NB = DV / 32, QB = 2, NW = NW_, BM = NW / 2 * 16 * QB;
+    static constexpr int kPlanes = DK / 64, kDv = DV;
+    static constexpr int kBlocks = kKeys / 8 / NW;  // blocks of 8 rows that a wavefront loads
+    static_assert(BM <= kPagedTileMost, "the limit of rows counts on it");
+    static_assert(DK % 64 == 0 && DV % 64 == 0 && kKeys % (8 * NW) == 0, "tile shape");
+};
+
+template <class G, class T>
+__global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t tiles) {
+    constexpr int QB = G::QB, QS = G::QS, NB = G::NB, NW = G::NW, kKeys = G::kKeys;
+    using Pl = Planes<kKeys>;
+    using Cr = Crossing<kKeys>;
+    __shared__ __align__(16) char tile0[G::kPlanes * Pl::kPlane];
+    __shared__ __align__(16) char tile1[G::kPlanes * Pl::kPlane];
+    __shared__ u32x4 probs[NW][QB][kWave];    // [wavefront that made them]
+    __shared__ float tops[NW][QB][16];
+    __shared__ int raise_s[2];                // some row's reference has to move
+    __shared__ unsigned long long wild_s[Cr::kTiles];  // see there
+    __shared__ int wrong_s;
+    const int tid = threadIdx.x, lane = lane_id();
+    const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int half = w & 1;
+    int64_t unit = xcd_block();
+    if (unit >= a.seqs * a.npieces * tiles) return;
+    const int tile = tiles - 1 - (int)(unit % tiles);  // the longest first
+    unit /= tiles;
+    const int piece = (int)(unit % a.npieces);
+    const int64_t s = unit / a.npieces;
+    const TileJob job = tile_job(a, s, tile, G::BM, piece);
+    if (job.idle) return;
+    const int n = lane & 15;
+    const int row0 = job.first + 16 * QB * (w >> 1);  // this pair's first row
+    TileRow r[QB];
+#pragma unroll
+    for (int b = 0; b < QB; ++b) r[b] = tile_row(a, job, row0 + 16 * b + n, 0);
+    if (job.sq.bad) {
+        if (piece == 0 && half == 0)
+#pragma unroll
+            for (int b = 0; b < QB; ++b) store_nan<T>(a, r[b]);
+        return;
+    }
+    if (job.k0 >= job.k1) return;
+    if (tid == 0) {
+        wrong_s = raise_s[0] = raise_s[1] = 0;
+#pragma unroll
+        for (int i = 0; i < Cr::kTiles; ++i) wild_s[i] = 0;
+    }
+    const Cr cross(job, job.first / a.s.group);
+    const int lo = __builtin_amdgcn_readfirstlane(r[0].t);
+    const int hi = __builtin_amdgcn_readlane(r[QB - 1].t, 15);
+    const int mine = row0 < job.rows ? min(job.k1, job.before + hi) : 0;  // some row sees
+    const int full = min(job.k1, job.before + lo);                       // all rows see
+
+    u32x4 q[QB][QS];
+#pragma unroll
+    for (int x = 0; x < QB; ++x)
+#pragma unroll
+        for (int t = 0; t < QS; ++t)
+            q[x][t] = load_query<G>(a, r[x], 64 * t + 16 * (lane >> 4), 2 * a.key_dim);
+    f32x4 o[QB][NB];
+    float ref[QB], sum[QB];  // ref: of this lane's query, in the whole pair; sum: of this lane
+#pragma unroll
+    for (int x = 0; x < QB; ++x) {
+        ref[x] = -INFINITY;
+        sum[x] = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) o[x][b] = f32x4{0, 0, 0, 0};
+    }
+    const int32_t* pages = a.col + job.sq.page0;
+    TileRows<Pl, G::kBlocks> mineload(w * G::kBlocks);
+    const auto load_tile = [&](char* dst, int t0) {
+#pragma unroll
+        for (int i = 0; i < G::kBlocks; ++i) {
+            const char* zero = reinterpret_cast<const char*>(g_zero) + mineload.byte[i];
+            const char* row = mineload.latent(a, t0, job.k1, i);
+            row = row ? row + mineload.byte[i] : zero;
+#pragma unroll
+            for (int g = 0; g < G::kPlanes; ++g)
+                load_to_lds(128 * g + mineload.byte[i] < 2 * a.key_dim ? row + 128 * g : zero,
+                            dst + g * Pl::kPlane + (w * G::kBlocks + i) * 1024);
+        }
+    };
+    mineload.look_up(a, pages, job.k0, job.k1);
+    __syncthreads();  // the flags
+    load_tile(tile0, job.k0);
+    mineload.look_up(a, pages, job.k0 + kKeys, job.k1);
+    wait_for_loads();
+    __syncthreads();
+
+    // One tile of keys, staged in `rows`; the next one is loaded into `next`.
+    const auto take = [&](char* rows, char* next, int t0, int par) {
+        if (t0 + kKeys < job.k1) {
+            load_tile(next, t0 + kKeys);
+            mineload.look_up(a, pages, t0 + 2 * kKeys, job.k1);
+        }
+        const bool active = t0 < mine;
+        f32x4 sc[QB][2];
+        float top[QB];
+        const auto put_probs = [&](float (&add)[QB]) {
+#pragma unroll
+            for (int x = 0; x < QB; ++x) {
+                float p[8];
+                add[x] = 0.f;
+                const float base = ref[x] == -INFINITY ? 0.f : ref[x];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    p[j] = weight_of(sc[x][j >> 2][j & 3], a.s.mag, base, kShift<T>);
+                    add[x] += p[j];
+                }
+                typename G::Probs pr;
+                G::pack_probs(p, pr);
+                probs[w][x][lane] = u32x4{pr.w[0], pr.w[1], pr.w[2], pr.w[3]};
+            }
+        };
+        float add[QB];
+        if (active) {
+            const int rb = Pl::row_base(32 * half);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                for (int x = 0; x < QB; ++x) sc[x][b] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < QS; ++i) {
+                    const u32x4 k = Pl::row(rows, rb, 16 * b, i);
+#pragma unroll
+                    for (int x = 0; x < QB; ++x) sc[x][b] = mfma32<T>(k, q[x][i], sc[x][b]);
+                }
+            }
+            const int t = t0 + 32 * half;
+            bool raise = false;
+#pragma unroll
+            for (int x = 0; x < QB; ++x) {
+                if (t + 32 > full)  // some row does not see some key
+                    Softmax<G, T>::hide(sc[x], Seen::first(min(job.k1, job.before + r[x].t) - t));
+                top[x] = sc[x][0][0];
+#pragma unroll
+                for (int j = 1; j < 8; ++j) top[x] = fmaxf(top[x], sc[x][j >> 2][j & 3]);
+                top[x] *= a.s.mag;
+                raise |= top[x] > ref[x] + kSlack;
+            }
+            if (__any(raise)) raise_s[par] = 1;
+            put_probs(add);
+        }
+        __syncthreads();
+        if (tid == 0) raise_s[par ^ 1] = 0;
+        if (raise_s[par]) {  // hardly ever after the first tiles
+            if (active) {
+#pragma unroll
+                for (int x = 0; x < QB; ++x) {
+                    top[x] = quad_max(top[x]);
+                    if (lane < 16) tops[w][x][lane] = top[x];
+                }
+            }
+            __syncthreads();
+            if (active) {
+#pragma unroll
+                for (int x = 0; x < QB; ++x) {
+                    const float fix = move(ref[x], fmaxf(top[x], tops[w ^ 1][x][n]));
+                    sum[x] *= fix;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) o[x][b] *= fix;
+                }
+                put_probs(add);
+            }
+            __syncthreads();
+        }
+        if (min(t0 + kKeys, job.k1) > job.before + job.first / a.s.group) {
+            Cr::template clear<G, NW * kWave>(rows, G::kDv / 64, &wild_s[(t0 - cross.from) / kKeys]);
+            __syncthreads();
+        }
+        if (active) {
+#pragma unroll
+            for (int x = 0; x < QB; ++x) sum[x] += add[x];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                typename G::Probs pr[QB];
+#pragma unroll
+                for (int x = 0; x < QB; ++x) {
+                    const u32x4 p = probs[(w & ~1) + j][x][lane];
+                    pr[x] = {{p[0], p[1], p[2], p[3]}};
+                }
+                const int vb = Pl::value_base(32 * j);
+                const char* vals = rows + half * (G::kDv / 128) * Pl::kPlane;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const u32x4 v = Pl::value(vals, vb, b);
+#pragma unroll
+                    for (int x = 0; x < QB; ++x) o[x][b] = G::add_block(v, pr[x], o[x][b]);
+                }
+            }
+        }
+        wait_for_loads();
+        __syncthreads();  // the next tile is there, this one's readers are done
+    };
+    for (int t0 = job.k0; t0 < job.k1; t0 += 2 * kKeys) {
+        take(tile0, tile1, t0, 0);
+        if (t0 + kKeys < job.k1) take(tile1, tile0, t0 + kKeys, 1);
+    }
+    if (mineload.wrong) wrong_s = 1;
+#pragma unroll
+    for (int x = 0; x < QB; ++x) {
+        sum[x] = quad_sum(sum[x]);
+        if (lane < 16) tops[w][x][lane] = sum[x];
+    }
+    __syncthreads();
+    if (row0 >= job.rows) return;
+#pragma unroll
+    for (int x = 0; x < QB; ++x) {
+        const int sees = job.before + r[x].t;
+        if (!r[x].has || sees <= job.k0) continue;
+        const float l = wrong_s ? NAN : tops[w & ~1][x][n] + tops[w | 1][x][n];
+        const int64_t line = r[x].token * a.s.hq + r[x].hq;
+        const bool part = sees > a.piece;
+        const int64_t at = (int64_t)piece * a.tokens * a.s.hq + line;
+        const float f = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        cross.template add<T>(wild_s, min(job.k1, sees), a.s.dim - half * (G::kDv / 2), [&](int key) -> const char* {
+            const uint32_t pg = a.page_div.div(key), id = (uint32_t)pages[pg];
+            if (id >= (uint64_t)a.npages) return nullptr;
+            return a.k + ((uint64_t)(id * a.k_page + (key - pg * a.page_div.d) * a.k_slot) << a.k_shift) +
+                   half * G::kDv;
+        }, o[x]);
+        char* row = part ? reinterpret_cast<char*>(a.part + at * a.s.dim)
+                         : a.out.base + r[x].token * a.out.row + r[x].hq * a.out.head;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int d = half * (G::kDv / 2) + 16 * b + 4 * (lane >> 4);
+            if (d >= a.s.dim) continue;
+            if (part)
+                *reinterpret_cast<f32x4*>(row + 4 * d) = o[x][b];
+            else
+                G::store_four(o[x][b] * f, row + 2 * d);
+        }
+        if (half == 0 && lane < 16) {
+            if (part) {
+                a.part_ml[2 * at] = ref[x];
+                a.part_ml[2 * at + 1] = l;
+            } else if (a.lse) {
+                a.lse[line] = l == 0.f ? -INFINITY : (ref[x] - kShift<T> + fast_log2(l)) * kLn2;
+            }
+        }
+    }
+}
+
+// One wavefront per token and query head joins its pieces, in their order.
+constexpr int kWaves = 4;
+template <class T>
+__global__ __launch_bounds__(kWaves* kWave) void k_latent_join(PagedArgs a) {
+    const int64_t unit = grid_block() * kWaves + threadIdx.x / kWave;
+    if (unit >= a.tokens * a.s.hq) return;
+    const int64_t token = unit / a.s.hq;
+    const int hq = (int)(unit - token * a.s.hq);
+    if (token < a.q_rowptr[0]) return;
+    const int64_t s = upper_index(a.q_rowptr, int64_t(0), a.seqs, token);
+    const Sequence sq = read_sequence(a, s);
+    if (sq.none || sq.bad || token < sq.q0 || token - sq.q0 >= sq.fresh) return;
+    const int sees = sq.length - sq.fresh + 1 + (int)(token - sq.q0);
+    if (sees <= a.piece) return;
+    const int count = (sees + a.piece - 1) / a.piece;
+    const int64_t step = a.tokens * a.s.hq;
+    const float* ml = a.part_ml + 2 * unit;
+    float m, l;
+    join_sums(ml, step, count, m, l);
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    char* row = a.out.base + token * a.out.row + hq * a.out.head;
+    for (int d = 4 * lane_id(); d < a.s.dim; d += 4 * kWave) {
+        f32x4 x{0, 0, 0, 0};
+#pragma unroll 4
+        for (int i = 0; i < count; ++i)
+            x += *reinterpret_cast<const f32x4*>(a.part + (i * step + unit) * a.s.dim + d) *
+                 fast_exp2(ml[2 * i * step] - m);
+        x *= f;
+        *reinterpret_cast<u32x2*>(row + 2 * d) = u32x2{pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3])};
+    }
+    if (a.lse && lane_id() == 0)
+        a.lse[unit] = l == 0.f ? -INFINITY : (m - kShift<T> + fast_log2(l)) * kLn2;
+}
+
+// ---------------------------------------------------------------- expanded
+// Keys and values of one head that k_expand made, of up to 64 MP and 64 VP
+// elements, each as two numbers of the type that add up to it: rounded to one,
+// a key's error would be that of the scores, and so of the log-sum-exp, and a
+// value's as large as the result's own rounding. The keys' last part, of up to
+// 64 elements, is the latent row's. A wavefront takes QB blocks of 16 rows.
+template <class T, int MP_, int VP_>
+struct ExpandedGeo : Tile<T, 64, true> {
+    static constexpr int kKeys = 32;
+    static constexpr int MP = MP_, VP = VP_, QS = 2 * MP + 2, NB = 4 * VP, QB = 2, NW = 4;
+    static constexpr int BM = NW * 16 * QB;
+    static constexpr int kLow = MP, kRope = 2 * MP, kValues = kRope + 1, kPlanes = kValues + 2 * VP;
+    static_assert(BM <= kPagedTileMost && kKeys == 8 * NW, "tile shape");
+};
+
+template <class G, class T>
+__global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int32_t tiles) {
+    constexpr int QB = G::QB, QS = G::QS, NB = G::NB, NW = G::NW, kKeys = G::kKeys;
+    using Pl = Planes<kKeys>;
+    using Cr = Crossing<kKeys>;
+    __shared__ __align__(16) char tile0[G::kPlanes * Pl::kPlane];
+    __shared__ __align__(16) char tile1[G::kPlanes * Pl::kPlane];
+    __shared__ unsigned long long wild_s[Cr::kTiles];  // see there
+    __shared__ int wrong_s;
+    const int tid = threadIdx.x, lane = lane_id();
+    const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
+    int64_t unit = xcd_block();
+    if (unit >= a.seqs * a.s.hkv * a.npieces * tiles) return;
+    const int tile = tiles - 1 - (int)(unit % tiles);  // the longest first
+    unit /= tiles;
+    const int piece = (int)(unit % a.npieces);
+    unit /= a.npieces;
+    const int64_t s = unit % a.seqs;
+    const int h = (int)(unit / a.seqs);
+    const TileJob job = tile_job(a, s, tile, G::BM, piece);
+    if (job.idle) return;
+    const int n = lane & 15;
+    const int row0 = job.first + 16 * QB * w;  // this wavefront's first row
+    TileRow r[QB];
+#pragma unroll
+    for (int b = 0; b < QB; ++b) r[b] = tile_row(a, job, row0 + 16 * b + n, h);
+    if (job.sq.bad) {
+        if (piece == 0)
+#pragma unroll
+            for (int b = 0; b < QB; ++b) store_nan<T>(a, r[b]);
+        return;
+    }
+    if (job.k0 >= job.k1) return;
+    if (tid == 0) {
+        wrong_s = 0;
+#pragma unroll
+        for (int i = 0; i < Cr::kTiles; ++i) wild_s[i] = 0;
+    }
+    const Cr cross(job, job.first);
+    const int lo = __builtin_amdgcn_readfirstlane(r[0].t);
+    const int hi = __builtin_amdgcn_readlane(r[QB - 1].t, 15);
+    const int mine = row0 < job.rows ? min(job.k1, job.before + hi) : 0;  // some row sees
+    const int full = min(job.k1, job.before + lo);                       // all rows see
+
+    u32x4 q[QB][QS];
+    f32x4 o[QB][NB];
+    float ref[QB], sum[QB];
+    const int made = 2 * a.made_dim, values = 2 * a.s.dim;  // bytes
+#pragma unroll
+    for (int x = 0; x < QB; ++x) {
+        ref[x] = -INFINITY;
+        sum[x] = 0.f;
+#pragma unroll
+        for (int t = 0; t < QS; ++t) {
+            const int at = 64 * t + 16 * (lane >> 4), rope = at - 128 * G::MP;
+            q[x][t] = t < 2 * G::MP ? load_query<G>(a, r[x], at, made)
+                                    : load_query<G>(a, r[x], made + rope, 2 * a.key_dim);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) o[x][b] = f32x4{0, 0, 0, 0};
+    }
+    const int32_t* pages = a.col + job.sq.page0;
+    // the sequence's first row of made keys and values
+    const int64_t made0 = h * a.made_rows +
+                          (a.made_step ? s * a.made_step : job.sq.page0 * (int64_t)a.page_div.d);
+    const char* made_v = a.made_v + made0 * 2 * values;
+    TileRows<Pl, 1> from(w);
+    const int byte = from.byte[0];
+    // of this lane's row of the next tile
+    const char* ksrc = a.made_k + (made0 + job.k0 + from.row[0]) * 2 * made + byte;
+    const char* vsrc = made_v + (int64_t)(job.k0 + from.row[0]) * 2 * values + byte;
+    const char* zero = reinterpret_cast<const char*>(g_zero);
+    const auto load_tile = [&](char* dst, int t0) {
+        const char* latent = from.latent(a, t0, job.k1, 0);
+        const bool in = latent != nullptr;
+        char* to = dst + w * 1024;
+#pragma unroll
+        for (int g = 0; g < G::MP; ++g) {
+            const bool has = in && 128 * g + byte < made;
+            load_to_lds(has ? ksrc + 128 * g : zero, to + g * Pl::kPlane);
+            load_to_lds(has ? ksrc + made + 128 * g : zero, to + (G::kLow + g) * Pl::kPlane);
+        }
+        load_to_lds(in && made + byte < 2 * a.key_dim ? latent + a.rope_at + byte : zero,
+                    to + G::kRope * Pl::kPlane);
+#pragma unroll
+        for (int g = 0; g < G::VP; ++g) {
+            const bool has = in && 128 * g + byte < values;
+            load_to_lds(has ? vsrc + 128 * g : zero, to + (G::kValues + g) * Pl::kPlane);
+            load_to_lds(has ? vsrc + values + 128 * g : zero,
+                        to + (G::kValues + G::VP + g) * Pl::kPlane);
+        }
+        ksrc += (int64_t)kKeys * 2 * made;
+        vsrc += (int64_t)kKeys * 2 * values;
+    };
+    from.look_up(a, pages, job.k0, job.k1);
+    __syncthreads();  // the flags
+    load_tile(tile0, job.k0);
+    from.look_up(a, pages, job.k0 + kKeys, job.k1);
+    wait_for_loads();
+    __syncthreads();
+
+    const int rb = Pl::row_base(0), vb = Pl::value_base(0);
+    // One tile of keys, staged in `rows`; the next one is loaded into `next`.
+    const auto take = [&](char* rows, char* next, int t0) {
+        char* vals = rows + G::kValues * Pl::kPlane;
+        if (t0 + kKeys < job.k1) {
+            load_tile(next, t0 + kKeys);
+            from.look_up(a, pages, t0 + 2 * kKeys, job.k1);
+        }
+        if (min(t0 + kKeys, job.k1) > job.before + job.first) {
+            Cr::template clear<G, NW * kWave>(vals, G::VP, &wild_s[(t0 - cross.from) / kKeys]);
+            __syncthreads();
+        }
+        if (t0 < mine) {
+            f32x4 sc[QB][2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                for (int x = 0; x < QB; ++x) sc[x][b] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < 4 * G::MP + 2; ++i) {  // the keys' low parts first
+                    const int t = i < 2 * G::MP ? i + 2 * G::MP : i < 4 * G::MP ? i - 2 * G::MP : i;
+                    const int step = t < 2 * G::MP ? t : t - 2 * G::MP;
+                    const u32x4 k = Pl::row(rows, rb, 16 * b, t);
+#pragma unroll
+                    for (int x = 0; x < QB; ++x) sc[x][b] = mfma32<T>(k, q[x][step], sc[x][b]);
+                }
+            }
+            bool raise = false;
+            float top[QB];
+#pragma unroll
+            for (int x = 0; x < QB; ++x) {
+                if (t0 + kKeys > full)  // some row does not see some key
+                    Softmax<G, T>::hide(sc[x], Seen::first(min(job.k1, job.before + r[x].t) - t0));
+                top[x] = sc[x][0][0];
+#pragma unroll
+                for (int j = 1; j < 8; ++j) top[x] = fmaxf(top[x], sc[x][j >> 2][j & 3]);
+                top[x] *= a.s.mag;
+                raise |= top[x] > ref[x] + kSlack;
+            }
+            if (__any(raise)) {  // hardly ever after the first tiles
+#pragma unroll
+                for (int x = 0; x < QB; ++x) {
+                    const float fix = move(ref[x], quad_max(top[x]));
+                    sum[x] *= fix;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) o[x][b] *= fix;
+                }
+            }
+            typename G::Probs pr[QB];
+#pragma unroll
+            for (int x = 0; x < QB; ++x) {
+                float p[8];
+                const float base = ref[x] == -INFINITY ? 0.f : ref[x];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    p[j] = weight_of(sc[x][j >> 2][j & 3], a.s.mag, base, kShift<T>);
+                    sum[x] += p[j];
+                }
+                G::pack_probs(p, pr[x]);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const u32x4 low = Pl::value(vals + G::VP * Pl::kPlane, vb, b);
+                const u32x4 high = Pl::value(vals, vb, b);
+#pragma unroll
+                for (int x = 0; x < QB; ++x) o[x][b] = G::add_block(low, pr[x], o[x][b]);
+#pragma unroll
+                for (int x = 0; x < QB; ++x) o[x][b] = G::add_block(high, pr[x], o[x][b]);
+            }
+        }
+        wait_for_loads();
+        __syncthreads();  // the next tile is there, this one's readers are done
+    };
+    for (int t0 = job.k0; t0 < job.k1; t0 += 2 * kKeys) {
+        take(tile0, tile1, t0);
+        if (t0 + kKeys < job.k1) take(tile1, tile0, t0 + kKeys);
+    }
+    if (from.wrong) wrong_s = 1;
+    __syncthreads();
+    if (row0 >= job.rows) return;
+#pragma unroll
+    for (int x = 0; x < QB; ++x) {
+        const int sees = job.before + r[x].t;
+        const float all = quad_sum(sum[x]);
+        if (!r[x].has || sees <= job.k0) continue;
+        const float l = wrong_s ? NAN : all;
+        const int64_t line = r[x].token * a.s.hq + r[x].hq;
+        const bool part = sees > a.piece;
+        const int64_t at = (int64_t)piece * a.tokens * a.s.hq + line;
+        const float f = l == 0.f ? 0.f : 1.f / l;
+        cross.template add<T>(wild_s, min(job.k1, sees), a.s.dim,
+                              [&](int key) { return made_v + (int64_t)key * 2 * values; }, o[x]);
+        char* row = part ? reinterpret_cast<char*>(a.part + at * a.s.dim)
+                         : a.out.base + r[x].token * a.out.row + r[x].hq * a.out.head;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int d = 16 * b + 4 * (lane >> 4);
+            if (d >= a.s.dim) continue;
+            if (part)
+                *reinterpret_cast<f32x4*>(row + 4 * d) = o[x][b];
+            else
+                G::store_four(o[x][b] * f, row + 2 * d);
+        }
+        if (lane < 16) {
+            if (part) {
+                a.part_ml[2 * at] = ref[x];
+                a.part_ml[2 * at + 1] = l;
+            } else if (a.lse) {
+                a.lse[line] = l == 0.f ? -INFINITY : (ref[x] - kShift<T> + fast_log2(l)) * kLn2;
+            }
+        }
+    }
+}
+
+// Every head's keys and values: C[row][m] = sum_x W[m][x] c[row][x], W the heads'
+// key rows, then their value rows. A work group makes 128 rows of W times 128
+// tokens, 64 values of x at a time.
+struct ExpandShape {
+    int64_t rows;        // of made keys and values per head
+    int32_t key_tiles;   // tiles of 128 of all heads' key rows
+    int32_t value_tiles;
+    FastDiv key_div, value_div;  // rows of a head
+    FastDiv tile_div;            // tiles of W
+};
+
+template <class T>
+__global__ __launch_bounds__(256) void k_expand(ExpandArgs e, ExpandShape z) {
+    constexpr int kM = 128, kPlane = kM * 128;
+    const LatentArgs& a = e.a;
+    __shared__ __align__(16) char wrows0[kPlane], wrows1[kPlane], crows0[kPlane], crows1[kPlane];
+    __shared__ const char* from_s[kM];
+    __shared__ int any_s;
+    using G = Tile<T, 64, true>;
+    const int tid = threadIdx.x, lane = lane_id();
+    const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int64_t unit = xcd_block();
+    const int wtiles = z.key_tiles + z.value_tiles;
+    const int64_t ctile = unit / wtiles;
+    const int wtile = (int)(unit - ctile * wtiles);
+    if (ctile * kM >= z.rows) return;
+    const bool keys = wtile < z.key_tiles;
+    const int m0 = kM * (keys ? wtile : wtile - z.key_tiles);
+    const int per = keys ? a.made_dim : a.s.dim, all = a.s.hq * per;
+    if (tid == 0) any_s = 0;
+    __syncthreads();
+    // the tokens' latent rows
+    if (tid < kM) {
+        const int64_t row = ctile * kM + tid;
+        const char* from = nullptr;
+        if (row < z.rows) {
+            int64_t s, key;
+            if (a.made_step) {
+                s = row / a.made_step;
+                key = row - s * a.made_step;
+            } else {
+                const int64_t entry = row / a.page_div.d;
+                s = upper_index(a.rowptr, int64_t(0), a.seqs, entry);
+                key = row - a.rowptr[s] * (int64_t)a.page_div.d;
+            }
+            const Sequence sq = read_sequence(a, s);
+            if (key >= 0 && key < sq.length && !sq.none) {
+                const uint32_t pg = a.page_div.div((uint32_t)key);
+                const uint32_t id = (uint32_t)a.col[sq.page0 + pg];
+                const uint32_t slot = (uint32_t)key - pg * a.page_div.d;
+                if (id < (uint64_t)a.npages) {
+                    from = a.k + ((uint64_t)(id * a.k_page + slot * a.k_slot) << a.k_shift);
+                    any_s = 1;
+                }
+            }
+        }
+        from_s[tid] = from;
+    }
+    __syncthreads();
+    if (!any_s) return;
+    // this lane's rows of W and c: of blocks of 8 rows 4 w + 0..3, row l / 8
+    const char* zero = reinterpret_cast<const char*>(g_zero);
+    const char *wsrc[4], *csrc[4];
+    int byte[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 8 * (4 * w + i) + (lane >> 3);
+        byte[i] = 16 * ((lane & 7) ^ Planes<kM>::swap(row));
+        const int m = m0 + row;
+        wsrc[i] = nullptr;
+        if (m < all) {
+            const int head = (int)(keys ? z.key_div : z.value_div).div(m);
+            const AttnRows& r = keys ? e.wk : e.wv;
+            wsrc[i] = r.base + head * r.row + (m - head * per) * r.head;
+        }
+        csrc[i] = from_s[row];
+    }
+    const auto load = [&](char* wrows, char* crows, int x0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = 2 * x0 + byte[i];
+            const bool in = at < 2 * e.latent_dim;
+            load_to_lds(wsrc[i] && in ? wsrc[i] + at : zero, wrows + (4 * w + i) * 1024);
+            load_to_lds(csrc[i] && in ? csrc[i] + at : zero, crows + (4 * w + i) * 1024);
+        }
+    };
+    f32x4 acc[4][4];  // rows of W, tokens
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    const auto product = [&](const char* wrows, const char* crows) {
+        const int wb = Planes<kM>::row_base(64 * (w >> 1)), cb = Planes<kM>::row_base(64 * (w & 1));
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            u32x4 x[4], y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = *reinterpret_cast<const u32x4*>(wrows + ((wb + 2048 * i) ^ (64 * t)));
+                y[i] = *reinterpret_cast<const u32x4*>(crows + ((cb + 2048 * i) ^ (64 * t)));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = mfma32<T>(x[i], y[j], acc[i][j]);
+        }
+    };
+    load(wrows0, crows0, 0);
+    wait_for_loads();
+    __syncthreads();
+    for (int x0 = 0; x0 < e.latent_dim; x0 += 128) {
+        if (x0 + 64 < e.latent_dim) load(wrows1, crows1, x0 + 64);
+        product(wrows0, crows0);
+        wait_for_loads();
+        __syncthreads();
+        if (x0 + 64 >= e.latent_dim) break;
+        if (x0 + 128 < e.latent_dim) load(wrows0, crows0, x0 + 128);
+        product(wrows1, crows1);
+        wait_for_loads();
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = m0 + 64 * (w >> 1) + 16 * i + 4 * (lane >> 4);
+        if (m >= all) continue;
+        const int head = (int)(keys ? z.key_div : z.value_div).div(m);
+        char* to = (keys ? a.made_k : a.made_v) + ((int64_t)head * z.rows * 2 * per + m - head * per) * 2;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int at = 64 * (w & 1) + 16 * j + (lane & 15);
+            if (!from_s[at]) continue;
+            // rounded, and what that leaves (nothing where it is not finite)
+            f32x4 left;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float high = (float)(T)acc[i][j][x];
+                left[x] = __builtin_isfinite(high) ? acc[i][j][x] - high : 0.f;
+            }
+            char* row = to + (ctile * kM + at) * 2 * per * 2;
+            G::store_four(acc[i][j], row);
+            G::store_four(left, row + 2 * per);
+        }
+    }
+}
+
+template <class F>
+void with_latent_type(int type, F&& f) {
+    if (type == SPGEMM_TYPE_BF16) f((__bf16*)nullptr);
+    else f((_Float16*)nullptr);
+}
+// f(geometry, type) of a call: the smallest widths that hold it.
+template <class F>
+void with_absorbed(const LatentArgs& a, F&& f) {
+    with_latent_type(a.s.type, [&](auto* t) {
+        using T = std::remove_pointer_t<decltype(t)>;
+        if (a.s.dim <= 128 && a.key_dim <= 192) f((AbsorbedGeo<T, 192, 128, 8>*)nullptr, t);
+        else if (a.s.dim <= 256 && a.key_dim <= 320) f((AbsorbedGeo<T, 320, 256, 8>*)nullptr, t);
+        else f((AbsorbedGeo<T, 576, 512, 4>*)nullptr, t);
+    });
+}
+template <class F>
+void with_expanded(const LatentArgs& a, F&& f) {
+    with_latent_type(a.s.type, [&](auto* t) {
+        using T = std::remove_pointer_t<decltype(t)>;
+        if (a.s.dim <= 64 && a.made_dim <= 64) f((ExpandedGeo<T, 1, 1>*)nullptr, t);
+        else f((ExpandedGeo<T, 2, 2>*)nullptr, t);
+    });
+}
+
+}  // namespace
+
+int latent_tile_rows(const LatentArgs& a, bool absorbed) {
+    int bm = 0;
+    const auto get = [&](auto* g, auto*) { bm = std::remove_pointer_t<decltype(g)>::BM; };
+    if (absorbed) with_absorbed(a, get);
+    else with_expanded(a, get);
+    return bm;
+}
+
+void latent_attention(const LatentArgs& a, bool absorbed, hipStream_t st) {
+    const int64_t tiles = ceil_div((int64_t)a.max_new * a.s.group, latent_tile_rows(a, absorbed));
+    const dim3 grid = grid_2d(xcd_grid(a.seqs * a.s.hkv * a.npieces * tiles));
+    if (absorbed) {
+        with_absorbed(a, [&](auto* geo, auto* t) {
+            using G = std::remove_pointer_t<decltype(geo)>;
+            auto run = k_absorbed<G, std::remove_pointer_t<decltype(t)>>;
+            hipLaunchKernelGGL(run, grid, dim3(G::NW * kWave), 0, st, a, (int32_t)tiles);
+        });
+    } else {
+        with_expanded(a, [&](auto* geo, auto* t) {
+            using G = std::remove_pointer_t<decltype(geo)>;
+            auto run = k_expanded<G, std::remove_pointer_t<decltype(t)>>;
+            hipLaunchKernelGGL(run, grid, dim3(G::NW * kWave), 0, st, a, (int32_t)tiles);
+        });
+    }
+    SG_LAUNCH_CHECK();
+    if (a.npieces == 1) return;
+    with_latent_type(a.s.type, [&](auto* t) {
+        hipLaunchKernelGGL(k_latent_join<std::remove_pointer_t<decltype(t)>>,
+                           grid_2d(ceil_div(a.tokens * a.s.hq, kWaves)), dim3(kWaves * kWave), 0, st, a);
+    });
+    SG_LAUNCH_CHECK();
+}
+
+void latent_expand(const ExpandArgs& e, hipStream_t st) {
+    const LatentArgs& a = e.a;
+    ExpandShape z;
+    z.rows = a.made_rows;
+    z.key_tiles = (int32_t)ceil_div((int64_t)a.s.hq * a.made_dim, 128);
+    z.value_tiles = (int32_t)ceil_div((int64_t)a.s.hq * a.s.dim, 128);
+    z.key_div = FastDiv((uint32_t)a.made_dim);
+    z.value_div = FastDiv((uint32_t)a.s.dim);
+    const int64_t units = ceil_div(z.rows, 128) * (z.key_tiles + z.value_tiles);
+    if (units == 0) return;
+    with_latent_type(a.s.type, [&](auto* t) {
+        hipLaunchKernelGGL(k_expand<std::remove_pointer_t<decltype(t)>>, grid_2d(xcd_grid(units)),
+                           dim3(256), 0, st, e, z);
+    });
+    SG_LAUNCH_CHECK();
+}
+
+}  // namespace sg

@@ -1,5 +1,6 @@
 // Argument checks and the C ABI of include/spgemm_cache.h.
 #include "attention_checks.h"
+#include "latent.h"
 #include "mx.h"
 
 using namespace sg;
@@ -151,6 +152,112 @@ void mx_pieces(PagedArgs* a, int format) {
     }
 }
 
+// ---------------------------------------------------------------- latent
+bool latent_desc_valid(const spgemm_latent_desc* d, bool absorbed) {
+    if (!d || (d->type != SPGEMM_TYPE_BF16 && d->type != SPGEMM_TYPE_F16)) return false;
+    if (d->heads < 1 || d->heads > SPGEMM_ATTENTION_MAX_HEADS) return false;
+    if (d->latent_dim < 32 || d->latent_dim > SPGEMM_LATENT_MAX_DIM || d->latent_dim % 32 != 0)
+        return false;
+    if (d->rope_dim < 0 || d->rope_dim > SPGEMM_LATENT_MAX_ROPE || d->rope_dim % 8 != 0)
+        return false;
+    const auto head = [](int32_t n) {
+        return n >= 16 && n <= SPGEMM_LATENT_MAX_HEAD && n % 16 == 0;
+    };
+    if (!absorbed && (!head(d->key_dim) || !head(d->value_dim))) return false;
+    return std::isfinite(d->scale) && std::fabs(d->scale) < 1e30;
+}
+
+// A tensor's description as the shared checks take it.
+spgemm_attention_desc rows_desc(const spgemm_latent_desc* d, int heads_q, int heads_kv, int dim) {
+    return {d->type, heads_q, heads_kv, dim, d->scale};
+}
+
+// What a call is launched with, from sizes alone.
+void latent_shape(const spgemm_latent_desc* d, const spgemm_paged_batch* b, bool absorbed,
+                  LatentArgs* a) {
+    const spgemm_attention_desc r =
+        rows_desc(d, d->heads, absorbed ? 1 : d->heads, absorbed ? d->latent_dim : d->value_dim);
+    batch_shape(b, make_shape(&r), a);
+    a->key_dim = (absorbed ? d->latent_dim : d->key_dim) + d->rope_dim;
+    a->made_dim = absorbed ? 0 : d->key_dim;
+    a->rope_at = 2 * d->latent_dim;
+    cut_pieces(a, latent_tile_rows(*a, absorbed), 256, 256, 64);
+}
+
+// Rows of made keys: one per place of the table, or per sequence and place,
+// whichever are fewer.
+void made_rows(const spgemm_paged_batch* b, int64_t page_size, LatentArgs* a) {
+    const __int128 by_table = (__int128)b->pages->nnz * page_size;
+    const __int128 by_length = (__int128)a->seqs * a->max_length;
+    a->made_step = by_table <= by_length ? 0 : a->max_length;
+    const __int128 rows = std::min(by_table, by_length);
+    if (rows > ((__int128)1 << 40)) throw OverflowError("rows of made keys");
+    a->made_rows = (int64_t)rows;
+}
+
+int64_t carve_made(void* ws, LatentArgs* a) {
+    Carver c{static_cast<char*>(ws)};
+    a->made_k = reinterpret_cast<char*>(c.take((__int128)a->made_rows * a->s.hq * a->made_dim));
+    a->made_v = reinterpret_cast<char*>(c.take((__int128)a->made_rows * a->s.hq * a->s.dim));
+    const int64_t used = c.used;
+    return used + carve_parts(ws ? static_cast<char*>(ws) + used : nullptr, a);
+}
+
+int latent_cache(const spgemm_latent_cache* c, LatentArgs* a) {
+    const int64_t counts[2] = {c->npages, c->page_size};
+    const int64_t s[2] = {stride_bytes(c->stride_page, counts[0], 2),
+                          stride_bytes(c->stride_slot, counts[1], 2)};
+    if (s[0] < 0 || s[1] < 0) return SPGEMM_ERR_INVALID_ARG;
+    a->k = static_cast<const char*>(c->data);
+    if (c->npages > 0 && (!a->k || reinterpret_cast<uintptr_t>(a->k) % 16 != 0))
+        return SPGEMM_ERR_INVALID_ARG;
+    if (!gather_unit(s, counts, 2, &a->k_shift)) return SPGEMM_ERR_OVERFLOW;
+    a->k_page = (uint32_t)(s[0] >> a->k_shift);
+    a->k_slot = (uint32_t)(s[1] >> a->k_shift);
+    return SPGEMM_OK;
+}
+
+// Both forms; w_k and w_v only of the expanded one.
+int latent_call(const spgemm_latent_desc* desc, const spgemm_rows* q, const spgemm_rows* w_k,
+                const spgemm_rows* w_v, const spgemm_latent_cache* cache,
+                const spgemm_paged_batch* batch, const spgemm_rows* out, float* lse, bool absorbed,
+                void* workspace, int64_t workspace_bytes, hipStream_t st) {
+    if (!latent_desc_valid(desc, absorbed) || !batch_sizes_valid(batch) || !cache)
+        return SPGEMM_ERR_INVALID_ARG;
+    const int dim = absorbed ? desc->latent_dim : desc->key_dim;
+    const spgemm_attention_desc dq = rows_desc(desc, desc->heads, 1, dim + desc->rope_dim);
+    const spgemm_attention_desc dout =
+        rows_desc(desc, desc->heads, 1, absorbed ? desc->latent_dim : desc->value_dim);
+    if (!batch_sizes_fit(batch, &dq)) return SPGEMM_ERR_OVERFLOW;
+    return guarded([&]() -> int {
+        ExpandArgs e;
+        LatentArgs& a = e.a;
+        latent_shape(desc, batch, absorbed, &a);
+        if (!rows_valid(q, a.tokens, a.s.hq, &dq, false, &a.q) ||
+            !rows_valid(out, a.tokens, a.s.hq, &dout, true, &a.out))
+            return SPGEMM_ERR_INVALID_ARG;
+        if (!absorbed) {
+            const spgemm_attention_desc dw = rows_desc(desc, 1, 1, desc->latent_dim);
+            if (!rows_valid(w_k, a.s.hq, desc->key_dim, &dw, false, &e.wk) ||
+                !rows_valid(w_v, a.s.hq, desc->value_dim, &dw, false, &e.wv))
+                return SPGEMM_ERR_INVALID_ARG;
+        }
+        bool empty = false;
+        int rc = paged_checks(batch, a.s, cache->npages, cache->page_size, &a, &empty);
+        if (rc != SPGEMM_OK || empty) return rc;
+        rc = latent_cache(cache, &a);
+        if (rc != SPGEMM_OK) return rc;
+        a.lse = lse;
+        e.latent_dim = desc->latent_dim;
+        if (!absorbed) made_rows(batch, cache->page_size, &a);
+        const int64_t need = absorbed ? carve_parts(workspace, &a) : carve_made(workspace, &a);
+        if (!workspace_valid(workspace, workspace_bytes, need)) return SPGEMM_ERR_INVALID_ARG;
+        if (!absorbed) latent_expand(e, st);
+        latent_attention(a, absorbed, st);
+        return SPGEMM_OK;
+    });
+}
+
 }  // namespace
 
 extern "C" {
@@ -207,6 +314,58 @@ SPGEMM_API int spgemm_mx_attention(const spgemm_attention_desc* desc, const spge
         mx_attention(a, (hipStream_t)stream);
         return SPGEMM_OK;
     });
+}
+
+SPGEMM_API int spgemm_latent_attention_workspace(const spgemm_latent_desc* desc,
+                                                 const spgemm_paged_batch* batch, int64_t* bytes) {
+    if (!latent_desc_valid(desc, true) || !batch_sizes_valid(batch) || !bytes)
+        return SPGEMM_ERR_INVALID_ARG;
+    const spgemm_attention_desc r = rows_desc(desc, desc->heads, 1, desc->latent_dim);
+    if (!batch_sizes_fit(batch, &r)) return SPGEMM_ERR_OVERFLOW;
+    return guarded([&]() -> int {
+        LatentArgs a;
+        latent_shape(desc, batch, true, &a);
+        *bytes = carve_parts(nullptr, &a);
+        return SPGEMM_OK;
+    });
+}
+
+SPGEMM_API int spgemm_latent_attention(const spgemm_latent_desc* desc, const spgemm_rows* q,
+                                       const spgemm_latent_cache* cache,
+                                       const spgemm_paged_batch* batch, const spgemm_rows* out,
+                                       float* lse, void* workspace, int64_t workspace_bytes,
+                                       void* stream) {
+    return latent_call(desc, q, nullptr, nullptr, cache, batch, out, lse, true, workspace,
+                       workspace_bytes, (hipStream_t)stream);
+}
+
+SPGEMM_API int spgemm_latent_expanded_workspace(const spgemm_latent_desc* desc,
+                                                const spgemm_latent_cache* cache,
+                                                const spgemm_paged_batch* batch, int64_t* bytes) {
+    if (!latent_desc_valid(desc, false) || !batch_sizes_valid(batch) || !cache || !bytes ||
+        cache->page_size < 1 || batch->pages->nnz < 0)
+        return SPGEMM_ERR_INVALID_ARG;
+    const spgemm_attention_desc r = rows_desc(desc, desc->heads, 1, desc->value_dim);
+    if (!batch_sizes_fit(batch, &r) || cache->page_size > kMaxTokens ||
+        batch->pages->nnz > 0x7fffffffLL)
+        return SPGEMM_ERR_OVERFLOW;
+    return guarded([&]() -> int {
+        LatentArgs a;
+        latent_shape(desc, batch, false, &a);
+        made_rows(batch, cache->page_size, &a);
+        *bytes = carve_made(nullptr, &a);
+        return SPGEMM_OK;
+    });
+}
+
+SPGEMM_API int spgemm_latent_expanded(const spgemm_latent_desc* desc, const spgemm_rows* q,
+                                      const spgemm_rows* w_k, const spgemm_rows* w_v,
+                                      const spgemm_latent_cache* cache,
+                                      const spgemm_paged_batch* batch, const spgemm_rows* out,
+                                      float* lse, void* workspace, int64_t workspace_bytes,
+                                      void* stream) {
+    return latent_call(desc, q, w_k, w_v, cache, batch, out, lse, false, workspace, workspace_bytes,
+                       (hipStream_t)stream);
 }
 
 }  // extern "C"
