@@ -187,33 +187,45 @@ struct Crossing {
 
 // ---------------------------------------------------------------- absorbed
 // Keys of up to DK and values of up to DV elements, a value the first part of its
-// key. NW wavefronts, in pairs: a pair takes 32 rows, each of the two half of a
-// tile's keys for the scores and half of the columns for the result.
-template <class T, int DK, int DV, int NW_>
+// key. A team of CG wavefronts takes 32 rows, each of them a part of a tile's keys
+// for the scores and a part of the columns for the result.
+template <class T, int DK, int DV, int CG_>
 struct AbsorbedGeo : Tile<T, 64, true> {
     static constexpr int kKeys = 64;
-    static constexpr int QS = DK / 32, NB = DV / 32, QB = 2, NW = NW_, BM = NW / 2 * 16 * QB;
+    static constexpr int CG = CG_, NW = 8, QB = 2, BM = NW / CG * 16 * QB;
+    static constexpr int QS = DK / 32, NB = DV / 16 / CG;
+    static constexpr int KS = kKeys / 16 / CG;  // 16-key results of a wavefront's scores
+    // Query operands that stay in LDS, from the last step on: at the largest size
+    // registers hold all but three. (More are spilled there, and a load from
+    // scratch waits for the next tile's.)
+    static constexpr int kKept = DK == 576 ? 3 : 0;
+    static constexpr int kept(int x, int t) {  // its place there, or below 0
+        const int from_end = QB * (QS - 1 - t) + QB - 1 - x;
+        return from_end < kKept ? from_end : -1;
+    }
     static constexpr int kPlanes = DK / 64, kDv = DV;
     static constexpr int kBlocks = kKeys / 8 / NW;  // blocks of 8 rows that a wavefront loads
     static_assert(BM <= kPagedTileMost, "the limit of rows counts on it");
-    static_assert(DK % 64 == 0 && DV % 64 == 0 && kKeys % (8 * NW) == 0, "tile shape");
+    static_assert(DK % 64 == 0 && DV % (64 * CG) == 0 && KS >= 1, "tile shape");
 };
 
 template <class G, class T>
 __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t tiles) {
-    constexpr int QB = G::QB, QS = G::QS, NB = G::NB, NW = G::NW, kKeys = G::kKeys;
+    constexpr int QB = G::QB, QS = G::QS, NB = G::NB, NW = G::NW, CG = G::CG, KS = G::KS;
+    constexpr int kKeys = G::kKeys;
     using Pl = Planes<kKeys>;
     using Cr = Crossing<kKeys>;
     __shared__ __align__(16) char tile0[G::kPlanes * Pl::kPlane];
     __shared__ __align__(16) char tile1[G::kPlanes * Pl::kPlane];
-    __shared__ u32x4 probs[NW][QB][kWave];    // [wavefront that made them]
-    __shared__ float tops[NW][QB][16];
+    __shared__ u32x4 probs[NW / CG][kKeys / 32][QB][kWave];  // of a team's rows, 32 keys each
+    __shared__ u32x4 kept[NW / CG][G::kKept ? G::kKept : 1][kWave];
+    __shared__ float tops[NW / CG][QB][CG][16];
     __shared__ int raise_s[2];                // some row's reference has to move
     __shared__ unsigned long long wild_s[Cr::kTiles];  // see there
     __shared__ int wrong_s;
     const int tid = threadIdx.x, lane = lane_id();
     const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int half = w & 1;
+    const int team = w / CG, part = w % CG;
     int64_t unit = xcd_block();
     if (unit >= a.seqs * a.npieces * tiles) return;
     const int tile = tiles - 1 - (int)(unit % tiles);  // the longest first
@@ -223,12 +235,12 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
     const TileJob job = tile_job(a, s, tile, G::BM, piece);
     if (job.idle) return;
     const int n = lane & 15;
-    const int row0 = job.first + 16 * QB * (w >> 1);  // this pair's first row
+    const int row0 = job.first + 16 * QB * team;  // the team's first row
     TileRow r[QB];
 #pragma unroll
     for (int b = 0; b < QB; ++b) r[b] = tile_row(a, job, row0 + 16 * b + n, 0);
     if (job.sq.bad) {
-        if (piece == 0 && half == 0)
+        if (piece == 0 && part == 0)
 #pragma unroll
             for (int b = 0; b < QB; ++b) store_nan<T>(a, r[b]);
         return;
@@ -242,6 +254,9 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
     const Cr cross(job, job.first / a.s.group);
     const int lo = __builtin_amdgcn_readfirstlane(r[0].t);
     const int hi = __builtin_amdgcn_readlane(r[QB - 1].t, 15);
+    int see[QB];  // keys that this lane's query sees
+#pragma unroll
+    for (int b = 0; b < QB; ++b) see[b] = min(job.k1, job.before + r[b].t);
     const int mine = row0 < job.rows ? min(job.k1, job.before + hi) : 0;  // some row sees
     const int full = min(job.k1, job.before + lo);                       // all rows see
 
@@ -249,10 +264,13 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
 #pragma unroll
     for (int x = 0; x < QB; ++x)
 #pragma unroll
-        for (int t = 0; t < QS; ++t)
-            q[x][t] = load_query<G>(a, r[x], 64 * t + 16 * (lane >> 4), 2 * a.key_dim);
+        for (int t = 0; t < QS; ++t) {
+            const u32x4 y = load_query<G>(a, r[x], 64 * t + 16 * (lane >> 4), 2 * a.key_dim);
+            if (G::kept(x, t) < 0) q[x][t] = y;
+            else if (part == 0) kept[team][G::kept(x, t)][lane] = y;
+        }
     f32x4 o[QB][NB];
-    float ref[QB], sum[QB];  // ref: of this lane's query, in the whole pair; sum: of this lane
+    float ref[QB], sum[QB];  // ref: of this lane's query, in the whole team; sum: of this lane
 #pragma unroll
     for (int x = 0; x < QB; ++x) {
         ref[x] = -INFINITY;
@@ -288,47 +306,57 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
             mineload.look_up(a, pages, t0 + 2 * kKeys, job.k1);
         }
         const bool active = t0 < mine;
-        f32x4 sc[QB][2];
+        f32x4 sc[QB][KS];
         float top[QB];
         const auto put_probs = [&](float (&add)[QB]) {
 #pragma unroll
             for (int x = 0; x < QB; ++x) {
-                float p[8];
                 add[x] = 0.f;
                 const float base = ref[x] == -INFINITY ? 0.f : ref[x];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    p[j] = weight_of(sc[x][j >> 2][j & 3], a.s.mag, base, kShift<T>);
-                    add[x] += p[j];
+                for (int b = 0; b < KS; ++b) {
+                    float p[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        p[j] = weight_of(sc[x][b][j], a.s.mag, base, kShift<T>);
+                        add[x] += p[j];
+                    }
+                    // as the second product's operand has them: its first 16 keys, its second
+                    const int at = KS * part + b;
+                    reinterpret_cast<u32x2*>(&probs[team][at / 2][x][lane])[at & 1] =
+                        u32x2{pack2<T>(p[0], p[1]), pack2<T>(p[2], p[3])};
                 }
-                typename G::Probs pr;
-                G::pack_probs(p, pr);
-                probs[w][x][lane] = u32x4{pr.w[0], pr.w[1], pr.w[2], pr.w[3]};
             }
         };
         float add[QB];
         if (active) {
-            const int rb = Pl::row_base(32 * half);
+            const int rb = Pl::row_base(16 * KS * part);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < KS; ++b) {
 #pragma unroll
                 for (int x = 0; x < QB; ++x) sc[x][b] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < QS; ++i) {
                     const u32x4 k = Pl::row(rows, rb, 16 * b, i);
 #pragma unroll
-                    for (int x = 0; x < QB; ++x) sc[x][b] = mfma32<T>(k, q[x][i], sc[x][b]);
+                    for (int x = 0; x < QB; ++x)
+                        sc[x][b] = mfma32<T>(
+                            k, G::kept(x, i) < 0 ? q[x][i] : kept[team][G::kept(x, i)][lane], sc[x][b]);
                 }
             }
-            const int t = t0 + 32 * half;
+            const int t = t0 + 16 * KS * part;
             bool raise = false;
 #pragma unroll
             for (int x = 0; x < QB; ++x) {
-                if (t + 32 > full)  // some row does not see some key
-                    Softmax<G, T>::hide(sc[x], Seen::first(min(job.k1, job.before + r[x].t) - t));
+                if (t + 16 * KS > full) {  // some row does not see some key
+                    const Seen seen = Seen::first(see[x] - t);
+#pragma unroll
+                    for (int j = 0; j < 4 * KS; ++j)
+                        sc[x][j >> 2][j & 3] = seen.pick(j, sc[x][j >> 2][j & 3], -INFINITY);
+                }
                 top[x] = sc[x][0][0];
 #pragma unroll
-                for (int j = 1; j < 8; ++j) top[x] = fmaxf(top[x], sc[x][j >> 2][j & 3]);
+                for (int j = 1; j < 4 * KS; ++j) top[x] = fmaxf(top[x], sc[x][j >> 2][j & 3]);
                 top[x] *= a.s.mag;
                 raise |= top[x] > ref[x] + kSlack;
             }
@@ -342,14 +370,16 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
 #pragma unroll
                 for (int x = 0; x < QB; ++x) {
                     top[x] = quad_max(top[x]);
-                    if (lane < 16) tops[w][x][lane] = top[x];
+                    if (lane < 16) tops[team][x][part][lane] = top[x];
                 }
             }
             __syncthreads();
             if (active) {
 #pragma unroll
                 for (int x = 0; x < QB; ++x) {
-                    const float fix = move(ref[x], fmaxf(top[x], tops[w ^ 1][x][n]));
+#pragma unroll
+                    for (int c = 0; c < CG; ++c) top[x] = fmaxf(top[x], tops[team][x][c][n]);
+                    const float fix = move(ref[x], top[x]);
                     sum[x] *= fix;
 #pragma unroll
                     for (int b = 0; b < NB; ++b) o[x][b] *= fix;
@@ -370,11 +400,11 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
                 typename G::Probs pr[QB];
 #pragma unroll
                 for (int x = 0; x < QB; ++x) {
-                    const u32x4 p = probs[(w & ~1) + j][x][lane];
+                    const u32x4 p = probs[team][j][x][lane];
                     pr[x] = {{p[0], p[1], p[2], p[3]}};
                 }
                 const int vb = Pl::value_base(32 * j);
-                const char* vals = rows + half * (G::kDv / 128) * Pl::kPlane;
+                const char* vals = rows + part * (G::kDv / 64 / CG) * Pl::kPlane;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     const u32x4 v = Pl::value(vals, vb, b);
@@ -394,38 +424,45 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
 #pragma unroll
     for (int x = 0; x < QB; ++x) {
         sum[x] = quad_sum(sum[x]);
-        if (lane < 16) tops[w][x][lane] = sum[x];
+        if (lane < 16) tops[team][x][part][lane] = sum[x];
     }
     __syncthreads();
     if (row0 >= job.rows) return;
+    // the rows again: kept, they would take registers from the loop
+    int first = row0;
+    asm volatile("" : "+s"(first));
 #pragma unroll
     for (int x = 0; x < QB; ++x) {
+        r[x] = tile_row(a, job, first + 16 * x + n, 0);
         const int sees = job.before + r[x].t;
         if (!r[x].has || sees <= job.k0) continue;
-        const float l = wrong_s ? NAN : tops[w & ~1][x][n] + tops[w | 1][x][n];
+        float l = 0.f;
+#pragma unroll
+        for (int c = 0; c < CG; ++c) l += tops[team][x][c][n];
+        if (wrong_s) l = NAN;
         const int64_t line = r[x].token * a.s.hq + r[x].hq;
-        const bool part = sees > a.piece;
+        const bool whole = sees <= a.piece;
         const int64_t at = (int64_t)piece * a.tokens * a.s.hq + line;
-        const float f = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
-        cross.template add<T>(wild_s, min(job.k1, sees), a.s.dim - half * (G::kDv / 2), [&](int key) -> const char* {
+        const float f = l == 0.f ? 0.f : 1.f / l;
+        cross.template add<T>(wild_s, min(job.k1, sees), a.s.dim - part * (G::kDv / CG), [&](int key) -> const char* {
             const uint32_t pg = a.page_div.div(key), id = (uint32_t)pages[pg];
             if (id >= (uint64_t)a.npages) return nullptr;
             return a.k + ((uint64_t)(id * a.k_page + (key - pg * a.page_div.d) * a.k_slot) << a.k_shift) +
-                   half * G::kDv;
+                   part * (2 * G::kDv / CG);
         }, o[x]);
-        char* row = part ? reinterpret_cast<char*>(a.part + at * a.s.dim)
-                         : a.out.base + r[x].token * a.out.row + r[x].hq * a.out.head;
+        char* row = whole ? a.out.base + r[x].token * a.out.row + r[x].hq * a.out.head
+                          : reinterpret_cast<char*>(a.part + at * a.s.dim);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const int d = half * (G::kDv / 2) + 16 * b + 4 * (lane >> 4);
+            const int d = part * (G::kDv / CG) + 16 * b + 4 * (lane >> 4);
             if (d >= a.s.dim) continue;
-            if (part)
-                *reinterpret_cast<f32x4*>(row + 4 * d) = o[x][b];
-            else
+            if (whole)
                 G::store_four(o[x][b] * f, row + 2 * d);
+            else
+                *reinterpret_cast<f32x4*>(row + 4 * d) = o[x][b];
         }
-        if (half == 0 && lane < 16) {
-            if (part) {
+        if (part == 0 && lane < 16) {
+            if (!whole) {
                 a.part_ml[2 * at] = ref[x];
                 a.part_ml[2 * at + 1] = l;
             } else if (a.lse) {
@@ -854,8 +891,8 @@ template <class F>
 void with_absorbed(const LatentArgs& a, F&& f) {
     with_latent_type(a.s.type, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;
-        if (a.s.dim <= 128 && a.key_dim <= 192) f((AbsorbedGeo<T, 192, 128, 8>*)nullptr, t);
-        else if (a.s.dim <= 256 && a.key_dim <= 320) f((AbsorbedGeo<T, 320, 256, 8>*)nullptr, t);
+        if (a.s.dim <= 128 && a.key_dim <= 192) f((AbsorbedGeo<T, 192, 128, 2>*)nullptr, t);
+        else if (a.s.dim <= 256 && a.key_dim <= 320) f((AbsorbedGeo<T, 320, 256, 2>*)nullptr, t);
         else f((AbsorbedGeo<T, 576, 512, 4>*)nullptr, t);
     });
 }
