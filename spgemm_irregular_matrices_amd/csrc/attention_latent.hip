@@ -39,15 +39,15 @@ struct Planes {
         return (base ^ (dbyte & 127)) + (dbyte >> 7) * kPlane + dr * 128;
     }
     // an operand of 16 rows: 16 bytes, of step t, of row first + l % 16
-    static __device__ __forceinline__ int row_base(int first) {
-        return at(first + (lane_id() & 15), 16 * (lane_id() >> 4));
+    static __device__ __forceinline__ int row_base(int first, int lane) {
+        return at(first + (lane & 15), 16 * (lane >> 4));
     }
     static __device__ __forceinline__ u32x4 row(const char* lds, int base, int dr, int t) {
         return *reinterpret_cast<const u32x4*>(lds + more(base, dr, 64 * t));
     }
     // 16 columns, block b's, of rows first + 4 (l / 16) + 0..3 and 16 more, turned over
-    static __device__ __forceinline__ int value_base(int first) {
-        const int l = lane_id() & 15, quad = lane_id() >> 4;
+    static __device__ __forceinline__ int value_base(int first, int lane) {
+        const int l = lane & 15, quad = lane >> 4;
         return at(first + 4 * quad + (l >> 2), 8 * (l & 3));
     }
     static __device__ __forceinline__ u32x4 value(const char* lds, int base, int b) {
@@ -61,50 +61,56 @@ struct Planes {
     }
 };
 
-// This lane's rows of a tile: of blocks of 8 rows first, first + 1, ... row l / 8.
-// Their pages are looked up a tile ahead.
+// A lane's rows of a tile: of blocks of 8 rows first, first + 1, ... row l / 8, and
+// of each the piece of 16 bytes that lies l % 8 places into LDS. Their pages are
+// looked up a tile ahead; the rest is made anew from the lane for every tile, as
+// registers are dearer than that.
 template <class P, int BLOCKS>
 struct TileRows {
-    int row[BLOCKS];
-    uint32_t id[BLOCKS];
-    int byte[BLOCKS];  // of the 128 of a plane, that this lane's piece holds
+    uint32_t id[BLOCKS] = {};
     bool wrong = false;
-    __device__ __forceinline__ explicit TileRows(int first) {
+    static __device__ __forceinline__ int row(int lane, int block) { return 8 * block + (lane >> 3); }
+    static __device__ __forceinline__ uint32_t byte(int lane, int block) {
+        return 16 * ((lane & 7) ^ P::swap(row(lane, block)));
+    }
+    static __device__ __forceinline__ int anew(int lane) {
+        asm volatile("" : "+v"(lane));
+        return lane;
+    }
+    __device__ __forceinline__ void look_up(const PagedArgs& a, const int32_t* pages, int lane, int first,
+                                            int t0, int k1) {
+        lane = anew(lane);
 #pragma unroll
         for (int i = 0; i < BLOCKS; ++i) {
-            row[i] = 8 * (first + i) + (lane_id() >> 3);
-            byte[i] = 16 * ((lane_id() & 7) ^ P::swap(row[i]));
-            id[i] = 0;
+            const int key = t0 + row(lane, first + i);
+            if (key < k1) id[i] = (uint32_t)pages[a.page_div.div(key)];
         }
     }
-    __device__ __forceinline__ void look_up(const PagedArgs& a, const int32_t* pages, int t0, int k1) {
-#pragma unroll
-        for (int i = 0; i < BLOCKS; ++i)
-            if (t0 + row[i] < k1) id[i] = (uint32_t)pages[a.page_div.div(t0 + row[i])];
-    }
-    // The i-th row's latent row; null past the end.
-    __device__ __forceinline__ const char* latent(const PagedArgs& a, int t0, int k1, int i) {
-        const uint32_t key = t0 + row[i];
-        if ((int)key >= k1) return nullptr;
-        if (id[i] >= (uint64_t)a.npages) {
-            wrong = true;
+    // The latent row of `key`, which is the i-th of this lane's in the tile; past
+    // the end the row of zeros.
+    __device__ __forceinline__ const char* latent(const PagedArgs& a, int key, int k1, int i) {
+        if (id[i] >= (uint32_t)a.npages) {
+            wrong |= key < k1;
             id[i] = 0;
         }
         const uint32_t slot = key - a.page_div.div(key) * a.page_div.d;
-        return a.k + ((uint64_t)(id[i] * a.k_page + slot * a.k_slot) << a.k_shift);
+        const uint64_t at = (uint64_t)(id[i] * a.k_page + slot * a.k_slot) << a.k_shift;
+        return key < k1 ? a.k + at : reinterpret_cast<const char*>(g_zero);
     }
 };
 
-// Step t of a query row as an operand: 16 bytes from byte `at` on, 0 past `end`,
-// with the sign of the scores' factor (0: see Softmax).
-template <class G>
+// 16 bytes of a query row from byte `at` on, 0 past `end`. (Whatever is done with
+// them waits for them: first all are asked for.)
 __device__ __forceinline__ u32x4 load_query(const LatentArgs& a, const TileRow& r, int at, int end) {
     const char* row = a.q.base + r.token * a.q.row + r.hq * a.q.head;
-    u32x4 q{0, 0, 0, 0};
-    if (r.has && at < end) q = *reinterpret_cast<const u32x4*>(row + at);
-    if (a.s.c < 0.f) q ^= 0x80008000u;
-    if (a.s.c == 0.f) q = u32x4{G::times0(q[0]), G::times0(q[1]), G::times0(q[2]), G::times0(q[3])};
-    return q;
+    return *reinterpret_cast<const u32x4*>(
+        r.has && at < end ? row + at : reinterpret_cast<const char*>(g_zero));
+}
+// Queries with the sign of the scores' factor (0: see Softmax).
+template <class G>
+__device__ __forceinline__ u32x4 sign_query(const LatentArgs& a, u32x4 q) {
+    if (a.s.c < 0.f) return q ^ 0x80008000u;
+    return u32x4{G::times0(q[0]), G::times0(q[1]), G::times0(q[2]), G::times0(q[3])};
 }
 
 // Weights are taken relative to a reference that only moves when a score
@@ -189,9 +195,11 @@ struct Crossing {
 // Keys of up to DK and values of up to DV elements, a value the first part of its
 // key. A team of CG wavefronts takes 32 rows, each of them a part of a tile's keys
 // for the scores and a part of the columns for the result.
-template <class T, int DK, int DV, int CG_>
+// FULL: the keys have DK elements, so that no piece of theirs needs a check.
+template <class T, int DK, int DV, int CG_, bool FULL>
 struct AbsorbedGeo : Tile<T, 64, true> {
-    static constexpr int kKeys = 64;
+    static constexpr bool kWhole = FULL;
+    static constexpr int kKeys = kAbsorbedKeys;
     static constexpr int CG = CG_, NW = 8, QB = 2, BM = NW / CG * 16 * QB;
     static constexpr int QS = DK / 32, NB = DV / 16 / CG;
     static constexpr int KS = kKeys / 16 / CG;  // 16-key results of a wavefront's scores
@@ -223,16 +231,47 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
     __shared__ int raise_s[2];                // some row's reference has to move
     __shared__ unsigned long long wild_s[Cr::kTiles];  // see there
     __shared__ int wrong_s;
-    const int tid = threadIdx.x, lane = lane_id();
-    const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int team = w / CG, part = w % CG;
     int64_t unit = xcd_block();
-    if (unit >= a.seqs * a.npieces * tiles) return;
+    if (unit >= (a.ranges ? a.ranges : a.seqs) * (int64_t)tiles) return;
     const int tile = tiles - 1 - (int)(unit % tiles);  // the longest first
     unit /= tiles;
-    const int piece = (int)(unit % a.npieces);
-    const int64_t s = unit / a.npieces;
-    const TileJob job = tile_job(a, s, tile, G::BM, piece);
+    // a sequence, or a range of all of them
+    int64_t s = unit, before = 0, pos = 0, end = 0, begin = 0;
+    if (a.ranges) {
+        const EvenSplit e(a, kKeys);
+        begin = pos = unit * e.per;
+        end = min(pos + e.per, e.total);
+        if (pos >= end) return;
+        e.locate(pos, s, before);
+    }
+#pragma unroll 1
+    for (;; ++s) {  // segments
+    // Nothing that is made from the lane is kept from one segment to the next:
+    // it would take the loop's registers.
+    int zero_here = 0;
+    asm volatile("" : "+s"(zero_here));
+    const int tid = threadIdx.x + zero_here, lane = tid & (kWave - 1);
+    const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int team = w / CG, part = w % CG;
+    TileJob job;
+    job.sq = read_sequence(a, s);
+    job.rows = job.sq.fresh * a.s.group;
+    job.first = tile * G::BM;
+    job.idle = job.sq.none || job.first >= job.rows;
+    job.before = job.sq.length - job.sq.fresh + 1;
+    job.k0 = 0;
+    job.k1 = job.before + (min(job.first + G::BM, job.rows) - 1) / a.s.group;
+    const int64_t first_pos = pos;
+    bool split = false;
+    if (a.ranges) {
+        const int own = job.sq.none ? 0 : job.sq.bad ? 1 : (job.sq.length + kKeys - 1) / kKeys;
+        split = pos > before || before + own > end;
+        job.k0 = (int)(pos - before) * kKeys;
+        job.k1 = (int)min((int64_t)job.k1, (end - before) * kKeys);
+        before += own;
+        pos = before;
+    }
+    const auto segment = [&] {
     if (job.idle) return;
     const int n = lane & 15;
     const int row0 = job.first + 16 * QB * team;  // the team's first row
@@ -240,7 +279,7 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
 #pragma unroll
     for (int b = 0; b < QB; ++b) r[b] = tile_row(a, job, row0 + 16 * b + n, 0);
     if (job.sq.bad) {
-        if (piece == 0 && part == 0)
+        if (part == 0)
 #pragma unroll
             for (int b = 0; b < QB; ++b) store_nan<T>(a, r[b]);
         return;
@@ -254,9 +293,6 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
     const Cr cross(job, job.first / a.s.group);
     const int lo = __builtin_amdgcn_readfirstlane(r[0].t);
     const int hi = __builtin_amdgcn_readlane(r[QB - 1].t, 15);
-    int see[QB];  // keys that this lane's query sees
-#pragma unroll
-    for (int b = 0; b < QB; ++b) see[b] = min(job.k1, job.before + r[b].t);
     const int mine = row0 < job.rows ? min(job.k1, job.before + hi) : 0;  // some row sees
     const int full = min(job.k1, job.before + lo);                       // all rows see
 
@@ -265,10 +301,19 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
     for (int x = 0; x < QB; ++x)
 #pragma unroll
         for (int t = 0; t < QS; ++t) {
-            const u32x4 y = load_query<G>(a, r[x], 64 * t + 16 * (lane >> 4), 2 * a.key_dim);
-            if (G::kept(x, t) < 0) q[x][t] = y;
-            else if (part == 0) kept[team][G::kept(x, t)][lane] = y;
+            const int at = 64 * t + 16 * (lane >> 4);
+            q[x][t] = load_query(a, r[x], at, 2 * a.key_dim);
         }
+    if (a.s.c <= 0.f)
+#pragma unroll
+        for (int x = 0; x < QB; ++x)
+#pragma unroll
+            for (int t = 0; t < QS; ++t) q[x][t] = sign_query<G>(a, q[x][t]);
+#pragma unroll
+    for (int x = 0; x < QB; ++x)
+#pragma unroll
+        for (int t = 0; t < QS; ++t)
+            if (part == 0 && G::kept(x, t) >= 0) kept[team][G::kept(x, t)][lane] = q[x][t];
     f32x4 o[QB][NB];
     float ref[QB], sum[QB];  // ref: of this lane's query, in the whole team; sum: of this lane
 #pragma unroll
@@ -279,23 +324,25 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
         for (int b = 0; b < NB; ++b) o[x][b] = f32x4{0, 0, 0, 0};
     }
     const int32_t* pages = a.col + job.sq.page0;
-    TileRows<Pl, G::kBlocks> mineload(w * G::kBlocks);
+    TileRows<Pl, G::kBlocks> from;
     const auto load_tile = [&](char* dst, int t0) {
+        const int l = from.anew(lane);
 #pragma unroll
         for (int i = 0; i < G::kBlocks; ++i) {
-            const char* zero = reinterpret_cast<const char*>(g_zero) + mineload.byte[i];
-            const char* row = mineload.latent(a, t0, job.k1, i);
-            row = row ? row + mineload.byte[i] : zero;
+            const int block = w * G::kBlocks + i;
+            const uint32_t byte = from.byte(l, block);
+            const char* zero = reinterpret_cast<const char*>(g_zero);
+            const char* row = from.latent(a, t0 + from.row(l, block), job.k1, i) + byte;
 #pragma unroll
             for (int g = 0; g < G::kPlanes; ++g)
-                load_to_lds(128 * g + mineload.byte[i] < 2 * a.key_dim ? row + 128 * g : zero,
-                            dst + g * Pl::kPlane + (w * G::kBlocks + i) * 1024);
+                load_to_lds(G::kWhole || 128 * g + (int)byte < 2 * a.key_dim ? row + 128 * g : zero,
+                            dst + g * Pl::kPlane + block * 1024);
         }
     };
-    mineload.look_up(a, pages, job.k0, job.k1);
+    from.look_up(a, pages, lane, w * G::kBlocks, job.k0, job.k1);
     __syncthreads();  // the flags
     load_tile(tile0, job.k0);
-    mineload.look_up(a, pages, job.k0 + kKeys, job.k1);
+    from.look_up(a, pages, lane, w * G::kBlocks, job.k0 + kKeys, job.k1);
     wait_for_loads();
     __syncthreads();
 
@@ -303,7 +350,7 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
     const auto take = [&](char* rows, char* next, int t0, int par) {
         if (t0 + kKeys < job.k1) {
             load_tile(next, t0 + kKeys);
-            mineload.look_up(a, pages, t0 + 2 * kKeys, job.k1);
+            from.look_up(a, pages, lane, w * G::kBlocks, t0 + 2 * kKeys, job.k1);
         }
         const bool active = t0 < mine;
         f32x4 sc[QB][KS];
@@ -330,7 +377,7 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
         };
         float add[QB];
         if (active) {
-            const int rb = Pl::row_base(16 * KS * part);
+            const int rb = Pl::row_base(16 * KS * part, lane);
 #pragma unroll
             for (int b = 0; b < KS; ++b) {
 #pragma unroll
@@ -349,7 +396,9 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
 #pragma unroll
             for (int x = 0; x < QB; ++x) {
                 if (t + 16 * KS > full) {  // some row does not see some key
-                    const Seen seen = Seen::first(see[x] - t);
+                    const int row = min(row0 + 16 * x + n, job.rows - 1);
+                    const int sees = job.before + (int)a.group_div.div(row);
+                    const Seen seen = Seen::first(min(job.k1, sees) - t);
 #pragma unroll
                     for (int j = 0; j < 4 * KS; ++j)
                         sc[x][j >> 2][j & 3] = seen.pick(j, sc[x][j >> 2][j & 3], -INFINITY);
@@ -403,7 +452,7 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
                     const u32x4 p = probs[team][j][x][lane];
                     pr[x] = {{p[0], p[1], p[2], p[3]}};
                 }
-                const int vb = Pl::value_base(32 * j);
+                const int vb = Pl::value_base(32 * j, lane);
                 const char* vals = rows + part * (G::kDv / 64 / CG) * Pl::kPlane;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
@@ -420,7 +469,7 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
         take(tile0, tile1, t0, 0);
         if (t0 + kKeys < job.k1) take(tile1, tile0, t0 + kKeys, 1);
     }
-    if (mineload.wrong) wrong_s = 1;
+    if (from.wrong) wrong_s = 1;
 #pragma unroll
     for (int x = 0; x < QB; ++x) {
         sum[x] = quad_sum(sum[x]);
@@ -441,8 +490,9 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
         for (int c = 0; c < CG; ++c) l += tops[team][x][c][n];
         if (wrong_s) l = NAN;
         const int64_t line = r[x].token * a.s.hq + r[x].hq;
-        const bool whole = sees <= a.piece;
-        const int64_t at = (int64_t)piece * a.tokens * a.s.hq + line;
+        // where a part of a split sequence goes
+        const int64_t at = ((2 * unit + (first_pos > begin)) * tiles + tile) * G::BM +
+                           first - job.first + 16 * x + n;
         const float f = l == 0.f ? 0.f : 1.f / l;
         cross.template add<T>(wild_s, min(job.k1, sees), a.s.dim - part * (G::kDv / CG), [&](int key) -> const char* {
             const uint32_t pg = a.page_div.div(key), id = (uint32_t)pages[pg];
@@ -450,19 +500,19 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
             return a.k + ((uint64_t)(id * a.k_page + (key - pg * a.page_div.d) * a.k_slot) << a.k_shift) +
                    part * (2 * G::kDv / CG);
         }, o[x]);
-        char* row = whole ? a.out.base + r[x].token * a.out.row + r[x].hq * a.out.head
+        char* row = !split ? a.out.base + r[x].token * a.out.row + r[x].hq * a.out.head
                           : reinterpret_cast<char*>(a.part + at * a.s.dim);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int d = part * (G::kDv / CG) + 16 * b + 4 * (lane >> 4);
             if (d >= a.s.dim) continue;
-            if (whole)
+            if (!split)
                 G::store_four(o[x][b] * f, row + 2 * d);
             else
                 *reinterpret_cast<f32x4*>(row + 4 * d) = o[x][b];
         }
         if (part == 0 && lane < 16) {
-            if (!whole) {
+            if (split) {
                 a.part_ml[2 * at] = ref[x];
                 a.part_ml[2 * at + 1] = l;
             } else if (a.lse) {
@@ -470,12 +520,18 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
             }
         }
     }
+    };
+    segment();
+    if (pos >= end) return;
+    __syncthreads();  // flags and sums are used again
+    }
 }
 
 // One wavefront per token and query head joins its pieces, in their order.
 constexpr int kWaves = 4;
 template <class T>
-__global__ __launch_bounds__(kWaves* kWave) void k_latent_join(PagedArgs a) {
+__global__ __launch_bounds__(kWaves* kWave) void k_latent_join(PagedArgs a, int32_t tiles, int32_t tile_rows,
+                                                               int32_t keys) {
     const int64_t unit = grid_block() * kWaves + threadIdx.x / kWave;
     if (unit >= a.tokens * a.s.hq) return;
     const int64_t token = unit / a.s.hq;
@@ -485,20 +541,39 @@ __global__ __launch_bounds__(kWaves* kWave) void k_latent_join(PagedArgs a) {
     const Sequence sq = read_sequence(a, s);
     if (sq.none || sq.bad || token < sq.q0 || token - sq.q0 >= sq.fresh) return;
     const int sees = sq.length - sq.fresh + 1 + (int)(token - sq.q0);
-    if (sees <= a.piece) return;
-    const int count = (sees + a.piece - 1) / a.piece;
-    const int64_t step = a.tokens * a.s.hq;
-    const float* ml = a.part_ml + 2 * unit;
-    float m, l;
-    join_sums(ml, step, count, m, l);
+    int count;
+    int64_t first, step, late = 0;  // in rows of parts
+    if (a.ranges) {
+        const EvenParts parts(EvenSplit(a, keys), s, keys, sees);
+        const int row = (int)(token - sq.q0) * a.s.hq + hq, tile = row / tile_rows;
+        count = parts.count;
+        step = (int64_t)2 * tiles * tile_rows;
+        first = ((2 * parts.range) * tiles + tile) * tile_rows + row - tile * tile_rows;
+        late = parts.late ? (int64_t)tiles * tile_rows : 0;
+    } else {
+        count = sees <= a.piece ? 0 : (sees + a.piece - 1) / a.piece;
+        step = a.tokens * a.s.hq;
+        first = unit;
+    }
+    if (count == 0) return;
+    // the rows of parts that lane i, i + 64, ... looks at
+    const auto at = [&](int i) { return first + i * step + (i == 0 ? late : 0); };
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane_id(); i < count; i += kWave) m = fmaxf(m, a.part_ml[2 * at(i)]);
+#pragma unroll
+    for (int d = kWave / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, kWave));
+    m = m == -INFINITY ? 0.f : m;
+    for (int i = lane_id(); i < count; i += kWave)
+        l += a.part_ml[2 * at(i) + 1] * fast_exp2(a.part_ml[2 * at(i)] - m);
+    l = wave_reduce_sum(l);
     const float f = l == 0.f ? 0.f : 1.f / l;
     char* row = a.out.base + token * a.out.row + hq * a.out.head;
     for (int d = 4 * lane_id(); d < a.s.dim; d += 4 * kWave) {
         f32x4 x{0, 0, 0, 0};
 #pragma unroll 4
         for (int i = 0; i < count; ++i)
-            x += *reinterpret_cast<const f32x4*>(a.part + (i * step + unit) * a.s.dim + d) *
-                 fast_exp2(ml[2 * i * step] - m);
+            x += *reinterpret_cast<const f32x4*>(a.part + at(i) * a.s.dim + d) *
+                 fast_exp2(a.part_ml[2 * at(i)] - m);
         x *= f;
         *reinterpret_cast<u32x2*>(row + 2 * d) = u32x2{pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3])};
     }
@@ -576,26 +651,31 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
 #pragma unroll
         for (int t = 0; t < QS; ++t) {
             const int at = 64 * t + 16 * (lane >> 4), rope = at - 128 * G::MP;
-            q[x][t] = t < 2 * G::MP ? load_query<G>(a, r[x], at, made)
-                                    : load_query<G>(a, r[x], made + rope, 2 * a.key_dim);
+            q[x][t] = t < 2 * G::MP ? load_query(a, r[x], at, made)
+                                    : load_query(a, r[x], made + rope, 2 * a.key_dim);
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) o[x][b] = f32x4{0, 0, 0, 0};
     }
+    if (a.s.c <= 0.f)
+#pragma unroll
+        for (int x = 0; x < QB; ++x)
+#pragma unroll
+            for (int t = 0; t < QS; ++t) q[x][t] = sign_query<G>(a, q[x][t]);
     const int32_t* pages = a.col + job.sq.page0;
     // the sequence's first row of made keys and values
     const int64_t made0 = h * a.made_rows +
                           (a.made_step ? s * a.made_step : job.sq.page0 * (int64_t)a.page_div.d);
     const char* made_v = a.made_v + made0 * 2 * values;
-    TileRows<Pl, 1> from(w);
-    const int byte = from.byte[0];
+    TileRows<Pl, 1> from;
+    const int byte = from.byte(lane, w), trow = from.row(lane, w);
     // of this lane's row of the next tile
-    const char* ksrc = a.made_k + (made0 + job.k0 + from.row[0]) * 2 * made + byte;
-    const char* vsrc = made_v + (int64_t)(job.k0 + from.row[0]) * 2 * values + byte;
+    const char* ksrc = a.made_k + (made0 + job.k0 + trow) * 2 * made + byte;
+    const char* vsrc = made_v + (int64_t)(job.k0 + trow) * 2 * values + byte;
     const char* zero = reinterpret_cast<const char*>(g_zero);
     const auto load_tile = [&](char* dst, int t0) {
-        const char* latent = from.latent(a, t0, job.k1, 0);
-        const bool in = latent != nullptr;
+        const char* latent = from.latent(a, t0 + trow, job.k1, 0);
+        const bool in = t0 + trow < job.k1;
         char* to = dst + w * 1024;
 #pragma unroll
         for (int g = 0; g < G::MP; ++g) {
@@ -615,20 +695,20 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
         ksrc += (int64_t)kKeys * 2 * made;
         vsrc += (int64_t)kKeys * 2 * values;
     };
-    from.look_up(a, pages, job.k0, job.k1);
+    from.look_up(a, pages, lane, w, job.k0, job.k1);
     __syncthreads();  // the flags
     load_tile(tile0, job.k0);
-    from.look_up(a, pages, job.k0 + kKeys, job.k1);
+    from.look_up(a, pages, lane, w, job.k0 + kKeys, job.k1);
     wait_for_loads();
     __syncthreads();
 
-    const int rb = Pl::row_base(0), vb = Pl::value_base(0);
+    const int rb = Pl::row_base(0, lane), vb = Pl::value_base(0, lane);
     // One tile of keys, staged in `rows`; the next one is loaded into `next`.
     const auto take = [&](char* rows, char* next, int t0) {
         char* vals = rows + G::kValues * Pl::kPlane;
         if (t0 + kKeys < job.k1) {
             load_tile(next, t0 + kKeys);
-            from.look_up(a, pages, t0 + 2 * kKeys, job.k1);
+            from.look_up(a, pages, lane, w, t0 + 2 * kKeys, job.k1);
         }
         if (min(t0 + kKeys, job.k1) > job.before + job.first) {
             Cr::template clear<G, NW * kWave>(vals, G::VP, &wild_s[(t0 - cross.from) / kKeys]);
@@ -828,7 +908,7 @@ __global__ __launch_bounds__(256) void k_expand(ExpandArgs e, ExpandShape z) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
     const auto product = [&](const char* wrows, const char* crows) {
-        const int wb = Planes<kM>::row_base(64 * (w >> 1)), cb = Planes<kM>::row_base(64 * (w & 1));
+        const int wb = Planes<kM>::row_base(64 * (w >> 1), lane), cb = Planes<kM>::row_base(64 * (w & 1), lane);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             u32x4 x[4], y[4];
@@ -886,14 +966,21 @@ void with_latent_type(int type, F&& f) {
     if (type == SPGEMM_TYPE_BF16) f((__bf16*)nullptr);
     else f((_Float16*)nullptr);
 }
+template <int N>
+using Int = std::integral_constant<int, N>;
 // f(geometry, type) of a call: the smallest widths that hold it.
 template <class F>
 void with_absorbed(const LatentArgs& a, F&& f) {
     with_latent_type(a.s.type, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;
-        if (a.s.dim <= 128 && a.key_dim <= 192) f((AbsorbedGeo<T, 192, 128, 2>*)nullptr, t);
-        else if (a.s.dim <= 256 && a.key_dim <= 320) f((AbsorbedGeo<T, 320, 256, 2>*)nullptr, t);
-        else f((AbsorbedGeo<T, 576, 512, 4>*)nullptr, t);
+        const auto width = [&](auto dk, auto dv, auto cg) {
+            constexpr int K = decltype(dk)::value, V = decltype(dv)::value, C = decltype(cg)::value;
+            if (a.key_dim == K) f((AbsorbedGeo<T, K, V, C, true>*)nullptr, t);
+            else f((AbsorbedGeo<T, K, V, C, false>*)nullptr, t);
+        };
+        if (a.s.dim <= 128 && a.key_dim <= 192) width(Int<192>{}, Int<128>{}, Int<2>{});
+        else if (a.s.dim <= 256 && a.key_dim <= 320) width(Int<320>{}, Int<256>{}, Int<2>{});
+        else width(Int<576>{}, Int<512>{}, Int<4>{});
     });
 }
 template <class F>
@@ -916,26 +1003,29 @@ int latent_tile_rows(const LatentArgs& a, bool absorbed) {
 }
 
 void latent_attention(const LatentArgs& a, bool absorbed, hipStream_t st) {
-    const int64_t tiles = ceil_div((int64_t)a.max_new * a.s.group, latent_tile_rows(a, absorbed));
-    const dim3 grid = grid_2d(xcd_grid(a.seqs * a.s.hkv * a.npieces * tiles));
+    const int rows = latent_tile_rows(a, absorbed);
+    const int32_t tiles = (int32_t)ceil_div((int64_t)a.max_new * a.s.group, rows);
     if (absorbed) {
+        const dim3 grid = grid_2d(xcd_grid((a.ranges ? a.ranges : a.seqs) * (int64_t)tiles));
         with_absorbed(a, [&](auto* geo, auto* t) {
             using G = std::remove_pointer_t<decltype(geo)>;
             auto run = k_absorbed<G, std::remove_pointer_t<decltype(t)>>;
-            hipLaunchKernelGGL(run, grid, dim3(G::NW * kWave), 0, st, a, (int32_t)tiles);
+            hipLaunchKernelGGL(run, grid, dim3(G::NW * kWave), 0, st, a, tiles);
         });
     } else {
+        const dim3 grid = grid_2d(xcd_grid(a.seqs * a.s.hkv * a.npieces * tiles));
         with_expanded(a, [&](auto* geo, auto* t) {
             using G = std::remove_pointer_t<decltype(geo)>;
             auto run = k_expanded<G, std::remove_pointer_t<decltype(t)>>;
-            hipLaunchKernelGGL(run, grid, dim3(G::NW * kWave), 0, st, a, (int32_t)tiles);
+            hipLaunchKernelGGL(run, grid, dim3(G::NW * kWave), 0, st, a, tiles);
         });
     }
     SG_LAUNCH_CHECK();
-    if (a.npieces == 1) return;
+    if (a.npieces == 1 && a.ranges == 0) return;
     with_latent_type(a.s.type, [&](auto* t) {
         hipLaunchKernelGGL(k_latent_join<std::remove_pointer_t<decltype(t)>>,
-                           grid_2d(ceil_div(a.tokens * a.s.hq, kWaves)), dim3(kWaves * kWave), 0, st, a);
+                           grid_2d(ceil_div(a.tokens * a.s.hq, kWaves)), dim3(kWaves * kWave), 0, st, a,
+                           tiles, rows, kAbsorbedKeys);
     });
     SG_LAUNCH_CHECK();
 }

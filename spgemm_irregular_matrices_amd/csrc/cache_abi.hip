@@ -55,9 +55,15 @@ void cut_pieces(PagedArgs* a, int64_t tile, int64_t target, int64_t least, int64
     a->npieces = (int32_t)std::max<int64_t>(ceil_div(a->max_length, a->piece), 1);
 }
 
-int64_t carve_parts(void* ws, PagedArgs* a) {
+// tile_rows: rows of a tile, heads: key heads whose ranges are apart.
+int64_t carve_parts(void* ws, PagedArgs* a, int64_t tile_rows = 1, int64_t heads = 1) {
+    const int64_t tiles = ceil_div((int64_t)a->max_new * a->s.group, tile_rows);
     Carver c{static_cast<char*>(ws)};
-    if (a->npieces > 1) {
+    if (a->ranges > 0) {
+        const __int128 rows = (__int128)2 * a->ranges * tiles * tile_rows * heads;
+        a->part = c.take(rows * a->s.dim);
+        a->part_ml = c.take(rows * 2);
+    } else if (a->npieces > 1) {
         const __int128 rows = (__int128)a->npieces * a->tokens * a->s.hq;
         a->part = c.take(rows * a->s.dim);
         a->part_ml = c.take(rows * 2);
@@ -181,7 +187,20 @@ void latent_shape(const spgemm_latent_desc* d, const spgemm_paged_batch* b, bool
     a->key_dim = (absorbed ? d->latent_dim : d->key_dim) + d->rope_dim;
     a->made_dim = absorbed ? 0 : d->key_dim;
     a->rope_at = 2 * d->latent_dim;
-    cut_pieces(a, latent_tile_rows(*a, absorbed), 256, 256, 64);
+    const int64_t tile = latent_tile_rows(*a, absorbed);
+    if (absorbed) {
+        // One work group per compute unit is there at once: where sequences and
+        // tiles of rows are fewer than two each, all keys are cut evenly.
+        const int64_t tiles = std::max<int64_t>(ceil_div((int64_t)a->max_new * a->s.group, tile), 1);
+        const int64_t most = a->seqs * ceil_div(a->max_length, kAbsorbedKeys);
+        a->piece = std::max(a->max_length, 1);
+        if (a->seqs <= 256 && a->seqs * tiles < 512 && most > a->seqs) {
+            a->least = 2;
+            a->ranges = (int32_t)std::max<int64_t>(std::min(ceil_div(most, a->least), 256 / tiles), 1);
+        }
+    } else {
+        cut_pieces(a, tile, 256, 256, 64);
+    }
 }
 
 // Rows of made keys: one per place of the table, or per sequence and place,
@@ -250,7 +269,8 @@ int latent_call(const spgemm_latent_desc* desc, const spgemm_rows* q, const spge
         a.lse = lse;
         e.latent_dim = desc->latent_dim;
         if (!absorbed) made_rows(batch, cache->page_size, &a);
-        const int64_t need = absorbed ? carve_parts(workspace, &a) : carve_made(workspace, &a);
+        const int64_t need = absorbed ? carve_parts(workspace, &a, latent_tile_rows(a, true))
+                                      : carve_made(workspace, &a);
         if (!workspace_valid(workspace, workspace_bytes, need)) return SPGEMM_ERR_INVALID_ARG;
         if (!absorbed) latent_expand(e, st);
         latent_attention(a, absorbed, st);
@@ -325,7 +345,7 @@ SPGEMM_API int spgemm_latent_attention_workspace(const spgemm_latent_desc* desc,
     return guarded([&]() -> int {
         LatentArgs a;
         latent_shape(desc, batch, true, &a);
-        *bytes = carve_parts(nullptr, &a);
+        *bytes = carve_parts(nullptr, &a, latent_tile_rows(a, true));
         return SPGEMM_OK;
     });
 }
