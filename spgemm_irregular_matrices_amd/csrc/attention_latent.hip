@@ -147,12 +147,16 @@ struct Crossing {
     int from;  // the first such tile's first key
     __device__ __forceinline__ Crossing(const TileJob& j, int first_token)
         : from(j.k0 + max(j.before + first_token - j.k0, 0) / kKeys * kKeys) {}
-    // Clears such elements of the planes at `vals`; keeps their keys in `wild`.
+    // Clears such elements of this thread's row of the planes at `vals` (8 threads
+    // to a row); whether there were any.
     template <class G, int THREADS>
-    static __device__ __forceinline__ void clear(char* vals, int planes, unsigned long long* wild) {
+    static __device__ __forceinline__ bool clear(char* vals, int planes) {
+        static_assert(THREADS == 8 * KEYS, "a thread stays with its row");
+        bool any = false;
 #pragma unroll 1
-        for (int at = threadIdx.x; at < planes * kKeys * 8; at += THREADS) {
-            u32x4 x = *reinterpret_cast<const u32x4*>(vals + 16 * at);
+        for (int g = 0; g < planes; ++g) {
+            char* at = vals + g * KEYS * 128 + 16 * threadIdx.x;
+            u32x4 x = *reinterpret_cast<const u32x4*>(at);
             const uint32_t words[4] = {x[0], x[1], x[2], x[3]};
             if (!G::words_wild(words)) continue;
 #pragma unroll
@@ -160,9 +164,20 @@ struct Crossing {
                 const uint32_t low[1] = {x[i] & 0xffffu}, high[1] = {x[i] & 0xffff0000u};
                 x[i] &= (G::words_wild(low) ? 0u : 0xffffu) | (G::words_wild(high) ? 0u : 0xffff0000u);
             }
-            *reinterpret_cast<u32x4*>(vals + 16 * at) = x;
-            atomicOr(wild, 1ull << (at / 8 % kKeys));
+            *reinterpret_cast<u32x4*>(at) = x;
+            any = true;
         }
+        return any;
+    }
+    // All threads' rows, from bit i of `mine` for the i-th such tile, in LDS that
+    // is not used otherwise any more.
+    static __device__ __forceinline__ void gather(uint32_t mine, unsigned long long* wild) {
+        if (threadIdx.x < kTiles) wild[threadIdx.x] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+            if (mine >> i & 1) atomicOr(&wild[i], 1ull << (threadIdx.x / 8));
+        __syncthreads();
     }
     // o plus the elements that are not finite of the keys below `sees` that were
     // cleared; row(key): where the key's values of o begin.
@@ -193,337 +208,369 @@ struct Crossing {
 
 // ---------------------------------------------------------------- absorbed
 // Keys of up to DK and values of up to DV elements, a value the first part of its
-// key. A team of CG wavefronts takes 32 rows, each of them a part of a tile's keys
-// for the scores and a part of the columns for the result.
-// FULL: the keys have DK elements, so that no piece of theirs needs a check.
-template <class T, int DK, int DV, int CG_, bool FULL>
+// key. A team of KH * DH wavefronts takes 32 rows. For the scores they cut a tile's
+// keys in KH and the sum over its elements in DH (2: whole queries of 576 elements
+// leave no registers to read keys ahead; partial sums go through LDS), for the
+// result its columns in KH * DH.
+template <class T, int DK, int DV, int KH_, int DH_>
 struct AbsorbedGeo : Tile<T, 64, true> {
-    static constexpr bool kWhole = FULL;
-    static constexpr int kKeys = kAbsorbedKeys;
-    static constexpr int CG = CG_, NW = 8, QB = 2, BM = NW / CG * 16 * QB;
-    static constexpr int QS = DK / 32, NB = DV / 16 / CG;
-    static constexpr int KS = kKeys / 16 / CG;  // 16-key results of a wavefront's scores
-    // Query operands that stay in LDS, from the last step on: at the largest size
-    // registers hold all but three. (More are spilled there, and a load from
-    // scratch waits for the next tile's.)
-    static constexpr int kKept = DK == 576 ? 3 : 0;
-    static constexpr int kept(int x, int t) {  // its place there, or below 0
-        const int from_end = QB * (QS - 1 - t) + QB - 1 - x;
-        return from_end < kKept ? from_end : -1;
-    }
-    static constexpr int kPlanes = DK / 64, kDv = DV;
-    static constexpr int kBlocks = kKeys / 8 / NW;  // blocks of 8 rows that a wavefront loads
+    static constexpr int kKeys = kAbsorbedKeys, kDv = DV, kPlanes = DK / 64;
+    static constexpr int KH = KH_, DH = DH_, CG = KH * DH, NW = 8, QB = 2, BM = NW / CG * 16 * QB;
+    static constexpr int QS = DK / 32 / DH, NB = DV / 16 / CG;
+    static constexpr int KS = kKeys / 16 / KH;  // 16-key blocks of a wavefront's products,
+    static constexpr int FB = KS / DH;          // and of those those whose weights it makes
+    // what a wavefront is sent and leaves in LDS: partial sums, then weights,
+    // largest scores and a flag
+    static constexpr int kTops = QB * FB * kWave * 8, kFlag = kTops + QB * 64;
+    static constexpr int kSlot = DH == 2 ? QB * FB * kWave * 16 : kFlag + 64;
     static_assert(BM <= kPagedTileMost, "the limit of rows counts on it");
-    static_assert(DK % 64 == 0 && DV % (64 * CG) == 0 && KS >= 1, "tile shape");
+    static_assert(DK % (32 * DH) == 0 && DV % (64 * CG) == 0 && KS >= DH && DH <= 2, "tile shape");
+    static_assert(kFlag + 4 <= kSlot && kKeys == 8 * NW, "slots and loads");
 };
 
 template <class G, class T>
 __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t tiles) {
-    constexpr int QB = G::QB, QS = G::QS, NB = G::NB, NW = G::NW, CG = G::CG, KS = G::KS;
+    constexpr int QB = G::QB, QS = G::QS, NB = G::NB, NW = G::NW, CG = G::CG, KS = G::KS, FB = G::FB;
     constexpr int kKeys = G::kKeys;
     using Pl = Planes<kKeys>;
     using Cr = Crossing<kKeys>;
     __shared__ __align__(16) char tile0[G::kPlanes * Pl::kPlane];
     __shared__ __align__(16) char tile1[G::kPlanes * Pl::kPlane];
-    __shared__ u32x4 probs[NW / CG][kKeys / 32][QB][kWave];  // of a team's rows, 32 keys each
-    __shared__ u32x4 kept[NW / CG][G::kKept ? G::kKept : 1][kWave];
-    __shared__ float tops[NW / CG][QB][CG][16];
-    __shared__ int raise_s[2];                // some row's reference has to move
-    __shared__ unsigned long long wild_s[Cr::kTiles];  // see there
-    __shared__ int wrong_s;
+    __shared__ __align__(16) char slots[NW * G::kSlot];
     int64_t unit = xcd_block();
     if (unit >= (a.ranges ? a.ranges : a.seqs) * (int64_t)tiles) return;
     const int tile = tiles - 1 - (int)(unit % tiles);  // the longest first
     unit /= tiles;
     // a sequence, or a range of all of them
-    int64_t s = unit, before = 0, pos = 0, end = 0, begin = 0;
+    int s = (int)unit, before = 0, pos = 0, end = 0, begin = 0;
     if (a.ranges) {
         const EvenSplit e(a, kKeys);
-        begin = pos = unit * e.per;
+        begin = pos = (int)min(unit * e.per, (int64_t)e.total);
         end = min(pos + e.per, e.total);
         if (pos >= end) return;
         e.locate(pos, s, before);
     }
 #pragma unroll 1
     for (;; ++s) {  // segments
-    // Nothing that is made from the lane is kept from one segment to the next:
-    // it would take the loop's registers.
-    int zero_here = 0;
-    asm volatile("" : "+s"(zero_here));
-    const int tid = threadIdx.x + zero_here, lane = tid & (kWave - 1);
-    const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int team = w / CG, part = w % CG;
-    TileJob job;
-    job.sq = read_sequence(a, s);
-    job.rows = job.sq.fresh * a.s.group;
-    job.first = tile * G::BM;
-    job.idle = job.sq.none || job.first >= job.rows;
-    job.before = job.sq.length - job.sq.fresh + 1;
-    job.k0 = 0;
-    job.k1 = job.before + (min(job.first + G::BM, job.rows) - 1) / a.s.group;
-    const int64_t first_pos = pos;
-    bool split = false;
-    if (a.ranges) {
-        const int own = job.sq.none ? 0 : job.sq.bad ? 1 : (job.sq.length + kKeys - 1) / kKeys;
-        split = pos > before || before + own > end;
-        job.k0 = (int)(pos - before) * kKeys;
-        job.k1 = (int)min((int64_t)job.k1, (end - before) * kKeys);
-        before += own;
-        pos = before;
-    }
-    const auto segment = [&] {
-    if (job.idle) return;
-    const int n = lane & 15;
-    const int row0 = job.first + 16 * QB * team;  // the team's first row
-    TileRow r[QB];
+        // Nothing that is made from the lane is kept from one segment to the next:
+        // it would take the loop's registers.
+        int zero_here = 0;
+        asm volatile("" : "+s"(zero_here));
+        const int tid = threadIdx.x + zero_here, lane = tid & (kWave - 1);
+        const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
+        const int team = w / CG, part = w % CG, kh = part / G::DH, dh = part % G::DH;
+        TileJob job;
+        job.sq = read_sequence(a, s);
+        job.rows = job.sq.fresh * a.s.group;
+        job.first = tile * G::BM;
+        job.idle = job.sq.none || job.first >= job.rows;
+        job.before = job.sq.length - job.sq.fresh + 1;
+        job.k0 = 0;
+        job.k1 = job.before + (min(job.first + G::BM, job.rows) - 1) / a.s.group;
+        const bool late = pos > begin;
+        bool split = false;
+        if (a.ranges) {
+            const int own =
+                job.sq.none ? 0 : job.sq.bad ? 1 : (job.sq.length + kKeys - 1) / kKeys;
+            split = pos > before || before + own > end;
+            job.k0 = (pos - before) * kKeys;
+            job.k1 = min(job.k1, (int)min((int64_t)(end - before) * kKeys, (int64_t)INT32_MAX));
+            before += own;
+            pos = before;
+        }
+        const auto segment = [&] {
+            if (job.idle) return;
+            const int n = lane & 15;
+            const int row0 = job.first + 16 * QB * team;  // the team's first row
+            TileRow r[QB];
 #pragma unroll
-    for (int b = 0; b < QB; ++b) r[b] = tile_row(a, job, row0 + 16 * b + n, 0);
-    if (job.sq.bad) {
-        if (part == 0)
+            for (int b = 0; b < QB; ++b) r[b] = tile_row(a, job, row0 + 16 * b + n, 0);
+            if (job.sq.bad) {
+                if (part == 0)
 #pragma unroll
-            for (int b = 0; b < QB; ++b) store_nan<T>(a, r[b]);
-        return;
-    }
-    if (job.k0 >= job.k1) return;
-    if (tid == 0) {
-        wrong_s = raise_s[0] = raise_s[1] = 0;
-#pragma unroll
-        for (int i = 0; i < Cr::kTiles; ++i) wild_s[i] = 0;
-    }
-    const Cr cross(job, job.first / a.s.group);
-    const int lo = __builtin_amdgcn_readfirstlane(r[0].t);
-    const int hi = __builtin_amdgcn_readlane(r[QB - 1].t, 15);
-    const int mine = row0 < job.rows ? min(job.k1, job.before + hi) : 0;  // some row sees
-    const int full = min(job.k1, job.before + lo);                       // all rows see
+                    for (int b = 0; b < QB; ++b) store_nan<T>(a, r[b]);
+                return;
+            }
+            if (job.k0 >= job.k1) return;
+            const Cr cross(job, job.first / a.s.group);
+            const int lo = __builtin_amdgcn_readfirstlane(r[0].t);
+            const int hi = __builtin_amdgcn_readlane(r[QB - 1].t, 15);
+            const int mine = row0 < job.rows ? min(job.k1, job.before + hi) : 0;  // some row sees
+            const int full = min(job.k1, job.before + lo);                       // all rows see
 
-    u32x4 q[QB][QS];
+            const int32_t* pages = a.col + job.sq.page0;
+            TileRows<Pl, 1> from;
+            from.look_up(a, pages, lane, w, job.k0, job.k1);
+            u32x4 q[QB][QS];
 #pragma unroll
-    for (int x = 0; x < QB; ++x)
+            for (int x = 0; x < QB; ++x)
 #pragma unroll
-        for (int t = 0; t < QS; ++t) {
-            const int at = 64 * t + 16 * (lane >> 4);
-            q[x][t] = load_query(a, r[x], at, 2 * a.key_dim);
-        }
-    if (a.s.c <= 0.f)
+                for (int t = 0; t < QS; ++t)
+                    q[x][t] = load_query(a, r[x], 64 * (QS * dh + t) + 16 * (lane >> 4), 2 * a.key_dim);
+            const auto load_tile = [&](char* dst, int t0) {
+                const int l = from.anew(lane);
+                const uint32_t byte = from.byte(l, w);
+                const char* row = from.latent(a, t0 + from.row(l, w), job.k1, 0) + byte;
 #pragma unroll
-        for (int x = 0; x < QB; ++x)
+                for (int g = 0; g < G::kPlanes; ++g)
+                    load_to_lds(128 * g + (int)byte < 2 * a.key_dim
+                                    ? row + 128 * g
+                                    : reinterpret_cast<const char*>(g_zero),
+                                dst + g * Pl::kPlane + w * 1024);
+            };
+            load_tile(tile0, job.k0);
+            from.look_up(a, pages, lane, w, job.k0 + kKeys, job.k1);
+            if (a.s.c <= 0.f)
 #pragma unroll
-            for (int t = 0; t < QS; ++t) q[x][t] = sign_query<G>(a, q[x][t]);
+                for (int x = 0; x < QB; ++x)
 #pragma unroll
-    for (int x = 0; x < QB; ++x)
-#pragma unroll
-        for (int t = 0; t < QS; ++t)
-            if (part == 0 && G::kept(x, t) >= 0) kept[team][G::kept(x, t)][lane] = q[x][t];
-    f32x4 o[QB][NB];
-    float ref[QB], sum[QB];  // ref: of this lane's query, in the whole team; sum: of this lane
-#pragma unroll
-    for (int x = 0; x < QB; ++x) {
-        ref[x] = -INFINITY;
-        sum[x] = 0.f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) o[x][b] = f32x4{0, 0, 0, 0};
-    }
-    const int32_t* pages = a.col + job.sq.page0;
-    TileRows<Pl, G::kBlocks> from;
-    const auto load_tile = [&](char* dst, int t0) {
-        const int l = from.anew(lane);
-#pragma unroll
-        for (int i = 0; i < G::kBlocks; ++i) {
-            const int block = w * G::kBlocks + i;
-            const uint32_t byte = from.byte(l, block);
-            const char* zero = reinterpret_cast<const char*>(g_zero);
-            const char* row = from.latent(a, t0 + from.row(l, block), job.k1, i) + byte;
-#pragma unroll
-            for (int g = 0; g < G::kPlanes; ++g)
-                load_to_lds(G::kWhole || 128 * g + (int)byte < 2 * a.key_dim ? row + 128 * g : zero,
-                            dst + g * Pl::kPlane + block * 1024);
-        }
-    };
-    from.look_up(a, pages, lane, w * G::kBlocks, job.k0, job.k1);
-    __syncthreads();  // the flags
-    load_tile(tile0, job.k0);
-    from.look_up(a, pages, lane, w * G::kBlocks, job.k0 + kKeys, job.k1);
-    wait_for_loads();
-    __syncthreads();
-
-    // One tile of keys, staged in `rows`; the next one is loaded into `next`.
-    const auto take = [&](char* rows, char* next, int t0, int par) {
-        if (t0 + kKeys < job.k1) {
-            load_tile(next, t0 + kKeys);
-            from.look_up(a, pages, lane, w * G::kBlocks, t0 + 2 * kKeys, job.k1);
-        }
-        const bool active = t0 < mine;
-        f32x4 sc[QB][KS];
-        float top[QB];
-        const auto put_probs = [&](float (&add)[QB]) {
+                    for (int t = 0; t < QS; ++t) q[x][t] = sign_query<G>(a, q[x][t]);
+            f32x4 o[QB][NB];
+            float ref[QB], sum[QB];  // ref: of this lane's query, in the whole team; sum: its own
 #pragma unroll
             for (int x = 0; x < QB; ++x) {
-                add[x] = 0.f;
-                const float base = ref[x] == -INFINITY ? 0.f : ref[x];
+                ref[x] = -INFINITY;
+                sum[x] = 0.f;
 #pragma unroll
-                for (int b = 0; b < KS; ++b) {
-                    float p[4];
+                for (int b = 0; b < NB; ++b) o[x][b] = f32x4{0, 0, 0, 0};
+            }
+            uint32_t wild = 0;  // see Crossing
+            char* const mail = slots + w * G::kSlot;
+            wait_for_loads();
+            __syncthreads();
+
+            // One tile of keys, staged in `rows`; the next one is loaded into `next`.
+            const auto take = [&](char* rows, char* next, int t0) {
+                if (t0 + kKeys < job.k1) {
+                    load_tile(next, t0 + kKeys);
+                    from.look_up(a, pages, lane, w, t0 + 2 * kKeys, job.k1);
+                }
+                const bool active = t0 < mine;
+                f32x4 sc[QB][KS];  // of the lane's query and its 4 keys of every block
+                if (active) {
+                    const int rb = Pl::row_base(16 * KS * kh, lane);
+                    const char* part_of = rows;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        p[j] = weight_of(sc[x][b][j], a.s.mag, base, kShift<T>);
-                        add[x] += p[j];
+                    for (int x = 0; x < QB; ++x)
+#pragma unroll
+                        for (int b = 0; b < KS; ++b) sc[x][b] = f32x4{0, 0, 0, 0};
+                    const auto products = [&](auto half) {
+                        constexpr int kFrom = decltype(half)::value * QS;
+#pragma unroll
+                        for (int i = 0; i < QS; ++i)
+#pragma unroll
+                            for (int b = 0; b < KS; ++b) {
+                                const u32x4 k = Pl::row(part_of, rb, 16 * b, kFrom + i);
+#pragma unroll
+                                for (int x = 0; x < QB; ++x)
+                                    sc[x][b] = mfma32<T>(k, q[x][i], sc[x][b]);
+                            }
+                    };
+                    if (G::DH == 1 || dh == 0) products(std::integral_constant<int, 0>{});
+                    else products(std::integral_constant<int, G::DH - 1>{});
+                }
+                if constexpr (G::DH == 2) {
+                    // the other half's sums of the blocks whose weights it makes
+                    char* const out = slots + (w ^ 1) * G::kSlot;
+                    if (active)
+#pragma unroll
+                        for (int x = 0; x < QB; ++x)
+#pragma unroll
+                            for (int f = 0; f < FB; ++f)
+                                *reinterpret_cast<f32x4*>(out + ((x * FB + f) * kWave + lane) * 16) =
+                                    dh == 0 ? sc[x][FB + f] : sc[x][f];
+                    __syncthreads();
+                    if (active)
+#pragma unroll
+                        for (int x = 0; x < QB; ++x)
+#pragma unroll
+                            for (int f = 0; f < FB; ++f) {
+                                const f32x4 y = *reinterpret_cast<const f32x4*>(
+                                    mail + ((x * FB + f) * kWave + lane) * 16);
+                                sc[x][f] = (dh == 0 ? sc[x][f] : sc[x][FB + f]) + y;
+                            }
+                }
+                const int first = t0 + 16 * (KS * kh + FB * dh);  // the blocks' first key
+                float top[QB], add[QB];
+                const auto put_probs = [&] {
+#pragma unroll
+                    for (int x = 0; x < QB; ++x) {
+                        add[x] = 0.f;
+                        const float base = ref[x] == -INFINITY ? 0.f : ref[x];
+#pragma unroll
+                        for (int f = 0; f < FB; ++f) {
+                            float p[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                p[j] = weight_of(sc[x][f][j], a.s.mag, base, kShift<T>);
+                                add[x] += p[j];
+                            }
+                            *reinterpret_cast<u32x2*>(mail + ((x * FB + f) * kWave + lane) * 8) =
+                                u32x2{pack2<T>(p[0], p[1]), pack2<T>(p[2], p[3])};
+                        }
                     }
-                    // as the second product's operand has them: its first 16 keys, its second
-                    const int at = KS * part + b;
-                    reinterpret_cast<u32x2*>(&probs[team][at / 2][x][lane])[at & 1] =
-                        u32x2{pack2<T>(p[0], p[1]), pack2<T>(p[2], p[3])};
+                };
+                bool raise = false;
+                if (active) {
+#pragma unroll
+                    for (int x = 0; x < QB; ++x) {
+                        if (first + 16 * FB > full) {  // some row does not see some key
+                            const int row = min(row0 + 16 * x + n, job.rows - 1);
+                            const int sees = job.before + (int)a.group_div.div(row);
+                            const Seen seen = Seen::first(min(job.k1, sees) - first);
+#pragma unroll
+                            for (int j = 0; j < 4 * FB; ++j)
+                                sc[x][j >> 2][j & 3] = seen.pick(j, sc[x][j >> 2][j & 3], -INFINITY);
+                        }
+                        top[x] = sc[x][0][0];
+#pragma unroll
+                        for (int j = 1; j < 4 * FB; ++j) top[x] = fmaxf(top[x], sc[x][j >> 2][j & 3]);
+                        top[x] *= a.s.mag;
+                        raise |= top[x] > ref[x] + kSlack;
+                    }
+                    put_probs();
+                }
+                const bool raised = __any(raise);
+                if (lane == 0) *reinterpret_cast<int*>(mail + G::kFlag) = raised;
+                __syncthreads();
+                const int flag =
+                    *reinterpret_cast<const int*>(slots + (lane % NW) * G::kSlot + G::kFlag);
+                if (__any(flag != 0)) {  // hardly ever after the first tiles
+                    if (active) {
+#pragma unroll
+                        for (int x = 0; x < QB; ++x) {
+                            top[x] = quad_max(top[x]);
+                            if (lane < 16)
+                                *reinterpret_cast<float*>(mail + G::kTops + 64 * x + 4 * lane) = top[x];
+                        }
+                    }
+                    __syncthreads();
+                    if (active) {
+#pragma unroll
+                        for (int x = 0; x < QB; ++x) {
+#pragma unroll
+                            for (int c = 0; c < CG; ++c)
+                                top[x] = fmaxf(top[x], *reinterpret_cast<const float*>(
+                                                           slots + (team * CG + c) * G::kSlot +
+                                                           G::kTops + 64 * x + 4 * n));
+                            const float fix = move(ref[x], top[x]);
+                            sum[x] *= fix;
+#pragma unroll
+                            for (int b = 0; b < NB; ++b) o[x][b] *= fix;
+                        }
+                        put_probs();
+                    }
+                    __syncthreads();
+                }
+                if (min(t0 + kKeys, job.k1) > job.before + job.first / a.s.group) {
+                    const bool any = Cr::template clear<G, NW * kWave>(rows, G::kDv / 64);
+                    wild |= (uint32_t)any << ((t0 - cross.from) / kKeys);
+                    __syncthreads();
+                }
+                if (active) {
+#pragma unroll
+                    for (int x = 0; x < QB; ++x) sum[x] += add[x];
+                    const char* vals = rows + part * (G::kDv / 64 / CG) * Pl::kPlane;
+#pragma unroll
+                    for (int j = 0; j < kKeys / 32; ++j) {
+                        typename G::Probs pr[QB];
+#pragma unroll
+                        for (int x = 0; x < QB; ++x)
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+                                // block 2 j + b: where its weights were left
+                                const int block = 2 * j + b, maker = block / FB, f = block % FB;
+                                const u32x2 p = *reinterpret_cast<const u32x2*>(
+                                    slots + (team * CG + maker) * G::kSlot +
+                                    ((x * FB + f) * kWave + lane) * 8);
+                                pr[x].w[2 * b] = p[0];
+                                pr[x].w[2 * b + 1] = p[1];
+                            }
+                        const int vb = Pl::value_base(32 * j, lane);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            const u32x4 v = Pl::value(vals, vb, b);
+#pragma unroll
+                            for (int x = 0; x < QB; ++x) o[x][b] = G::add_block(v, pr[x], o[x][b]);
+                        }
+                    }
+                }
+                wait_for_loads();
+                __syncthreads();  // the next tile is there, this one's readers are done
+            };
+            for (int t0 = job.k0; t0 < job.k1; t0 += 2 * kKeys) {
+                take(tile0, tile1, t0);
+                if (t0 + kKeys < job.k1) take(tile1, tile0, t0 + kKeys);
+            }
+            auto* const wild_s = reinterpret_cast<unsigned long long*>(tile0);
+            const bool crossed = job.k1 > job.before + job.first / a.s.group;
+            if (crossed) Cr::gather(wild, wild_s);
+#pragma unroll
+            for (int x = 0; x < QB; ++x) {
+                sum[x] = quad_sum(sum[x]);
+                if (lane < 16) *reinterpret_cast<float*>(mail + G::kTops + 64 * x + 4 * lane) = sum[x];
+            }
+            const bool wrong = __any(from.wrong);
+            if (lane == 0) *reinterpret_cast<int*>(mail + G::kFlag) = wrong;
+            __syncthreads();
+            if (row0 >= job.rows) return;
+            const int flag = *reinterpret_cast<const int*>(slots + (lane % NW) * G::kSlot + G::kFlag);
+            const bool any_wrong = __any(flag != 0);
+            // the rows again: kept, they would take registers from the loop
+            int again = row0;
+            asm volatile("" : "+s"(again));
+#pragma unroll
+            for (int x = 0; x < QB; ++x) {
+                r[x] = tile_row(a, job, again + 16 * x + n, 0);
+                const int sees = job.before + r[x].t;
+                if (!r[x].has || sees <= job.k0) continue;
+                float l = 0.f;
+#pragma unroll
+                for (int c = 0; c < CG; ++c)
+                    l += *reinterpret_cast<const float*>(slots + (team * CG + c) * G::kSlot +
+                                                         G::kTops + 64 * x + 4 * n);
+                if (any_wrong) l = NAN;
+                const int64_t line = r[x].token * a.s.hq + r[x].hq;
+                // where a part of a split sequence goes
+                const int64_t at =
+                    ((2 * unit + late) * tiles + tile) * G::BM + again - job.first + 16 * x + n;
+                const float f = l == 0.f ? 0.f : 1.f / l;
+                if (crossed)
+                    cross.template add<T>(
+                        wild_s, min(job.k1, sees), a.s.dim - part * (G::kDv / CG),
+                        [&](int key) -> const char* {
+                            const uint32_t pg = a.page_div.div(key), id = (uint32_t)pages[pg];
+                            if (id >= (uint64_t)a.npages) return nullptr;
+                            const uint32_t slot = key - pg * a.page_div.d;
+                            return a.k + ((uint64_t)(id * a.k_page + slot * a.k_slot) << a.k_shift) +
+                                   part * (2 * G::kDv / CG);
+                        },
+                        o[x]);
+                char* row = !split ? a.out.base + r[x].token * a.out.row + r[x].hq * a.out.head
+                                   : reinterpret_cast<char*>(a.part + at * a.s.dim);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const int d = part * (G::kDv / CG) + 16 * b + 4 * (lane >> 4);
+                    if (d >= a.s.dim) continue;
+                    if (!split)
+                        G::store_four(o[x][b] * f, row + 2 * d);
+                    else
+                        *reinterpret_cast<f32x4*>(row + 4 * d) = o[x][b];
+                }
+                if (part == 0 && lane < 16) {
+                    if (split) {
+                        a.part_ml[2 * at] = ref[x];
+                        a.part_ml[2 * at + 1] = l;
+                    } else if (a.lse) {
+                        a.lse[line] =
+                            l == 0.f ? -INFINITY : (ref[x] - kShift<T> + fast_log2(l)) * kLn2;
+                    }
                 }
             }
         };
-        float add[QB];
-        if (active) {
-            const int rb = Pl::row_base(16 * KS * part, lane);
-#pragma unroll
-            for (int b = 0; b < KS; ++b) {
-#pragma unroll
-                for (int x = 0; x < QB; ++x) sc[x][b] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int i = 0; i < QS; ++i) {
-                    const u32x4 k = Pl::row(rows, rb, 16 * b, i);
-#pragma unroll
-                    for (int x = 0; x < QB; ++x)
-                        sc[x][b] = mfma32<T>(
-                            k, G::kept(x, i) < 0 ? q[x][i] : kept[team][G::kept(x, i)][lane], sc[x][b]);
-                }
-            }
-            const int t = t0 + 16 * KS * part;
-            bool raise = false;
-#pragma unroll
-            for (int x = 0; x < QB; ++x) {
-                if (t + 16 * KS > full) {  // some row does not see some key
-                    const int row = min(row0 + 16 * x + n, job.rows - 1);
-                    const int sees = job.before + (int)a.group_div.div(row);
-                    const Seen seen = Seen::first(min(job.k1, sees) - t);
-#pragma unroll
-                    for (int j = 0; j < 4 * KS; ++j)
-                        sc[x][j >> 2][j & 3] = seen.pick(j, sc[x][j >> 2][j & 3], -INFINITY);
-                }
-                top[x] = sc[x][0][0];
-#pragma unroll
-                for (int j = 1; j < 4 * KS; ++j) top[x] = fmaxf(top[x], sc[x][j >> 2][j & 3]);
-                top[x] *= a.s.mag;
-                raise |= top[x] > ref[x] + kSlack;
-            }
-            if (__any(raise)) raise_s[par] = 1;
-            put_probs(add);
-        }
-        __syncthreads();
-        if (tid == 0) raise_s[par ^ 1] = 0;
-        if (raise_s[par]) {  // hardly ever after the first tiles
-            if (active) {
-#pragma unroll
-                for (int x = 0; x < QB; ++x) {
-                    top[x] = quad_max(top[x]);
-                    if (lane < 16) tops[team][x][part][lane] = top[x];
-                }
-            }
-            __syncthreads();
-            if (active) {
-#pragma unroll
-                for (int x = 0; x < QB; ++x) {
-#pragma unroll
-                    for (int c = 0; c < CG; ++c) top[x] = fmaxf(top[x], tops[team][x][c][n]);
-                    const float fix = move(ref[x], top[x]);
-                    sum[x] *= fix;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) o[x][b] *= fix;
-                }
-                put_probs(add);
-            }
-            __syncthreads();
-        }
-        if (min(t0 + kKeys, job.k1) > job.before + job.first / a.s.group) {
-            Cr::template clear<G, NW * kWave>(rows, G::kDv / 64, &wild_s[(t0 - cross.from) / kKeys]);
-            __syncthreads();
-        }
-        if (active) {
-#pragma unroll
-            for (int x = 0; x < QB; ++x) sum[x] += add[x];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                typename G::Probs pr[QB];
-#pragma unroll
-                for (int x = 0; x < QB; ++x) {
-                    const u32x4 p = probs[team][j][x][lane];
-                    pr[x] = {{p[0], p[1], p[2], p[3]}};
-                }
-                const int vb = Pl::value_base(32 * j, lane);
-                const char* vals = rows + part * (G::kDv / 64 / CG) * Pl::kPlane;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const u32x4 v = Pl::value(vals, vb, b);
-#pragma unroll
-                    for (int x = 0; x < QB; ++x) o[x][b] = G::add_block(v, pr[x], o[x][b]);
-                }
-            }
-        }
-        wait_for_loads();
-        __syncthreads();  // the next tile is there, this one's readers are done
-    };
-    for (int t0 = job.k0; t0 < job.k1; t0 += 2 * kKeys) {
-        take(tile0, tile1, t0, 0);
-        if (t0 + kKeys < job.k1) take(tile1, tile0, t0 + kKeys, 1);
-    }
-    if (from.wrong) wrong_s = 1;
-#pragma unroll
-    for (int x = 0; x < QB; ++x) {
-        sum[x] = quad_sum(sum[x]);
-        if (lane < 16) tops[team][x][part][lane] = sum[x];
-    }
-    __syncthreads();
-    if (row0 >= job.rows) return;
-    // the rows again: kept, they would take registers from the loop
-    int first = row0;
-    asm volatile("" : "+s"(first));
-#pragma unroll
-    for (int x = 0; x < QB; ++x) {
-        r[x] = tile_row(a, job, first + 16 * x + n, 0);
-        const int sees = job.before + r[x].t;
-        if (!r[x].has || sees <= job.k0) continue;
-        float l = 0.f;
-#pragma unroll
-        for (int c = 0; c < CG; ++c) l += tops[team][x][c][n];
-        if (wrong_s) l = NAN;
-        const int64_t line = r[x].token * a.s.hq + r[x].hq;
-        // where a part of a split sequence goes
-        const int64_t at = ((2 * unit + (first_pos > begin)) * tiles + tile) * G::BM +
-                           first - job.first + 16 * x + n;
-        const float f = l == 0.f ? 0.f : 1.f / l;
-        cross.template add<T>(wild_s, min(job.k1, sees), a.s.dim - part * (G::kDv / CG), [&](int key) -> const char* {
-            const uint32_t pg = a.page_div.div(key), id = (uint32_t)pages[pg];
-            if (id >= (uint64_t)a.npages) return nullptr;
-            return a.k + ((uint64_t)(id * a.k_page + (key - pg * a.page_div.d) * a.k_slot) << a.k_shift) +
-                   part * (2 * G::kDv / CG);
-        }, o[x]);
-        char* row = !split ? a.out.base + r[x].token * a.out.row + r[x].hq * a.out.head
-                          : reinterpret_cast<char*>(a.part + at * a.s.dim);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const int d = part * (G::kDv / CG) + 16 * b + 4 * (lane >> 4);
-            if (d >= a.s.dim) continue;
-            if (!split)
-                G::store_four(o[x][b] * f, row + 2 * d);
-            else
-                *reinterpret_cast<f32x4*>(row + 4 * d) = o[x][b];
-        }
-        if (part == 0 && lane < 16) {
-            if (split) {
-                a.part_ml[2 * at] = ref[x];
-                a.part_ml[2 * at + 1] = l;
-            } else if (a.lse) {
-                a.lse[line] = l == 0.f ? -INFINITY : (ref[x] - kShift<T> + fast_log2(l)) * kLn2;
-            }
-        }
-    }
-    };
-    segment();
-    if (pos >= end) return;
-    __syncthreads();  // flags and sums are used again
+        segment();
+        if (pos >= end) return;
+        __syncthreads();  // what is in LDS is used again
     }
 }
 
@@ -544,11 +591,11 @@ __global__ __launch_bounds__(kWaves* kWave) void k_latent_join(PagedArgs a, int3
     int count;
     int64_t first, step, late = 0;  // in rows of parts
     if (a.ranges) {
-        const EvenParts parts(EvenSplit(a, keys), s, keys, sees);
+        const EvenParts parts(EvenSplit(a, keys), __builtin_amdgcn_readfirstlane((int)s), keys, sees);
         const int row = (int)(token - sq.q0) * a.s.hq + hq, tile = row / tile_rows;
         count = parts.count;
         step = (int64_t)2 * tiles * tile_rows;
-        first = ((2 * parts.range) * tiles + tile) * tile_rows + row - tile * tile_rows;
+        first = ((int64_t)2 * parts.range * tiles + tile) * tile_rows + row - tile * tile_rows;
         late = parts.late ? (int64_t)tiles * tile_rows : 0;
     } else {
         count = sees <= a.piece ? 0 : (sees + a.piece - 1) / a.piece;
@@ -603,7 +650,6 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
     using Cr = Crossing<kKeys>;
     __shared__ __align__(16) char tile0[G::kPlanes * Pl::kPlane];
     __shared__ __align__(16) char tile1[G::kPlanes * Pl::kPlane];
-    __shared__ unsigned long long wild_s[Cr::kTiles];  // see there
     __shared__ int wrong_s;
     const int tid = threadIdx.x, lane = lane_id();
     const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -629,11 +675,8 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
         return;
     }
     if (job.k0 >= job.k1) return;
-    if (tid == 0) {
-        wrong_s = 0;
-#pragma unroll
-        for (int i = 0; i < Cr::kTiles; ++i) wild_s[i] = 0;
-    }
+    if (tid == 0) wrong_s = 0;
+    uint32_t wild = 0;  // see Crossing
     const Cr cross(job, job.first);
     const int lo = __builtin_amdgcn_readfirstlane(r[0].t);
     const int hi = __builtin_amdgcn_readlane(r[QB - 1].t, 15);
@@ -711,7 +754,8 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
             from.look_up(a, pages, lane, w, t0 + 2 * kKeys, job.k1);
         }
         if (min(t0 + kKeys, job.k1) > job.before + job.first) {
-            Cr::template clear<G, NW * kWave>(vals, G::VP, &wild_s[(t0 - cross.from) / kKeys]);
+            const bool any = Cr::template clear<G, NW * kWave>(vals, G::VP);
+            wild |= (uint32_t)any << ((t0 - cross.from) / kKeys);
             __syncthreads();
         }
         if (t0 < mine) {
@@ -780,7 +824,10 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
         if (t0 + kKeys < job.k1) take(tile1, tile0, t0 + kKeys);
     }
     if (from.wrong) wrong_s = 1;
-    __syncthreads();
+    auto* const wild_s = reinterpret_cast<unsigned long long*>(tile0);
+    const bool crossed = job.k1 > job.before + job.first;
+    if (crossed) Cr::gather(wild, wild_s);
+    else __syncthreads();
     if (row0 >= job.rows) return;
 #pragma unroll
     for (int x = 0; x < QB; ++x) {
@@ -792,7 +839,8 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
         const bool part = sees > a.piece;
         const int64_t at = (int64_t)piece * a.tokens * a.s.hq + line;
         const float f = l == 0.f ? 0.f : 1.f / l;
-        cross.template add<T>(wild_s, min(job.k1, sees), a.s.dim,
+        if (crossed)
+            cross.template add<T>(wild_s, min(job.k1, sees), a.s.dim,
                               [&](int key) { return made_v + (int64_t)key * 2 * values; }, o[x]);
         char* row = part ? reinterpret_cast<char*>(a.part + at * a.s.dim)
                          : a.out.base + r[x].token * a.out.row + r[x].hq * a.out.head;
@@ -966,21 +1014,14 @@ void with_latent_type(int type, F&& f) {
     if (type == SPGEMM_TYPE_BF16) f((__bf16*)nullptr);
     else f((_Float16*)nullptr);
 }
-template <int N>
-using Int = std::integral_constant<int, N>;
 // f(geometry, type) of a call: the smallest widths that hold it.
 template <class F>
 void with_absorbed(const LatentArgs& a, F&& f) {
     with_latent_type(a.s.type, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;
-        const auto width = [&](auto dk, auto dv, auto cg) {
-            constexpr int K = decltype(dk)::value, V = decltype(dv)::value, C = decltype(cg)::value;
-            if (a.key_dim == K) f((AbsorbedGeo<T, K, V, C, true>*)nullptr, t);
-            else f((AbsorbedGeo<T, K, V, C, false>*)nullptr, t);
-        };
-        if (a.s.dim <= 128 && a.key_dim <= 192) width(Int<192>{}, Int<128>{}, Int<2>{});
-        else if (a.s.dim <= 256 && a.key_dim <= 320) width(Int<320>{}, Int<256>{}, Int<2>{});
-        else width(Int<576>{}, Int<512>{}, Int<4>{});
+        if (a.s.dim <= 128 && a.key_dim <= 192) f((AbsorbedGeo<T, 192, 128, 2, 1>*)nullptr, t);
+        else if (a.s.dim <= 256 && a.key_dim <= 320) f((AbsorbedGeo<T, 320, 256, 2, 1>*)nullptr, t);
+        else f((AbsorbedGeo<T, 576, 512, 2, 2>*)nullptr, t);
     });
 }
 template <class F>

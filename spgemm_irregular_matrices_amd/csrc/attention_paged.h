@@ -130,87 +130,77 @@ __device__ __forceinline__ void store_row(const PagedArgs& a, const TileJob& j, 
     }
 }
 
-// A value that all lanes hold alike, as the compiler's scalars.
-__device__ __forceinline__ int64_t uniform(int64_t x) {
-    return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)x) |
-           (int64_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32;
-}
-
 // A batch's tiles of `keys` keys, one sequence after another, cut into ranges of
 // one length: wavefronts or work groups that take a range each end together,
 // whatever the texts' lengths. A sequence's part of a range is a segment; the
 // segments of a sequence that lies in several ranges are joined. Range i leaves
 // such a part in slot 2 i if the range begins with it, else in 2 i + 1. By a whole
-// wavefront; up to kEvenSeqs sequences.
-constexpr int kEvenSeqs = 256;
+// wavefront; up to kEvenSeqs sequences of less than 2^31 tiles.
+
 struct EvenSplit {
     static constexpr int kEach = kEvenSeqs / kWave;
     int n[kEach];  // tiles of sequences lane, 64 + lane, ...
-    int64_t total, per;
+    int total = 0, per;
     __device__ __forceinline__ EvenSplit(const PagedArgs& a, int keys) {
-        int64_t sum = 0;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int64_t s = i * kWave + lane_id();
             n[i] = 0;
+            if (i * kWave >= a.seqs) continue;
+            const int64_t s = i * kWave + lane_id();
             if (s < a.seqs) {
                 const Sequence sq = read_sequence(a, s);
                 n[i] = sq.none ? 0 : sq.bad ? 1 : (sq.length + keys - 1) / keys;
             }
-            sum += n[i];
+            total += last(wave_inclusive_scan_i32(n[i]));
         }
-        total = uniform(wave_reduce_sum(sum));
-        per = max((total + a.ranges - 1) / a.ranges, (int64_t)a.least);
+        per = max((total + a.ranges - 1) / a.ranges, a.least);
     }
+    static __device__ __forceinline__ int last(int x) { return __builtin_amdgcn_readlane(x, kWave - 1); }
     // The sequence that tile `pos` < total is of, and the tiles before it.
-    __device__ __forceinline__ void locate(int64_t pos, int64_t& s, int64_t& before) const {
-        before = 0;
-        s = 0;
+    __device__ __forceinline__ void locate(int pos, int& s, int& before) const {
+        before = s = 0;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int64_t in = wave_inclusive_scan((int64_t)n[i]);
+            const int in = wave_inclusive_scan_i32(n[i]);
             const uint64_t past = __ballot(before + in > pos);
             if (past) {
                 const int l = __builtin_ctzll(past);
                 s = i * kWave + l;
-                before += uniform(__shfl(in - n[i], l, kWave));
+                before += __builtin_amdgcn_readlane(in - n[i], l);
                 return;
             }
-            before += uniform(__shfl(in, kWave - 1, kWave));
+            before += last(in);
         }
     }
-    // The tiles before sequence s, and its own.
-    __device__ __forceinline__ void sequence(int64_t s, int64_t& before, int& own) const {
-        int64_t sum = 0;
-        own = 0;
+    // The tiles before sequence s (the same in all lanes), and its own.
+    __device__ __forceinline__ void sequence(int s, int& before, int& own) const {
+        before = own = 0;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int64_t at = i * kWave + lane_id();
-            sum += at < s ? n[i] : 0;
-            if (s / kWave == i) own = __shfl(n[i], (int)(s % kWave), kWave);
+            if (s < i * kWave) continue;
+            const int in = wave_inclusive_scan_i32(n[i]);
+            if (s >= (i + 1) * kWave) {
+                before += last(in);
+            } else {
+                own = __builtin_amdgcn_readlane(n[i], s % kWave);
+                before += __builtin_amdgcn_readlane(in, s % kWave) - own;
+            }
         }
-        before = uniform(wave_reduce_sum(sum));
     }
 };
-// A row's parts under an even split: of `count` ranges from `range` on, the first
-// of which begins with the row's sequence or (late) with another one.
+// A row's parts under an even split: of `count` ranges (0: its result is whole) from
+// `range` on, the first of which begins with the row's sequence or (late) with
+// another one; only those that begin with a key that the row sees.
 struct EvenParts {
-    int64_t range;
-    int count;
+    int range, count;
     bool late;
-    // only those that begin with a key that the row sees
-    __device__ __forceinline__ EvenParts(const EvenSplit& e, int64_t s, int keys, int sees) {
-        int64_t before;
-        int own;
+    __device__ __forceinline__ EvenParts(const EvenSplit& e, int s, int keys, int sees) {
+        int before, own;
         e.sequence(s, before, own);
         range = before / e.per;
         late = before > range * e.per;
-        const int64_t last = before + (sees + keys - 1) / keys - 1;
         const bool whole = (before + own - 1) / e.per == range;
-        count = whole ? 0 : (int)(last / e.per - range + 1);
-    }
-    __device__ __forceinline__ int64_t slot(int i) const {
-        return 2 * (range + i) + (i == 0 && late ? 1 : 0);
+        count = whole ? 0 : (before + (sees + keys - 1) / keys - 1) / e.per - range + 1;
     }
 };
 

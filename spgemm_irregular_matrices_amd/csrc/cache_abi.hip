@@ -194,7 +194,7 @@ void latent_shape(const spgemm_latent_desc* d, const spgemm_paged_batch* b, bool
         const int64_t tiles = std::max<int64_t>(ceil_div((int64_t)a->max_new * a->s.group, tile), 1);
         const int64_t most = a->seqs * ceil_div(a->max_length, kAbsorbedKeys);
         a->piece = std::max(a->max_length, 1);
-        if (a->seqs <= 256 && a->seqs * tiles < 512 && most > a->seqs) {
+        if (a->seqs <= kEvenSeqs && a->seqs * tiles < 512 && most > a->seqs && most < INT32_MAX / 2) {
             a->least = 2;
             a->ranges = (int32_t)std::max<int64_t>(std::min(ceil_div(most, a->least), 256 / tiles), 1);
         }
