@@ -212,13 +212,21 @@ struct Crossing {
 // keys in KH and the sum over its elements in DH (2: whole queries of 576 elements
 // leave no registers to read keys ahead; partial sums go through LDS), for the
 // result its columns in KH * DH.
-template <class T, int DK, int DV, int KH_, int DH_>
+// FULL: the keys have DK elements, so that no piece of theirs needs a check.
+template <class T, int DK, int DV, int KH_, int DH_, bool FULL>
 struct AbsorbedGeo : Tile<T, 64, true> {
+    static constexpr bool kWhole = FULL;
     static constexpr int kKeys = kAbsorbedKeys, kDv = DV, kPlanes = DK / 64;
     static constexpr int KH = KH_, DH = DH_, CG = KH * DH, NW = 8, QB = 2, BM = NW / CG * 16 * QB;
     static constexpr int QS = DK / 32 / DH, NB = DV / 16 / CG;
     static constexpr int KS = kKeys / 16 / KH;  // 16-key blocks of a wavefront's products,
     static constexpr int FB = KS / DH;          // and of those those whose weights it makes
+    // Planes of the next tile that are asked for during the scores' products, around
+    // the weights and during the results' products. A compute unit has some 12 KB
+    // under way at once, and further loads stop the wavefront that asks: spread
+    // over the tile's time they do not.
+    static constexpr int kLoad0 = (4 * kPlanes + 8) / 9, kLoad1 = kLoad0 + (kPlanes - kLoad0 + 3) / 4,
+                         kLoad2 = kLoad1 + (kPlanes - kLoad1 + 2) / 4;
     // what a wavefront is sent and leaves in LDS: partial sums, then weights,
     // largest scores and a flag
     static constexpr int kTops = QB * FB * kWave * 8, kFlag = kTops + QB * 64;
@@ -307,18 +315,23 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
 #pragma unroll
                 for (int t = 0; t < QS; ++t)
                     q[x][t] = load_query(a, r[x], 64 * (QS * dh + t) + 16 * (lane >> 4), 2 * a.key_dim);
-            const auto load_tile = [&](char* dst, int t0) {
+            // this lane's row of a tile, and what it loads of plane g of it
+            const char* row = nullptr;
+            uint32_t byte = 0;
+            const auto open_tile = [&](int t0) {
                 const int l = from.anew(lane);
-                const uint32_t byte = from.byte(l, w);
-                const char* row = from.latent(a, t0 + from.row(l, w), job.k1, 0) + byte;
-#pragma unroll
-                for (int g = 0; g < G::kPlanes; ++g)
-                    load_to_lds(128 * g + (int)byte < 2 * a.key_dim
-                                    ? row + 128 * g
-                                    : reinterpret_cast<const char*>(g_zero),
-                                dst + g * Pl::kPlane + w * 1024);
+                byte = from.byte(l, w);
+                row = from.latent(a, t0 + from.row(l, w), job.k1, 0) + byte;
             };
-            load_tile(tile0, job.k0);
+            const auto load_plane = [&](char* dst, int g) {
+                load_to_lds(G::kWhole || 128 * g + (int)byte < 2 * a.key_dim
+                                ? row + 128 * g
+                                : reinterpret_cast<const char*>(g_zero),
+                            dst + g * Pl::kPlane + w * 1024);
+            };
+            open_tile(job.k0);
+#pragma unroll
+            for (int g = 0; g < G::kPlanes; ++g) load_plane(tile0, g);
             from.look_up(a, pages, lane, w, job.k0 + kKeys, job.k1);
             if (a.s.c <= 0.f)
 #pragma unroll
@@ -341,33 +354,52 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
 
             // One tile of keys, staged in `rows`; the next one is loaded into `next`.
             const auto take = [&](char* rows, char* next, int t0) {
-                if (t0 + kKeys < job.k1) {
-                    load_tile(next, t0 + kKeys);
-                    from.look_up(a, pages, lane, w, t0 + 2 * kKeys, job.k1);
-                }
+                // (past the end it loads zeros: the loads go between the products,
+                // as memory takes them no faster)
+                open_tile(t0 + kKeys);
+                from.look_up(a, pages, lane, w, t0 + 2 * kKeys, job.k1);
                 const bool active = t0 < mine;
                 f32x4 sc[QB][KS];  // of the lane's query and its 4 keys of every block
                 if (active) {
                     const int rb = Pl::row_base(16 * KS * kh, lane);
-                    const char* part_of = rows;
 #pragma unroll
                     for (int x = 0; x < QB; ++x)
 #pragma unroll
                         for (int b = 0; b < KS; ++b) sc[x][b] = f32x4{0, 0, 0, 0};
                     const auto products = [&](auto half) {
                         constexpr int kFrom = decltype(half)::value * QS;
+                        // keys are read kAhead steps before their products, a plane of
+                        // the next tile is asked for between; left to the compiler, every
+                        // product waits for its own read
+                        constexpr int kAhead = 2;
+                        u32x4 k[kAhead + 1][KS];
+                        const auto read = [&](int i) {
 #pragma unroll
-                        for (int i = 0; i < QS; ++i)
+                            for (int b = 0; b < KS; ++b)
+                                k[i % (kAhead + 1)][b] = Pl::row(rows, rb, 16 * b, kFrom + i);
+                        };
 #pragma unroll
-                            for (int b = 0; b < KS; ++b) {
-                                const u32x4 k = Pl::row(part_of, rb, 16 * b, kFrom + i);
+                        for (int i = 0; i < kAhead; ++i) read(i);
+#pragma unroll
+                        for (int i = 0; i < QS; ++i) {
+                            __builtin_amdgcn_sched_barrier(0);
+                            if (i + kAhead < QS) read(i + kAhead);
+#pragma unroll
+                            for (int g = 0; g < G::kLoad0; ++g)
+                                if (g * QS / G::kLoad0 == i) load_plane(next, g);
+#pragma unroll
+                            for (int b = 0; b < KS; ++b)
 #pragma unroll
                                 for (int x = 0; x < QB; ++x)
-                                    sc[x][b] = mfma32<T>(k, q[x][i], sc[x][b]);
-                            }
+                                    sc[x][b] = mfma32<T>(k[i % (kAhead + 1)][b], q[x][i], sc[x][b]);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
                     };
                     if (G::DH == 1 || dh == 0) products(std::integral_constant<int, 0>{});
                     else products(std::integral_constant<int, G::DH - 1>{});
+                } else {
+#pragma unroll
+                    for (int g = 0; g < G::kLoad0; ++g) load_plane(next, g);
                 }
                 if constexpr (G::DH == 2) {
                     // the other half's sums of the blocks whose weights it makes
@@ -410,6 +442,8 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
                         }
                     }
                 };
+#pragma unroll
+                for (int g = G::kLoad0; g < G::kLoad1; ++g) load_plane(next, g);
                 bool raise = false;
                 if (active) {
 #pragma unroll
@@ -435,6 +469,8 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
                 __syncthreads();
                 const int flag =
                     *reinterpret_cast<const int*>(slots + (lane % NW) * G::kSlot + G::kFlag);
+#pragma unroll
+                for (int g = G::kLoad1; g < G::kLoad2; ++g) load_plane(next, g);
                 if (__any(flag != 0)) {  // hardly ever after the first tiles
                     if (active) {
 #pragma unroll
@@ -491,9 +527,16 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
                         for (int b = 0; b < NB; ++b) {
                             const u32x4 v = Pl::value(vals, vb, b);
 #pragma unroll
+                            for (int g = G::kLoad2; g < G::kPlanes; ++g)
+                                if (j == 0 && (g - G::kLoad2) * NB / (G::kPlanes - G::kLoad2) == b)
+                                    load_plane(next, g);
+#pragma unroll
                             for (int x = 0; x < QB; ++x) o[x][b] = G::add_block(v, pr[x], o[x][b]);
                         }
                     }
+                } else {
+#pragma unroll
+                    for (int g = G::kLoad2; g < G::kPlanes; ++g) load_plane(next, g);
                 }
                 wait_for_loads();
                 __syncthreads();  // the next tile is there, this one's readers are done
@@ -1014,14 +1057,21 @@ void with_latent_type(int type, F&& f) {
     if (type == SPGEMM_TYPE_BF16) f((__bf16*)nullptr);
     else f((_Float16*)nullptr);
 }
+template <int N>
+using Int = std::integral_constant<int, N>;
 // f(geometry, type) of a call: the smallest widths that hold it.
 template <class F>
 void with_absorbed(const LatentArgs& a, F&& f) {
     with_latent_type(a.s.type, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;
-        if (a.s.dim <= 128 && a.key_dim <= 192) f((AbsorbedGeo<T, 192, 128, 2, 1>*)nullptr, t);
-        else if (a.s.dim <= 256 && a.key_dim <= 320) f((AbsorbedGeo<T, 320, 256, 2, 1>*)nullptr, t);
-        else f((AbsorbedGeo<T, 576, 512, 2, 2>*)nullptr, t);
+        const auto width = [&](auto dk, auto dv, auto dh) {
+            constexpr int K = decltype(dk)::value, V = decltype(dv)::value, D = decltype(dh)::value;
+            if (a.key_dim == K) f((AbsorbedGeo<T, K, V, 2, D, true>*)nullptr, t);
+            else f((AbsorbedGeo<T, K, V, 2, D, false>*)nullptr, t);
+        };
+        if (a.s.dim <= 128 && a.key_dim <= 192) width(Int<192>{}, Int<128>{}, Int<1>{});
+        else if (a.s.dim <= 256 && a.key_dim <= 320) width(Int<320>{}, Int<256>{}, Int<1>{});
+        else width(Int<576>{}, Int<512>{}, Int<2>{});
     });
 }
 template <class F>
