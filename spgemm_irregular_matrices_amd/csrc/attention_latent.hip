@@ -1,5 +1,7 @@
 // Attention over a paged cache of latent vectors, in the latents' space
 // (absorbed) or over keys and values that were made from them (expanded).
+#include <algorithm>
+
 #include "latent.h"
 
 namespace sg {
@@ -233,7 +235,8 @@ struct AbsorbedGeo : Tile<T, 64, true> {
     static constexpr int kSlot = DH == 2 ? QB * FB * kWave * 16 : kFlag + 64;
     static_assert(BM <= kPagedTileMost, "the limit of rows counts on it");
     static_assert(DK % (32 * DH) == 0 && DV % (64 * CG) == 0 && KS >= DH && DH <= 2, "tile shape");
-    static_assert(kFlag + 4 <= kSlot && kKeys == 8 * NW, "slots and loads");
+    static_assert(kFlag + 4 <= kSlot && kKeys == 8 * NW && 2 * (kPlanes - kLoad2) <= NB + 1,
+                  "slots and loads");
 };
 
 template <class G, class T>
@@ -528,8 +531,7 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
                             const u32x4 v = Pl::value(vals, vb, b);
 #pragma unroll
                             for (int g = G::kLoad2; g < G::kPlanes; ++g)
-                                if (j == 0 && (g - G::kLoad2) * NB / (G::kPlanes - G::kLoad2) == b)
-                                    load_plane(next, g);
+                                if (j == 0 && 2 * (g - G::kLoad2) == b) load_plane(next, g);
 #pragma unroll
                             for (int x = 0; x < QB; ++x) o[x][b] = G::add_block(v, pr[x], o[x][b]);
                         }
@@ -804,18 +806,33 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
         if (t0 < mine) {
             f32x4 sc[QB][2];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int x = 0; x < QB; ++x) sc[x][0] = sc[x][1] = f32x4{0, 0, 0, 0};
+            // the keys' low parts first; read kAhead steps before their products, as in
+            // k_absorbed
+            constexpr int kSteps = 4 * G::MP + 2, kAhead = 2;
+            u32x4 k[kAhead + 1][2];
+            const auto step = [&](int i) {
+                return i < 2 * G::MP ? i + 2 * G::MP : i < 4 * G::MP ? i - 2 * G::MP : i;
+            };
+            const auto read = [&](int i) {
 #pragma unroll
-                for (int x = 0; x < QB; ++x) sc[x][b] = f32x4{0, 0, 0, 0};
+                for (int b = 0; b < 2; ++b)
+                    k[i % (kAhead + 1)][b] = Pl::row(rows, rb, 16 * b, step(i));
+            };
 #pragma unroll
-                for (int i = 0; i < 4 * G::MP + 2; ++i) {  // the keys' low parts first
-                    const int t = i < 2 * G::MP ? i + 2 * G::MP : i < 4 * G::MP ? i - 2 * G::MP : i;
-                    const int step = t < 2 * G::MP ? t : t - 2 * G::MP;
-                    const u32x4 k = Pl::row(rows, rb, 16 * b, t);
+            for (int i = 0; i < kAhead; ++i) read(i);
 #pragma unroll
-                    for (int x = 0; x < QB; ++x) sc[x][b] = mfma32<T>(k, q[x][step], sc[x][b]);
-                }
+            for (int i = 0; i < kSteps; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (i + kAhead < kSteps) read(i + kAhead);
+                const int t = step(i) < 2 * G::MP ? step(i) : step(i) - 2 * G::MP;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int x = 0; x < QB; ++x)
+                        sc[x][b] = mfma32<T>(k[i % (kAhead + 1)][b], q[x][t], sc[x][b]);
             }
+            __builtin_amdgcn_sched_barrier(0);
             bool raise = false;
             float top[QB];
 #pragma unroll
@@ -908,34 +925,36 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
 }
 
 // Every head's keys and values: C[row][m] = sum_x W[m][x] c[row][x], W the heads'
-// key rows, then their value rows. A work group makes 128 rows of W times 128
-// tokens, 64 values of x at a time.
+// key rows, then their value rows. A work group makes 128 tokens' rows, 128 rows of
+// W at a time and 64 values of x at a step; the next step's are under way meanwhile.
+// It takes `each` such tiles of W, so that looking its tokens up is a small part.
 struct ExpandShape {
     int64_t rows;        // of made keys and values per head
     int32_t key_tiles;   // tiles of 128 of all heads' key rows
     int32_t value_tiles;
+    int32_t each, groups;
     FastDiv key_div, value_div;  // rows of a head
-    FastDiv tile_div;            // tiles of W
 };
 
 template <class T>
-__global__ __launch_bounds__(256) void k_expand(ExpandArgs e, ExpandShape z) {
+__global__ __launch_bounds__(256, 2) void k_expand(ExpandArgs e, ExpandShape z) {
     constexpr int kM = 128, kPlane = kM * 128;
     const LatentArgs& a = e.a;
-    __shared__ __align__(16) char wrows0[kPlane], wrows1[kPlane], crows0[kPlane], crows1[kPlane];
+    __shared__ __align__(16) char wrows0[kPlane];
+    __shared__ __align__(16) char wrows1[kPlane];
+    __shared__ __align__(16) char crows0[kPlane];
+    __shared__ __align__(16) char crows1[kPlane];
     __shared__ const char* from_s[kM];
     __shared__ int any_s;
     using G = Tile<T, 64, true>;
+    using Pl = Planes<kM>;
     const int tid = threadIdx.x, lane = lane_id();
     const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int64_t unit = xcd_block();
-    const int wtiles = z.key_tiles + z.value_tiles;
-    const int64_t ctile = unit / wtiles;
-    const int wtile = (int)(unit - ctile * wtiles);
+    const int64_t ctile = unit / z.groups;
     if (ctile * kM >= z.rows) return;
-    const bool keys = wtile < z.key_tiles;
-    const int m0 = kM * (keys ? wtile : wtile - z.key_tiles);
-    const int per = keys ? a.made_dim : a.s.dim, all = a.s.hq * per;
+    const int first = (int)(unit - ctile * z.groups) * z.each;
+    const int count = min(z.each, z.key_tiles + z.value_tiles - first);
     if (tid == 0) any_s = 0;
     __syncthreads();
     // the tokens' latent rows
@@ -974,16 +993,35 @@ __global__ __launch_bounds__(256) void k_expand(ExpandArgs e, ExpandShape z) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = 8 * (4 * w + i) + (lane >> 3);
-        byte[i] = 16 * ((lane & 7) ^ Planes<kM>::swap(row));
-        const int m = m0 + row;
-        wsrc[i] = nullptr;
-        if (m < all) {
-            const int head = (int)(keys ? z.key_div : z.value_div).div(m);
-            const AttnRows& r = keys ? e.wk : e.wv;
-            wsrc[i] = r.base + head * r.row + (m - head * per) * r.head;
-        }
+        byte[i] = 16 * ((lane & 7) ^ Pl::swap(row));
         csrc[i] = from_s[row];
     }
+    // W's tile t of this work group: its rows' side, first row, rows of a head and of all
+    struct Side {
+        bool keys;
+        int m0, per, all;
+    };
+    const auto side = [&](int t) {
+        Side x;
+        x.keys = first + t < z.key_tiles;
+        x.m0 = kM * (x.keys ? first + t : first + t - z.key_tiles);
+        x.per = x.keys ? a.made_dim : a.s.dim;
+        x.all = a.s.hq * x.per;
+        return x;
+    };
+    const auto open = [&](int t) {
+        const Side x = side(t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = x.m0 + 8 * (4 * w + i) + (lane >> 3);
+            wsrc[i] = nullptr;
+            if (m < x.all) {
+                const int head = (int)(x.keys ? z.key_div : z.value_div).div(m);
+                const AttnRows& r = x.keys ? e.wk : e.wv;
+                wsrc[i] = r.base + head * r.row + (m - head * x.per) * r.head;
+            }
+        }
+    };
     const auto load = [&](char* wrows, char* crows, int x0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -994,19 +1032,21 @@ __global__ __launch_bounds__(256) void k_expand(ExpandArgs e, ExpandShape z) {
         }
     };
     f32x4 acc[4][4];  // rows of W, tokens
+    const auto clear = [&] {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+            for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    };
+    const int wb = Pl::row_base(64 * (w >> 1), lane), cb = Pl::row_base(64 * (w & 1), lane);
     const auto product = [&](const char* wrows, const char* crows) {
-        const int wb = Planes<kM>::row_base(64 * (w >> 1), lane), cb = Planes<kM>::row_base(64 * (w & 1), lane);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             u32x4 x[4], y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[i] = *reinterpret_cast<const u32x4*>(wrows + ((wb + 2048 * i) ^ (64 * t)));
-                y[i] = *reinterpret_cast<const u32x4*>(crows + ((cb + 2048 * i) ^ (64 * t)));
+                x[i] = Pl::row(wrows, wb, 16 * i, t);
+                y[i] = Pl::row(crows, cb, 16 * i, t);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -1014,41 +1054,59 @@ __global__ __launch_bounds__(256) void k_expand(ExpandArgs e, ExpandShape z) {
                 for (int j = 0; j < 4; ++j) acc[i][j] = mfma32<T>(x[i], y[j], acc[i][j]);
         }
     };
+    const auto store = [&](int t) {
+        const Side x = side(t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = x.m0 + 64 * (w >> 1) + 16 * i + 4 * (lane >> 4);
+            if (m >= x.all) continue;
+            const int head = (int)(x.keys ? z.key_div : z.value_div).div(m);
+            char* to = (x.keys ? a.made_k : a.made_v) +
+                       ((int64_t)head * z.rows * 2 * x.per + m - head * x.per) * 2;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = 64 * (w & 1) + 16 * j + (lane & 15);
+                if (!from_s[at]) continue;
+                // rounded, and what that leaves (nothing where it is not finite)
+                f32x4 left;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float high = (float)(T)acc[i][j][c];
+                    left[c] = __builtin_isfinite(high) ? acc[i][j][c] - high : 0.f;
+                }
+                char* row = to + (ctile * kM + at) * 2 * x.per * 2;
+                G::store_four(acc[i][j], row);
+                G::store_four(left, row + 2 * x.per);
+            }
+        }
+    };
+    // steps of 64 values of x, of tile after tile
+    const int steps = (e.latent_dim + 63) / 64;
+    int tile = 0, at = 0, ahead = 0;  // of the step that is computed; of the next one's load
+    clear();
+    open(0);
     load(wrows0, crows0, 0);
     wait_for_loads();
     __syncthreads();
-    for (int x0 = 0; x0 < e.latent_dim; x0 += 128) {
-        if (x0 + 64 < e.latent_dim) load(wrows1, crows1, x0 + 64);
-        product(wrows0, crows0);
-        wait_for_loads();
-        __syncthreads();
-        if (x0 + 64 >= e.latent_dim) break;
-        if (x0 + 128 < e.latent_dim) load(wrows0, crows0, x0 + 128);
-        product(wrows1, crows1);
-        wait_for_loads();
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = m0 + 64 * (w >> 1) + 16 * i + 4 * (lane >> 4);
-        if (m >= all) continue;
-        const int head = (int)(keys ? z.key_div : z.value_div).div(m);
-        char* to = (keys ? a.made_k : a.made_v) + ((int64_t)head * z.rows * 2 * per + m - head * per) * 2;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int at = 64 * (w & 1) + 16 * j + (lane & 15);
-            if (!from_s[at]) continue;
-            // rounded, and what that leaves (nothing where it is not finite)
-            f32x4 left;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const float high = (float)(T)acc[i][j][x];
-                left[x] = __builtin_isfinite(high) ? acc[i][j][x] - high : 0.f;
-            }
-            char* row = to + (ctile * kM + at) * 2 * per * 2;
-            G::store_four(acc[i][j], row);
-            G::store_four(left, row + 2 * per);
+    const auto take = [&](char* wrows, char* crows, char* wnext, char* cnext) {
+        if (++ahead == steps) {
+            ahead = 0;
+            if (tile + 1 < count) open(tile + 1);
         }
+        if (at + 1 < steps || tile + 1 < count) load(wnext, cnext, 64 * ahead);
+        product(wrows, crows);
+        if (++at == steps) {
+            store(tile);
+            clear();
+            at = 0;
+            ++tile;
+        }
+        wait_for_loads();
+        __syncthreads();
+    };
+    while (tile < count) {
+        take(wrows0, crows0, wrows1, crows1);
+        if (tile < count) take(wrows1, crows1, wrows0, crows0);
     }
 }
 
@@ -1129,7 +1187,11 @@ void latent_expand(const ExpandArgs& e, hipStream_t st) {
     z.value_tiles = (int32_t)ceil_div((int64_t)a.s.hq * a.s.dim, 128);
     z.key_div = FastDiv((uint32_t)a.made_dim);
     z.value_div = FastDiv((uint32_t)a.s.dim);
-    const int64_t units = ceil_div(z.rows, 128) * (z.key_tiles + z.value_tiles);
+    const int64_t ctiles = ceil_div(z.rows, 128), wtiles = z.key_tiles + z.value_tiles;
+    // two work groups per compute unit, replaced a few times over
+    z.each = (int32_t)std::min<int64_t>(std::max<int64_t>(ctiles * wtiles / 2048, 1), 16);
+    z.groups = (int32_t)ceil_div(wtiles, z.each);
+    const int64_t units = ctiles * z.groups;
     if (units == 0) return;
     with_latent_type(a.s.type, [&](auto* t) {
         hipLaunchKernelGGL(k_expand<std::remove_pointer_t<decltype(t)>>, grid_2d(xcd_grid(units)),

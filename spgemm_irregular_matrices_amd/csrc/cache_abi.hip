@@ -199,7 +199,8 @@ void latent_shape(const spgemm_latent_desc* d, const spgemm_paged_batch* b, bool
             a->ranges = (int32_t)std::max<int64_t>(std::min(ceil_div(most, a->least), 256 / tiles), 1);
         }
     } else {
-        cut_pieces(a, tile, 256, 256, 64);
+        // two work groups per compute unit are there at once; the texts differ
+        cut_pieces(a, tile, 3072, 1024, 64);
     }
 }
 
