@@ -134,8 +134,8 @@ __device__ __forceinline__ float move(float& ref, float top) {
 }
 __device__ __forceinline__ float weight_of(float s, float c, float ref, float shift) {
 #pragma clang fp contract(off)
-    const float x = s * c;
-    return fast_exp2((x - ref) + shift);
+    const float x = s * c - ref;
+    return fast_exp2(shift == 0.f ? x : x + shift);
 }
 
 // Keys that not all rows of a work group see. An infinity or a NaN in one's value
@@ -925,78 +925,89 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
 }
 
 // Every head's keys and values: C[row][m] = sum_x W[m][x] c[row][x], W the heads'
-// key rows, then their value rows. A work group makes 128 tokens' rows, 128 rows of
-// W at a time and 64 values of x at a step; the next step's are under way meanwhile.
-// It takes `each` such tiles of W, so that looking its tokens up is a small part.
+// key rows, then their value rows. A wavefront keeps 32 tokens' rows of c in
+// registers (NS steps of 32 values of x), a work group of 8 of them takes `each`
+// tiles of 128 rows of W through LDS, 128 values of x at a step: what has to come
+// from memory per product is a fourth of what tiles of 128 x 128 read.
 struct ExpandShape {
     int64_t rows;        // of made keys and values per head
     int32_t key_tiles;   // tiles of 128 of all heads' key rows
     int32_t value_tiles;
-    int32_t each, groups;
+    int32_t each, ctiles;
     FastDiv key_div, value_div;  // rows of a head
 };
 
-template <class T>
-__global__ __launch_bounds__(256, 2) void k_expand(ExpandArgs e, ExpandShape z) {
-    constexpr int kM = 128, kPlane = kM * 128;
+// W's rows in LDS, as Planes, but read in another order: the operand of block 2 j + h
+// has in place 4 q + r row 32 j + 8 q + 4 h + r, so that a lane's results of two blocks
+// are 8 neighbours, and those of four lanes 64 bytes.
+struct WRows {
+    static constexpr int kPlane = 128 * 128;
+    static constexpr __device__ __forceinline__ int swap(int r) {
+        return ((r >> 1) & 1) | ((r >> 3) & 1) << 1 | ((r >> 4) & 1) << 2;
+    }
+    static __device__ __forceinline__ int base(int lane) {
+        const int r = 8 * ((lane & 15) >> 2) + (lane & 3);
+        return r * 128 + ((16 * (lane >> 4)) ^ (swap(r) << 4));
+    }
+    // block i of 8, step t of 4
+    static __device__ __forceinline__ u32x4 row(const char* lds, int base, int i, int t) {
+        const int r = 32 * (i >> 1) + 4 * (i & 1);  // (shares no bit with base's, nor with swap's)
+        return *reinterpret_cast<const u32x4*>(lds + (base ^ (64 * (t & 1))) + r * 128 +
+                                               (t >> 1) * kPlane);
+    }
+};
+
+template <class T, int NS>
+__global__ __launch_bounds__(512) void k_expand(ExpandArgs e, ExpandShape z) {
+    constexpr int NW = 8, kRows = 32 * NW, kSteps = NS / 4;
     const LatentArgs& a = e.a;
-    __shared__ __align__(16) char wrows0[kPlane];
-    __shared__ __align__(16) char wrows1[kPlane];
-    __shared__ __align__(16) char crows0[kPlane];
-    __shared__ __align__(16) char crows1[kPlane];
-    __shared__ const char* from_s[kM];
-    __shared__ int any_s;
+    __shared__ __align__(16) char w0[2 * WRows::kPlane];
+    __shared__ __align__(16) char w1[2 * WRows::kPlane];
     using G = Tile<T, 64, true>;
-    using Pl = Planes<kM>;
     const int tid = threadIdx.x, lane = lane_id();
     const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int64_t unit = xcd_block();
-    const int64_t ctile = unit / z.groups;
-    if (ctile * kM >= z.rows) return;
-    const int first = (int)(unit - ctile * z.groups) * z.each;
+    const int group = (int)(unit / z.ctiles);
+    const int first = group * z.each;
     const int count = min(z.each, z.key_tiles + z.value_tiles - first);
-    if (tid == 0) any_s = 0;
-    __syncthreads();
-    // the tokens' latent rows
-    if (tid < kM) {
-        const int64_t row = ctile * kM + tid;
-        const char* from = nullptr;
-        if (row < z.rows) {
-            int64_t s, key;
-            if (a.made_step) {
-                s = row / a.made_step;
-                key = row - s * a.made_step;
-            } else {
-                const int64_t entry = row / a.page_div.d;
-                s = upper_index(a.rowptr, int64_t(0), a.seqs, entry);
-                key = row - a.rowptr[s] * (int64_t)a.page_div.d;
-            }
-            const Sequence sq = read_sequence(a, s);
-            if (key >= 0 && key < sq.length && !sq.none) {
-                const uint32_t pg = a.page_div.div((uint32_t)key);
-                const uint32_t id = (uint32_t)a.col[sq.page0 + pg];
-                const uint32_t slot = (uint32_t)key - pg * a.page_div.d;
-                if (id < (uint64_t)a.npages) {
-                    from = a.k + ((uint64_t)(id * a.k_page + slot * a.k_slot) << a.k_shift);
-                    any_s = 1;
-                }
-            }
-        }
-        from_s[tid] = from;
-    }
-    __syncthreads();
-    if (!any_s) return;
-    // this lane's rows of W and c: of blocks of 8 rows 4 w + 0..3, row l / 8
-    const char* zero = reinterpret_cast<const char*>(g_zero);
-    const char *wsrc[4], *csrc[4];
-    int byte[4];
+    if (count <= 0) return;
+    // this lane's two tokens: their latent rows, null where there is none
+    const int64_t row0 = (unit - (int64_t)group * z.ctiles) * kRows + 32 * w;
+    const char* from[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = 8 * (4 * w + i) + (lane >> 3);
-        byte[i] = 16 * ((lane & 7) ^ Pl::swap(row));
-        csrc[i] = from_s[row];
+    for (int x = 0; x < 2; ++x) {
+        const int64_t row = row0 + 16 * x + (lane & 15);
+        from[x] = nullptr;
+        if (row >= z.rows) continue;
+        int64_t s, key;
+        if (a.made_step) {
+            s = row / a.made_step;
+            key = row - s * a.made_step;
+        } else {
+            const int64_t entry = row / a.page_div.d;
+            s = upper_index(a.rowptr, int64_t(0), a.seqs, entry);
+            key = row - a.rowptr[s] * (int64_t)a.page_div.d;
+        }
+        const Sequence sq = read_sequence(a, s);
+        if (key < 0 || key >= sq.length || sq.none) continue;
+        const uint32_t pg = a.page_div.div((uint32_t)key);
+        const uint32_t id = (uint32_t)a.col[sq.page0 + pg];
+        const uint32_t slot = (uint32_t)key - pg * a.page_div.d;
+        if (id < (uint64_t)a.npages)
+            from[x] = a.k + ((uint64_t)(id * a.k_page + slot * a.k_slot) << a.k_shift);
     }
-    // W's tile t of this work group: its rows' side, first row, rows of a head and of all
+    if (!__syncthreads_or(from[0] || from[1])) return;
+    const char* zero = reinterpret_cast<const char*>(g_zero);
+    u32x4 c[2][NS];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int t = 0; t < NS; ++t) {
+            const int at = 64 * t + 16 * (lane >> 4);
+            c[x][t] = *reinterpret_cast<const u32x4*>(
+                from[x] && at < 2 * e.latent_dim ? from[x] + at : zero);
+        }
+    // W's tile t of this work group: its side, first row, rows of a head and of all
     struct Side {
         bool keys;
         int m0, per, all;
@@ -1004,109 +1015,117 @@ __global__ __launch_bounds__(256, 2) void k_expand(ExpandArgs e, ExpandShape z) 
     const auto side = [&](int t) {
         Side x;
         x.keys = first + t < z.key_tiles;
-        x.m0 = kM * (x.keys ? first + t : first + t - z.key_tiles);
+        x.m0 = 128 * (x.keys ? first + t : first + t - z.key_tiles);
         x.per = x.keys ? a.made_dim : a.s.dim;
         x.all = a.s.hq * x.per;
         return x;
     };
+    const char* wsrc[2];  // this lane's rows of blocks of 8 rows 2 w and 2 w + 1
     const auto open = [&](int t) {
         const Side x = side(t);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = x.m0 + 8 * (4 * w + i) + (lane >> 3);
+        for (int i = 0; i < 2; ++i) {
+            const int r = 8 * (2 * w + i) + (lane >> 3), m = x.m0 + r;
             wsrc[i] = nullptr;
             if (m < x.all) {
                 const int head = (int)(x.keys ? z.key_div : z.value_div).div(m);
-                const AttnRows& r = x.keys ? e.wk : e.wv;
-                wsrc[i] = r.base + head * r.row + (m - head * x.per) * r.head;
+                const AttnRows& y = x.keys ? e.wk : e.wv;
+                wsrc[i] = y.base + head * y.row + (m - head * x.per) * y.head;
             }
         }
     };
-    const auto load = [&](char* wrows, char* crows, int x0) {
+    const auto load = [&](char* to, int step) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int at = 2 * x0 + byte[i];
-            const bool in = at < 2 * e.latent_dim;
-            load_to_lds(wsrc[i] && in ? wsrc[i] + at : zero, wrows + (4 * w + i) * 1024);
-            load_to_lds(csrc[i] && in ? csrc[i] + at : zero, crows + (4 * w + i) * 1024);
-        }
-    };
-    f32x4 acc[4][4];  // rows of W, tokens
-    const auto clear = [&] {
+        for (int i = 0; i < 2; ++i) {
+            const int r = 8 * (2 * w + i) + (lane >> 3);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-    };
-    const int wb = Pl::row_base(64 * (w >> 1), lane), cb = Pl::row_base(64 * (w & 1), lane);
-    const auto product = [&](const char* wrows, const char* crows) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            u32x4 x[4], y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = Pl::row(wrows, wb, 16 * i, t);
-                y[i] = Pl::row(crows, cb, 16 * i, t);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = mfma32<T>(x[i], y[j], acc[i][j]);
-        }
-    };
-    const auto store = [&](int t) {
-        const Side x = side(t);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = x.m0 + 64 * (w >> 1) + 16 * i + 4 * (lane >> 4);
-            if (m >= x.all) continue;
-            const int head = (int)(x.keys ? z.key_div : z.value_div).div(m);
-            char* to = (x.keys ? a.made_k : a.made_v) +
-                       ((int64_t)head * z.rows * 2 * x.per + m - head * x.per) * 2;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int at = 64 * (w & 1) + 16 * j + (lane & 15);
-                if (!from_s[at]) continue;
-                // rounded, and what that leaves (nothing where it is not finite)
-                f32x4 left;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float high = (float)(T)acc[i][j][c];
-                    left[c] = __builtin_isfinite(high) ? acc[i][j][c] - high : 0.f;
-                }
-                char* row = to + (ctile * kM + at) * 2 * x.per * 2;
-                G::store_four(acc[i][j], row);
-                G::store_four(left, row + 2 * x.per);
+            for (int g = 0; g < 2; ++g) {
+                const int at = 256 * step + 128 * g + 16 * ((lane & 7) ^ WRows::swap(r));
+                load_to_lds(wsrc[i] && at < 2 * e.latent_dim ? wsrc[i] + at : zero,
+                            to + g * WRows::kPlane + (2 * w + i) * 1024);
             }
         }
     };
-    // steps of 64 values of x, of tile after tile
-    const int steps = (e.latent_dim + 63) / 64;
-    int tile = 0, at = 0, ahead = 0;  // of the step that is computed; of the next one's load
-    clear();
-    open(0);
-    load(wrows0, crows0, 0);
-    wait_for_loads();
-    __syncthreads();
-    const auto take = [&](char* wrows, char* crows, char* wnext, char* cnext) {
-        if (++ahead == steps) {
-            ahead = 0;
-            if (tile + 1 < count) open(tile + 1);
+    f32x4 acc[8][2];  // blocks of 16 rows of W, of 16 tokens
+    const int wb = WRows::base(lane);
+    // tile t, whose step `at` is in `rows`; the next one is loaded into `next`
+    const auto take = [&](const char* rows, char* next, int t, auto at) {
+        constexpr int kAt = decltype(at)::value;
+        if constexpr (kAt == 0)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
+        if (kAt + 1 < kSteps) {
+            load(next, kAt + 1);
+        } else if (t + 1 < count) {
+            open(t + 1);
+            load(next, 0);
         }
-        if (at + 1 < steps || tile + 1 < count) load(wnext, cnext, 64 * ahead);
-        product(wrows, crows);
-        if (++at == steps) {
-            store(tile);
-            clear();
-            at = 0;
-            ++tile;
+        // operands are read kAhead before their products, as in k_absorbed
+        constexpr int kAhead = 4;
+        u32x4 y[kAhead + 1];
+#pragma unroll
+        for (int n = -kAhead; n < 32; ++n) {
+            __builtin_amdgcn_sched_barrier(0);
+            const int r = n + kAhead;
+            if (r < 32) y[r % (kAhead + 1)] = WRows::row(rows, wb, r % 8, r / 8);
+            if (n < 0) continue;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                acc[n % 8][x] = mfma32<T>(y[n % (kAhead + 1)], c[x][4 * kAt + n / 8], acc[n % 8][x]);
         }
+        __builtin_amdgcn_sched_barrier(0);
         wait_for_loads();
         __syncthreads();
+        if constexpr (kAt + 1 == kSteps) {  // (after the wait, which would be theirs too)
+            const Side d = side(t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // 8 neighbours of each token's row
+                const int m = d.m0 + 32 * j + 8 * (lane >> 4);
+                if (m >= d.all) continue;
+                const int head = (int)(d.keys ? z.key_div : z.value_div).div(m);
+                char* to = (d.keys ? a.made_k : a.made_v) +
+                           ((int64_t)head * z.rows * 2 * d.per + m - head * d.per) * 2;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (!from[x]) continue;
+                    char* row = to + (row0 + 16 * x + (lane & 15)) * 4 * d.per;
+                    // rounded, and what that leaves (nothing where it is not finite)
+                    uint32_t high[4], low[4];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const f32x4& y = acc[2 * j + h / 2][x];
+                        const float y0 = y[2 * (h & 1)], y1 = y[2 * (h & 1) + 1];
+                        high[h] = pack2<T>(y0, y1);
+                        float r0, r1;
+                        unpack2<T>(high[h], r0, r1);
+                        low[h] = pack2<T>(__builtin_isfinite(r0) ? y0 - r0 : 0.f,
+                                          __builtin_isfinite(r1) ? y1 - r1 : 0.f);
+                    }
+                    *reinterpret_cast<u32x4*>(row) = u32x4{high[0], high[1], high[2], high[3]};
+                    *reinterpret_cast<u32x4*>(row + 2 * d.per) = u32x4{low[0], low[1], low[2], low[3]};
+                }
+            }
+        }
     };
-    while (tile < count) {
-        take(wrows0, crows0, wrows1, crows1);
-        if (tile < count) take(wrows1, crows1, wrows0, crows0);
+    open(0);
+    load(w0, 0);
+    wait_for_loads();
+    __syncthreads();
+    using I0 = std::integral_constant<int, 0>;
+    if constexpr (kSteps == 1) {
+        for (int t = 0; t < count; t += 2) {
+            take(w0, w1, t, I0{});
+            if (t + 1 < count) take(w1, w0, t + 1, I0{});
+        }
+    } else {
+        for (int t = 0; t < count; ++t) {
+            take(w0, w1, t, I0{});
+            take(w1, w0, t, std::integral_constant<int, 1>{});
+            if constexpr (kSteps == 4) {
+                take(w0, w1, t, std::integral_constant<int, 2>{});
+                take(w1, w0, t, std::integral_constant<int, 3>{});
+            }
+        }
     }
 }
 
@@ -1187,15 +1206,19 @@ void latent_expand(const ExpandArgs& e, hipStream_t st) {
     z.value_tiles = (int32_t)ceil_div((int64_t)a.s.hq * a.s.dim, 128);
     z.key_div = FastDiv((uint32_t)a.made_dim);
     z.value_div = FastDiv((uint32_t)a.s.dim);
-    const int64_t ctiles = ceil_div(z.rows, 128), wtiles = z.key_tiles + z.value_tiles;
-    // two work groups per compute unit, replaced a few times over
-    z.each = (int32_t)std::min<int64_t>(std::max<int64_t>(ctiles * wtiles / 2048, 1), 16);
-    z.groups = (int32_t)ceil_div(wtiles, z.each);
-    const int64_t units = ctiles * z.groups;
-    if (units == 0) return;
+    const int64_t ctiles = ceil_div(z.rows, 256), wtiles = z.key_tiles + z.value_tiles;
+    if (ctiles == 0) return;
+    if (ctiles > INT32_MAX) throw OverflowError("rows of made keys");
+    // one work group per compute unit, replaced a few times over
+    z.each = (int32_t)std::min<int64_t>(std::max<int64_t>(ctiles * wtiles / 1024, 1), 16);
+    z.ctiles = (int32_t)ctiles;
+    const dim3 grid = grid_2d(xcd_grid(ctiles * ceil_div(wtiles, z.each)));
     with_latent_type(a.s.type, [&](auto* t) {
-        hipLaunchKernelGGL(k_expand<std::remove_pointer_t<decltype(t)>>, grid_2d(xcd_grid(units)),
-                           dim3(256), 0, st, e, z);
+        using T = std::remove_pointer_t<decltype(t)>;
+        const auto run = e.latent_dim <= 128   ? k_expand<T, 4>
+                         : e.latent_dim <= 256 ? k_expand<T, 8>
+                                               : k_expand<T, 16>;
+        hipLaunchKernelGGL(run, grid, dim3(512), 0, st, e, z);
     });
     SG_LAUNCH_CHECK();
 }
