@@ -143,9 +143,9 @@ __device__ __forceinline__ float weight_of(float s, float c, float ref, float sh
 // hold such keys those elements are made 0 in LDS, and at the end they are added
 // to the rows that see their keys, whose results are what the elements make of
 // them whatever the weights.
-template <int KEYS>
+template <int KEYS, int ROWS>
 struct Crossing {
-    static constexpr int kKeys = KEYS, kTiles = kPagedTileMost / KEYS + 2;
+    static constexpr int kKeys = KEYS, kTiles = ROWS / KEYS + 2;
     int from;  // the first such tile's first key
     __device__ __forceinline__ Crossing(const TileJob& j, int first_token)
         : from(j.k0 + max(j.before + first_token - j.k0, 0) / kKeys * kKeys) {}
@@ -244,7 +244,7 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
     constexpr int QB = G::QB, QS = G::QS, NB = G::NB, NW = G::NW, CG = G::CG, KS = G::KS, FB = G::FB;
     constexpr int kKeys = G::kKeys;
     using Pl = Planes<kKeys>;
-    using Cr = Crossing<kKeys>;
+    using Cr = Crossing<kKeys, G::BM>;
     __shared__ __align__(16) char tile0[G::kPlanes * Pl::kPlane];
     __shared__ __align__(16) char tile1[G::kPlanes * Pl::kPlane];
     __shared__ __align__(16) char slots[NW * G::kSlot];
@@ -679,20 +679,19 @@ __global__ __launch_bounds__(kWaves* kWave) void k_latent_join(PagedArgs a, int3
 // a key's error would be that of the scores, and so of the log-sum-exp, and a
 // value's as large as the result's own rounding. The keys' last part, of up to
 // 64 elements, is the latent row's. A wavefront takes QB blocks of 16 rows.
-template <class T, int MP_, int VP_>
+template <class T, int MP_, int VP_, int NW_>
 struct ExpandedGeo : Tile<T, 64, true> {
-    static constexpr int kKeys = 32;
-    static constexpr int MP = MP_, VP = VP_, QS = 2 * MP + 2, NB = 4 * VP, QB = 2, NW = 4;
-    static constexpr int BM = NW * 16 * QB;
+    static constexpr int NW = NW_, QB = 2, BM = NW * 16 * QB, kKeys = 8 * NW;
+    static constexpr int MP = MP_, VP = VP_, QS = 2 * MP + 2, NB = 4 * VP;
     static constexpr int kLow = MP, kRope = 2 * MP, kValues = kRope + 1, kPlanes = kValues + 2 * VP;
-    static_assert(BM <= kPagedTileMost && kKeys == 8 * NW, "tile shape");
+    static_assert(kKeys % 32 == 0, "tile shape");
 };
 
 template <class G, class T>
 __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int32_t tiles) {
     constexpr int QB = G::QB, QS = G::QS, NB = G::NB, NW = G::NW, kKeys = G::kKeys;
     using Pl = Planes<kKeys>;
-    using Cr = Crossing<kKeys>;
+    using Cr = Crossing<kKeys, G::BM>;
     __shared__ __align__(16) char tile0[G::kPlanes * Pl::kPlane];
     __shared__ __align__(16) char tile1[G::kPlanes * Pl::kPlane];
     __shared__ int wrong_s;
@@ -754,38 +753,40 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
     // the sequence's first row of made keys and values
     const int64_t made0 = h * a.made_rows +
                           (a.made_step ? s * a.made_step : job.sq.page0 * (int64_t)a.page_div.d);
+    const char* made_k = a.made_k + made0 * 2 * made;
     const char* made_v = a.made_v + made0 * 2 * values;
     TileRows<Pl, 1> from;
-    const int byte = from.byte(lane, w), trow = from.row(lane, w);
-    // of this lane's row of the next tile
-    const char* ksrc = a.made_k + (made0 + job.k0 + trow) * 2 * made + byte;
-    const char* vsrc = made_v + (int64_t)(job.k0 + trow) * 2 * values + byte;
+    const uint32_t byte = from.byte(lane, w), trow = from.row(lane, w);
+    // what this lane loads of plane g of a tile: its row's sources
     const char* zero = reinterpret_cast<const char*>(g_zero);
-    const auto load_tile = [&](char* dst, int t0) {
-        const char* latent = from.latent(a, t0 + trow, job.k1, 0);
-        const bool in = t0 + trow < job.k1;
-        char* to = dst + w * 1024;
-#pragma unroll
-        for (int g = 0; g < G::MP; ++g) {
-            const bool has = in && 128 * g + byte < made;
-            load_to_lds(has ? ksrc + 128 * g : zero, to + g * Pl::kPlane);
-            load_to_lds(has ? ksrc + made + 128 * g : zero, to + (G::kLow + g) * Pl::kPlane);
+    const char *ksrc = zero, *vsrc = zero, *rsrc = zero;
+    bool in = false;
+    const auto open_tile = [&](int t0) {
+        const int64_t key = t0 + (int)trow;
+        in = key < job.k1;
+        ksrc = made_k + key * 2 * made + byte;
+        vsrc = made_v + key * 2 * values + byte;
+        rsrc = from.latent(a, (int)key, job.k1, 0) + a.rope_at + byte;
+    };
+    const auto load_plane = [&](char* dst, int g) {
+        char* to = dst + g * Pl::kPlane + w * 1024;
+        if (g < G::kRope) {
+            const bool low = g >= G::MP;
+            const int at = 128 * (low ? g - G::MP : g);
+            load_to_lds(in && at + (int)byte < made ? ksrc + (low ? made : 0) + at : zero, to);
+        } else if (g == G::kRope) {
+            load_to_lds(in && made + (int)byte < 2 * a.key_dim ? rsrc : zero, to);
+        } else {
+            const bool low = g >= G::kValues + G::VP;
+            const int at = 128 * (low ? g - G::kValues - G::VP : g - G::kValues);
+            load_to_lds(in && at + (int)byte < values ? vsrc + (low ? values : 0) + at : zero, to);
         }
-        load_to_lds(in && made + byte < 2 * a.key_dim ? latent + a.rope_at + byte : zero,
-                    to + G::kRope * Pl::kPlane);
-#pragma unroll
-        for (int g = 0; g < G::VP; ++g) {
-            const bool has = in && 128 * g + byte < values;
-            load_to_lds(has ? vsrc + 128 * g : zero, to + (G::kValues + g) * Pl::kPlane);
-            load_to_lds(has ? vsrc + values + 128 * g : zero,
-                        to + (G::kValues + G::VP + g) * Pl::kPlane);
-        }
-        ksrc += (int64_t)kKeys * 2 * made;
-        vsrc += (int64_t)kKeys * 2 * values;
     };
     from.look_up(a, pages, lane, w, job.k0, job.k1);
     __syncthreads();  // the flags
-    load_tile(tile0, job.k0);
+    open_tile(job.k0);
+#pragma unroll
+    for (int g = 0; g < G::kPlanes; ++g) load_plane(tile0, g);
     from.look_up(a, pages, lane, w, job.k0 + kKeys, job.k1);
     wait_for_loads();
     __syncthreads();
@@ -794,16 +795,28 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
     // One tile of keys, staged in `rows`; the next one is loaded into `next`.
     const auto take = [&](char* rows, char* next, int t0) {
         char* vals = rows + G::kValues * Pl::kPlane;
-        if (t0 + kKeys < job.k1) {
-            load_tile(next, t0 + kKeys);
-            from.look_up(a, pages, lane, w, t0 + 2 * kKeys, job.k1);
-        }
+        // (past the end it loads zeros)
+        open_tile(t0 + kKeys);
+        from.look_up(a, pages, lane, w, t0 + 2 * kKeys, job.k1);
         if (min(t0 + kKeys, job.k1) > job.before + job.first) {
             const bool any = Cr::template clear<G, NW * kWave>(vals, G::VP);
             wild |= (uint32_t)any << ((t0 - cross.from) / kKeys);
             __syncthreads();
         }
-        if (t0 < mine) {
+        // 32 keys, from staged row `at` on; the next tile is asked for during the first
+        // step's products: the scores', and of several steps the results' too
+        const auto step_of = [&](int at, auto loads) {
+            constexpr bool kLoads = decltype(loads)::value;
+            constexpr int kFirst = kKeys > 32 ? (G::kPlanes + 1) / 2 : G::kPlanes;
+            const int t = t0 + at;
+            if (t >= mine) {
+                if (kLoads)
+#pragma unroll
+                    for (int g = 0; g < G::kPlanes; ++g) load_plane(next, g);
+                return;
+            }
+            const char* krows = rows + at * 128;
+            const char* vrows = vals + at * 128;
             f32x4 sc[QB][2];
 #pragma unroll
             for (int x = 0; x < QB; ++x) sc[x][0] = sc[x][1] = f32x4{0, 0, 0, 0};
@@ -817,7 +830,7 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
             const auto read = [&](int i) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
-                    k[i % (kAhead + 1)][b] = Pl::row(rows, rb, 16 * b, step(i));
+                    k[i % (kAhead + 1)][b] = Pl::row(krows, rb, 16 * b, step(i));
             };
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) read(i);
@@ -825,20 +838,24 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
             for (int i = 0; i < kSteps; ++i) {
                 __builtin_amdgcn_sched_barrier(0);
                 if (i + kAhead < kSteps) read(i + kAhead);
-                const int t = step(i) < 2 * G::MP ? step(i) : step(i) - 2 * G::MP;
+                if (kLoads)
+#pragma unroll
+                    for (int g = 0; g < kFirst; ++g)
+                        if (g * kSteps / kFirst == i) load_plane(next, g);
+                const int part = step(i) < 2 * G::MP ? step(i) : step(i) - 2 * G::MP;
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int x = 0; x < QB; ++x)
-                        sc[x][b] = mfma32<T>(k[i % (kAhead + 1)][b], q[x][t], sc[x][b]);
+                        sc[x][b] = mfma32<T>(k[i % (kAhead + 1)][b], q[x][part], sc[x][b]);
             }
             __builtin_amdgcn_sched_barrier(0);
             bool raise = false;
             float top[QB];
 #pragma unroll
             for (int x = 0; x < QB; ++x) {
-                if (t0 + kKeys > full)  // some row does not see some key
-                    Softmax<G, T>::hide(sc[x], Seen::first(min(job.k1, job.before + r[x].t) - t0));
+                if (t + 32 > full)  // some row does not see some key
+                    Softmax<G, T>::hide(sc[x], Seen::first(min(job.k1, job.before + r[x].t) - t));
                 top[x] = sc[x][0][0];
 #pragma unroll
                 for (int j = 1; j < 8; ++j) top[x] = fmaxf(top[x], sc[x][j >> 2][j & 3]);
@@ -868,14 +885,21 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const u32x4 low = Pl::value(vals + G::VP * Pl::kPlane, vb, b);
-                const u32x4 high = Pl::value(vals, vb, b);
+                const u32x4 low = Pl::value(vrows + G::VP * Pl::kPlane, vb, b);
+                const u32x4 high = Pl::value(vrows, vb, b);
+                if (kLoads)
+#pragma unroll
+                    for (int g = kFirst; g < G::kPlanes; ++g)
+                        if ((g - kFirst) * NB / (G::kPlanes - kFirst + 1) == b) load_plane(next, g);
 #pragma unroll
                 for (int x = 0; x < QB; ++x) o[x][b] = G::add_block(low, pr[x], o[x][b]);
 #pragma unroll
                 for (int x = 0; x < QB; ++x) o[x][b] = G::add_block(high, pr[x], o[x][b]);
             }
-        }
+        };
+        step_of(0, std::true_type{});
+#pragma unroll 1
+        for (int at = 32; at < kKeys; at += 32) step_of(at, std::false_type{});
         wait_for_loads();
         __syncthreads();  // the next tile is there, this one's readers are done
     };
@@ -1155,8 +1179,13 @@ template <class F>
 void with_expanded(const LatentArgs& a, F&& f) {
     with_latent_type(a.s.type, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;
-        if (a.s.dim <= 64 && a.made_dim <= 64) f((ExpandedGeo<T, 1, 1>*)nullptr, t);
-        else f((ExpandedGeo<T, 2, 2>*)nullptr, t);
+        const auto width = [&](auto planes) {
+            constexpr int P = decltype(planes)::value;
+            if (a.max_new >= 256) f((ExpandedGeo<T, P, P, 8>*)nullptr, t);
+            else f((ExpandedGeo<T, P, P, 4>*)nullptr, t);
+        };
+        if (a.s.dim <= 64 && a.made_dim <= 64) width(Int<1>{});
+        else width(Int<2>{});
     });
 }
 
@@ -1209,8 +1238,18 @@ void latent_expand(const ExpandArgs& e, hipStream_t st) {
     const int64_t ctiles = ceil_div(z.rows, 256), wtiles = z.key_tiles + z.value_tiles;
     if (ctiles == 0) return;
     if (ctiles > INT32_MAX) throw OverflowError("rows of made keys");
-    // one work group per compute unit, replaced a few times over
-    z.each = (int32_t)std::min<int64_t>(std::max<int64_t>(ctiles * wtiles / 1024, 1), 16);
+    // One work group per compute unit is there at once; looking its tokens up and
+    // reading them takes as long as 1.2 tiles (26 of 23 thousand cycles). 22.9 K
+    // tokens, 64 tiles of W: 5 tiles each 340 us, 8 each 300.
+    int64_t best = INT64_MAX;
+    for (int each = 1; each <= std::min<int64_t>(wtiles, 64); ++each) {
+        const int64_t rounds = ceil_div(ctiles * ceil_div(wtiles, each), 256);
+        const int64_t cost = rounds * (5 * each + 6);
+        if (cost < best) {
+            best = cost;
+            z.each = each;
+        }
+    }
     z.ctiles = (int32_t)ctiles;
     const dim3 grid = grid_2d(xcd_grid(ctiles * ceil_div(wtiles, z.each)));
     with_latent_type(a.s.type, [&](auto* t) {

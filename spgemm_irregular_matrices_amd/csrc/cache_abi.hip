@@ -200,7 +200,7 @@ void latent_shape(const spgemm_latent_desc* d, const spgemm_paged_batch* b, bool
         }
     } else {
         // two work groups per compute unit are there at once; the texts differ
-        cut_pieces(a, tile, 3072, 1024, 64);
+        cut_pieces(a, tile, tile == 256 ? 1536 : 3072, 1024, 64);
     }
 }
 
