@@ -2,6 +2,7 @@
 // (absorbed) or over keys and values that were made from them (expanded).
 #include <algorithm>
 
+#include "attention_join.h"
 #include "latent.h"
 
 namespace sg {
@@ -619,60 +620,6 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
     }
 }
 
-// One wavefront per token and query head joins its pieces, in their order.
-constexpr int kWaves = 4;
-template <class T>
-__global__ __launch_bounds__(kWaves* kWave) void k_latent_join(PagedArgs a, int32_t tiles, int32_t tile_rows,
-                                                               int32_t keys) {
-    const int64_t unit = grid_block() * kWaves + threadIdx.x / kWave;
-    if (unit >= a.tokens * a.s.hq) return;
-    const int64_t token = unit / a.s.hq;
-    const int hq = (int)(unit - token * a.s.hq);
-    if (token < a.q_rowptr[0]) return;
-    const int64_t s = upper_index(a.q_rowptr, int64_t(0), a.seqs, token);
-    const Sequence sq = read_sequence(a, s);
-    if (sq.none || sq.bad || token < sq.q0 || token - sq.q0 >= sq.fresh) return;
-    const int sees = sq.length - sq.fresh + 1 + (int)(token - sq.q0);
-    int count;
-    int64_t first, step, late = 0;  // in rows of parts
-    if (a.ranges) {
-        const EvenParts parts(EvenSplit(a, keys), __builtin_amdgcn_readfirstlane((int)s), keys, sees);
-        const int row = (int)(token - sq.q0) * a.s.hq + hq, tile = row / tile_rows;
-        count = parts.count;
-        step = (int64_t)2 * tiles * tile_rows;
-        first = ((int64_t)2 * parts.range * tiles + tile) * tile_rows + row - tile * tile_rows;
-        late = parts.late ? (int64_t)tiles * tile_rows : 0;
-    } else {
-        count = sees <= a.piece ? 0 : (sees + a.piece - 1) / a.piece;
-        step = a.tokens * a.s.hq;
-        first = unit;
-    }
-    if (count == 0) return;
-    // the rows of parts that lane i, i + 64, ... looks at
-    const auto at = [&](int i) { return first + i * step + (i == 0 ? late : 0); };
-    float m = -INFINITY, l = 0.f;
-    for (int i = lane_id(); i < count; i += kWave) m = fmaxf(m, a.part_ml[2 * at(i)]);
-#pragma unroll
-    for (int d = kWave / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, kWave));
-    m = m == -INFINITY ? 0.f : m;
-    for (int i = lane_id(); i < count; i += kWave)
-        l += a.part_ml[2 * at(i) + 1] * fast_exp2(a.part_ml[2 * at(i)] - m);
-    l = wave_reduce_sum(l);
-    const float f = l == 0.f ? 0.f : 1.f / l;
-    char* row = a.out.base + token * a.out.row + hq * a.out.head;
-    for (int d = 4 * lane_id(); d < a.s.dim; d += 4 * kWave) {
-        f32x4 x{0, 0, 0, 0};
-#pragma unroll 4
-        for (int i = 0; i < count; ++i)
-            x += *reinterpret_cast<const f32x4*>(a.part + at(i) * a.s.dim + d) *
-                 fast_exp2(a.part_ml[2 * at(i)] - m);
-        x *= f;
-        *reinterpret_cast<u32x2*>(row + 2 * d) = u32x2{pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3])};
-    }
-    if (a.lse && lane_id() == 0)
-        a.lse[unit] = l == 0.f ? -INFINITY : (m - kShift<T> + fast_log2(l)) * kLn2;
-}
-
 // ---------------------------------------------------------------- expanded
 // Keys and values of one head that k_expand made, of up to 64 MP and 64 VP
 // elements, each as two numbers of the type that add up to it: rounded to one,
@@ -1220,11 +1167,9 @@ void latent_attention(const LatentArgs& a, bool absorbed, hipStream_t st) {
     SG_LAUNCH_CHECK();
     if (a.npieces == 1 && a.ranges == 0) return;
     with_latent_type(a.s.type, [&](auto* t) {
-        hipLaunchKernelGGL(k_latent_join<std::remove_pointer_t<decltype(t)>>,
-                           grid_2d(ceil_div(a.tokens * a.s.hq, kWaves)), dim3(kWaves * kWave), 0, st, a,
-                           tiles, rows, kAbsorbedKeys);
+        using T = std::remove_pointer_t<decltype(t)>;
+        join_parts<T>(a, tiles, rows, kAbsorbedKeys, kShift<T>, st);
     });
-    SG_LAUNCH_CHECK();
 }
 
 void latent_expand(const ExpandArgs& e, hipStream_t st) {

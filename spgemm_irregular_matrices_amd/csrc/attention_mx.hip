@@ -3,6 +3,7 @@
 // as NP bfloat16 parts that add up to it (8, 11 and 24 bits: 1, 2 and 3 parts),
 // and so do the probabilities, with 8, 16 or 24 bits. Single precision runs at a
 // third of the bfloat16 rate that way, five times its own.
+#include "attention_join.h"
 #include "mx.h"
 
 namespace sg {
@@ -189,19 +190,47 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_mx(Mx
                                                                               int32_t tiles) {
     using R = MxRuns<BITS, G::kDim>;
     constexpr int NP = G::NP, KT = G::KT;
+    static_assert(KT == kMxKeys, "the host cuts keys by whole tiles");
     __shared__ __align__(16) char stage[kWaves][KT * G::kRowBytes];
     const int lane = lane_id();
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     char* vrows = stage[w];
     int64_t unit = xcd_block() * kWaves + w;
-    if (unit >= a.seqs * a.s.hkv * a.npieces * tiles) return;
+    if (unit >= (a.ranges ? a.ranges : a.seqs * a.npieces) * a.s.hkv * tiles) return;
     const int tile = (int)(unit % tiles);
     unit /= tiles;
-    const int piece = (int)(unit % a.npieces);
-    unit /= a.npieces;
-    const int64_t s = unit % a.seqs;
-    const int h = (int)(unit / a.seqs);
-    const TileJob job = tile_job(a, s, tile, 16, piece);
+    int range = 0, piece = 0, s = 0, h;
+    int pos = 0, end = 0, before = 0;  // tiles of all sequences' keys, of a range
+    if (a.ranges) {
+        range = (int)(unit % a.ranges);
+        h = (int)(unit / a.ranges);
+        const EvenSplit e(a, KT);
+        pos = (int)min((int64_t)range * e.per, (int64_t)e.total);
+        end = min(pos + e.per, e.total);
+        if (pos >= end) return;
+        e.locate(pos, s, before);
+    } else {
+        piece = (int)(unit % a.npieces);
+        unit /= a.npieces;
+        s = (int)(unit % a.seqs);
+        h = (int)(unit / a.seqs);
+    }
+    const int begin = pos;
+#pragma unroll 1
+    for (;; ++s) {  // segments
+    TileJob job = tile_job(a, s, tile, 16, piece);
+    const bool late = pos > begin;
+    bool split = false;
+    if (a.ranges) {
+        const int own = job.sq.none ? 0 : job.sq.bad ? 1 : (job.sq.length + KT - 1) / KT;
+        split = pos > before || before + own > end;
+        const int last = job.before + (min(job.first + 16, job.rows) - 1) / a.s.group;
+        job.k0 = (pos - before) * KT;
+        job.k1 = min(last, (int)min((int64_t)(end - before) * KT, (int64_t)INT32_MAX));
+        before += own;
+        pos = before;
+    }
+    const auto segment = [&] {
     if (job.idle) return;
     const int n = lane & 15;
     const TileRow r = tile_row(a, job, job.first + n, h);
@@ -369,7 +398,16 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_mx(Mx
     }
     sm.finish(a.s.mag);
     if (__any(wrong)) sm.l = NAN;
-    store_row<G, T>(a, job, r, piece, o, sm);
+    if (!a.ranges)
+        store_row<G, T>(a, job, r, piece, o, sm);
+    else if (r.has && job.before + r.t > job.k0)
+        store_row_at<G, T>(
+            a, r, !split,
+            ((((int64_t)2 * range + late) * a.s.hkv + h) * tiles + tile) * 16 + n, o, sm);
+    };
+    segment();
+    if (pos >= end) return;
+    }
 }
 
 // Many rows: a work group of 4 wavefronts takes 4 * 16 * QB rows, a wavefront
@@ -690,7 +728,7 @@ void mx_attention(const MxArgs& a, hipStream_t st) {
     const int64_t rows = (int64_t)a.max_new * a.s.group;
     const int64_t tiles = ceil_div(rows, mx_tile_rows(a.s, a.format, rows));
     if (a.seqs == 0 || a.tokens == 0 || tiles == 0) return;
-    const int64_t units = a.seqs * a.s.hkv * a.npieces * tiles;
+    const int64_t units = (a.ranges ? a.ranges : a.seqs * a.npieces) * a.s.hkv * tiles;
     with_mx(a.s, a.format, [&](auto* geo, auto* t, auto bits) {
         using G = std::remove_pointer_t<decltype(geo)>;
         using T = std::remove_pointer_t<decltype(t)>;
@@ -705,8 +743,11 @@ void mx_attention(const MxArgs& a, hipStream_t st) {
                                dim3(kWaves * kWave), 0, st, a, (int32_t)tiles);
         }
         SG_LAUNCH_CHECK();
+        if (a.ranges)
+            join_parts<T>(a, (int32_t)tiles, 16, G::KT, kProbShift<T>, st);
+        else if (a.npieces > 1)
+            paged_join(a, st);
     });
-    if (a.npieces > 1) paged_join(a, st);
 }
 
 }  // namespace sg

@@ -110,24 +110,29 @@ __device__ __forceinline__ void store_values(const typename G::AccB& o, float f,
             G::store_four(o.o[b] * f, at + d * (int)sizeof(T));
     }
 }
+// at: where it goes as a part
 template <class G, class T, class A>
-__device__ __forceinline__ void store_row(const PagedArgs& a, const TileJob& j, const TileRow& r,
-                                          int piece, const A& o, const Softmax<G, T>& sm) {
-    const int sees = j.before + r.t;
-    if (!r.has || sees <= j.k0) return;
-    const int64_t line = r.token * a.s.hq + r.hq;
-    if (sees <= a.piece) {
+__device__ __forceinline__ void store_row_at(const PagedArgs& a, const TileRow& r, bool whole,
+                                             int64_t at, const A& o, const Softmax<G, T>& sm) {
+    if (whole) {
         store_values<G, T>(o, sm.factor(), false,
                            a.out.base + r.token * a.out.row + r.hq * a.out.head, a.s.dim);
-        if (a.lse && lane_id() < 16) a.lse[line] = sm.lse();
+        if (a.lse && lane_id() < 16) a.lse[r.token * a.s.hq + r.hq] = sm.lse();
     } else {
-        const int64_t at = (int64_t)piece * a.tokens * a.s.hq + line;
         store_values<G, T>(o, 1.f, true, reinterpret_cast<char*>(a.part + at * a.s.dim), a.s.dim);
         if (lane_id() < 16) {
             a.part_ml[2 * at] = sm.m;
             a.part_ml[2 * at + 1] = sm.l;
         }
     }
+}
+template <class G, class T, class A>
+__device__ __forceinline__ void store_row(const PagedArgs& a, const TileJob& j, const TileRow& r,
+                                          int piece, const A& o, const Softmax<G, T>& sm) {
+    const int sees = j.before + r.t;
+    if (!r.has || sees <= j.k0) return;
+    store_row_at<G, T>(a, r, sees <= a.piece,
+                       (int64_t)piece * a.tokens * a.s.hq + r.token * a.s.hq + r.hq, o, sm);
 }
 
 // A batch's tiles of `keys` keys, one sequence after another, cut into ranges of

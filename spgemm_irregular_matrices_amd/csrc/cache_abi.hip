@@ -154,7 +154,18 @@ void mx_pieces(PagedArgs* a, int format) {
         const bool ragged = rows > tile && a->tokens * 4 < a->seqs * a->max_new * 3;
         cut_pieces(a, tile, each * (ragged ? 512 : 256), 256, 64);
     } else {
-        cut_pieces(a, tile, each * 1024, 64, 32);
+        const int64_t tiles = std::max<int64_t>(ceil_div(rows, tile), 1);
+        const int64_t most = a->seqs * ceil_div(a->max_length, kMxKeys);
+        if (a->seqs <= kEvenSeqs && a->seqs * a->s.hkv * tiles < each * 2048 && most > a->seqs &&
+            most < INT32_MAX / 2) {
+            // all keys cut evenly for the wavefronts that are there at once
+            a->piece = std::max(a->max_length, 1);
+            a->least = 2;
+            a->ranges = (int32_t)std::max<int64_t>(
+                std::min(ceil_div(most, a->least), each * 1024 / (a->s.hkv * tiles)), 1);
+        } else {
+            cut_pieces(a, tile, each * 1024, 64, 32);
+        }
     }
 }
 
@@ -305,7 +316,7 @@ SPGEMM_API int spgemm_mx_attention_workspace(const spgemm_attention_desc* desc,
         MxArgs a;
         batch_shape(batch, make_shape(desc), &a);
         mx_pieces(&a, 0);
-        *bytes = carve_parts(nullptr, &a);
+        *bytes = carve_parts(nullptr, &a, mx_tile_rows(a.s, 0, (int64_t)a.max_new * a.s.group), a.s.hkv);
         return SPGEMM_OK;
     });
 }
@@ -330,7 +341,8 @@ SPGEMM_API int spgemm_mx_attention(const spgemm_attention_desc* desc, const spge
         rc = mx_cache(cache, a.s, &a);
         if (rc != SPGEMM_OK) return rc;
         a.lse = lse;
-        if (!workspace_valid(workspace, workspace_bytes, carve_parts(workspace, &a)))
+        const int tile = mx_tile_rows(a.s, 0, (int64_t)a.max_new * a.s.group);
+        if (!workspace_valid(workspace, workspace_bytes, carve_parts(workspace, &a, tile, a.s.hkv)))
             return SPGEMM_ERR_INVALID_ARG;
         mx_attention(a, (hipStream_t)stream);
         return SPGEMM_OK;
