@@ -181,13 +181,16 @@ __device__ __forceinline__ f32x4 add_codes(const char* codes, const uint8_t* sca
     return o;
 }
 
+// Work groups of k_mx that a compute unit holds at once.
+template <int DP>
+constexpr int kMxResident = DP <= 64 ? 3 : DP <= 128 ? 2 : 1;
+
 // Few rows per sequence and key head: one wavefront takes 16 rows and one
 // piece of the keys, straight from memory. Codes of a tile of 32 keys are
 // turned into operands in registers (keys) and into rows in LDS (values, read
 // back transposed), and the next tile's are under way from then on.
 template <int BITS, class G, class T>
-__global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_mx(MxArgs a,
-                                                                              int32_t tiles) {
+__global__ __launch_bounds__(kWaves* kWave, kMxResident<G::kDim>) void k_mx(MxArgs a, int32_t tiles) {
     using R = MxRuns<BITS, G::kDim>;
     constexpr int NP = G::NP, KT = G::KT;
     static_assert(KT == kMxKeys, "the host cuts keys by whole tiles");
@@ -201,9 +204,12 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_mx(Mx
     unit /= tiles;
     int range = 0, piece = 0, s = 0, h;
     int pos = 0, end = 0, before = 0;  // tiles of all sequences' keys, of a range
+    // The heads of the same keys run side by side: a line of the cache's codes or
+    // scales often holds several heads' and is then read once per chiplet.
+    h = (int)(unit % a.s.hkv);
+    unit /= a.s.hkv;
     if (a.ranges) {
-        range = (int)(unit % a.ranges);
-        h = (int)(unit / a.ranges);
+        range = (int)unit;
         const EvenSplit e(a, KT);
         pos = (int)min((int64_t)range * e.per, (int64_t)e.total);
         end = min(pos + e.per, e.total);
@@ -211,202 +217,202 @@ __global__ __launch_bounds__(kWaves* kWave, G::kDim <= 128 ? 2 : 1) void k_mx(Mx
         e.locate(pos, s, before);
     } else {
         piece = (int)(unit % a.npieces);
-        unit /= a.npieces;
-        s = (int)(unit % a.seqs);
-        h = (int)(unit / a.seqs);
+        s = (int)(unit / a.npieces);
     }
     const int begin = pos;
 #pragma unroll 1
     for (;; ++s) {  // segments
-    TileJob job = tile_job(a, s, tile, 16, piece);
-    const bool late = pos > begin;
-    bool split = false;
-    if (a.ranges) {
-        const int own = job.sq.none ? 0 : job.sq.bad ? 1 : (job.sq.length + KT - 1) / KT;
-        split = pos > before || before + own > end;
-        const int last = job.before + (min(job.first + 16, job.rows) - 1) / a.s.group;
-        job.k0 = (pos - before) * KT;
-        job.k1 = min(last, (int)min((int64_t)(end - before) * KT, (int64_t)INT32_MAX));
-        before += own;
-        pos = before;
-    }
-    const auto segment = [&] {
-    if (job.idle) return;
-    const int n = lane & 15;
-    const TileRow r = tile_row(a, job, job.first + n, h);
-    if (job.sq.bad) {
-        if (piece == 0) store_nan<T>(a, r);
-        return;
-    }
-    if (job.k0 >= job.k1) return;
-    const int lo = __builtin_amdgcn_readfirstlane(r.t);
-
-    typename G::RowFrag q[NP];
-#pragma unroll
-    for (int p = 0; p < NP; ++p) G::zero_row(q[p]);
-    if (r.has) {
-        const char* row = a.q.base + r.token * a.q.row + r.hq * a.q.head;
-#pragma unroll
-        for (int t = 0; t < R::kLoads; ++t)
-#pragma unroll
-            for (int u = 0; u < R::kSteps; ++u)
-                G::load_query(row, R::first(t) + 8 * u, a.s.dim, t * R::kSteps + u, q);
-    }
-#pragma unroll
-    for (int p = 0; p < NP; ++p) G::sign_row(q[p], a.s.c);
-    const char* kb = a.k + h * a.k_head;
-    const char* vb = a.v + h * a.v_head;
-    const uint8_t* ksb = a.ks + h * a.ks_head;
-    const uint8_t* vsb = a.vs + h * a.vs_head;
-    const int32_t* pages = a.col + job.sq.page0;
-    bool wrong = false;  // a page outside the cache
-    struct Place {
-        uint32_t id[2], slot[2];  // of this lane's two keys
-    };
-    // keys past the piece's end repeat its last one
-    const auto place = [&](int t0) {
-        Place x;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t key = (uint32_t)min(t0 + 16 * j + n, job.k1 - 1);
-            const uint32_t pg = a.page_div.div(key);
-            x.id[j] = (uint32_t)pages[pg];
-            x.slot[j] = key - pg * a.page_div.d;
+        TileJob job = tile_job(a, s, tile, 16, piece);
+        const bool late = pos > begin;
+        bool split = false;
+        if (a.ranges) {
+            const int own = job.sq.none ? 0 : job.sq.bad ? 1 : (job.sq.length + KT - 1) / KT;
+            split = pos > before || before + own > end;
+            const int last = job.before + (min(job.first + 16, job.rows) - 1) / a.s.group;
+            job.k0 = (pos - before) * KT;
+            job.k1 = min(last, (int)min((int64_t)(end - before) * KT, (int64_t)INT32_MAX));
+            before += own;
+            pos = before;
         }
-        return x;
-    };
-    const auto checked = [&](Place& x) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (x.id[j] >= (uint64_t)a.npages) {
-                wrong = true;
-                x.id[j] = 0;
+        const auto segment = [&] {
+            if (job.idle) return;
+            const int n = lane & 15;
+            const TileRow r = tile_row(a, job, job.first + n, h);
+            if (job.sq.bad) {
+                if (piece == 0) store_nan<T>(a, r);
+                return;
             }
-    };
-    typename R::Codes k[2], v[2];
-    const auto load = [&](const Place& x) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            R::template load<G::kFull>(
-                kb + ((uint64_t)(x.id[j] * a.k_page + x.slot[j] * a.k_slot) << a.k_shift),
-                ksb + ((uint64_t)(x.id[j] * a.ks_page + x.slot[j] * a.ks_slot) << a.ks_shift),
-                a.s.dim, k[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            R::template load<G::kFull>(
-                vb + ((uint64_t)(x.id[j] * a.v_page + x.slot[j] * a.v_slot) << a.v_shift),
-                vsb + ((uint64_t)(x.id[j] * a.vs_page + x.slot[j] * a.vs_slot) << a.vs_shift),
-                a.s.dim, v[j]);
-        }
-    };
-    Place now = place(job.k0), next = now;
-    if (job.k0 + KT < job.k1) next = place(job.k0 + KT);
-    checked(now);
-    load(now);
+            if (job.k0 >= job.k1) return;
+            const int lo = __builtin_amdgcn_readfirstlane(r.t);
 
-    typename G::AccB o;
+            typename G::RowFrag q[NP];
 #pragma unroll
-    for (int b = 0; b < G::NB; ++b) o.o[b] = f32x4{0, 0, 0, 0};
-    Softmax<G, T> sm;
-    const int vbase = G::value_base(0);
-    for (int t0 = job.k0; t0 < job.k1; t0 += KT) {
-        const int left = job.k1 - t0;
-        const bool more = left > KT;
-        f32x4 sc[1][G::KSUB];
+            for (int p = 0; p < NP; ++p) G::zero_row(q[p]);
+            if (r.has) {
+                const char* row = a.q.base + r.token * a.q.row + r.hq * a.q.head;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            f32x4 x{0, 0, 0, 0};
+                for (int t = 0; t < R::kLoads; ++t)
 #pragma unroll
-            for (int t = 0; t < R::kLoads; ++t)
+                    for (int u = 0; u < R::kSteps; ++u)
+                        G::load_query(row, R::first(t) + 8 * u, a.s.dim, t * R::kSteps + u, q);
+            }
 #pragma unroll
-                for (int u = 0; u < R::kSteps; ++u) {
-                    const u32x4 y = R::decode(k[j], t, u);
+            for (int p = 0; p < NP; ++p) G::sign_row(q[p], a.s.c);
+            const char* kb = a.k + h * a.k_head;
+            const char* vb = a.v + h * a.v_head;
+            const uint8_t* ksb = a.ks + h * a.ks_head;
+            const uint8_t* vsb = a.vs + h * a.vs_head;
+            const int32_t* pages = a.col + job.sq.page0;
+            bool wrong = false;  // a page outside the cache
+            struct Place {
+                uint32_t id[2], slot[2];  // of this lane's two keys
+            };
+            // keys past the end repeat the last one (also where a whole tile is past it:
+            // a load under a branch would make every wait the wait for all loads)
+            const uint32_t each = a.page_div.d == 1 ? ~0u : 0u;  // (of one slot: no branch either)
+            const auto place = [&](int t0) {
+                Place x;
 #pragma unroll
-                    for (int p = NP - 1; p >= 0; --p)
-                        x = mfma32<__bf16>(y, q[p].w[t * R::kSteps + u], x);
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t key = (uint32_t)min(t0 + 16 * j + n, job.k1 - 1);
+                    const uint32_t pg = (__umulhi(key, a.page_div.mul) >> a.page_div.shift) | (key & each);
+                    x.id[j] = (uint32_t)pages[pg];
+                    x.slot[j] = key - pg * a.page_div.d;
                 }
-            sc[0][j] = x;
-        }
-        // a key that a row does not see must not reach it as 0 times an
-        // infinity or a NaN: its row is staged as 0 and added on its own below
-        const bool crosses = t0 + KT > job.before + lo;
-        uint32_t wild = 0;
-        wave_lds_sync();
+                return x;
+            };
+            const auto checked = [&](Place& x) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            u32x4 y[R::kLoads * R::kSteps];
-            bool off = false;
-#pragma unroll
-            for (int t = 0; t < R::kLoads; ++t)
-#pragma unroll
-                for (int u = 0; u < R::kSteps; ++u) {
-                    u32x4& x = y[t * R::kSteps + u];
-                    x = R::decode(v[j], t, u);
-                    if (crosses) {
-                        const uint32_t words[4] = {x[0], x[1], x[2], x[3]};
-                        off |= G::words_wild(words);
+                for (int j = 0; j < 2; ++j)
+                    if (x.id[j] >= (uint64_t)a.npages) {
+                        wrong = true;
+                        x.id[j] = 0;
                     }
+            };
+            typename R::Codes k[2], v[2];
+            const auto load = [&](const Place& x) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    R::template load<G::kFull>(
+                        kb + ((uint64_t)(x.id[j] * a.k_page + x.slot[j] * a.k_slot) << a.k_shift),
+                        ksb + ((uint64_t)(x.id[j] * a.ks_page + x.slot[j] * a.ks_slot) << a.ks_shift),
+                        a.s.dim, k[j]);
                 }
-            if (crosses) {
-                uint64_t b = __ballot(off);
-                b |= b >> 32;
-                b |= b >> 16;
-                wild |= (uint32_t)(b & 0xffff) << (16 * j);
-            }
-            // 0 weight times what the row that they repeat holds may be NaN
-            const bool zero = 16 * j + n >= left || (wild >> (16 * j + n) & 1);
 #pragma unroll
-            for (int t = 0; t < R::kLoads; ++t)
-#pragma unroll
-                for (int u = 0; u < R::kSteps; ++u)
-                    *reinterpret_cast<u32x4*>(
-                        vrows + G::stage_at(16 * j + n, 2 * (R::first(t) + 8 * u))) =
-                        zero ? u32x4{0, 0, 0, 0} : y[t * R::kSteps + u];
-        }
-        wave_lds_sync();
-        const Place here = now;
-        if (more) {
-            now = next;
+                for (int j = 0; j < 2; ++j) {
+                    R::template load<G::kFull>(
+                        vb + ((uint64_t)(x.id[j] * a.v_page + x.slot[j] * a.v_slot) << a.v_shift),
+                        vsb + ((uint64_t)(x.id[j] * a.vs_page + x.slot[j] * a.vs_slot) << a.vs_shift),
+                        a.s.dim, v[j]);
+                }
+            };
+            Place now = place(job.k0), next = place(job.k0 + KT);
             checked(now);
             load(now);
-            if (left > 2 * KT) next = place(t0 + 2 * KT);
-        }
-        sm.hide(sc[0], Seen::first(min(left, job.before + r.t - t0)));
-        typename G::Probs pr[1];
-        bool far;
-        const float fix = sm.template weigh<true>(sc, a.s.mag, pr, far);
-        if (__any(fix != 1.f)) G::scale_acc(o, fix);
+
+            typename G::AccB o;
 #pragma unroll
-        for (int b = 0; b < G::NB; ++b)
-            o.o[b] = G::add_block(G::value_frag(vrows, vbase, b), pr[0], o.o[b]);
-        for (; wild; wild &= wild - 1) {
-            const int key = __builtin_ctz(wild);
-            const uint32_t id = __shfl(key < 16 ? here.id[0] : here.id[1], key & 15, kWave);
-            const uint32_t slot = __shfl(key < 16 ? here.slot[0] : here.slot[1], key & 15, kWave);
-            const float p = G::prob_of(pr[0], key);
-            if (t0 + key >= min(job.k1, job.before + r.t)) continue;
-            const char* codes = vb + ((uint64_t)(id * a.v_page + slot * a.v_slot) << a.v_shift);
-            const uint8_t* scales =
-                vsb + ((uint64_t)(id * a.vs_page + slot * a.vs_slot) << a.vs_shift);
+            for (int b = 0; b < G::NB; ++b) o.o[b] = f32x4{0, 0, 0, 0};
+            Softmax<G, T> sm;
+            const int vbase = G::value_base(0);
+#pragma unroll 1
+            for (int t0 = job.k0; t0 < job.k1; t0 += KT) {
+                const int left = job.k1 - t0;
+                f32x4 sc[1][G::KSUB];
 #pragma unroll
-            for (int b = 0; b < G::NB; ++b) {
-                const int d = 16 * b + 4 * (lane >> 4);
-                if (G::kFull || d < a.s.dim) o.o[b] = add_codes<BITS>(codes, scales, d, p, o.o[b]);
+                for (int j = 0; j < 2; ++j) {
+                    f32x4 x{0, 0, 0, 0};
+#pragma unroll
+                    for (int t = 0; t < R::kLoads; ++t)
+#pragma unroll
+                        for (int u = 0; u < R::kSteps; ++u) {
+                            const u32x4 y = R::decode(k[j], t, u);
+#pragma unroll
+                            for (int p = NP - 1; p >= 0; --p)
+                                x = mfma32<__bf16>(y, q[p].w[t * R::kSteps + u], x);
+                        }
+                    sc[0][j] = x;
+                }
+                // a key that a row does not see must not reach it as 0 times an
+                // infinity or a NaN: its row is staged as 0 and added on its own below
+                const bool crosses = t0 + KT > job.before + lo;
+                uint32_t wild = 0;
+                wave_lds_sync();
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    u32x4 y[R::kLoads * R::kSteps];
+                    bool off = false;
+#pragma unroll
+                    for (int t = 0; t < R::kLoads; ++t)
+#pragma unroll
+                        for (int u = 0; u < R::kSteps; ++u) y[t * R::kSteps + u] = R::decode(v[j], t, u);
+                    if (crosses) {
+#pragma unroll
+                        for (const u32x4& x : y) {
+                            const uint32_t words[4] = {x[0], x[1], x[2], x[3]};
+                            off |= G::words_wild(words);
+                        }
+                        uint64_t is = __ballot(off);
+                        is |= is >> 32;
+                        is |= is >> 16;
+                        wild |= (uint32_t)(is & 0xffff) << (16 * j);
+                    }
+                    // 0 weight times what the row that they repeat holds may be NaN
+                    if (left < KT || wild) {
+                        const bool zero = 16 * j + n >= left || (wild >> (16 * j + n) & 1);
+#pragma unroll
+                        for (u32x4& x : y) x = zero ? u32x4{0, 0, 0, 0} : x;
+                    }
+#pragma unroll
+                    for (int t = 0; t < R::kLoads; ++t)
+#pragma unroll
+                        for (int u = 0; u < R::kSteps; ++u)
+                            *reinterpret_cast<u32x4*>(
+                                vrows + G::stage_at(16 * j + n, 2 * (R::first(t) + 8 * u))) =
+                                y[t * R::kSteps + u];
+                }
+                wave_lds_sync();
+                const Place here = now;
+                // (the pages first: loads end in the order that they began in)
+                now = next;
+                checked(now);
+                next = place(t0 + 2 * KT);
+                load(now);
+                sm.hide(sc[0], Seen::first(min(left, job.before + r.t - t0)));
+                typename G::Probs pr[1];
+                bool far;
+                const float fix = sm.template weigh<true>(sc, a.s.mag, pr, far);
+                if (__any(fix != 1.f)) G::scale_acc(o, fix);
+#pragma unroll
+                for (int i = 0; i < G::NB; ++i)
+                    o.o[i] = G::add_block(G::value_frag(vrows, vbase, i), pr[0], o.o[i]);
+                for (; wild; wild &= wild - 1) {
+                    const int key = __builtin_ctz(wild);
+                    const uint32_t id = __shfl(key < 16 ? here.id[0] : here.id[1], key & 15, kWave);
+                    const uint32_t slot = __shfl(key < 16 ? here.slot[0] : here.slot[1], key & 15, kWave);
+                    const float p = G::prob_of(pr[0], key);
+                    if (t0 + key >= min(job.k1, job.before + r.t)) continue;
+                    const char* codes = vb + ((uint64_t)(id * a.v_page + slot * a.v_slot) << a.v_shift);
+                    const uint8_t* scales =
+                        vsb + ((uint64_t)(id * a.vs_page + slot * a.vs_slot) << a.vs_shift);
+#pragma unroll
+                    for (int i = 0; i < G::NB; ++i) {
+                        const int d = 16 * i + 4 * (lane >> 4);
+                        if (G::kFull || d < a.s.dim) o.o[i] = add_codes<BITS>(codes, scales, d, p, o.o[i]);
+                    }
+                }
             }
-        }
-    }
-    sm.finish(a.s.mag);
-    if (__any(wrong)) sm.l = NAN;
-    if (!a.ranges)
-        store_row<G, T>(a, job, r, piece, o, sm);
-    else if (r.has && job.before + r.t > job.k0)
-        store_row_at<G, T>(
-            a, r, !split,
-            ((((int64_t)2 * range + late) * a.s.hkv + h) * tiles + tile) * 16 + n, o, sm);
-    };
-    segment();
-    if (pos >= end) return;
+            sm.finish(a.s.mag);
+            if (__any(wrong)) sm.l = NAN;
+            if (!a.ranges)
+                store_row<G, T>(a, job, r, piece, o, sm);
+            else if (r.has && job.before + r.t > job.k0)
+                store_row_at<G, T>(
+                    a, r, !split,
+                    ((((int64_t)2 * range + late) * a.s.hkv + h) * tiles + tile) * 16 + n, o, sm);
+        };
+        segment();
+        if (pos >= end) return;
     }
 }
 
