@@ -723,23 +723,23 @@ void with_mx(const AttnShape& s, int format, F&& f) {
 
 }  // namespace
 
-bool mx_wide(const AttnShape& s, int, int64_t rows) { return rows > (s.dim > 128 ? 48 : 16); }
+bool mx_wide(const AttnShape& s, int64_t rows) { return rows > (s.dim > 128 ? 48 : 16); }
 
-int mx_tile_rows(const AttnShape& s, int format, int64_t rows) {
-    if (!mx_wide(s, format, rows)) return 16;
+int mx_tile_rows(const AttnShape& s, int64_t rows) {
+    if (!mx_wide(s, rows)) return 16;
     return s.dim <= 128 && s.type == SPGEMM_TYPE_BF16 ? 128 : 64;
 }
 
 void mx_attention(const MxArgs& a, hipStream_t st) {
     const int64_t rows = (int64_t)a.max_new * a.s.group;
-    const int64_t tiles = ceil_div(rows, mx_tile_rows(a.s, a.format, rows));
+    const int64_t tiles = ceil_div(rows, mx_tile_rows(a.s, rows));
     if (a.seqs == 0 || a.tokens == 0 || tiles == 0) return;
     const int64_t units = (a.ranges ? a.ranges : a.seqs * a.npieces) * a.s.hkv * tiles;
     with_mx(a.s, a.format, [&](auto* geo, auto* t, auto bits) {
         using G = std::remove_pointer_t<decltype(geo)>;
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int B = decltype(bits)::value;
-        if (mx_wide(a.s, a.format, rows)) {
+        if (mx_wide(a.s, rows)) {
             auto run = k_mx_wide<B, G, T>;
             hipLaunchKernelGGL(run, grid_2d(xcd_grid(units)), dim3(kWaves * kWave), 0, st, a,
                                (int32_t)tiles);

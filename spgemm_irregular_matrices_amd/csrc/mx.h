@@ -24,8 +24,8 @@ constexpr int kMxKeys = 32;  // keys per tile of single wavefronts
 void mx_write(const MxRowsArgs& a, hipStream_t st);
 void mx_read(const MxRowsArgs& a, hipStream_t st);
 void mx_attention(const MxArgs& a, hipStream_t st);
-bool mx_wide(const AttnShape& s, int format, int64_t rows);
-int mx_tile_rows(const AttnShape& s, int format, int64_t rows);
+bool mx_wide(const AttnShape& s, int64_t rows);
+int mx_tile_rows(const AttnShape& s, int64_t rows);
 
 // A scale's byte as the conversions take it (0 is 2^-127, 255 NaN).
 __device__ __forceinline__ float mx_scale(uint32_t byte) {
