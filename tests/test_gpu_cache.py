@@ -318,6 +318,50 @@ def test_long_texts_in_pieces():
         _check(c, index, kept, seqs, q, out, lse, 0.125)
 
 
+@pytest.mark.parametrize("count", [256, 257, 600])
+def test_attention_over_many_sequences(count):
+    """Short texts and empty ones among a few long ones, as many as are cut evenly
+    and more; one breaks its batch's rules."""
+    rng = np.random.default_rng(count)
+    seqs = [(int(n), int(min(n, rng.integers(0, 3)))) for n in rng.integers(0, 90, count)]
+    seqs[3], seqs[100], seqs[count - 2] = (900, 2), (0, 0), (1500, 1)
+    c, index, kept, tokens = _filled(rng, seqs, 64, 2, 16, "e4m3", pad=1)
+    q = _query(rng, tokens, 6, 64, BF16)
+    _check(c, index, kept, seqs, q, *c.attention(q, **index), 64 ** -0.5)
+    lengths = index["lengths"].clone()
+    lengths[3] = 10 ** 6
+    out, lse = c.attention(q, **{**index, "lengths": lengths})
+    _check(c, index, kept, seqs, q, out, lse, 64 ** -0.5, skip=(3,))
+    start = index["q_rowptr"][3]
+    assert torch.isnan(out[start:start + 2]).all() and torch.isnan(lse[start:start + 2]).all()
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=str)
+def test_wild_tokens_of_evenly_cut_texts(dtype, form):
+    """A block of a long text's token becomes NaN: so do its values in the rows that
+    see it, whichever range it lies in, and no other row changes."""
+    rng = np.random.default_rng(33)
+    seqs = [(2100, 4), (60, 3), (1000, 4)]
+    c, index, kept, tokens = _filled(rng, seqs, 128, 1, 16, form, pad=0)
+    q = _query(rng, tokens, 4, 128, dtype)
+    clean = c.attention(q, **index)
+    _check(c, index, kept, seqs, q, *clean, 128 ** -0.5)
+    for at in (0, 1030, 2098):
+        page = int(index["pages"].col[at // 16])
+        old = c.v_scales[page, at % 16].clone()
+        c.v_scales[page, at % 16, 0, 2] = 255
+        out, lse = c.attention(q, **index)
+        first = max(0, at - 2096)
+        assert torch.isnan(out[first:4, :, 64:96]).all() and torch.equal(lse, clean[1])
+        out[first:4, :, 64:96] = clean[0][first:4, :, 64:96]
+        assert torch.equal(out[:first], clean[0][:first]) and torch.equal(out[4:], clean[0][4:])
+        # its other values are added apart from the matrix products, by one product and
+        # one sum in floats each: 2 roundings of the 2 * count that the bound has
+        _check(c, index, kept, seqs, q, out, lse, 128 ** -0.5)
+        c.v_scales[page, at % 16] = old
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
 @pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=str)
 def test_scales_of_the_scores(dtype, scale):

@@ -184,6 +184,45 @@ def test_chunks_and_wild_tokens(dl, new, dtype, form):
         assert not torch.isfinite(got[0][sees].float()).all(-1).any()
 
 
+@pytest.mark.parametrize("dtype,dl,dr,dn,dv", [(BF16, 128, 64, 128, 128), (F16, 96, 32, 64, 48), (F16, 64, 0, 16, 80)])
+def test_long_chunks_of_many_heads(dtype, dl, dr, dn, dv):
+    """As many tiles of 256 rows as fill the card, most with room left in them; then
+    a token that only later ones see is NaN, or infinite in one value."""
+    rng = np.random.default_rng(32)
+    seqs = [(300, 300), (700, 513), (5, 2), (0, 0), (257, 257)]
+    c = _case(rng, dtype, seqs, 48, dl, dr, 16, dn, dv)
+    clean = _run(c)
+    _check(c, seqs, *clean)
+    page, sees = int(c["table"].col[(300 + 15) // 16 + 500 // 16]), slice(300 + 500 - 187, 300 + 513)
+    some = sum(m for _, m in seqs)
+    row = c["cache"][page, 500 % 16].clone()
+    for where, value in ((slice(None), float("nan")), (slice(5, 6), -float("inf"))):
+        c["cache"][page, 500 % 16] = row
+        c["cache"][page, 500 % 16, where] = value
+        got = _run(c)
+        for a, b in zip(got, clean):
+            assert torch.equal(a[:sees.start], b[:sees.start]) and torch.equal(a[sees.stop:some], b[sees.stop:some])
+        assert not torch.isfinite(got[0][sees].float()).all(-1).any()
+
+
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
+@pytest.mark.parametrize("count", [256, 257, 700])
+def test_many_sequences(count, form):
+    """Short texts and empty ones among a few long ones, as many as are cut evenly
+    and more; one breaks its batch's rules."""
+    rng = np.random.default_rng(count)
+    seqs = [(int(n), int(min(n, rng.integers(0, 3)))) for n in rng.integers(0, 90, count)]
+    seqs[3], seqs[100], seqs[count - 2] = (900, 2), (0, 0), (1500, 1)
+    extra = dict(dn=32, dv=16) if form == "expanded" else {}
+    c = _case(rng, BF16, seqs, 2, 64, 8, 16, pad=1, **extra)
+    _check(c, seqs, *_run(c))
+    c["lengths"][3] = 10 ** 6
+    out, lse = _run(c)
+    _check(c, seqs, out, lse, skip=(3,))
+    start = c["q_rowptr"][3]
+    assert torch.isnan(out[start:start + 2]).all() and torch.isnan(lse[start:start + 2]).all()
+
+
 def test_an_infinite_value_reaches_its_column_alone():
     """The weights do not depend on it where the queries have 0 there: its column is
     infinite in the rows that see it, the other columns are as the formula has them."""
