@@ -54,7 +54,8 @@ typedef struct {
 /* A quantised paged cache: head_dim bytes of codes (half as many in 4 bits)
  * and head_dim / 32 scales for the key and for the value of every slot and
  * head. head_dim is a multiple of 32. Codes' data and strides are multiples of
- * 16 bytes; scales have any. Bytes that are written must not overlap. */
+ * 16 bytes; scales have any. A cache whose places overlap (a stride that does
+ * not pass what smaller ones reach) is read, and refused where it is written. */
 typedef struct {
     int32_t format;    /* spgemm_mx_format                                     */
     int32_t reserved;  /* 0                                                    */
@@ -88,6 +89,8 @@ SPGEMM_API int spgemm_mx_read(const spgemm_attention_desc* desc, const spgemm_mx
  * values for k and v. They enter the products as they are; queries do too (in
  * two or three bfloat16 parts where they are half or float), and the
  * probabilities with 8 (bfloat16), 16 (half) or 24 (float) significant bits.
+ * (A value past bfloat16's range enters as what the conversion makes of it, an
+ * infinity or NaN.)
  * Errors and broken batches: as there. */
 SPGEMM_API int spgemm_mx_attention_workspace(const spgemm_attention_desc* desc,
                                              const spgemm_paged_batch* batch, int64_t* bytes);
@@ -156,9 +159,9 @@ SPGEMM_API int spgemm_latent_attention(const spgemm_latent_desc* desc, const spg
  * the batch, as two numbers of the type each (the rounded product, and what
  * that leaves, rounded): that is for chunks of many new tokens; a few are the
  * absorbed form's, with W_k and W_v multiplied into q and out. A product past
- * the type's range is infinite. The workspace grows with min(room of the page table * page_size,
- * sequences * max_length). Errors and broken batches: as
- * spgemm_paged_attention; the workspace call needs the cache's page size. */
+ * the type's range is infinite. The workspace grows with the smaller of the page
+ * table's room * page_size and sequences * max_length. Errors and broken batches:
+ * as spgemm_paged_attention; the workspace call needs the cache's page size. */
 SPGEMM_API int spgemm_latent_expanded_workspace(const spgemm_latent_desc* desc,
                                                 const spgemm_latent_cache* cache,
                                                 const spgemm_paged_batch* batch, int64_t* bytes);

@@ -77,7 +77,8 @@ class QuantizedCache:
     every 32 values: codes [pages, slots, heads_kv, dim] or [..., dim / 2] and
     scales [..., dim / 32], uint8 (what they stand for: see
     ``include/spgemm_cache.h``). The tensors may be views with any strides whose
-    last dimension is contiguous; they are used as they are, not copied.
+    last dimension is contiguous; they are used as they are, not copied (views
+    whose places overlap, as expanded ones, are read but not written).
 
     The index tensors of a call are ``paged_attention``'s: row s of the CSR
     matrix ``pages`` lists sequence s's pages, rows [q_rowptr[s],

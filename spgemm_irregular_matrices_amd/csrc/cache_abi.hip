@@ -1,4 +1,6 @@
 // Argument checks and the C ABI of include/spgemm_cache.h.
+#include <algorithm>
+
 #include "attention_checks.h"
 #include "latent.h"
 #include "mx.h"
@@ -119,6 +121,21 @@ bool mx_format_valid(const spgemm_mx_cache* c) {
     return c && (c->format == SPGEMM_MX_E4M3 || c->format == SPGEMM_MX_E2M1) && c->reserved == 0;
 }
 
+// Whether no two of a tensor's places share a byte: in ascending order, every
+// stride passes all that is reached by those below it.
+bool bytes_apart(const spgemm_mx_bytes& x, const spgemm_mx_cache* c, int heads, int width) {
+    struct { int64_t stride, count; } dims[3] = {
+        {x.stride_page, c->npages}, {x.stride_slot, c->page_size}, {x.stride_head, heads}};
+    std::sort(dims, dims + 3, [](const auto& a, const auto& b) { return a.stride < b.stride; });
+    __int128 span = width;
+    for (const auto& d : dims) {
+        if (d.count <= 1) continue;
+        if (d.stride < span) return false;
+        span += (__int128)d.stride * (d.count - 1);
+    }
+    return true;
+}
+
 // Writing and reading: everything but the direction.
 template <class Run>
 int mx_rows(const spgemm_attention_desc* desc, const spgemm_rows* k, const spgemm_rows* v,
@@ -140,6 +157,13 @@ int mx_rows(const spgemm_attention_desc* desc, const spgemm_rows* k, const spgem
         if (rc != SPGEMM_OK || empty) return rc;
         rc = mx_cache(cache, a.s, &a);
         if (rc != SPGEMM_OK) return rc;
+        const int codes = cache->format == SPGEMM_MX_E4M3 ? a.s.dim : a.s.dim / 2;
+        const int scales = a.s.dim / SPGEMM_MX_BLOCK;
+        if (!output && !(bytes_apart(cache->k_codes, cache, a.s.hkv, codes) &&
+                         bytes_apart(cache->v_codes, cache, a.s.hkv, codes) &&
+                         bytes_apart(cache->k_scales, cache, a.s.hkv, scales) &&
+                         bytes_apart(cache->v_scales, cache, a.s.hkv, scales)))
+            return SPGEMM_ERR_INVALID_ARG;
         run(a);
         return SPGEMM_OK;
     });

@@ -127,6 +127,27 @@ def test_null_and_broken_arguments_are_refused():
     assert codes(b=none) == 0
 
 
+def test_a_cache_whose_places_overlap_is_not_written():
+    """Each tensor's strides, in any order, must pass the bytes of what they step over."""
+    lib, ref = cache.load(), ctypes.byref
+    d = attention.Desc(0, 2, 2, 64, 0.1)
+    rows = attention.Rows(1 << 20, 128, 64)
+    table = binding.CSRStruct(4, 10, 0, 256, 256, None)
+    batch = attention.PagedBatch(ctypes.pointer(table), 256, 256, 4, 1, 1000)
+    part, scales = cache.MxBytes(1 << 20, 2048, 128, 64), cache.MxBytes(3, 64, 4, 2)
+
+    def write(npages=10, **changed):
+        t = {**dict(kc=part, ks=scales, vc=part, vs=scales), **changed}
+        c = cache.MxCache(0, 0, npages, 16, t["kc"], t["ks"], t["vc"], t["vs"])
+        table.ncols = npages
+        return lib.spgemm_mx_write(ref(d), ref(rows), ref(rows), ref(c), ref(batch), None)
+
+    for bad in ((2048, 128, 0), (2048, 64, 64), (2048, 0, 64), (128, 128, 64), (2032, 128, 64), (64, 640, 16)):
+        assert write(kc=cache.MxBytes(1 << 20, *bad)) == -1 and write(vc=cache.MxBytes(1 << 20, *bad)) == -1, bad
+    for bad in ((64, 4, 1), (63, 4, 2), (64, 2, 2), (2, 4, 2)):
+        assert write(ks=cache.MxBytes(3, *bad)) == -1 and write(vs=cache.MxBytes(3, *bad)) == -1, bad
+
+
 def _cache(**changed):
     shape = (3, 16, 2, 64)
     parts = dict(k_codes=torch.zeros(shape, dtype=torch.uint8), v_codes=torch.zeros(shape, dtype=torch.uint8),
