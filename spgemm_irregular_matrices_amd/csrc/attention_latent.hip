@@ -216,6 +216,14 @@ struct Crossing {
 // leave no registers to read keys ahead; partial sums go through LDS), for the
 // result its columns in KH * DH.
 // FULL: the keys have DK elements, so that no piece of theirs needs a check.
+//
+// A token's row is read once from memory for all heads and serves both products.
+// At 128 heads bytes and products take about as long (70 and 54 us for the next token
+// of 32 texts of up to 16384, rows of 512 + 64): 164 us, 2.0 TB/s and 470 TFLOP/s. A
+// tile of 64 keys takes 7500 cycles, its bytes 4900: scores 1400, their exchange 1500,
+// weights 700, a barrier 800, results 2100, with one work group per compute unit (its
+// two tiles fill LDS), so that these follow each other. Two tiles a step would need
+// LDS twice.
 template <class T, int DK, int DV, int KH_, int DH_, bool FULL>
 struct AbsorbedGeo : Tile<T, 64, true> {
     static constexpr bool kWhole = FULL;
@@ -626,6 +634,10 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
 // a key's error would be that of the scores, and so of the log-sum-exp, and a
 // value's as large as the result's own rounding. The keys' last part, of up to
 // 64 elements, is the latent row's. A wavefront takes QB blocks of 16 rows.
+// Bound by the products, 1.8 times the formula's for the second numbers: chunks of
+// 2048 of two texts of up to 16384, 32 heads of 128 + 64 and 128, bfloat16, 1350 us,
+// some 880 TFLOP/s with them; the matrix units are busy for half of the time, softmax
+// and the exchange of tiles take the other.
 template <class T, int MP_, int VP_, int NW_>
 struct ExpandedGeo : Tile<T, 64, true> {
     static constexpr int NW = NW_, QB = 2, BM = NW * 16 * QB, kKeys = 8 * NW;
@@ -899,7 +911,9 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
 // key rows, then their value rows. A wavefront keeps 32 tokens' rows of c in
 // registers (NS steps of 32 values of x), a work group of 8 of them takes `each`
 // tiles of 128 rows of W through LDS, 128 values of x at a step: what has to come
-// from memory per product is a fourth of what tiles of 128 x 128 read.
+// from memory per product is a fourth of what tiles of 128 x 128 read. Bound by the
+// products and by what is written: 22.9 K tokens, 32 heads of 128 + 128 rows, x of 512:
+// 321 us, 600 TFLOP/s and 0.75 GB (in tiles of 128 x 128, both through LDS, 487 us).
 struct ExpandShape {
     int64_t rows;        // of made keys and values per head
     int32_t key_tiles;   // tiles of 128 of all heads' key rows

@@ -181,14 +181,20 @@ __device__ __forceinline__ f32x4 add_codes(const char* codes, const uint8_t* sca
     return o;
 }
 
-// Work groups of k_mx that a compute unit holds at once.
+// Work groups of k_mx that a compute unit holds at once. (A third of heads of 128
+// leaves 168 registers and spills: 325 us for 282 in 8 bits, 351 for 221 in 4.)
 template <int DP>
 constexpr int kMxResident = DP <= 64 ? 3 : DP <= 128 ? 2 : 1;
 
-// Few rows per sequence and key head: one wavefront takes 16 rows and one
-// piece of the keys, straight from memory. Codes of a tile of 32 keys are
-// turned into operands in registers (keys) and into rows in LDS (values, read
-// back transposed), and the next tile's are under way from then on.
+// Few rows per sequence and key head: one wavefront takes 16 rows and one range
+// or piece of the keys, straight from memory, in one pass with a running maximum
+// and sum. Codes of a tile of 32 keys are turned into operands in registers (keys)
+// and into rows in LDS (values, read back transposed), and the next tile's are
+// under way from then on. Bound by the codes' and scales' bytes, once each: a new
+// token of 64 texts of up to 16384, 64 / 8 heads of 128, 8 bits, 1.14 GB, takes
+// 265 us with the join (4.3 TB/s); 4 of 32 / 8 heads, 4 bits, 0.59 GB, 163 us
+// (3.6 TB/s, the vector unit a third busy with turning codes). A second tile under
+// way, in 40 more registers, gained nothing (282 and 231 us for 282 and 221).
 template <int BITS, class G, class T>
 __global__ __launch_bounds__(kWaves* kWave, kMxResident<G::kDim>) void k_mx(MxArgs a, int32_t tiles) {
     using R = MxRuns<BITS, G::kDim>;
@@ -418,7 +424,12 @@ __global__ __launch_bounds__(kWaves* kWave, kMxResident<G::kDim>) void k_mx(MxAr
 
 // Many rows: a work group of 4 wavefronts takes 4 * 16 * QB rows, a wavefront
 // 16 * QB of them, and BK keys at a time are turned into bfloat16 rows in LDS
-// for all of them.
+// for all of them. Bound by the softmax and the turning of codes on the vector unit
+// (47 % busy) beside the products (31 %), with two wavefronts per SIMD: chunks of
+// 2048 of two texts of up to 32768, 32 / 8 heads of 128, 1500 us, 787 TFLOP/s. Tiles
+// of 256 rows, whose codes are turned half as often, take 1611 us with one work
+// group per compute unit, and a second buffer for one barrier a tile instead of two
+// 1526.
 template <class G, class T>
 struct MxWide {
     static constexpr int QB = G::kDim <= 128 && G::NP == 1 ? 2 : 1;  // 16-row blocks per wavefront
@@ -723,6 +734,8 @@ void with_mx(const AttnShape& s, int format, F&& f) {
 
 }  // namespace
 
+// Whether rows of a sequence and key head are worth keys in LDS for all of them:
+// the limits of k_paged_wide, whose tiles these are. (Measured there.)
 bool mx_wide(const AttnShape& s, int64_t rows) { return rows > (s.dim > 128 ? 48 : 16); }
 
 int mx_tile_rows(const AttnShape& s, int64_t rows) {

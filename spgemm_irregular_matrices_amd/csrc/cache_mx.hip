@@ -7,7 +7,8 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kEach = 8;   // values per lane and step
-constexpr int kSteps = 4;  // steps per wavefront, all under way at once
+constexpr int kSteps = 4;  // steps per wavefront, all under way at once: keys and values in turn
+constexpr int kSides = 2;
 
 // Largest index s in [0, n) with a[s] <= x (ascending, a[0] <= x), 64 lanes at a time.
 __device__ __forceinline__ int64_t wave_upper_index(const int64_t* a, int64_t n, int64_t x) {
@@ -38,26 +39,56 @@ __device__ __forceinline__ Slot find_slot(const MxRowsArgs& a, int64_t token) {
     if (sq.bad) return x;
     const uint32_t at = (uint32_t)(sq.length - sq.fresh + (int)(token - sq.q0));
     const uint32_t pg = a.page_div.div(at);
-    x.id = (uint32_t)a.col[sq.page0 + pg];
-    x.slot = at - pg * a.page_div.d;
+    x.id = __builtin_amdgcn_readfirstlane(a.col[sq.page0 + pg]);  // (all lanes have the same)
+    x.slot = __builtin_amdgcn_readfirstlane(at - pg * a.page_div.d);
     x.there = x.id < (uint64_t)a.npages;
     return x;
 }
 
-// The i-th step's values of this lane: of keys or values, head, first value.
+// This lane's values of a pair of steps: head, first value. (Whether a step is of
+// keys or of values is known where the kernel is compiled, and a token's place is
+// the same in all lanes: addresses but for these are made once, in scalars. By
+// lanes, the vector unit was 87 % busy with them: 15 K tokens were written and read
+// in 26 + 22 us for 22 + 15.)
 struct Part {
-    bool has, value;
+    bool has;
     int h, d;
 };
-__device__ __forceinline__ Part part_of(const MxRowsArgs& a, FastDiv per_head, int part, int i) {
-    const int x = (part * kSteps + i) * kWave + lane_id();
-    const int heads = (int)per_head.div(x);
+__device__ __forceinline__ Part part_of(const MxRowsArgs& a, FastDiv per_head, int part, int pair) {
+    const int x = (part * (kSteps / kSides) + pair) * kWave + lane_id();
     Part p;
-    p.has = heads < 2 * a.s.hkv;
-    p.value = heads >= a.s.hkv;
-    p.h = p.value ? heads - a.s.hkv : heads;
-    p.d = kEach * (x - heads * (int)per_head.d);
+    p.h = (int)per_head.div(x);
+    p.has = p.h < a.s.hkv;
+    p.d = kEach * (x - p.h * (int)per_head.d);
     return p;
+}
+// Of one side of the cache or of the rows: where a token's begin, and its heads' stride.
+struct Side {
+    char* at;
+    int64_t head;
+};
+__device__ __forceinline__ Side codes_of(const MxRowsArgs& a, const Slot& t, bool value) {
+    const uint32_t place = value ? t.id * a.v_page + t.slot * a.v_slot : t.id * a.k_page + t.slot * a.k_slot;
+    return {const_cast<char*>(value ? a.v : a.k) + ((uint64_t)place << (value ? a.v_shift : a.k_shift)),
+            value ? a.v_head : a.k_head};
+}
+__device__ __forceinline__ Side scales_of(const MxRowsArgs& a, const Slot& t, bool value) {
+    const uint32_t place =
+        value ? t.id * a.vs_page + t.slot * a.vs_slot : t.id * a.ks_page + t.slot * a.ks_slot;
+    return {(char*)const_cast<uint8_t*>(value ? a.vs : a.ks) +
+                ((uint64_t)place << (value ? a.vs_shift : a.ks_shift)),
+            value ? a.vs_head : a.ks_head};
+}
+__device__ __forceinline__ Side rows_of(const MxRowsArgs& a, int64_t token, bool value) {
+    const AttnRows& r = value ? a.rv : a.rk;
+    return {r.base + token * r.row, r.head};
+}
+// This wavefront's token and part of it.
+__device__ __forceinline__ int64_t token_of(int32_t parts, int& part) {
+    const int64_t unit = grid_block() * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t token = parts == 1 ? unit : unit / parts;
+    part = (int)(unit - token * parts);
+    return token;
 }
 
 template <class T>
@@ -83,22 +114,24 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x) {
 }
 
 // One wavefront takes kSteps * 64 pieces of 8 values of one token. Its rows are
-// on their way before it looks its token's place up.
+// on their way before it looks its token's place up. Bound by bytes where tokens are
+// many (15 K, 8 heads of 128, half to 4 bits, 78 MB: 22 us), by the chain of loads to
+// the place where they are few (one token: 3 us).
 template <class T, int BITS>
 __global__ __launch_bounds__(kWaves* kWave) void k_mx_write(MxRowsArgs a, int32_t parts,
                                                             FastDiv per_head) {
-    const int64_t unit = grid_block() * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int64_t token = unit / parts;
+    int part;
+    const int64_t token = token_of(parts, part);
     if (token >= a.tokens) return;
-    const int part = (int)(unit - token * parts);
     float x[kSteps][kEach];
-    Part p[kSteps];
+    Part p[kSteps / kSides];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-        p[i] = part_of(a, per_head, part, i);
-        if (!p[i].has) continue;
-        const AttnRows& r = p[i].value ? a.rv : a.rk;
-        load_values<T>(r.base + token * r.row + p[i].h * r.head + p[i].d * (int)sizeof(T), x[i]);
+        Part& y = p[i / kSides];
+        if (i % kSides == 0) y = part_of(a, per_head, part, i / kSides);
+        if (!y.has) continue;
+        const Side r = rows_of(a, token, i % kSides);
+        load_values<T>(r.at + y.h * r.head + y.d * (int)sizeof(T), x[i]);
     }
     const Slot at = find_slot(a, token);
     if (!at.there) return;
@@ -106,7 +139,8 @@ __global__ __launch_bounds__(kWaves* kWave) void k_mx_write(MxRowsArgs a, int32_
     constexpr int kTop = BITS == 8 ? 8 : 2;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-        if (!p[i].has) continue;  // (whole blocks: head_dim is a multiple of 32)
+        const Part& y = p[i / kSides];
+        if (!y.has) continue;  // (whole blocks: head_dim is a multiple of 32)
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < kEach; ++j)
@@ -136,47 +170,39 @@ __global__ __launch_bounds__(kWaves* kWave) void k_mx_write(MxRowsArgs a, int32_
             c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[i][6], x[i][7], scale, 3);
             w[0] = wild ? 0u : c;
         }
-        const bool v = p[i].value;
-        char* codes = const_cast<char*>(v ? a.v : a.k) + p[i].h * (v ? a.v_head : a.k_head) +
-                      ((uint64_t)(at.id * (v ? a.v_page : a.k_page) + at.slot * (v ? a.v_slot : a.k_slot))
-                       << (v ? a.v_shift : a.k_shift)) + p[i].d * BITS / 8;
+        const Side c = codes_of(a, at, i % kSides), z = scales_of(a, at, i % kSides);
+        char* codes = c.at + y.h * c.head + y.d * BITS / 8;
         if constexpr (BITS == 8)
             *reinterpret_cast<u32x2*>(codes) = u32x2{w[0], w[1]};
         else
             *reinterpret_cast<uint32_t*>(codes) = w[0];
-        if ((lane_id() & 3) == 0) {
-            uint8_t* scales = const_cast<uint8_t*>(v ? a.vs : a.ks) + p[i].h * (v ? a.vs_head : a.ks_head) +
-                              ((uint64_t)(at.id * (v ? a.vs_page : a.ks_page) +
-                                          at.slot * (v ? a.vs_slot : a.ks_slot))
-                               << (v ? a.vs_shift : a.ks_shift)) + p[i].d / SPGEMM_MX_BLOCK;
-            *scales = (uint8_t)byte;
-        }
+        if ((lane_id() & 3) == 0)
+            z.at[y.h * z.head + y.d / SPGEMM_MX_BLOCK] = (char)byte;
     }
 }
 
+// The reverse, split alike; bound by bytes: 921 MB of 8-bit texts read and written as
+// bfloat16 take 178 us, 5.2 TB/s.
 template <class T, int BITS>
 __global__ __launch_bounds__(kWaves* kWave) void k_mx_read(MxRowsArgs a, int32_t parts,
                                                            FastDiv per_head) {
-    const int64_t unit = grid_block() * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int64_t token = unit / parts;
+    int part;
+    const int64_t token = token_of(parts, part);
     if (token >= a.tokens) return;
-    const int part = (int)(unit - token * parts);
     const Slot at = find_slot(a, token);
     if (!at.row) return;
     uint32_t w[kSteps][BITS / 4], scale[kSteps];
-    Part p[kSteps];
+    Part p[kSteps / kSides];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-        p[i] = part_of(a, per_head, part, i);
+        Part& y = p[i / kSides];
+        if (i % kSides == 0) y = part_of(a, per_head, part, i / kSides);
         scale[i] = 255;
 #pragma unroll
         for (int j = 0; j < BITS / 4; ++j) w[i][j] = 0;
-        if (!p[i].has || !at.there) continue;
-        const bool v = p[i].value;
-        const char* codes = (v ? a.v : a.k) + p[i].h * (v ? a.v_head : a.k_head) +
-                            ((uint64_t)(at.id * (v ? a.v_page : a.k_page) +
-                                        at.slot * (v ? a.v_slot : a.k_slot))
-                             << (v ? a.v_shift : a.k_shift)) + p[i].d * BITS / 8;
+        if (!y.has || !at.there) continue;
+        const Side c = codes_of(a, at, i % kSides), z = scales_of(a, at, i % kSides);
+        const char* codes = c.at + y.h * c.head + y.d * BITS / 8;
         if constexpr (BITS == 8) {
             const u32x2 y = *reinterpret_cast<const u32x2*>(codes);
             w[i][0] = y[0];
@@ -184,16 +210,14 @@ __global__ __launch_bounds__(kWaves* kWave) void k_mx_read(MxRowsArgs a, int32_t
         } else {
             w[i][0] = *reinterpret_cast<const uint32_t*>(codes);
         }
-        scale[i] = *((v ? a.vs : a.ks) + p[i].h * (v ? a.vs_head : a.ks_head) +
-                     ((uint64_t)(at.id * (v ? a.vs_page : a.ks_page) +
-                                 at.slot * (v ? a.vs_slot : a.ks_slot))
-                      << (v ? a.vs_shift : a.ks_shift)) + p[i].d / SPGEMM_MX_BLOCK);
+        scale[i] = (uint8_t)z.at[y.h * z.head + y.d / SPGEMM_MX_BLOCK];
     }
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-        if (!p[i].has) continue;
-        const AttnRows& r = p[i].value ? a.rv : a.rk;
-        char* row = r.base + token * r.row + p[i].h * r.head + p[i].d * (int)sizeof(T);
+        const Part& y = p[i / kSides];
+        if (!y.has) continue;
+        const Side r = rows_of(a, token, i % kSides);
+        char* row = r.at + y.h * r.head + y.d * (int)sizeof(T);
         if constexpr (std::is_same<T, __bf16>::value) {
             *reinterpret_cast<u32x4*>(row) = mx_decode8<BITS>(w[i], mx_scale(scale[i]));
         } else {
@@ -225,7 +249,7 @@ template <class Kernel>
 void launch_rows(Kernel run, const MxRowsArgs& a, hipStream_t st) {
     if (a.tokens == 0 || a.seqs == 0) return;
     const int per_head = a.s.dim / kEach;
-    const int parts = (int)ceil_div((int64_t)2 * a.s.hkv * per_head, kSteps * kWave);
+    const int parts = (int)ceil_div((int64_t)a.s.hkv * per_head, kSteps / kSides * kWave);
     hipLaunchKernelGGL(run, grid_2d(ceil_div(a.tokens * parts, kWaves)), dim3(kWaves * kWave), 0, st,
                        a, parts, FastDiv((uint32_t)per_head));
     SG_LAUNCH_CHECK();
