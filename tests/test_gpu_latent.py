@@ -247,6 +247,23 @@ def test_an_infinite_value_reaches_its_column_alone():
 
 @pytest.mark.parametrize("form", ["absorbed", "expanded"])
 @pytest.mark.parametrize("dtype", [BF16, F16], ids=str)
+@pytest.mark.parametrize("new", [1, 20])
+def test_infinite_and_nan_queries_stay_in_their_rows(new, dtype, form):
+    rng = np.random.default_rng(42)
+    seqs = [(900, new), (70, new)]
+    c = _case(rng, dtype, seqs, 16, 256, 32, 16, pad=0, **(dict(dn=64, dv=64) if form == "expanded" else {}))
+    clean = _run(c)
+    wild = torch.zeros(2 * new, 16, dtype=torch.bool, device="cuda")
+    for t, h, d, x in ((0, 3, 5, float("nan")), (new - 1, 0, 64, float("inf")), (new, 15, 0, -float("inf"))):
+        c["q"][t, h, d] = x
+        wild[t, h] = True
+    for a, b in zip(_run(c), clean):
+        assert torch.equal(a[~wild], b[~wild])
+        assert not torch.isfinite(a[wild].float().reshape(int(wild.sum()), -1)).all(-1).any()
+
+
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=str)
 @pytest.mark.parametrize("scale", [0.0, -0.1, 2.0])
 def test_scales_of_the_scores(scale, dtype, form):
     rng = np.random.default_rng(7)
