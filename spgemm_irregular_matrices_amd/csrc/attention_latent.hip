@@ -1142,9 +1142,9 @@ void with_expanded(const LatentArgs& a, F&& f) {
         using T = std::remove_pointer_t<decltype(t)>;
         const auto width = [&](auto planes) {
             constexpr int P = decltype(planes)::value;
-            // Tiles of 256 rows where they fill the compute units: 64K pairs of a
-            // chunk of 2048 and its head take 1590 us in them, 1836 in tiles of 128;
-            // 27 pairs of chunks of 500 33 and 30 us. (Their numbers fit 31 bits.)
+            // Tiles of 256 rows where they fill the compute units: chunks of 2048 in 2
+            // texts and 32 heads take 1590 us in them, 1836 in tiles of 128; chunks
+            // of up to 500 in 6 texts and 9 heads 51 and 46 us. (Rows fit 31 bits.)
             const int64_t tall = a.s.hq * (a.seqs + a.tokens / 256);
             if (a.max_new >= 256 && a.max_new <= 1 << 30 && tall >= 256)
                 f((ExpandedGeo<T, P, P, 8>*)nullptr, t);
@@ -1203,8 +1203,9 @@ void latent_expand(const ExpandArgs& e, hipStream_t st) {
     if (ctiles == 0) return;
     if (ctiles > INT32_MAX) throw OverflowError("rows of made keys");
     // One work group per compute unit is there at once; looking its tokens up and
-    // reading them takes as long as 1.2 tiles (26 of 23 thousand cycles). 22.9 K
-    // tokens, 64 tiles of W: 5 tiles each 340 us, 8 each 300.
+    // reading them takes as long as 1.2 tiles (26 of 23 thousand cycles): so many
+    // tiles each as end first. 22.9 K tokens, 64 tiles of W: 8 each, 3 rounds, 321 us;
+    // 5 each, 5 rounds, 340.
     int64_t best = INT64_MAX;
     for (int each = 1; each <= std::min<int64_t>(wtiles, 64); ++each) {
         const int64_t rounds = ceil_div(ctiles * ceil_div(wtiles, each), 256);

@@ -193,7 +193,7 @@ constexpr int kMxResident = DP <= 64 ? 3 : DP <= 128 ? 2 : 1;
 // under way from then on. Bound by the codes' and scales' bytes, once each: a new
 // token of 64 texts of up to 16384, 64 / 8 heads of 128, 8 bits, 1.14 GB, takes
 // 265 us with the join (4.3 TB/s); 4 of 32 / 8 heads, 4 bits, 0.59 GB, 163 us
-// (3.6 TB/s, the vector unit a third busy with turning codes). A second tile under
+// (3.6 TB/s, the vector unit half busy, most of it with codes). A second tile under
 // way, in 40 more registers, gained nothing (282 and 231 us for 282 and 221).
 template <int BITS, class G, class T>
 __global__ __launch_bounds__(kWaves* kWave, kMxResident<G::kDim>) void k_mx(MxArgs a, int32_t tiles) {
@@ -425,7 +425,7 @@ __global__ __launch_bounds__(kWaves* kWave, kMxResident<G::kDim>) void k_mx(MxAr
 // Many rows: a work group of 4 wavefronts takes 4 * 16 * QB rows, a wavefront
 // 16 * QB of them, and BK keys at a time are turned into bfloat16 rows in LDS
 // for all of them. Bound by the softmax and the turning of codes on the vector unit
-// (47 % busy) beside the products (31 %), with two wavefronts per SIMD: chunks of
+// (52 % busy) beside the products (35 %), with two wavefronts per SIMD: chunks of
 // 2048 of two texts of up to 32768, 32 / 8 heads of 128, 1500 us, 787 TFLOP/s. Tiles
 // of 256 rows, whose codes are turned half as often, take 1611 us with one work
 // group per compute unit, and a second buffer for one barrier a tile instead of two
