@@ -123,7 +123,6 @@ struct PagedArgs {
     int32_t piece = 0;     // keys per piece, a multiple of 32
     int32_t npieces = 1;   // ceil(max_length / piece)
     int32_t ranges = 0;    // not 0: EvenSplit's, instead of pieces
-    int32_t least = 1;     // tiles of keys per range at least
     float* lse = nullptr;
     float* part = nullptr;     // [piece][token][hq][dim]
     float* part_ml = nullptr;  // [piece][token][hq][2]

@@ -158,7 +158,7 @@ struct EvenSplit {
             }
             total += last(wave_inclusive_scan_i32(n[i]));
         }
-        per = max((total + a.ranges - 1) / a.ranges, a.least);
+        per = max((total + a.ranges - 1) / a.ranges, 1);
     }
     static __device__ __forceinline__ int last(int x) { return __builtin_amdgcn_readlane(x, kWave - 1); }
     // The sequence that tile `pos` < total is of, and the tiles before it.

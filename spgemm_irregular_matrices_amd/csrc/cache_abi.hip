@@ -172,7 +172,9 @@ int mx_rows(const spgemm_attention_desc* desc, const spgemm_rows* k, const spgem
 // How keys are cut. Many rows: in pieces, as for a cache of 16-bit values. Few:
 // evenly over the wavefronts that are there at once, whatever the texts' lengths
 // (64 ragged texts of up to 16384 tokens, 8 bits: 291 us, in pieces of each text
-// 437), where EvenSplit takes so many texts and each wavefront has few of them.
+// 437), where EvenSplit takes so many texts and each wavefront has few of them. A
+// range may be one tile: one token over 1000 takes 15.7 us then, with two tiles at
+// least 16.3, with four 19.0 (absorbed, 5 texts of up to 3000: 23.5, 27.2, 29.3).
 void mx_pieces(PagedArgs* a) {
     const int64_t rows = (int64_t)a->max_new * a->s.group;
     const int64_t tile = mx_tile_rows(a->s, rows);
@@ -186,9 +188,7 @@ void mx_pieces(PagedArgs* a) {
         if (a->seqs <= kEvenSeqs && a->seqs * a->s.hkv * tiles < each * 2048 &&
             most > a->seqs && most < INT32_MAX / 2) {
             a->piece = std::max(a->max_length, 1);
-            a->least = 2;
-            a->ranges = (int32_t)std::max<int64_t>(
-                std::min(ceil_div(most, a->least), each * 1024 / (a->s.hkv * tiles)), 1);
+            a->ranges = (int32_t)std::max<int64_t>(std::min(most, each * 1024 / (a->s.hkv * tiles)), 1);
         } else {
             cut_pieces(a, tile, each * 1024, 64, 32);
         }
@@ -231,13 +231,12 @@ void latent_shape(const spgemm_latent_desc* d, const spgemm_paged_batch* b, bool
         const int64_t tiles = std::max<int64_t>(ceil_div((int64_t)a->max_new * a->s.group, tile), 1);
         const int64_t most = a->seqs * ceil_div(a->max_length, kAbsorbedKeys);
         a->piece = std::max(a->max_length, 1);
-        if (a->seqs <= kEvenSeqs && a->seqs * tiles < 512 && most > a->seqs && most < INT32_MAX / 2) {
-            a->least = 2;
-            a->ranges = (int32_t)std::max<int64_t>(std::min(ceil_div(most, a->least), 256 / tiles), 1);
-        }
+        if (a->seqs <= kEvenSeqs && a->seqs * tiles < 512 && most > a->seqs && most < INT32_MAX / 2)
+            a->ranges = (int32_t)std::max<int64_t>(std::min(most, 256 / tiles), 1);
     } else {
-        // two work groups per compute unit are there at once; the texts differ
-        cut_pieces(a, tile, tile == 256 ? 1536 : 3072, 1024, 64);
+        // one work group of 256 rows per compute unit or two of 128 are there at once, in
+        // six rounds, since the texts differ
+        cut_pieces(a, tile, (tile == 256 ? 6 : 12) * 256, 1024, 64);
     }
 }
 
