@@ -6,7 +6,7 @@
 namespace sg {
 
 // One wavefront per token and query head joins its parts, in their order, so that
-// the bits are the same every time. A chain of loads (5 to 8 us): where the text and
+// the bits are the same every time. A chain of loads (6 to 10 us for few rows): where the text and
 // its range are, the parts' maxima and sums, then the parts, four at a time. Parts of
 // ranges lie as [slot][key head][tile][row of tile_rows], of pieces as PagedArgs
 // has it; their weights are held times 2^shift.
