@@ -215,7 +215,8 @@ struct Crossing {
 // keys in KH and the sum over its elements in DH (2: whole queries of 576 elements
 // leave no registers to read keys ahead; partial sums go through LDS), for the
 // result its columns in KH * DH.
-// FULL: the keys have DK elements, so that no piece of theirs needs a check.
+// FULL: the keys have DK elements, so that no piece of theirs needs a check (the
+// time below; with the checks 179 us).
 //
 // A token's row is read once from memory for all heads and serves both products.
 // At 128 heads bytes and products take about as long (70 and 54 us for the next token
