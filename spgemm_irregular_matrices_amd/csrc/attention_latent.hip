@@ -959,11 +959,20 @@ __global__ __launch_bounds__(512) void k_expand(ExpandArgs e, ExpandShape z) {
     if (count <= 0) return;
     // this lane's two tokens: their latent rows, null where there is none
     const int64_t row0 = (unit - (int64_t)group * z.ctiles) * kRows + 32 * w;
-    const char* from[2];
+    const char* from[2] = {nullptr, nullptr};
+    bool none = false;  // a row that no sequence was found to need
+    const auto take_row = [&](int x, const Sequence& sq, int64_t key) {
+        if (key < 0 || key >= sq.length || sq.none) return false;
+        const uint32_t pg = a.page_div.div((uint32_t)key);
+        const uint32_t id = (uint32_t)a.col[sq.page0 + pg];
+        const uint32_t slot = (uint32_t)key - pg * a.page_div.d;
+        if (id < (uint64_t)a.npages)
+            from[x] = a.k + ((uint64_t)(id * a.k_page + slot * a.k_slot) << a.k_shift);
+        return true;
+    };
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int64_t row = row0 + 16 * x + (lane & 15);
-        from[x] = nullptr;
         if (row >= z.rows) continue;
         int64_t s, key;
         if (a.made_step) {
@@ -974,13 +983,26 @@ __global__ __launch_bounds__(512) void k_expand(ExpandArgs e, ExpandShape z) {
             s = upper_index(a.rowptr, int64_t(0), a.seqs, entry);
             key = row - a.rowptr[s] * (int64_t)a.page_div.d;
         }
-        const Sequence sq = read_sequence(a, s);
-        if (key < 0 || key >= sq.length || sq.none) continue;
-        const uint32_t pg = a.page_div.div((uint32_t)key);
-        const uint32_t id = (uint32_t)a.col[sq.page0 + pg];
-        const uint32_t slot = (uint32_t)key - pg * a.page_div.d;
-        if (id < (uint64_t)a.npages)
-            from[x] = a.k + ((uint64_t)(id * a.k_page + slot * a.k_slot) << a.k_shift);
+        none |= !take_row(x, read_sequence(a, s), key);
+    }
+    // A broken sequence's place in the table may be out of order, which misleads the search
+    // for those of others. Most rows that nobody needs are just behind a text's end: only
+    // where the table descends are all sequences asked for them.
+    if (!a.made_step && __syncthreads_or(none)) {
+        bool descends = false;
+        for (int64_t s = tid; s < a.seqs; s += NW * kWave) descends |= a.rowptr[s] > a.rowptr[s + 1];
+        if (__syncthreads_or(descends)) {
+#pragma unroll 1
+            for (int64_t s = 0; s < a.seqs; ++s) {
+                const Sequence sq = read_sequence(a, s);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int64_t row = row0 + 16 * x + (lane & 15);
+                    if (row < z.rows && !from[x])
+                        take_row(x, sq, row - sq.page0 * (int64_t)a.page_div.d);
+                }
+            }
+        }
     }
     if (!__syncthreads_or(from[0] || from[1])) return;
     const char* zero = reinterpret_cast<const char*>(g_zero);
