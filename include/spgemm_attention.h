@@ -181,7 +181,9 @@ SPGEMM_API int spgemm_paged_attention_workspace(const spgemm_attention_desc* des
  * that has more than max_new new tokens, or that needs a page outside [0,
  * npages), gets NaN in those of its first max_new rows that exist (a page
  * that only some of its tokens need: in those tokens' rows at least); no
- * memory outside the arrays is touched. `lse` may be NULL. Errors:
+ * memory outside the arrays is touched. A sequence is judged by its own
+ * entries alone: another's broken row pointer or start costs it nothing, but
+ * what a row holds that two sequences name is not said. `lse` may be NULL. Errors:
  * INVALID_ARG, OVERFLOW (as spgemm_attention_forward; tokens, max_length or
  * the page size over 2^30, 2^30 or more sequences, more than 2^31 - 128 pairs
  * of token and query head, 2^31 or more pages or entries of their table), HIP. */

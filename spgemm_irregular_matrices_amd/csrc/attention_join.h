@@ -18,10 +18,10 @@ __global__ __launch_bounds__(4 * kWave) void k_join_parts(PagedArgs a, int32_t t
     if (unit >= a.tokens * a.s.hq) return;
     const int64_t token = unit / a.s.hq;
     const int hq = (int)(unit - token * a.s.hq);
-    if (token < a.q_rowptr[0]) return;
-    const int64_t s = upper_index(a.q_rowptr, int64_t(0), a.seqs, token);
-    const Sequence sq = read_sequence(a, s);
-    if (sq.none || sq.bad || token < sq.q0 || token - sq.q0 >= sq.fresh) return;
+    Sequence sq;
+    int64_t s;
+    if (!find_sequence(a, token, upper_index(a.q_rowptr, int64_t(0), a.seqs, token), sq, &s) || sq.bad)
+        return;
     const int sees = sq.length - sq.fresh + 1 + (int)(token - sq.q0);
     int count;
     int64_t first, step, late = 0;  // in rows of parts

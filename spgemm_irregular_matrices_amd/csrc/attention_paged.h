@@ -31,6 +31,39 @@ __device__ __forceinline__ Sequence read_sequence(const PagedArgs& a, int64_t s)
     return x;
 }
 
+// The sequence that has `token` (the same in all lanes) among its new ones, by a whole
+// wavefront; s: the one that a search of ascending starts finds. A broken sequence's
+// start may be out of order and mislead that search. So where it finds none that keeps
+// the rules, all sequences are looked at, 64 at a time, and one that keeps them goes
+// before one that does not: that is paid by the rows of broken sequences and by those of
+// none. Whether there is one.
+__device__ __forceinline__ bool find_sequence(const PagedArgs& a, int64_t token, int64_t s,
+                                              Sequence& sq, int64_t* at = nullptr) {
+    const auto has = [&](const Sequence& x) {
+        return !x.none && token >= x.q0 && token - x.q0 < x.fresh;
+    };
+    sq = read_sequence(a, s);
+    if (at) *at = s;
+    if (has(sq) && !sq.bad) return true;
+    bool found = false;
+#pragma unroll 1
+    for (int64_t first = 0; first < a.seqs; first += kWave) {
+        const int64_t i = first + lane_id();
+        uint64_t may = __ballot(i < a.seqs && a.q_rowptr[i] <= token && a.q_rowptr[i + 1] > token);
+#pragma unroll 1
+        for (; may; may &= may - 1) {
+            s = first + __builtin_ctzll(may);
+            const Sequence x = read_sequence(a, s);
+            if (!has(x) || (found && x.bad)) continue;
+            sq = x;
+            if (at) *at = s;
+            found = true;
+            if (!x.bad) return true;
+        }
+    }
+    return found;
+}
+
 // What a work group or wavefront has to do for a tile of `rows` rows of one
 // sequence (its new tokens' query heads of one key head, the heads of a token
 // next to each other) and one piece of its keys.

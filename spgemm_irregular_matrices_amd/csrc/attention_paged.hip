@@ -424,10 +424,9 @@ __global__ __launch_bounds__(kWaves* kWave) void k_paged_join(PagedArgs a) {
     if (unit >= a.tokens * a.s.hq) return;
     const int64_t token = unit / a.s.hq;
     const int hq = (int)(unit - token * a.s.hq);
-    if (token < a.q_rowptr[0]) return;
-    const int64_t s = upper_index(a.q_rowptr, int64_t(0), a.seqs, token);
-    const Sequence sq = read_sequence(a, s);
-    if (sq.none || sq.bad || token < sq.q0 || token - sq.q0 >= sq.fresh) return;
+    Sequence sq;
+    if (!find_sequence(a, token, upper_index(a.q_rowptr, int64_t(0), a.seqs, token), sq) || sq.bad)
+        return;
     const int sees = sq.length - sq.fresh + 1 + (int)(token - sq.q0);
     if (sees <= a.piece) return;
     const int count = (sees + a.piece - 1) / a.piece;

@@ -10,7 +10,7 @@ constexpr int kEach = 8;   // values per lane and step
 constexpr int kSteps = 4;  // steps per wavefront, all under way at once: keys and values in turn
 constexpr int kSides = 2;
 
-// Largest index s in [0, n) with a[s] <= x (ascending, a[0] <= x), 64 lanes at a time.
+// Largest index s in [0, n) with a[s] <= x (ascending; 0 if there is none), 64 lanes at a time.
 __device__ __forceinline__ int64_t wave_upper_index(const int64_t* a, int64_t n, int64_t x) {
     int64_t lo = 0;
     while (n > 1) {
@@ -32,9 +32,8 @@ struct Slot {
 };
 __device__ __forceinline__ Slot find_slot(const MxRowsArgs& a, int64_t token) {
     Slot x{false, false, 0, 0};
-    if (token < a.q_rowptr[0]) return x;
-    const Sequence sq = read_sequence(a, wave_upper_index(a.q_rowptr, a.seqs, token));
-    if (sq.none || token < sq.q0 || token - sq.q0 >= sq.fresh) return x;
+    Sequence sq;
+    if (!find_sequence(a, token, wave_upper_index(a.q_rowptr, a.seqs, token), sq)) return x;
     x.row = true;
     if (sq.bad) return x;
     const uint32_t at = (uint32_t)(sq.length - sq.fresh + (int)(token - sq.q0));
