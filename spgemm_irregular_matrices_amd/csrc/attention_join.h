@@ -19,9 +19,8 @@ __global__ __launch_bounds__(4 * kWave) void k_join_parts(PagedArgs a, int32_t t
     const int64_t token = unit / a.s.hq;
     const int hq = (int)(unit - token * a.s.hq);
     Sequence sq;
-    int64_t s;
-    if (!find_sequence(a, token, upper_index(a.q_rowptr, int64_t(0), a.seqs, token), sq, &s) || sq.bad)
-        return;
+    int64_t s = upper_index(a.q_rowptr, int64_t(0), a.seqs, token);
+    if (!find_sequence(a, token, s, sq) || sq.bad) return;
     const int sees = sq.length - sq.fresh + 1 + (int)(token - sq.q0);
     int count;
     int64_t first, step, late = 0;  // in rows of parts

@@ -31,37 +31,31 @@ __device__ __forceinline__ Sequence read_sequence(const PagedArgs& a, int64_t s)
     return x;
 }
 
-// The sequence that has `token` (the same in all lanes) among its new ones, by a whole
-// wavefront; s: the one that a search of ascending starts finds. A broken sequence's
-// start may be out of order and mislead that search. So where it finds none that keeps
-// the rules, all sequences are looked at, 64 at a time, and one that keeps them goes
-// before one that does not: that is paid by the rows of broken sequences and by those of
-// none. Whether there is one.
-__device__ __forceinline__ bool find_sequence(const PagedArgs& a, int64_t token, int64_t s,
-                                              Sequence& sq, int64_t* at = nullptr) {
-    const auto has = [&](const Sequence& x) {
-        return !x.none && token >= x.q0 && token - x.q0 < x.fresh;
+// The sequence s that has `token` (the same in all lanes) among its new ones, and
+// whether there is one; by a whole wavefront. s: what a search of ascending starts finds.
+// A broken sequence's start may be out of order and mislead that search, so where it
+// finds none whose starts fit, all are looked at, 64 at a time, and one whose starts fit
+// goes before one that has too many new tokens: rows of no sequence pay for that.
+__device__ __forceinline__ bool find_sequence(const PagedArgs& a, int64_t token, int64_t& s,
+                                              Sequence& sq) {
+    const auto has = [&](int64_t q0, int64_t q1) {
+        return q0 >= 0 && q0 <= token && token < min(q1, q0 + a.max_new);
     };
-    sq = read_sequence(a, s);
-    if (at) *at = s;
-    if (has(sq) && !sq.bad) return true;
-    bool found = false;
+    const auto fits = [&](int64_t q0, int64_t q1) { return q1 <= a.tokens && q1 - q0 <= a.max_new; };
+    const int64_t q0 = a.q_rowptr[s], q1 = a.q_rowptr[s + 1];
+    if (!has(q0, q1) || !fits(q0, q1)) {
+        s = -1;
 #pragma unroll 1
-    for (int64_t first = 0; first < a.seqs; first += kWave) {
-        const int64_t i = first + lane_id();
-        uint64_t may = __ballot(i < a.seqs && a.q_rowptr[i] <= token && a.q_rowptr[i + 1] > token);
-#pragma unroll 1
-        for (; may; may &= may - 1) {
-            s = first + __builtin_ctzll(may);
-            const Sequence x = read_sequence(a, s);
-            if (!has(x) || (found && x.bad)) continue;
-            sq = x;
-            if (at) *at = s;
-            found = true;
-            if (!x.bad) return true;
+        for (int64_t first = 0; first < a.seqs; first += kWave) {
+            const int64_t i = min(first + lane_id(), a.seqs - 1), x0 = a.q_rowptr[i], x1 = a.q_rowptr[i + 1];
+            const uint64_t any = __ballot(has(x0, x1)), best = __ballot(has(x0, x1) && fits(x0, x1));
+            if (best || (any && s < 0)) s = first + __builtin_ctzll(best ? best : any);
+            if (best) break;
         }
+        if (s < 0) return false;
     }
-    return found;
+    sq = read_sequence(a, s);
+    return true;
 }
 
 // What a work group or wavefront has to do for a tile of `rows` rows of one

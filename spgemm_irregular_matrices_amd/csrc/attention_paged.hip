@@ -425,8 +425,8 @@ __global__ __launch_bounds__(kWaves* kWave) void k_paged_join(PagedArgs a) {
     const int64_t token = unit / a.s.hq;
     const int hq = (int)(unit - token * a.s.hq);
     Sequence sq;
-    if (!find_sequence(a, token, upper_index(a.q_rowptr, int64_t(0), a.seqs, token), sq) || sq.bad)
-        return;
+    int64_t s = upper_index(a.q_rowptr, int64_t(0), a.seqs, token);
+    if (!find_sequence(a, token, s, sq) || sq.bad) return;
     const int sees = sq.length - sq.fresh + 1 + (int)(token - sq.q0);
     if (sees <= a.piece) return;
     const int count = (sees + a.piece - 1) / a.piece;

@@ -33,7 +33,8 @@ struct Slot {
 __device__ __forceinline__ Slot find_slot(const MxRowsArgs& a, int64_t token) {
     Slot x{false, false, 0, 0};
     Sequence sq;
-    if (!find_sequence(a, token, wave_upper_index(a.q_rowptr, a.seqs, token), sq)) return x;
+    int64_t s = wave_upper_index(a.q_rowptr, a.seqs, token);
+    if (!find_sequence(a, token, s, sq)) return x;
     x.row = true;
     if (sq.bad) return x;
     const uint32_t at = (uint32_t)(sq.length - sq.fresh + (int)(token - sq.q0));
@@ -184,7 +185,7 @@ __global__ __launch_bounds__(kWaves* kWave) void k_mx_write(MxRowsArgs a, int32_
 // bfloat16 take 178 us, 5.2 TB/s.
 template <class T, int BITS>
 __global__ __launch_bounds__(kWaves* kWave) void k_mx_read(MxRowsArgs a, int32_t parts,
-                                                           FastDiv per_head) {
+                                                              FastDiv per_head) {
     int part;
     const int64_t token = token_of(parts, part);
     if (token >= a.tokens) return;
