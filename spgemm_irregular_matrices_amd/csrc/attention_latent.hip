@@ -125,10 +125,13 @@ __device__ __forceinline__ u32x4 sign_query(const LatentArgs& a, u32x4 q) {
 constexpr float kSlack = 8.f;
 template <class T>
 constexpr float kShift = std::is_same<T, _Float16>::value ? 7.f : 0.f;
+// (The difference, not the sum: where floats' steps are 16, ref + 8 may be ref + 16, and a
+// weight of 2^16 passes half precision's range. Of two infinities it is a NaN: no.)
+__device__ __forceinline__ bool passes(float ref, float top) { return top - ref > kSlack; }
 // Moves a query's reference if its keys' largest score asks for it (whatever other
 // queries ask for), and returns the factor of what was summed before.
 __device__ __forceinline__ float move(float& ref, float top) {
-    if (!(top > ref + kSlack)) return 1.f;
+    if (!passes(ref, top)) return 1.f;
     const float fix = fast_exp2(ref - top);
     ref = top;
     return fix;
@@ -473,7 +476,7 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
 #pragma unroll
                         for (int j = 1; j < 4 * FB; ++j) top[x] = fmaxf(top[x], sc[x][j >> 2][j & 3]);
                         top[x] *= a.s.mag;
-                        raise |= top[x] > ref[x] + kSlack;
+                        raise |= passes(ref[x], top[x]);
                     }
                     put_probs();
                 }
@@ -820,7 +823,7 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
 #pragma unroll
                 for (int j = 1; j < 8; ++j) top[x] = fmaxf(top[x], sc[x][j >> 2][j & 3]);
                 top[x] *= a.s.mag;
-                raise |= top[x] > ref[x] + kSlack;
+                raise |= passes(ref[x], top[x]);
             }
             if (__any(raise)) {  // hardly ever after the first tiles
 #pragma unroll
