@@ -145,8 +145,9 @@ __device__ __forceinline__ float weight_of(float s, float c, float ref, float sh
 // Keys that not all rows of a work group see. An infinity or a NaN in one's value
 // must not reach a row that does not see it as 0 times it: in the tiles that
 // hold such keys those elements are made 0 in LDS, and at the end they are added
-// to the rows that see their keys, whose results are what the elements make of
-// them whatever the weights.
+// to the rows that see their keys, times their weights: any weight gives the element
+// itself but that of a score of -infinity, which is 0 and gives NaN. (So does a weight
+// that its type rounds to 0, in the tiles that all rows see.)
 template <int KEYS, int ROWS>
 struct Crossing {
     static constexpr int kKeys = KEYS, kTiles = ROWS / KEYS + 2;
@@ -186,10 +187,11 @@ struct Crossing {
         __syncthreads();
     }
     // o plus the elements that are not finite of the keys below `sees` that were
-    // cleared; row(key): where the key's values of o begin.
-    template <class T, int NB, class Row>
+    // cleared; row(key): where the key's values of o begin, weight(key): 0 if its
+    // weight is, else 1.
+    template <class T, int NB, class Row, class Weight>
     __device__ __forceinline__ void add(const unsigned long long* wild, int sees, int dim, Row&& row,
-                                        f32x4 (&o)[NB]) const {
+                                        Weight&& weight, f32x4 (&o)[NB]) const {
 #pragma unroll 1
         for (int i = 0; i < kTiles; ++i)
 #pragma unroll 1
@@ -198,6 +200,7 @@ struct Crossing {
                 if (key >= sees) break;
                 const char* at = row(key);
                 if (!at) break;
+                const float w = weight(key);
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     if (16 * b + 4 * (lane_id() >> 4) >= dim) continue;
@@ -206,7 +209,7 @@ struct Crossing {
                     unpack2<T>(x[0], y[0], y[1]);
                     unpack2<T>(x[1], y[2], y[3]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) o[b][j] += __builtin_isfinite(y[j]) ? 0.f : y[j];
+                    for (int j = 0; j < 4; ++j) o[b][j] += __builtin_isfinite(y[j]) ? 0.f : y[j] * w;
                 }
             }
     }
@@ -603,7 +606,9 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
                             return a.k + ((uint64_t)(id * a.k_page + slot * a.k_slot) << a.k_shift) +
                                    part * (2 * G::kDv / CG);
                         },
-                        o[x]);
+                        // (The element is one of the key's too: its score is an infinity or
+                        // a NaN, and but for -infinity the row's sum is NaN anyway.)
+                        [](int) { return 0.f; }, o[x]);
                 char* row = !split ? a.out.base + r[x].token * a.out.row + r[x].hq * a.out.head
                                    : reinterpret_cast<char*>(a.part + at * a.s.dim);
 #pragma unroll
@@ -876,6 +881,35 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
     if (crossed) Cr::gather(wild, wild_s);
     else __syncthreads();
     if (row0 >= job.rows) return;
+    // The score (before its factor's size) of the lane's query x and a key, without
+    // the key's low parts: whether it is -infinity.
+    const auto score_of = [&](int x, int key) {
+        const uint32_t pg = a.page_div.div(key), id = (uint32_t)pages[pg];
+        const char* row = id < (uint64_t)a.npages
+                              ? a.k + ((uint64_t)(id * a.k_page + (key - pg * a.page_div.d) * a.k_slot)
+                                       << a.k_shift)
+                              : zero;
+        float y = 0.f;
+#pragma unroll 1
+        for (int t = 0; t < QS; ++t) {
+            u32x4 qt = q[x][0];
+#pragma unroll
+            for (int i = 1; i < QS; ++i) qt = i == t ? q[x][i] : qt;
+            const int at = 64 * t + 16 * (lane >> 4), rope = at - 128 * G::MP;
+            const char* from = rope < 0 ? made_k + (int64_t)key * 2 * made + at : row + a.rope_at + rope;
+            const bool has = rope < 0 ? at < made : made + rope < 2 * a.key_dim;
+            const u32x4 kt = *reinterpret_cast<const u32x4*>(has ? from : zero);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float q0, q1, k0, k1;
+                unpack2<T>(qt[i], q0, q1);
+                unpack2<T>(kt[i], k0, k1);
+                y = fmaf(q1, k1, fmaf(q0, k0, y));
+            }
+        }
+        y += __shfl_xor(y, 16, kWave);
+        return y + __shfl_xor(y, 32, kWave);
+    };
 #pragma unroll
     for (int x = 0; x < QB; ++x) {
         const int sees = job.before + r[x].t;
@@ -887,8 +921,10 @@ __global__ __launch_bounds__(G::NW* kWave, 2) void k_expanded(LatentArgs a, int3
         const int64_t at = (int64_t)piece * a.tokens * a.s.hq + line;
         const float f = l == 0.f ? 0.f : 1.f / l;
         if (crossed)
-            cross.template add<T>(wild_s, min(job.k1, sees), a.s.dim,
-                              [&](int key) { return made_v + (int64_t)key * 2 * values; }, o[x]);
+            cross.template add<T>(
+                wild_s, min(job.k1, sees), a.s.dim,
+                [&](int key) { return made_v + (int64_t)key * 2 * values; },
+                [&](int key) { return score_of(x, key) == -INFINITY ? 0.f : 1.f; }, o[x]);
         char* row = part ? reinterpret_cast<char*>(a.part + at * a.s.dim)
                          : a.out.base + r[x].token * a.out.row + r[x].hq * a.out.head;
 #pragma unroll

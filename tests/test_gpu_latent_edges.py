@@ -66,3 +66,108 @@ def test_scores_in_steps_past_the_slack(dtype, odd, heads, new, form):
         assert (np.abs(got - want) <= bound + 2.0 ** -25).all()
         # two sums of 2^27 in base 2, to 8 each; ln 2 to 2^-25 of it; the result to 4
         assert (np.abs(f64(lse[t]) - (2.0 ** 27 + 16 * (odd + 2)) * np.log(2.0) - np.log(total)) <= 20).all()
+
+
+def _wild_columns(c, clean, got, seqs, seen_from, columns, head=None):
+    """The first sequence's rows from seen_from on have these values in these columns (of one head)
+    and are else within the bounds of the clean ones; all other rows are the clean ones."""
+    new = seqs[0][1]
+    rows = slice(seen_from, new)
+    heads = range(c["q"].shape[1])
+    for h in heads:
+        for m, value in columns.items():
+            if head is None or h == head:
+                x = f64(got[0][rows, h, m])
+                assert (np.isnan(x) if np.isnan(value) else x == value).all(), (h, m, x)
+                got[0][rows, h, m] = clean[0][rows, h, m]
+    assert torch.equal(got[0][:seen_from], clean[0][:seen_from]) and torch.equal(got[1][:seen_from], clean[1][:seen_from])
+    some = sum(m for _, m in seqs)
+    assert torch.equal(got[0][new:some], clean[0][new:some]) and torch.equal(got[1][new:some], clean[1][new:some])
+    latents._check(c, seqs, *got)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=str)
+@pytest.mark.parametrize("heads,new,dv", [(3, 40, 48), (48, 300, 128)])
+def test_infinite_made_values_reach_their_columns_alone(heads, new, dv, dtype):
+    """Values past the type's range in some columns of one head, of keys that all rows of a tile see
+    and of such that only later ones do: infinite there, and NaN where two signs meet."""
+    rng = np.random.default_rng(61)
+    # (of 48 heads in tiles of 256 rows)
+    seqs = [(400 + new, new), *([(300, 300), (257, 257)] if new == 300 else [(31, 7)])]
+    c = latents._case(rng, dtype, seqs, heads, 128, 32, 16, 64, dv, pad=0)
+    # what latents hold in place 7 gets to no key, and only in one head to two columns
+    for w in c["w"]:
+        w[:, :, 7] = 0
+    for s, (n, _) in enumerate(seqs):
+        c["kept"][s][:, 7] = 0
+        page = c["table"].col[int(c["table"].rowptr[s]):int(c["table"].rowptr[s + 1])].long()
+        c["cache"][page, :, 7] = 0
+    big = {BF16: 2.0 ** 100, F16: 2.0 ** 15}[dtype]
+    clean = latents._run(c)
+    latents._check(c, seqs, *clean)
+    one = c["w"][1][1].clone()
+    c["w"][1][1, 2, 7], c["w"][1][1, dv - 1, 7] = big, -big
+    inf = float("inf")
+    for token in (0, 390, 400, 400 + new // 2, 400 + new - 1):
+        _put(c, token, {7: big})
+        got = [x.clone() for x in latents._run(c)]
+        c["w"][1][1], whole = one, c["w"][1][1].clone()  # (the bounds' values are the clean ones)
+        _wild_columns(c, clean, got, seqs, max(0, token - 400), {2: inf, dv - 1: -inf}, head=1)
+        c["w"][1][1] = whole
+        if token >= 400:  # another one, of the other sign, that all rows see
+            _put(c, 60, {7: -big})
+            got = [x.clone() for x in latents._run(c)]
+            x = f64(got[0][:new, 1, 2])
+            assert np.isnan(x[token - 400:]).all() and (x[:token - 400] == -inf).all()
+            x = f64(got[0][:new, 1, dv - 1])
+            assert np.isnan(x[token - 400:]).all() and (x[:token - 400] == inf).all()
+            _put(c, 60, {7: 0.0})
+        _put(c, token, {7: 0.0})
+
+
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=str)
+@pytest.mark.parametrize("scale", [0.1, -0.1])
+@pytest.mark.parametrize("new", [3, 40])
+def test_an_infinite_value_of_weight_0(new, scale, dtype, form):
+    """A key whose score is -infinity has no weight, and 0 times its infinite value is NaN: in that
+    value's column, wherever the key lies, and in no other, whose results do not know the key."""
+    rng = np.random.default_rng(62)
+    seqs = [(400 + new, new), (31, min(new, 7))]
+    c = latents._case(rng, dtype, seqs, 3, 128, 32, 16, pad=0, **(dict(dn=64, dv=48) if form == "expanded" else {}))
+    column = 7
+    for s, (n, _) in enumerate(seqs):
+        c["kept"][s][:, 7] = 0
+        page = c["table"].col[int(c["table"].rowptr[s]):int(c["table"].rowptr[s + 1])].long()
+        c["cache"][page, :, 7] = 0
+    c["q"][:, :, 7] = -1.0 if scale > 0 else 1.0
+    value = float("inf")
+    if form == "expanded":  # one value of the keys and one of the values are infinite
+        big = {BF16: 2.0 ** 100, F16: 2.0 ** 15}[dtype]
+        value, column = big, 5
+        for w in c["w"]:
+            w[:, :, 7] = 0
+        c["w"][0][:, 7, 7] = c["w"][1][:, 5, 7] = big
+    c["scale"] = scale
+    clean = latents._run(c)
+    latents._check(c, seqs, *clean)
+    for token in (0, 390, 400, 400 + new - 1):
+        page = int(c["table"].col[token // 16])
+        old = c["cache"][page, token % 16].clone()
+        c["cache"][page, token % 16, 7] = value
+        out, lse = latents._run(c)
+        # the same without the key, by a score that leaves it no weight either
+        c["cache"][page, token % 16] = 0
+        c["cache"][page, token % 16, 7] = 2.0 ** 14
+        if form == "expanded":
+            c["w"][1][:, 5, 7] = 0
+        want, wlse = latents._run(c)
+        if form == "expanded":
+            c["w"][1][:, 5, 7] = big
+        c["cache"][page, token % 16] = old
+        first = max(0, token - 400)
+        assert torch.isnan(out[first:new, :, column]).all(), token
+        out[first:new, :, column] = want[first:new, :, column]
+        assert torch.equal(out[first:new], want[first:new]) and torch.equal(lse[first:new], wlse[first:new]), token
+        assert torch.equal(out[:first], clean[0][:first]) and torch.equal(lse[:first], clean[1][:first])
+        assert torch.equal(out[new:], clean[0][new:]) and torch.equal(lse[new:], clean[1][new:])
