@@ -55,7 +55,10 @@ typedef struct {
  * and head_dim / 32 scales for the key and for the value of every slot and
  * head. head_dim is a multiple of 32. Codes' data and strides are multiples of
  * 16 bytes; scales have any. A cache whose places overlap (a stride that does
- * not pass what smaller ones reach) is read, and refused where it is written. */
+ * not pass what smaller ones reach, or a byte that two of the four tensors have)
+ * is read, and refused where it is written. Tensors may lie between each other's
+ * places, as parts of one allocation do; where their strides are so unlike that
+ * telling them apart takes thousands of steps, they count as overlapping. */
 typedef struct {
     int32_t format;    /* spgemm_mx_format                                     */
     int32_t reserved;  /* 0                                                    */

@@ -77,8 +77,8 @@ class QuantizedCache:
     every 32 values: codes [pages, slots, heads_kv, dim] or [..., dim / 2] and
     scales [..., dim / 32], uint8 (what they stand for: see
     ``include/spgemm_cache.h``). The tensors may be views with any strides whose
-    last dimension is contiguous; they are used as they are, not copied (views
-    whose places overlap, as expanded ones, are read but not written). Where they
+    last dimension is contiguous; they are used as they are, not copied (where
+    places overlap, of one as in expanded views or of two, they are read but not written). Where they
     lie is looked up in every call: their memory may be given back and taken
     again between calls, and another tensor of the same shape may be put in place
     of one (``k_codes``, ``k_scales``, ``v_codes``, ``v_scales``).

@@ -4,6 +4,7 @@
 #include "attention_checks.h"
 #include "latent.h"
 #include "mx.h"
+#include "overlap.h"
 
 using namespace sg;
 
@@ -121,18 +122,19 @@ bool mx_format_valid(const spgemm_mx_cache* c) {
     return c && (c->format == SPGEMM_MX_E4M3 || c->format == SPGEMM_MX_E2M1) && c->reserved == 0;
 }
 
-// Whether no two of a tensor's places share a byte: in ascending order, every
-// stride passes all that is reached by those below it.
-bool bytes_apart(const spgemm_mx_bytes& x, const spgemm_mx_cache* c, int heads, int width) {
-    struct { int64_t stride, count; } dims[3] = {
-        {x.stride_page, c->npages}, {x.stride_slot, c->page_size}, {x.stride_head, heads}};
-    std::sort(dims, dims + 3, [](const auto& a, const auto& b) { return a.stride < b.stride; });
-    __int128 span = width;
-    for (const auto& d : dims) {
-        if (d.count <= 1) continue;
-        if (d.stride < span) return false;
-        span += (__int128)d.stride * (d.count - 1);
-    }
+// Whether no two places of a cache share a byte, in one of its tensors or in two.
+bool cache_apart(const spgemm_mx_cache* c, int heads, int codes, int scales) {
+    const auto places = [&](const spgemm_mx_bytes& x, int width) {
+        return Places{(int64_t) reinterpret_cast<intptr_t>(x.data), width,
+                      {x.stride_page, x.stride_slot, x.stride_head}, {c->npages, c->page_size, heads}};
+    };
+    const Places all[4] = {places(c->k_codes, codes), places(c->v_codes, codes),
+                           places(c->k_scales, scales), places(c->v_scales, scales)};
+    for (const Places& p : all)
+        if (!places_apart(p)) return false;
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (places_meet(all[i], all[j])) return false;
     return true;
 }
 
@@ -159,10 +161,7 @@ int mx_rows(const spgemm_attention_desc* desc, const spgemm_rows* k, const spgem
         if (rc != SPGEMM_OK) return rc;
         const int codes = cache->format == SPGEMM_MX_E4M3 ? a.s.dim : a.s.dim / 2;
         const int scales = a.s.dim / SPGEMM_MX_BLOCK;
-        if (!output && !(bytes_apart(cache->k_codes, cache, a.s.hkv, codes) &&
-                         bytes_apart(cache->v_codes, cache, a.s.hkv, codes) &&
-                         bytes_apart(cache->k_scales, cache, a.s.hkv, scales) &&
-                         bytes_apart(cache->v_scales, cache, a.s.hkv, scales)))
+        if (!output && cache->npages > 0 && !cache_apart(cache, a.s.hkv, codes, scales))
             return SPGEMM_ERR_INVALID_ARG;
         run(a);
         return SPGEMM_OK;

@@ -159,3 +159,32 @@ def test_paged_starts_out_of_order(count):
         paths._paged_check(c, seqs, 0.125, out, lse, skip=bad)
         assert (out[:len(rows)][rows] == 7).all() and (lse[:len(rows)][rows] == 9).all()
         assert torch.isnan(out[nan]).all() and torch.isnan(lse[nan]).all()
+
+
+@pytest.mark.parametrize("form", quantized.FORMS)
+def test_tensors_of_one_allocation_are_written(form):
+    """Tensors that lie between each other's places, by page, by slot and by head, are apart; the
+    same bytes for keys and values are not, and are read."""
+    from spgemm_irregular_matrices_amd import cache
+    rng = np.random.default_rng(55)
+    index, pool, order, rowptr, tokens = quantized._index(rng, [(40, 7), (33, 5)], 16, 0)
+    x = quantized._query(rng, tokens, 2, 64, BF16)
+    plain = quantized._empty(pool, 16, 2, 64, form)
+    plain.write(x, -x, **index)
+    want = plain.read(**index, tokens=tokens)
+    w = 64 if form == "e4m3" else 32
+    for cut in range(4):  # the axis inside which the four lie one after another
+        lead, places = (pool, 16, 2)[:cut], (pool, 16, 2)[cut:]
+        size = [int(np.prod(places)) * n for n in (w, 2, w, 2)]
+        at = np.concatenate([[0], np.cumsum([(n + 15) // 16 * 16 for n in size])])
+        room = torch.zeros(*lead, int(at[-1]), dtype=torch.uint8, device="cuda")
+        parts = [room[..., a:a + n].unflatten(-1, (*places, -1)) for a, n in zip(at, size)]
+        c = cache.QuantizedCache(*parts, form)
+        c.write(x, -x, **index)
+        got = c.read(**index, tokens=tokens)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    both = cache.QuantizedCache(plain.k_codes, plain.k_scales, plain.k_codes, plain.k_scales, form)
+    k, v = both.read(**index, tokens=tokens)
+    assert torch.equal(k, want[0]) and torch.equal(v, want[0])
+    with pytest.raises(binding.SpgemmError):
+        both.write(x, x, **index)
