@@ -7,7 +7,8 @@ tensors, every step runs in the HIP library's kernels. All tensors of a call
 are on one device; the call runs on ``stream`` (default: that device's current
 stream), which the tensors it allocates then belong to. Nothing here waits for
 the GPU, except making and closing a plan. Calls are not recorded by autograd:
-while it records, tensors that require gradients are refused.
+while it records, tensors that require gradients are refused, outputs among them,
+and so are tensors with a tangent in forward mode.
 """
 from __future__ import annotations
 
@@ -154,14 +155,36 @@ def _dims(q, k):
     return a[1], b[1], a[2]
 
 
-def _unrecorded():
-    """For tensors that require gradients: autograd does not see the library's
-    calls, and a result would be cut off from its inputs."""
+_forward_ad = None
+
+
+def _forward_mode() -> bool:
+    """Whether tensors may have a tangent: a level of forward mode is open."""
+    global _forward_ad
+    if _forward_ad is None:
+        from torch.autograd import forward_ad as _forward_ad
+    return getattr(_forward_ad, "_current_level", 0) >= 0
+
+
+def _given_requires(a, b, c=None) -> bool:
+    """Whether one of these outputs, if it was given, requires gradients."""
+    return (a is not None and a.requires_grad or b is not None and b.requires_grad
+            or c is not None and c.requires_grad)
+
+
+def _unrecorded(*tensors):
+    """For tensors that require gradients, or have a tangent: autograd does not see the
+    library's calls, and a result would be cut off from its inputs."""
     import torch
-    if torch.is_grad_enabled():
+    given = [t for t in tensors if t is not None]
+    if torch.is_grad_enabled() and any(t.requires_grad for t in given):
         raise ValueError("attention calls are not recorded by autograd: call them under "
                          "torch.no_grad(), or from a torch.autograd.Function of forward and "
                          "backward, for tensors that require gradients")
+    if any(torch.autograd.forward_ad.unpack_dual(t).tangent is not None for t in given):
+        raise ValueError("attention calls are not recorded by autograd's forward mode: call them "
+                         "with primal tensors, or from a torch.autograd.Function with a jvp, for "
+                         "tensors that have a tangent")
 
 
 def _scale(scale, dim) -> float:
@@ -249,8 +272,9 @@ class AttentionPlan:
         may be passed to be written into. scale defaults to dim ** -0.5."""
         import torch
         hq, hkv, dim = _dims(q, k)
-        if q.requires_grad or k.requires_grad or v.requires_grad:
-            _unrecorded()
+        if (q.requires_grad or k.requires_grad or v.requires_grad or _given_requires(out, lse)
+                or _forward_mode()):
+            _unrecorded(q, k, v, out, lse)
         dtype, device = q.dtype, q.device
         self._ready(device)
         big, small, line = (self.nrows, hq, dim), (self.ncols, hkv, dim), (self.nrows, hq)
@@ -280,8 +304,9 @@ class AttentionPlan:
         import torch
         hq, hkv, dim = _dims(q, k)
         if (q.requires_grad or k.requires_grad or v.requires_grad or dout.requires_grad
-                or out.requires_grad):
-            _unrecorded()
+                or out.requires_grad or lse.requires_grad or _given_requires(dq, dk, dv)
+                or _forward_mode()):
+            _unrecorded(q, k, v, dout, out, lse, dq, dk, dv)
         dtype, device = q.dtype, q.device
         self._ready(device)
         big, small = (self.nrows, hq, dim), (self.ncols, hkv, dim)
@@ -333,8 +358,9 @@ def paged_attention(q, k_cache, v_cache, pages: DeviceCSR, q_rowptr, lengths, ma
         raise ValueError(f"q {tuple(q.shape)}, k_cache {tuple(k_cache.shape)} and v_cache "
                          f"{tuple(v_cache.shape)} do not fit: expected (tokens, heads, dim) and "
                          "twice (pages, slots, kv heads, dim)")
-    if q.requires_grad or k_cache.requires_grad or v_cache.requires_grad:
-        _unrecorded()
+    if (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad
+            or _given_requires(out, lse) or _forward_mode()):
+        _unrecorded(q, k_cache, v_cache, out, lse)
     tokens, hq, dim = q.shape
     npages, slots, hkv, _ = k_cache.shape
     dtype, device, seqs = q.dtype, q.device, pages.nrows

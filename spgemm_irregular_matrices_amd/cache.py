@@ -11,7 +11,8 @@ import ctypes
 
 from . import attention as _a
 from . import binding as _b
-from .attention import _check, _flat, _heads, _new, _on_device, _raw_stream, _type_code, _unrecorded
+from .attention import (_check, _flat, _forward_mode, _given_requires, _heads, _new, _on_device,
+                        _raw_stream, _type_code, _unrecorded)
 from .binding import DeviceCSR, SpgemmError  # noqa: F401  (SpgemmError: what calls raise)
 
 EXPORTS = ["spgemm_mx_write", "spgemm_mx_read", "spgemm_mx_attention_workspace",
@@ -170,8 +171,8 @@ class QuantizedCache:
         nearest code; a block of 32 with an infinity or a NaN becomes NaN.
         Nothing of a sequence that breaks the rules is written."""
         lib = load()
-        if k.requires_grad or v.requires_grad:
-            _unrecorded()
+        if k.requires_grad or v.requires_grad or _forward_mode():
+            _unrecorded(k, v)
         desc, ks, vs = self._rows(k, v, "k")
         ref = ctypes.byref
         with _on_device(self.device, stream):
@@ -189,8 +190,8 @@ class QuantizedCache:
         that breaks the rules become NaN."""
         import torch
         lib = load()
-        if k is not None and k.requires_grad or v is not None and v.requires_grad:
-            _unrecorded()
+        if _given_requires(k, v) or _forward_mode():
+            _unrecorded(k, v)
         with _on_device(self.device, stream):
             given = k if k is not None else v
             if given is not None:
@@ -220,8 +221,8 @@ class QuantizedCache:
         lib = load()
         if q.dim() != 3 or q.shape[2] != self.dim:
             raise ValueError(f"q has shape {tuple(q.shape)}, expected (tokens, heads, {self.dim})")
-        if q.requires_grad:
-            _unrecorded()
+        if q.requires_grad or _given_requires(out, lse) or _forward_mode():
+            _unrecorded(q, out, lse)
         tokens, hq, dim = q.shape
         dtype, device = q.dtype, self.device
         desc = _a.Desc(_type_code(dtype), hq, self.heads, dim, _a._scale(scale, dim))

@@ -10,7 +10,8 @@ from __future__ import annotations
 import ctypes
 
 from . import attention as _a
-from .attention import _check, _flat, _heads, _on_device, _raw_stream, _unrecorded
+from .attention import (_check, _flat, _forward_mode, _given_requires, _heads, _on_device,
+                        _raw_stream, _unrecorded)
 from .binding import DeviceCSR, SpgemmError  # noqa: F401  (SpgemmError: what calls raise)
 from .cache import _batch
 
@@ -95,8 +96,8 @@ def latent_attention(q, cache, pages: DeviceCSR, q_rowptr, lengths, max_q: int, 
     if q.dim() != 3 or cache.dim() != 3 or cache.shape[2] != q.shape[2]:
         raise ValueError(f"q {tuple(q.shape)} and cache {tuple(cache.shape)} do not fit: expected "
                          "(tokens, heads, dim) and (pages, slots, dim)")
-    if q.requires_grad or cache.requires_grad:
-        _unrecorded()
+    if q.requires_grad or cache.requires_grad or _given_requires(out, lse) or _forward_mode():
+        _unrecorded(q, cache, out, lse)
     tokens, heads, dim = q.shape
     if not 0 < value_dim <= dim:
         raise ValueError(f"value_dim is {value_dim}, the cache's rows have {dim} values")
@@ -144,8 +145,9 @@ def latent_attention_expanded(q, cache, w_k, w_v, pages: DeviceCSR, q_rowptr, le
                          f"w_v {tuple(w_v.shape)} do not fit: expected (tokens, heads, key_dim + "
                          "rope_dim), (pages, slots, latent_dim + rope_dim), (heads, key_dim, "
                          "latent_dim) and (heads, value_dim, latent_dim)")
-    if q.requires_grad or cache.requires_grad or w_k.requires_grad or w_v.requires_grad:
-        _unrecorded()
+    if (q.requires_grad or cache.requires_grad or w_k.requires_grad or w_v.requires_grad
+            or _given_requires(out, lse) or _forward_mode()):
+        _unrecorded(q, cache, w_k, w_v, out, lse)
     dtype, device = q.dtype, q.device
     desc = LatentDesc(_type_code(dtype), heads, latent_dim, rope_dim, key_dim, value_dim,
                       _a._scale(scale, dim))
