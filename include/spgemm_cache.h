@@ -164,7 +164,10 @@ SPGEMM_API int spgemm_latent_attention(const spgemm_latent_desc* desc, const spg
  * that leaves, rounded): that is for chunks of many new tokens; a few are the
  * absorbed form's, with W_k and W_v multiplied into q and out. A product past
  * the type's range is infinite. The workspace grows with the smaller of the page
- * table's room * page_size and sequences * max_length. Errors and broken batches:
+ * table's room * page_size and sequences * max_length, times the call's heads (4
+ * bytes a value: 17 GB for 128 heads of 128 + 128 over 128 K tokens); a caller
+ * bounds it by calls for groups of heads, whose q, w_k, w_v and out are slices of
+ * the whole ones. Errors and broken batches:
  * as spgemm_paged_attention; the workspace call needs the cache's page size. */
 SPGEMM_API int spgemm_latent_expanded_workspace(const spgemm_latent_desc* desc,
                                                 const spgemm_latent_cache* cache,

@@ -131,7 +131,9 @@ def latent_attention_expanded(q, cache, w_k, w_v, pages: DeviceCSR, q_rowptr, le
     head's key as they are. q is [tokens, heads, key_dim + rope_dim], out
     [tokens, heads, value_dim]; scale defaults to (key_dim + rope_dim) ** -0.5.
     The index arguments are ``paged_attention``'s, and so is what a broken
-    batch gets."""
+    batch gets. The keys and values are made in a workspace, 4 (key_dim +
+    value_dim) bytes for a cached token and head: calls for groups of heads, on
+    slices of q, w_k, w_v and out, need a part of it at a time."""
     lib = load()
     if q.dim() != 3 or cache.dim() != 3 or w_k.dim() != 3 or w_v.dim() != 3:
         raise ValueError(f"q {tuple(q.shape)}, cache {tuple(cache.shape)}, w_k {tuple(w_k.shape)} and "

@@ -188,3 +188,37 @@ def test_tensors_of_one_allocation_are_written(form):
     assert torch.equal(k, want[0]) and torch.equal(v, want[0])
     with pytest.raises(binding.SpgemmError):
         both.write(x, x, **index)
+
+
+class _WithoutLse:
+    """The library, with NULL for a call's lse (its argument before the workspace)."""
+
+    def __init__(self, lib):
+        self._lib = lib
+
+    def __getattr__(self, name):
+        entry = getattr(self._lib, name)
+        if name.endswith("_workspace"):
+            return entry
+        return lambda *args: entry(*args[:-4], None, *args[-3:])
+
+
+@pytest.mark.parametrize("seqs", [[(900, 1), (5, 1), (70, 1)], [(900, 40), (5, 5), (130, 64)]])
+@pytest.mark.parametrize("call", ["absorbed", "expanded", "quantized"])
+def test_results_without_lse(call, seqs, monkeypatch):
+    """The log-sum-exps may be left out: the results are the same, whole or joined."""
+    from spgemm_irregular_matrices_amd import cache, latent
+    if call == "quantized":
+        c, index, _, tokens = quantized._filled(np.random.default_rng(56), seqs, 64, 2, 16, "e4m3")
+        q = quantized._query(np.random.default_rng(57), tokens, 8, 64, BF16)
+        run = lambda **more: c.attention(q, **index, **more)  # noqa: E731
+    else:
+        c = _latent_batch(call, seqs)
+        run = lambda **more: latents._run(c, **more)  # noqa: E731
+    want, lse = run()
+    for module in (cache, latent):
+        monkeypatch.setattr(module, "load", lambda lib=_WithoutLse(module.load()): lib)
+    untouched = torch.full_like(lse, 9.0)
+    out, _ = run(lse=untouched)
+    some = sum(m for _, m in seqs)
+    assert torch.equal(out[:some], want[:some]) and (untouched == 9).all()
