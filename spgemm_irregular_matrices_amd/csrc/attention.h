@@ -134,7 +134,6 @@ void paged_join(const PagedArgs& a, hipStream_t st);
 // tokens times the query heads of a key head), and the rows of its tiles.
 bool paged_wide(const AttnShape& s, int64_t rows);
 constexpr int kPagedTileMost = 128;
-constexpr int kEvenSeqs = 256;  // sequences that EvenSplit takes
 int paged_tile_rows(const AttnShape& s, int64_t rows);
 
 // The grid of at least that many work groups, which kernels number along x, then

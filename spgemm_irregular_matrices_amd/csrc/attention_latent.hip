@@ -271,7 +271,7 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
     // a sequence, or a range of all of them
     int s = (int)unit, before = 0, pos = 0, end = 0, begin = 0;
     if (a.ranges) {
-        const EvenSplit e(a, kKeys);
+        const EvenSplit<kAbsorbedEvenSeqs> e(a, kKeys);
         begin = pos = (int)min(unit * e.per, (int64_t)e.total);
         end = min(pos + e.per, e.total);
         if (pos >= end) return;
@@ -1249,7 +1249,8 @@ void latent_attention(const LatentArgs& a, bool absorbed, hipStream_t st) {
     if (a.npieces == 1 && a.ranges == 0) return;
     with_latent_type(a.s.type, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;
-        join_parts<T>(a, tiles, rows, kAbsorbedKeys, kShift<T>, st);
+        if (a.seqs <= 256) join_parts<T, 256>(a, tiles, rows, kAbsorbedKeys, kShift<T>, st);
+        else join_parts<T, kAbsorbedEvenSeqs>(a, tiles, rows, kAbsorbedKeys, kShift<T>, st);
     });
 }
 

@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kWaves* kWave, kMxResident<G::kDim>) void k_mx(MxAr
     unit /= a.s.hkv;
     if (a.ranges) {
         range = (int)unit;
-        const EvenSplit e(a, KT);
+        const EvenSplit<kMxEvenSeqs> e(a, KT);
         pos = (int)min((int64_t)range * e.per, (int64_t)e.total);
         end = min(pos + e.per, e.total);
         if (pos >= end) return;
@@ -763,7 +763,7 @@ void mx_attention(const MxArgs& a, hipStream_t st) {
         }
         SG_LAUNCH_CHECK();
         if (a.ranges)
-            join_parts<T>(a, (int32_t)tiles, 16, G::KT, kProbShift<T>, st);
+            join_parts<T, kMxEvenSeqs>(a, (int32_t)tiles, 16, G::KT, kProbShift<T>, st);
         else if (a.npieces > 1)
             paged_join(a, st);
     });

@@ -167,17 +167,18 @@ __device__ __forceinline__ void store_row(const PagedArgs& a, const TileJob& j, 
 // whatever the texts' lengths. A sequence's part of a range is a segment; the
 // segments of a sequence that lies in several ranges are joined. Range i leaves
 // such a part in slot 2 i if the range begins with it, else in 2 i + 1. By a whole
-// wavefront; up to kEvenSeqs sequences of less than 2^31 tiles.
-
+// wavefront; up to SEQS sequences of less than 2^31 tiles.
+template <int SEQS>
 struct EvenSplit {
-    static constexpr int kEach = kEvenSeqs / kWave;
+    static constexpr int kEach = SEQS / kWave;
     int n[kEach];  // tiles of sequences lane, 64 + lane, ...
     int total = 0, per;
     __device__ __forceinline__ EvenSplit(const PagedArgs& a, int keys) {
 #pragma unroll
+        for (int i = 0; i < kEach; ++i) n[i] = 0;
+#pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            n[i] = 0;
-            if (i * kWave >= a.seqs) continue;
+            if (i * kWave >= a.seqs) break;
             const int64_t s = i * kWave + lane_id();
             if (s < a.seqs) {
                 const Sequence sq = read_sequence(a, s);
@@ -209,7 +210,7 @@ struct EvenSplit {
         before = own = 0;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            if (s < i * kWave) continue;
+            if (s < i * kWave) break;
             const int in = wave_inclusive_scan_i32(n[i]);
             if (s >= (i + 1) * kWave) {
                 before += last(in);
@@ -226,7 +227,8 @@ struct EvenSplit {
 struct EvenParts {
     int range, count;
     bool late;
-    __device__ __forceinline__ EvenParts(const EvenSplit& e, int s, int keys, int sees) {
+    template <int SEQS>
+    __device__ __forceinline__ EvenParts(const EvenSplit<SEQS>& e, int s, int keys, int sees) {
         int before, own;
         e.sequence(s, before, own);
         range = before / e.per;

@@ -184,7 +184,7 @@ void mx_pieces(PagedArgs* a) {
     } else {
         const int64_t tiles = std::max<int64_t>(ceil_div(rows, tile), 1);
         const int64_t most = a->seqs * ceil_div(a->max_length, kMxKeys);
-        if (a->seqs <= kEvenSeqs && a->seqs * a->s.hkv * tiles < each * 2048 &&
+        if (a->seqs <= kMxEvenSeqs && a->seqs * a->s.hkv * tiles < each * 2048 &&
             most > a->seqs && most < INT32_MAX / 2) {
             a->piece = std::max(a->max_length, 1);
             a->ranges = (int32_t)std::max<int64_t>(std::min(most, each * 1024 / (a->s.hkv * tiles)), 1);
@@ -225,12 +225,21 @@ void latent_shape(const spgemm_latent_desc* d, const spgemm_paged_batch* b, bool
     a->rope_at = 2 * d->latent_dim;
     const int64_t tile = latent_tile_rows(*a, absorbed);
     if (absorbed) {
-        // One work group per compute unit is there at once: where sequences and
-        // tiles of rows are fewer than two each, all keys are cut evenly.
+        // One work group per compute unit is there at once, and a text by itself is as
+        // slow as it is long: all keys are cut evenly over them, by what a wavefront can look
+        // over. (128 heads: 300 texts up to 512 tokens, one of 32 K, take 178 us, in a work
+        // group a text 1563; 64 up to 1000, one of 32 K, 4 new tokens each, 212 and 1549; 300
+        // up to 4096 374 and 397; 600 of 2048 each, which end together anyway, 640 and 563;
+        // 1100 up to 512, one of 32 K, are not cut: 1710.) Not where most tiles of rows
+        // would be empty, as where a chunk's are everybody's: 1000 texts up to 1000, one of
+        // them with 30 new tokens, 1103 us uncut.
         const int64_t tiles = std::max<int64_t>(ceil_div((int64_t)a->max_new * a->s.group, tile), 1);
+        const int64_t full = std::max(a->seqs, a->tokens * a->s.group / tile);
+        const bool even = a->seqs <= kAbsorbedEvenSeqs &&
+                          (a->seqs * tiles < 512 || (tiles <= 64 && a->seqs * tiles <= 4 * full));
         const int64_t most = a->seqs * ceil_div(a->max_length, kAbsorbedKeys);
         a->piece = std::max(a->max_length, 1);
-        if (a->seqs <= kEvenSeqs && a->seqs * tiles < 512 && most > a->seqs && most < INT32_MAX / 2)
+        if (even && most > a->seqs && most < INT32_MAX / 2)
             a->ranges = (int32_t)std::max<int64_t>(std::min(most, 256 / tiles), 1);
     } else {
         // one work group of 256 rows per compute unit or two of 128 are there at once, in

@@ -19,6 +19,7 @@ struct LatentArgs : PagedArgs {
     int64_t made_rows = 0;
     int64_t made_step = 0;   // rows per sequence; 0: a row per place of the table
 };
+constexpr int kAbsorbedEvenSeqs = 1024;  // sequences that are cut evenly
 constexpr int kAbsorbedKeys = 64;  // keys per tile of the absorbed form
 int latent_tile_rows(const LatentArgs& a, bool absorbed);
 void latent_attention(const LatentArgs& a, bool absorbed, hipStream_t st);

@@ -20,6 +20,7 @@ struct MxArgs : PagedArgs {  // k, v and their strides: the codes'
 struct MxRowsArgs : MxArgs {
     AttnRows rk, rv;
 };
+constexpr int kMxEvenSeqs = 256;  // sequences that are cut evenly
 constexpr int kMxKeys = 32;  // keys per tile of single wavefronts
 void mx_write(const MxRowsArgs& a, hipStream_t st);
 void mx_read(const MxRowsArgs& a, hipStream_t st);

@@ -189,3 +189,23 @@ def test_expanded_in_groups_of_heads(dtype):
         lse.append(part)
     latents._check(c, seqs, out, torch.cat(lse, 1))
     assert (out[-2:] == 7).all()
+
+
+@pytest.mark.parametrize("count,heads,new", [(256, 128, 1), (300, 128, 1), (1024, 16, 1), (1025, 16, 1), (64, 128, 4), (90, 40, 5)])
+def test_a_long_text_among_many(count, heads, new):
+    """Cut evenly over the card, with those around it, up to 1024 texts; with one that breaks the
+    rules. Every call gives the same bits."""
+    rng = np.random.default_rng(count)
+    seqs = [(int(n) + new, new) for n in rng.integers(0, 60, count)]
+    seqs[count // 3], seqs[count - 1] = (2500, new), (700, min(2, new))
+    c = latents._case(rng, BF16, seqs, heads, 64, 16, 16, pad=1)
+    out, lse = latents._run(c)
+    latents._check(c, seqs, out, lse)
+    again = latents._run(c)
+    some = sum(m for _, m in seqs)
+    assert torch.equal(out[:some], again[0][:some]) and torch.equal(lse[:some], again[1][:some])
+    c["lengths"][count // 2] = 10 ** 6
+    out, lse = latents._run(c)
+    latents._check(c, seqs, out, lse, skip=(count // 2,))
+    start = int(c["q_rowptr"][count // 2])
+    assert torch.isnan(out[start:start + new]).all() and torch.isnan(lse[start:start + new]).all()
