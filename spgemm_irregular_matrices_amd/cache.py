@@ -107,10 +107,12 @@ class QuantizedCache:
         self.npages, self.slots, self.heads = npages, slots, heads
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self._last = None
+        self._descs = {}  # of rows, by their type
+        self._space = None, 0  # the last call's sizes and the workspace that they ask for
         self._described()
 
     def __getstate__(self):
-        return {**self.__dict__, "_last": None}  # (addresses are not a copy's)
+        return {**self.__dict__, "_last": None, "_descs": {}}  # (addresses are not a copy's)
 
     def _described(self) -> MxCache:
         """The cache as the library takes it, from its tensors as they are now. (Where they
@@ -161,7 +163,9 @@ class QuantizedCache:
             raise ValueError(f"{what} has shape {tuple(k.shape)}, expected (tokens, {self.heads}, "
                              f"{self.dim})")
         dtype = k.dtype
-        desc = _a.Desc(_type_code(dtype), self.heads, self.heads, self.dim, 0.0)
+        desc = self._descs.get(dtype)
+        if desc is None:
+            desc = self._descs[dtype] = _a.Desc(_type_code(dtype), self.heads, self.heads, self.dim, 0.0)
         return desc, _heads("k", k, k.shape, dtype, self.device), _heads("v", v, k.shape, dtype,
                                                                          self.device)
 
@@ -237,11 +241,16 @@ class QuantizedCache:
             qs = _heads("q", q, q.shape, dtype, device)
             os = _heads("out", out, q.shape, dtype, device)
             batch = _batch(pages, self.npages, q_rowptr, lengths, tokens, max_q, max_len, device)
-            n = ctypes.c_int64(0)
-            _check(lib.spgemm_mx_attention_workspace(ref(desc), ref(batch), ref(n)),
-                   "spgemm_mx_attention_workspace")
-            space, ws = _a._workspace(n.value, device)
+            sizes = dtype, hq, pages.nrows, tokens, max_q, max_len
+            known, n = self._space
+            if sizes != known:
+                size = ctypes.c_int64(0)
+                _check(lib.spgemm_mx_attention_workspace(ref(desc), ref(batch), ref(size)),
+                       "spgemm_mx_attention_workspace")
+                n = size.value
+                self._space = sizes, n
+            space, ws = _a._workspace(n, device)
             _check(lib.spgemm_mx_attention(
                 ref(desc), ref(qs), ref(self._described()), ref(batch), ref(os), lse.data_ptr() or None,
-                ws, n.value, _raw_stream(device)), "spgemm_mx_attention")
+                ws, n, _raw_stream(device)), "spgemm_mx_attention")
         return out, lse
