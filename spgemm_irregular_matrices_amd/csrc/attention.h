@@ -120,12 +120,16 @@ struct PagedArgs {
     const int64_t* q_rowptr = nullptr;
     const int64_t* lengths = nullptr;
     int32_t max_new = 0, max_length = 0;
-    int32_t piece = 0;     // keys per piece, a multiple of 32
-    int32_t npieces = 1;   // ceil(max_length / piece)
+    // Keys per piece, a multiple of 32, and ceil(max_length / piece); where keys are not
+    // cut, or cut in ranges, one piece that holds all (max_length, whatever it divides).
+    int32_t piece = 0;
+    int32_t npieces = 1;
     int32_t ranges = 0;    // not 0: EvenSplit's, instead of pieces
     float* lse = nullptr;
-    float* part = nullptr;     // [piece][token][hq][dim]
-    float* part_ml = nullptr;  // [piece][token][hq][2]
+    // Rows' parts, as pieces [piece][token][hq], as ranges [2 range + late][key head]
+    // [tile][row of the tile]: of each dim values, and its maximum and sum.
+    float* part = nullptr;
+    float* part_ml = nullptr;
 };
 void paged_attention(const PagedArgs& a, hipStream_t st);
 // Joins the pieces of every token and query head (npieces > 1).

@@ -644,8 +644,8 @@ __global__ __launch_bounds__(G::NW* kWave) void k_absorbed(LatentArgs a, int32_t
 // value's as large as the result's own rounding. The keys' last part, of up to
 // 64 elements, is the latent row's. A wavefront takes QB blocks of 16 rows.
 // Bound by the products, 1.8 times the formula's for the second numbers: chunks of
-// 2048 of two texts of up to 16384, 32 heads of 128 + 64 and 128, bfloat16, 1350 us,
-// some 880 TFLOP/s with them; the matrix units are busy for half of the time, softmax
+// 2048 of two texts of up to 16384, 32 heads of 128 + 64 and 128, bfloat16, 1290 us,
+// some 920 TFLOP/s with them; the matrix units are busy for half of the time, softmax
 // and the exchange of tiles take the other.
 template <class T, int MP_, int VP_, int NW_>
 struct ExpandedGeo : Tile<T, 64, true> {

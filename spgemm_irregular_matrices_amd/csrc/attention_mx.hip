@@ -734,8 +734,19 @@ void with_mx(const AttnShape& s, int format, F&& f) {
 
 }  // namespace
 
-// Whether rows of a sequence and key head are worth keys in LDS for all of them:
-// the limits of k_paged_wide, whose tiles these are. (Measured there.)
+// Whether a sequence's rows of a key head are worth keys in LDS for all of them. k_mx cuts
+// ragged texts evenly but turns the codes anew for every 16 rows, k_mx_wide turns them
+// once for 128 (64) and cuts by the longest text, which is all that the host knows of them:
+// between 16 and some 64 rows the texts decide which is better, and the limit lies between.
+// us by k_mx and k_mx_wide, 4 heads (8 where texts are of one length), heads of 128:
+//   8 bits, bf16, 16 rows   64 texts to 8192 85, 142   64 of 3000 63, 64    200 to 400 49, 30
+//                 32 rows                    120, 145  64 of 6000 365, 203             74, 32
+//   4 bits, bf16, 32 rows                    82, 140              208, 191             69, 31
+//   8 bits, fp32, 32 rows                    127, 211             369, 299             79, 42
+//   8 bits, fp16, 64 rows (64 to 16 K, 8 heads) 967, 648          686, 295             101, 39
+// and of 256:
+//   8 bits, bf16, 48 rows   64 to 8192 405, 436        64 of 3000 285, 173  200 to 400 124, 84
+//                 64 rows              524, 445                   353, 177             146, 88
 bool mx_wide(const AttnShape& s, int64_t rows) { return rows > (s.dim > 128 ? 48 : 16); }
 
 int mx_tile_rows(const AttnShape& s, int64_t rows) {
