@@ -230,13 +230,13 @@ void latent_shape(const spgemm_latent_desc* d, const spgemm_paged_batch* b, bool
         // over. (128 heads: 300 texts up to 512 tokens, one of 32 K, take 178 us, in a work
         // group a text 1563; 64 up to 1000, one of 32 K, 4 new tokens each, 212 and 1549; 300
         // up to 4096 374 and 397; 600 of 2048 each, which end together anyway, 640 and 563;
-        // 1100 up to 512, one of 32 K, are not cut: 1710.) Not where most tiles of rows
-        // would be empty, as where a chunk's are everybody's: 1000 texts up to 1000, one of
-        // them with 30 new tokens, 1103 us uncut.
+        // 1100 up to 512, one of 32 K, are not cut: 1710.) Where they are many, only if most
+        // have as many new tokens as the longest chunk, whose tiles are everybody's: a range's
+        // empty tiles leave compute units idle (300 of 2000, half with 4 new tokens and half
+        // with one, 1087 us cut evenly, 825 not).
         const int64_t tiles = std::max<int64_t>(ceil_div((int64_t)a->max_new * a->s.group, tile), 1);
-        const int64_t full = std::max(a->seqs, a->tokens * a->s.group / tile);
-        const bool even = a->seqs <= kAbsorbedEvenSeqs &&
-                          (a->seqs * tiles < 512 || (tiles <= 64 && a->seqs * tiles <= 4 * full));
+        const bool alike = 5 * a->tokens >= 4 * a->seqs * a->max_new;
+        const bool even = a->seqs <= kAbsorbedEvenSeqs && (a->seqs * tiles < 512 || (tiles <= 64 && alike));
         const int64_t most = a->seqs * ceil_div(a->max_length, kAbsorbedKeys);
         a->piece = std::max(a->max_length, 1);
         if (even && most > a->seqs && most < INT32_MAX / 2)
