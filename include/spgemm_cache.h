@@ -140,9 +140,10 @@ typedef struct {
  *
  * with q [tokens, heads, latent_dim + rope_dim] and out [tokens, heads,
  * latent_dim]; lse (may be NULL) as there. Probabilities are rounded to the
- * type before the second product, the result once (both forms; an infinite
- * value whose probability that rounds to 0 gives NaN or itself). Errors and
- * broken batches: as spgemm_paged_attention. */
+ * type before the second product, the result once. (Both forms. An infinite
+ * value whose probability that rounds to 0 gives NaN or itself. Sums are held
+ * times up to 2^8 before the result's division: bfloat16 values past 2^119 may
+ * overflow them.) Errors and broken batches: as spgemm_paged_attention. */
 SPGEMM_API int spgemm_latent_attention_workspace(const spgemm_latent_desc* desc,
                                                  const spgemm_paged_batch* batch, int64_t* bytes);
 SPGEMM_API int spgemm_latent_attention(const spgemm_latent_desc* desc, const spgemm_rows* q,
